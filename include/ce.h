@@ -362,6 +362,150 @@ ce_status ce_fwd_bwd_noalloc(void* logits, ce_dtype dtype, ce_layout layout, int
  * fails. */
 ce_status ce_noalloc_get_error(void* stream, uint32_t* host_err);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the pass at the two ends of the vocabulary: the
+ * embedding rows of the (tied) vocabulary matrix, the norm in front of the
+ * lm_head, and what is applied to the logits before a token is taken from
+ * them.  The conventions above hold; rows of activations are N rows of H
+ * elements, unit stride within a row and one stride (in elements) between
+ * rows.  Any base that is a multiple of the element size and any row stride
+ * work; bases and strides on the 16-byte grid move 16 bytes per load.  All
+ * sums are float32 and taken in an order fixed by the sizes, so results are
+ * the same on every run.
+ */
+
+/* out_i = scale * weight[token_i], computed in float32 and rounded once.
+ *   tokens       int64 (dim0, dim1), token (i, j) at tokens[i*token_strides[0] +
+ *                j*token_strides[1]]; output row i*dim1 + j.  A token equal to
+ *                ignore_idx gives a row of zeros; any other token outside
+ *                [0, V) a row of NaN.
+ *   weight       (V, H) rows weight_stride elements apart, in `dtype`.
+ *   out          rows out_stride elements apart, in `dtype`; no overlap with
+ *                the weight.
+ *   workspace    NULL, or >= 256 bytes, 16-byte aligned: its error word is
+ *                cleared, then gets CE_DEVERR_TARGET_RANGE for an out-of-range
+ *                token (ce_get_error). */
+ce_status ce_embed_fwd(const int64_t* tokens, int64_t dim0, int64_t dim1,
+                       const int64_t token_strides[2], const void* weight, ce_dtype dtype,
+                       int64_t V, int64_t H, int64_t weight_stride, float scale,
+                       int64_t ignore_idx, void* out, int64_t out_stride, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Gradient of ce_embed_fwd:  dW_v = scale * (sum of grad_out_i over tokens
+ * i = v, in float32, in the order of the tokens sorted stably by value).
+ * Ignored and out-of-range tokens give nothing; the latter set
+ * CE_DEVERR_TARGET_RANGE in the workspace.
+ *   grad_out     N = dim0*dim1 rows in `dtype`, grad_out_stride apart (0 for
+ *                one row that all tokens share).
+ *   grad_weight  (V, H) rows grad_weight_stride apart, in grad_dtype: CE_F32, or
+ *                `dtype`.
+ *   accumulate   0: every element is written (zeros for tokens that do not
+ *                occur).  1 (CE_F32 only): added to what is there, rows of
+ *                tokens that do not occur are not touched -- the tied matrix's
+ *                float32 gradient that ce_linear_fwd_bwd has added to.
+ *   workspace    ce_embed_bwd_workspace_bytes(N, H, V) bytes, 16-byte aligned,
+ *                no initialisation; not shared by calls that may overlap. */
+size_t ce_embed_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V);
+ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t grad_out_stride,
+                       const int64_t* tokens, int64_t dim0, int64_t dim1,
+                       const int64_t token_strides[2], int64_t V, int64_t H, float scale,
+                       int64_t ignore_idx, void* grad_weight, ce_dtype grad_dtype,
+                       int64_t grad_weight_stride, int accumulate, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* 8-bit outputs of ce_rmsnorm_fwd. */
+typedef enum { CE_QUANT_NONE = 0, CE_QUANT_E4M3 = 1, CE_QUANT_E5M2 = 2 } ce_quant;
+
+/* The residual's addition and the root-mean-square norm:
+ *   h = x + residual,  y_j = h_j * weight_j / sqrt(mean_j h_j^2 + eps)
+ * in float32; h and y are each rounded once, y from the unrounded h.
+ *   residual     NULL (h = x; residual_out is then optional) or N rows.
+ *   weight       H contiguous elements in weight_dtype: `dtype` or CE_F32.
+ *   out          y: N rows in `dtype`, or with quant N rows of H bytes
+ *                (out_stride in bytes): y_j / scale rounded to nearest even and
+ *                saturated, scale = max(max |y_j| / top, 2^-126) over each run of
+ *                group_size columns (32, 64 or 128; 0: the row), top = 448
+ *                (e4m3) or 57344 (e5m2).  A group that holds an infinity or a
+ *                NaN has no finite values to give.
+ *   scales       with quant: float32 (N, ceil(H / group)) contiguous.
+ *   residual_out h: N rows in `dtype`.  It may replace x or residual, and out (without
+ *                quant) x or residual, with the same strides; other overlaps
+ *                are not allowed.
+ * H up to 2^20. */
+ce_status ce_rmsnorm_fwd(const void* x, const void* residual, const void* weight, ce_dtype dtype,
+                         ce_dtype weight_dtype, int64_t N, int64_t H, int64_t x_stride,
+                         int64_t residual_stride, float eps, void* out, int64_t out_stride,
+                         ce_quant quant, int group_size, float* scales, void* residual_out,
+                         int64_t residual_out_stride, void* stream);
+
+/* Gradients of ce_rmsnorm_fwd (without quant) from the stored h: with
+ * n_j = h_j / sqrt(mean h^2 + eps) and c = mean_j(g_j w_j n_j),
+ *   grad_x_j = (g_j w_j - n_j c) / sqrt(mean h^2 + eps) + grad_h_j
+ *   grad_weight_j = sum over rows of g_j n_j          (float32, written)
+ *   grad_h       the gradient that reaches h from the residual stream, or NULL.
+ *   grad_x       the gradient of x and of the residual alike, rounded once;
+ *                may replace grad_out, h or grad_h with the same strides.
+ *   grad_weight  NULL to skip (no workspace needed then).
+ *   workspace    ce_rmsnorm_bwd_workspace_bytes(N, H) bytes, 16-byte aligned. */
+size_t ce_rmsnorm_bwd_workspace_bytes(int64_t N, int64_t H);
+ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const void* weight,
+                         const void* grad_h, ce_dtype dtype, ce_dtype weight_dtype, int64_t N,
+                         int64_t H, int64_t grad_out_stride, int64_t h_stride,
+                         int64_t grad_h_stride, float eps, void* grad_x, int64_t grad_x_stride,
+                         float* grad_weight, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* What is applied to the logits of a row before a token is taken from them.
+ * Every pointer may be NULL (that step is left out); rows are flattened, r =
+ * i*dim1 + j. */
+typedef struct {
+    const int64_t* history;         /* token k of row r at history[r*history_stride + k];
+                                       tokens outside [0, V) count nowhere */
+    int64_t history_stride;
+    int64_t history_max;            /* tokens a row has room for */
+    const int64_t* history_lengths; /* [N] tokens in use (clamped to [0, history_max]);
+                                       NULL: all */
+    const int64_t* prompt_lengths;  /* [N] the first ones are the prompt: they count for
+                                       the repetition penalty only; NULL: 0 */
+    const float* repetition_penalty; /* [N] > 0 */
+    const float* frequency_penalty; /* [N] */
+    const float* presence_penalty;  /* [N] */
+    const int64_t* bias_tokens;     /* bias k of row r for token bias_tokens[r*stride + k]
+                                       (outside [0, V): none); equal tokens add up in order */
+    const float* bias_values;
+    int64_t bias_tokens_stride, bias_values_stride;
+    int64_t bias_max;               /* biases per row */
+    const int32_t* mask;            /* bit v % 32 of word v / 32: token v is allowed */
+    int64_t mask_stride;            /* words between rows, 0: one mask for all */
+    const float* temperature;       /* [N] > 0 */
+    float mask_value;               /* output of a token that is not allowed */
+    int reserved[2];                /* must be zero */
+} ce_logits_params;
+
+/* Per row, in float32, rounded once, with s_j: token j is in the history, c_j:
+ * its count after the prompt, b_j: its summed biases,
+ *   z_j = s_j ? (x_j > 0 ? x_j / repetition : x_j * repetition) : x_j
+ *   y_j = (z_j - frequency * c_j - presence * [c_j > 0] + b_j) / temperature
+ *   out_j = allowed_j ? y_j : mask_value
+ * A token that is not allowed gives mask_value whatever its logit (NaN
+ * included); a row that allows none is mask_value throughout.  ce_fwd_bwd on
+ * the result needs a finite mask_value (say -3e4: its smoothing term sums the
+ * logits).  out may be the logits themselves (same strides). */
+ce_status ce_logits_process(const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1,
+                            int64_t V, const int64_t strides[3], const ce_logits_params* params,
+                            void* out, const int64_t out_strides[3], void* stream);
+
+/* Gradient of ce_logits_process with respect to the logits:
+ *   grad_j = allowed_j ? grad_out_j / temperature * (s_j ? (x_j > 0 ? 1 / repetition
+ *                        : repetition) : 1) : 0
+ * The logits are read where the history holds their token; the biases, the counts
+ * and mask_value play no part.  grad may be grad_out (same strides), not the logits. */
+ce_status ce_logits_process_bwd(const void* grad_out, const int64_t grad_out_strides[3],
+                                const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1,
+                                int64_t V, const int64_t strides[3],
+                                const ce_logits_params* params, void* grad,
+                                const int64_t grad_strides[3], void* stream);
+
 /* Waits for `stream`, then copies the device error word of the last pass that
  * used `workspace` into *host_err (host pointer).  Returns CE_OK,
  * CE_ERR_TARGET_RANGE or CE_ERR_DEVICE_TIMEOUT from its bits, CE_ERR_LAUNCH if

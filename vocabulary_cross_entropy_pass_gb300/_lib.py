@@ -18,6 +18,7 @@ CE_F32, CE_BF16, CE_F16 = 0, 1, 2
 CE_LAYOUT_BSV, CE_LAYOUT_SBV = 0, 1
 (CE_PATH_AUTO, CE_PATH_ROW, CE_PATH_CLUSTER, CE_PATH_TWO_STAGE, CE_PATH_STREAM, CE_PATH_WARP,
  CE_PATH_VECROW) = (0, 1, 2, 3, 4, 5, 6)
+CE_QUANT_NONE, CE_QUANT_E4M3, CE_QUANT_E5M2 = 0, 1, 2
 CE_DEVERR_TARGET_RANGE, CE_DEVERR_TIMEOUT = 0x1, 0x2
 
 STATUS = {
@@ -36,7 +37,9 @@ STATUS = {
 EXPORTS = ("ce_workspace_bytes", "ce_fwd_bwd", "ce_fwd_only", "ce_get_error", "ce_status_string",
            "ce_plan_path", "ce_fwd_bwd_noalloc", "ce_bwd", "ce_vp_partials", "ce_vp_combine",
            "ce_vp_bwd", "ce_linear_workspace_bytes", "ce_linear_fwd_bwd", "ce_wait_timeout_probe",
-           "ce_noalloc_get_error")
+           "ce_noalloc_get_error", "ce_embed_fwd", "ce_embed_bwd_workspace_bytes", "ce_embed_bwd",
+           "ce_rmsnorm_fwd", "ce_rmsnorm_bwd_workspace_bytes", "ce_rmsnorm_bwd",
+           "ce_logits_process", "ce_logits_process_bwd")
 
 
 class ce_options(ctypes.Structure):
@@ -51,6 +54,29 @@ class ce_options(ctypes.Structure):
         ("tune_l2_keep", ctypes.c_int),
         ("tune_tile_kb", ctypes.c_int),
         ("class_weights", ctypes.c_void_p),
+        ("reserved", ctypes.c_int * 2),
+    ]
+
+
+class ce_logits_params(ctypes.Structure):
+    _fields_ = [
+        ("history", ctypes.c_void_p),
+        ("history_stride", ctypes.c_int64),
+        ("history_max", ctypes.c_int64),
+        ("history_lengths", ctypes.c_void_p),
+        ("prompt_lengths", ctypes.c_void_p),
+        ("repetition_penalty", ctypes.c_void_p),
+        ("frequency_penalty", ctypes.c_void_p),
+        ("presence_penalty", ctypes.c_void_p),
+        ("bias_tokens", ctypes.c_void_p),
+        ("bias_values", ctypes.c_void_p),
+        ("bias_tokens_stride", ctypes.c_int64),
+        ("bias_values_stride", ctypes.c_int64),
+        ("bias_max", ctypes.c_int64),
+        ("mask", ctypes.c_void_p),
+        ("mask_stride", ctypes.c_int64),
+        ("temperature", ctypes.c_void_p),
+        ("mask_value", ctypes.c_float),
         ("reserved", ctypes.c_int * 2),
     ]
 
@@ -107,6 +133,29 @@ def load(path: str = LIB_PATH):
         lib.ce_linear_fwd_bwd.restype = i32
         lib.ce_linear_fwd_bwd.argtypes = [vp, vp, i32, i64, i64, i64, vp, f32, i64, i32, vp, vp, vp,
                                           vp, vp, i64, vp, ctypes.c_size_t, vp]
+        size = ctypes.c_size_t
+        lp = ctypes.POINTER(ce_logits_params)
+        lib.ce_embed_fwd.restype = i32
+        lib.ce_embed_fwd.argtypes = [vp, i64, i64, I64_3, vp, i32, i64, i64, i64, f32, i64, vp, i64,
+                                     vp, size, vp]
+        lib.ce_embed_bwd_workspace_bytes.restype = size
+        lib.ce_embed_bwd_workspace_bytes.argtypes = [i64, i64, i64]
+        lib.ce_embed_bwd.restype = i32
+        lib.ce_embed_bwd.argtypes = [vp, i32, i64, vp, i64, i64, I64_3, i64, i64, f32, i64, vp, i32,
+                                     i64, i32, vp, size, vp]
+        lib.ce_rmsnorm_fwd.restype = i32
+        lib.ce_rmsnorm_fwd.argtypes = [vp, vp, vp, i32, i32, i64, i64, i64, i64, f32, vp, i64, i32,
+                                       i32, vp, vp, i64, vp]
+        lib.ce_rmsnorm_bwd_workspace_bytes.restype = size
+        lib.ce_rmsnorm_bwd_workspace_bytes.argtypes = [i64, i64]
+        lib.ce_rmsnorm_bwd.restype = i32
+        lib.ce_rmsnorm_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i64, i64, i64, i64, i64, f32, vp,
+                                       i64, vp, vp, size, vp]
+        lib.ce_logits_process.restype = i32
+        lib.ce_logits_process.argtypes = [vp, i32, i64, i64, i64, I64_3, lp, vp, I64_3, vp]
+        lib.ce_logits_process_bwd.restype = i32
+        lib.ce_logits_process_bwd.argtypes = [vp, I64_3, vp, i32, i64, i64, i64, I64_3, lp, vp,
+                                              I64_3, vp]
         lib.ce_wait_timeout_probe.restype = i32
         lib.ce_wait_timeout_probe.argtypes = [vp, ctypes.c_size_t, vp]
         lib.ce_get_error.restype = i32

@@ -1,0 +1,600 @@
+// ce_embed.cu -- rows of the (V, H) vocabulary matrix by token, and their
+// gradient.
+//
+//   out_i = scale * W[t_i]           (t_i == ignore_idx: zeros; outside [0, V): NaN)
+//   dW_v (+)= scale * sum over i with t_i = v of g_i
+//
+// Forward: one gathered read and one write per element, bound by HBM.
+//
+// Gradient: equal tokens meet, so the sum is taken over the tokens in sorted
+// order, which makes it the same on every run.
+//   1. ce_embed_sort_kernel: a stable radix sort of (token, position), one
+//      launch, one cluster of up to eight CTAs: each warp counts the digits of
+//      its own run of tokens in shared memory, the CTAs exchange their counts
+//      over distributed shared memory, each warp then writes its run in order.
+//      Ignored and out-of-range tokens become key V and sort to the end.
+//   2. ce_embed_grad_kernel: a CTA sums a fixed number of sorted entries over
+//      a slab of columns, in registers, a gradient row at a time; a token
+//      whose entries all lie in the chunk is written at once, one that crosses
+//      a chunk border leaves its float32 part in the workspace.  Further CTAs
+//      of the same launch zero the rows of tokens that do not occur.
+//   3. ce_embed_join_kernel: the parts of tokens that cross chunk borders,
+//      added in chunk order.
+#include "ce_device.cuh"
+#include "ce_internal.h"
+#include "ce_pack.cuh"
+
+namespace gbce {
+namespace {
+
+struct EmbedFwdArgs {
+    const int64_t* tok;
+    int64_t dim1, ts0, ts1, N;
+    int flat;
+    const char* w;
+    char* out;
+    int64_t ws, os;        // row strides in bytes
+    int64_t V, ignore;
+    int nv;                // vectors per row
+    float scale;
+    uint32_t* err;         // or NULL
+};
+
+__device__ __forceinline__ int64_t token_at(const int64_t* tok, int64_t dim1, int64_t ts0, int64_t ts1, int flat,
+                                            int64_t i) {
+    if (flat) return __ldg(tok + i * ts1);
+    const int64_t a = i / dim1;
+    return __ldg(tok + a * ts0 + (i - a * dim1) * ts1);
+}
+
+// One CTA per token and slab of 128 * U vectors.
+template <typename T, int VEC, int U>
+__global__ void __launch_bounds__(128) ce_embed_fwd_kernel(const __grid_constant__ EmbedFwdArgs p) {
+    constexpr int ES = sizeof(T);
+    const int64_t row = blockIdx.x;
+    const int v0 = blockIdx.y * (128 * U) + threadIdx.x;
+    const int64_t t = token_at(p.tok, p.dim1, p.ts0, p.ts1, p.flat, row);
+    char* out = p.out + row * p.os;
+    const bool in = t >= 0 && t < p.V && t != p.ignore;
+    if (!in) {
+        const float fill = t == p.ignore ? 0.f : __int_as_float(0x7fc00000);
+        Pack<T, VEC> o;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o.set(i, fill);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v0 + u * 128 < p.nv) o.store(out + (int64_t)(v0 + u * 128) * VEC * ES);
+        if (t != p.ignore && p.err && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.err, CE_DEVERR_TARGET_RANGE);
+        return;
+    }
+    const char* src = p.w + t * p.ws;
+    Pack<T, VEC> a[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (v0 + u * 128 < p.nv) a[u].load_nc(src + (int64_t)(v0 + u * 128) * VEC * ES);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (v0 + u * 128 < p.nv) {
+            Pack<T, VEC> o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o.set(i, a[u].f(i) * p.scale);
+            o.store(out + (int64_t)(v0 + u * 128) * VEC * ES);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- sorted tokens
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = 32;
+constexpr int kMaxDigitBits = 10;
+constexpr int kMaxBins = 1 << kMaxDigitBits;
+constexpr int kSortCluster = 8;
+constexpr size_t kWsInvalidOffset = 16;  // uint32 tokens without a gradient
+
+struct SortArgs {
+    const int64_t* tok;
+    int64_t dim1, ts0, ts1;
+    int flat;
+    uint32_t N, V;
+    int64_t ignore;
+    int passes, bits;      // digits of `bits` bits, least first
+    uint32_t* err;
+    uint32_t* invalid;
+    uint2* a;              // (key, position); the sorted ones end in `a`
+    uint2* b;
+    uint32_t* used;        // bit v: token v occurs; or NULL
+};
+
+__device__ __forceinline__ uint32_t ld_dsmem_u32(const uint32_t* local, uint32_t rank) {
+    uint32_t remote, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __grid_constant__ SortArgs p) {
+    extern __shared__ __align__(16) uint32_t sm[];
+    const int bins = 1 << p.bits;
+    uint32_t* hist = sm;                          // [32][bins]: a warp's digit counts, then its next places
+    uint32_t* total = sm + kSortWarps * bins;     // [bins]: this CTA's counts
+    uint32_t* wsum = total + bins;                // [32]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_ctarank(), nc = cluster_nctarank();
+    const uint32_t mask = (uint32_t)bins - 1;
+
+    // each warp owns a run of tokens, in order over warps and CTAs
+    const uint32_t per = (p.N + nc * kSortWarps * 32 - 1) / (nc * kSortWarps * 32) * 32;
+    const uint64_t first = (uint64_t)(rank * kSortWarps + warp) * per;
+    const uint32_t i0 = (uint32_t)(first < p.N ? first : p.N);
+    const uint32_t i1 = (uint32_t)(first + per < p.N ? first + per : p.N);
+
+    if (rank == 0 && tid == 0) {
+        *p.err = 0u;
+        *p.invalid = 0u;
+    }
+    if (p.used) {
+        const uint32_t words = (p.V + 31) / 32;
+        for (uint32_t i = rank * kSortThreads + tid; i < words; i += nc * kSortThreads) p.used[i] = 0u;
+    }
+    __threadfence();
+    cluster_sync();
+
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const uint2* src = (pass & 1) ? p.b : p.a;
+        uint2* dst = (pass & 1) ? p.a : p.b;
+        const int shift = pass * p.bits;
+        for (int i = tid; i < kSortWarps * bins / 4; i += kSortThreads)
+            reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        uint32_t* mine = hist + warp * bins;
+        for (uint32_t base = i0; base < i1; base += 32) {
+            const uint32_t i = base + lane;
+            const bool on = i < i1;
+            uint32_t key = 0;
+            if (pass == 0) {
+                bool ok = true;
+                if (on) {
+                    const int64_t t = token_at(p.tok, p.dim1, p.ts0, p.ts1, p.flat, i);
+                    ok = t >= 0 && t < (int64_t)p.V && t != p.ignore;
+                    key = ok ? (uint32_t)t : p.V;
+                    if (!ok && t != p.ignore) atomicOr(p.err, CE_DEVERR_TARGET_RANGE);
+                    if (ok && p.used) atomicOr(p.used + (key >> 5), 1u << (key & 31));
+                    p.a[i] = make_uint2(key, i);  // what this thread scatters below
+                }
+                const unsigned bad = __ballot_sync(kFull, !ok);
+                if (bad && lane == 0) atomicAdd(p.invalid, (uint32_t)__popc(bad));
+            } else if (on) {
+                key = __ldcg(src + i).x;
+            }
+            const uint32_t d = on ? (key >> shift) & mask : 0xffffffffu;
+            const unsigned peers = __match_any_sync(kFull, d);
+            if (on && lane == __ffs(peers) - 1) mine[d] += __popc(peers);
+            __syncwarp();
+        }
+        __syncthreads();
+        // each bin: exclusive prefix over the warps, then the CTA's total
+        for (int b = tid; b < bins; b += kSortThreads) {
+            uint32_t run = 0;
+#pragma unroll 8
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t c = hist[w * bins + b];
+                hist[w * bins + b] = run;
+                run += c;
+            }
+            total[b] = run;
+        }
+        cluster_sync();
+        uint32_t before = 0, all = 0;  // bins <= threads: one bin per thread
+        if (tid < bins)
+            for (uint32_t r = 0; r < nc; ++r) {
+                const uint32_t c = ld_dsmem_u32(total + tid, r);
+                if (r < rank) before += c;
+                all += c;
+            }
+        // exclusive scan of `all` over the bins
+        uint32_t inc = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        uint32_t ws = wsum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(kFull, ws, o);
+            if (lane >= o) ws += u;
+        }
+        const uint32_t upto = __shfl_sync(kFull, ws, warp == 0 ? 0 : warp - 1);
+        const uint32_t start = (warp == 0 ? 0u : upto) + inc - all + before;
+        if (tid < bins)
+#pragma unroll 8
+            for (int w = 0; w < kSortWarps; ++w) hist[w * bins + tid] += start;
+        __syncthreads();
+        for (uint32_t base = i0; base < i1; base += 32) {
+            const uint32_t i = base + lane;
+            const bool on = i < i1;
+            uint2 e = make_uint2(0, 0);
+            if (on) e = __ldcg(src + i);
+            const uint32_t d = on ? (e.x >> shift) & mask : 0xffffffffu;
+            const unsigned peers = __match_any_sync(kFull, d);
+            uint32_t at = 0;
+            if (on) at = mine[d] + __popc(peers & ((1u << lane) - 1u));
+            __syncwarp();
+            if (on && lane == __ffs(peers) - 1) mine[d] += __popc(peers);
+            __syncwarp();
+            if (on) dst[at] = e;
+        }
+        __threadfence();
+        cluster_sync();  // the next pass reads what all CTAs wrote; no CTA leaves while its counts are read
+    }
+}
+
+// ----------------------------------------------------------------- sums of runs
+struct GradArgs {
+    const uint2* ent;      // sorted (token, position)
+    const uint32_t* invalid;
+    uint32_t N, V;
+    int64_t H;
+    const char* g;
+    int64_t gs;            // gradient row stride in bytes
+    char* dw;
+    int64_t dws;           // in bytes
+    float* part;           // [chunks][2][H]
+    const uint32_t* used;  // or NULL: rows of absent tokens stay as they are
+    int nv;                // vectors per row
+    int R;                 // entries per chunk
+    int chunks;
+    int zero_ctas;         // CTAs per column slab that zero absent rows
+    int accumulate;
+    float scale;
+};
+
+constexpr int kGradThreads = 128;
+constexpr int kMaxR = 64;
+
+template <typename TW, int VEC>
+__device__ __forceinline__ void write_row(char* row, int64_t col, const float* acc, float scale, int accumulate) {
+    if constexpr (sizeof(TW) == 4) {
+        float* q = reinterpret_cast<float*>(row) + col;
+        float o[VEC];
+        if (accumulate) {
+            load_f32<VEC>(q, o);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = fmaf(acc[i], scale, o[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o[i] = acc[i] * scale;
+        }
+        store_f32<VEC>(q, o);
+    } else {
+        Pack<TW, VEC> o;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o.set(i, acc[i] * scale);
+        o.store(row + col * (int64_t)sizeof(TW));
+    }
+}
+
+template <typename T, typename TW, int VEC>
+__global__ void __launch_bounds__(kGradThreads) ce_embed_grad_kernel(const __grid_constant__ GradArgs p) {
+    constexpr int ES = sizeof(T);
+    constexpr int U = 8;
+    const int v = blockIdx.y * kGradThreads + threadIdx.x;
+    const bool on = v < p.nv;
+    const int64_t col = (int64_t)v * VEC;
+    if ((int)blockIdx.x >= p.chunks) {
+        // absent tokens' rows
+        if (!on) return;
+        float z[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) z[i] = 0.f;
+        for (uint32_t r = blockIdx.x - p.chunks; r < p.V; r += p.zero_ctas) {
+            if ((__ldg(p.used + (r >> 5)) >> (r & 31)) & 1u) continue;
+            write_row<TW, VEC>(p.dw + (int64_t)r * p.dws, col, z, 0.f, 0);
+        }
+        return;
+    }
+    __shared__ uint2 ent[kMaxR + 2];  // the chunk's entries between its neighbours
+    const uint32_t n = p.N - *p.invalid;
+    const uint32_t c0 = blockIdx.x * (uint32_t)p.R;
+    if (c0 >= n) return;
+    const int len = (int)min((uint32_t)p.R, n - c0);
+    for (int i = threadIdx.x; i < len + 2; i += kGradThreads) {
+        const int64_t at = (int64_t)c0 + i - 1;
+        ent[i] = (at >= 0 && at < (int64_t)n) ? p.ent[at] : make_uint2(0xffffffffu, 0u);
+    }
+    __syncthreads();
+    if (!on) return;
+    const char* g = p.g + col * ES;
+    float acc[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+    int begin = 1;  // first entry of the current run
+    for (int b = 1; b <= len; b += U) {
+        Pack<T, VEC> x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (b + u <= len) x[u].load_cs(g + (int64_t)ent[b + u].y * p.gs);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = b + u;
+            if (k > len) break;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[i] += x[u].f(i);
+            const uint32_t key = ent[k].x;
+            const bool last = ent[k + 1].x != key;
+            if (last || k == len) {
+                const bool from_here = begin > 1 || ent[0].x != key;
+                if (from_here && last) {
+                    write_row<TW, VEC>(p.dw + (int64_t)key * p.dws, col, acc, p.scale, p.accumulate);
+                } else {
+                    float* q = p.part + ((int64_t)blockIdx.x * 2 + (from_here ? 1 : 0)) * p.H + col;
+                    store_f32<VEC>(q, acc);
+                }
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+                begin = k + 1;
+            }
+        }
+    }
+}
+
+template <typename TW>
+__global__ void __launch_bounds__(kGradThreads) ce_embed_join_kernel(const __grid_constant__ GradArgs p) {
+    const uint32_t n = p.N - *p.invalid;
+    const uint64_t c0 = (uint64_t)blockIdx.x * p.R, c1 = c0 + p.R;
+    if (c1 >= n) return;                        // the last chunk's last run ends there
+    const uint32_t key = p.ent[c1 - 1].x;
+    if (p.ent[c1].x != key) return;             // no run crosses this border
+    if (p.ent[c0].x == key && c0 > 0 && p.ent[c0 - 1].x == key) return;  // it began in an earlier chunk
+    // the run's end: first entry past it
+    uint32_t lo = (uint32_t)c1, hi = n;
+    while (lo < hi) {
+        const uint32_t m = lo + (hi - lo) / 2;
+        if (p.ent[m].x == key) lo = m + 1; else hi = m;
+    }
+    const int64_t last = (lo - 1) / (uint32_t)p.R;  // chunk of its last entry
+    const int64_t col = (int64_t)blockIdx.y * kGradThreads + threadIdx.x;
+    if (col >= p.H) return;
+    float acc = p.part[((int64_t)blockIdx.x * 2 + 1) * p.H + col];
+#pragma unroll 8
+    for (int64_t c = blockIdx.x + 1; c <= last; ++c) acc += p.part[c * 2 * p.H + col];
+    write_row<TW, 1>(p.dw + (int64_t)key * p.dws, col, &acc, p.scale, p.accumulate);
+}
+
+// entries per chunk, from the sizes alone (the workspace holds two float32
+// rows for each chunk)
+int chunk_entries(int64_t N) { return N >= 8192 ? 32 : (N >= 1024 ? 16 : 8); }
+
+struct EmbedWs {
+    size_t a, b, used, part, bytes;
+    int R, chunks;
+};
+EmbedWs embed_ws(int64_t N, int64_t H, int64_t V) {
+    EmbedWs w;
+    w.R = chunk_entries(N);
+    w.chunks = (int)((N + w.R - 1) / w.R);
+    w.a = kWsHeaderBytes;
+    w.b = w.a + align_up((size_t)N * 8, 256);
+    w.used = w.b + align_up((size_t)N * 8, 256);
+    w.part = w.used + align_up((size_t)(V + 31) / 32 * 4, 256);
+    w.bytes = w.part + (size_t)w.chunks * 2 * (size_t)H * 4;
+    return w;
+}
+
+bool bad_dtype(int d) { return d < CE_F32 || d > CE_F16; }
+bool off_grid(const void* p, int es) { return reinterpret_cast<uintptr_t>(p) % es != 0; }
+bool bad_sizes(int64_t N, int64_t H, int64_t V) {
+    return N < 0 || N > 0x7ffffff0LL || H < 1 || H > (1 << 20) || V < 1 || V > 0x7fffffffLL;
+}
+// N of (dim0, dim1), or -1
+int64_t count_of(int64_t d0, int64_t d1) {
+    if (d0 < 0 || d1 < 0 || d0 > 0x7fffffffLL || d1 > 0x7fffffffLL) return -1;
+    return d0 * d1;
+}
+bool tokens_flat(int64_t d0, int64_t d1, const int64_t* ts) { return d0 == 1 || ts[0] == d1 * ts[1]; }
+
+template <typename T, int VEC>
+cudaError_t launch_fwd(EmbedFwdArgs& a, int64_t H, cudaStream_t s) {
+    a.nv = (int)(H / VEC);
+    // few tokens: a vector a thread over more CTAs
+    if (a.N * ((a.nv + 511) / 512) < 1024) {
+        const dim3 grid((unsigned)a.N, (unsigned)((a.nv + 127) / 128));
+        ce_embed_fwd_kernel<T, VEC, 1><<<grid, 128, 0, s>>>(a);
+    } else {
+        const dim3 grid((unsigned)a.N, (unsigned)((a.nv + 511) / 512));
+        ce_embed_fwd_kernel<T, VEC, 4><<<grid, 128, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_fwd_t(EmbedFwdArgs& a, int64_t H, int vb, cudaStream_t s) {
+    constexpr int ES = sizeof(T);
+    if (vb == 16) return launch_fwd<T, 16 / ES>(a, H, s);
+    if constexpr (ES == 2)
+        if (vb == 4) return launch_fwd<T, 2>(a, H, s);
+    return launch_fwd<T, 1>(a, H, s);
+}
+
+template <typename T, typename TW, int VEC>
+cudaError_t launch_grad(GradArgs& a, cudaStream_t s) {
+    a.nv = (int)(a.H / VEC);
+    const unsigned slabs = (unsigned)((a.nv + kGradThreads - 1) / kGradThreads);
+    a.zero_ctas = a.used ? (int)(a.V < 2048 ? a.V : 2048) : 0;
+    ce_embed_grad_kernel<T, TW, VEC><<<dim3((unsigned)(a.chunks + a.zero_ctas), slabs), kGradThreads, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (a.chunks > 1) {
+        const dim3 grid((unsigned)(a.chunks - 1), (unsigned)((a.H + kGradThreads - 1) / kGradThreads));
+        ce_embed_join_kernel<TW><<<grid, kGradThreads, 0, s>>>(a);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+template <typename T>
+cudaError_t launch_grad_t(GradArgs& a, bool w32, int vb, cudaStream_t s) {
+    constexpr int ES = sizeof(T);
+    if (w32) {
+        if (vb == 16) return launch_grad<T, float, 16 / ES>(a, s);
+        if constexpr (ES == 2)
+            if (vb == 4) return launch_grad<T, float, 2>(a, s);
+        return launch_grad<T, float, 1>(a, s);
+    }
+    if constexpr (ES == 2) {
+        if (vb == 16) return launch_grad<T, T, 8>(a, s);
+        if (vb == 4) return launch_grad<T, T, 2>(a, s);
+        return launch_grad<T, T, 1>(a, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_sort(const SortArgs& a, cudaStream_t s) {
+    const int bins = 1 << a.bits;
+    const size_t smem = (size_t)(kSortWarps * bins + bins + 32) * 4;
+    cudaError_t e = cudaFuncSetAttribute(ce_embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)((kSortWarps * kMaxBins + kMaxBins + 32) * 4));
+    if (e != cudaSuccess) return e;
+    int nc = 1;
+    while (nc < kSortCluster && (int64_t)nc * 2048 < a.N) nc *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(nc);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = nc;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ce_embed_sort_kernel, a);
+}
+
+}  // namespace
+}  // namespace gbce
+
+using namespace gbce;
+
+extern "C" ce_status ce_embed_fwd(const int64_t* tokens, int64_t dim0, int64_t dim1, const int64_t token_strides[2],
+                                  const void* weight, ce_dtype dtype, int64_t V, int64_t H, int64_t weight_stride,
+                                  float scale, int64_t ignore_idx, void* out, int64_t out_stride, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    if (bad_dtype(dtype)) return CE_ERR_UNSUPPORTED_DTYPE;
+    const int64_t N = count_of(dim0, dim1);
+    if (bad_sizes(N, H, V) || !token_strides) return CE_ERR_INVALID_ARG;
+    if (workspace && (reinterpret_cast<uintptr_t>(workspace) % 16)) return CE_ERR_INVALID_ARG;
+    if (workspace && workspace_bytes < kWsHeaderBytes) return CE_ERR_WORKSPACE_TOO_SMALL;
+    if (N > 0) {
+        if (!tokens || !weight || !out) return CE_ERR_INVALID_ARG;
+        const int es = elem_size(dtype);
+        if (off_grid(weight, es) || off_grid(out, es) || off_grid(tokens, 8)) return CE_ERR_INVALID_ARG;
+        if (token_strides[0] < 0 || token_strides[1] < 0) return CE_ERR_BAD_STRIDE;
+        if ((V > 1 && weight_stride < H) || (N > 1 && out_stride < H)) return CE_ERR_BAD_STRIDE;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    EmbedFwdArgs a;
+    a.err = workspace ? reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kWsErrOffset) : nullptr;
+    if (a.err && cudaMemsetAsync(a.err, 0, 4, s) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (N == 0) return CE_OK;
+    const int es = elem_size(dtype);
+    a.tok = tokens;
+    a.dim1 = dim1;
+    a.ts0 = token_strides[0];
+    a.ts1 = token_strides[1];
+    a.N = N;
+    a.flat = tokens_flat(dim0, dim1, token_strides);
+    a.w = static_cast<const char*>(weight);
+    a.out = static_cast<char*>(out);
+    a.ws = weight_stride * es;
+    a.os = out_stride * es;
+    a.V = V;
+    a.ignore = ignore_idx;
+    a.scale = scale;
+    const uint64_t vals[] = {(uint64_t)(uintptr_t)weight, (uint64_t)(uintptr_t)out, (uint64_t)(V > 1 ? a.ws : 0),
+                             (uint64_t)(N > 1 ? a.os : 0), (uint64_t)H * es};
+    const int vb = common_vector_bytes(vals, 5, es);
+    cudaError_t e = dtype == CE_F32    ? launch_fwd_t<float>(a, H, vb, s)
+                    : dtype == CE_BF16 ? launch_fwd_t<__nv_bfloat16>(a, H, vb, s)
+                                       : launch_fwd_t<__half>(a, H, vb, s);
+    return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
+}
+
+extern "C" size_t ce_embed_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V) {
+    if (bad_sizes(N, H, V)) return 0;
+    return embed_ws(N, H, V).bytes;
+}
+
+extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t grad_out_stride,
+                                  const int64_t* tokens, int64_t dim0, int64_t dim1,
+                                  const int64_t token_strides[2], int64_t V, int64_t H, float scale,
+                                  int64_t ignore_idx, void* grad_weight, ce_dtype grad_dtype,
+                                  int64_t grad_weight_stride, int accumulate, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    if (bad_dtype(dtype) || (grad_dtype != CE_F32 && grad_dtype != dtype)) return CE_ERR_UNSUPPORTED_DTYPE;
+    if (accumulate && grad_dtype != CE_F32) return CE_ERR_UNSUPPORTED_DTYPE;
+    const int64_t N = count_of(dim0, dim1);
+    if (bad_sizes(N, H, V) || !token_strides || !grad_weight || !workspace) return CE_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(workspace) % 16) return CE_ERR_INVALID_ARG;
+    const int es = elem_size(dtype), wes = elem_size(grad_dtype);
+    if (off_grid(grad_weight, wes)) return CE_ERR_INVALID_ARG;
+    if (V > 1 && grad_weight_stride < H) return CE_ERR_BAD_STRIDE;
+    if (N > 0) {
+        if (!grad_out || !tokens || off_grid(grad_out, es) || off_grid(tokens, 8)) return CE_ERR_INVALID_ARG;
+        if (token_strides[0] < 0 || token_strides[1] < 0 || grad_out_stride < 0) return CE_ERR_BAD_STRIDE;
+    }
+    const EmbedWs w = embed_ws(N, H, V);
+    if (workspace_bytes < w.bytes) return CE_ERR_WORKSPACE_TOO_SMALL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* base = static_cast<char*>(workspace);
+
+    SortArgs sa;
+    sa.tok = tokens;
+    sa.dim1 = dim1 > 0 ? dim1 : 1;
+    sa.ts0 = token_strides[0];
+    sa.ts1 = token_strides[1];
+    sa.flat = tokens_flat(dim0, dim1, token_strides);
+    sa.N = (uint32_t)N;
+    sa.V = (uint32_t)V;
+    sa.ignore = ignore_idx;
+    int bits = 1;
+    while (((uint64_t)V >> bits) != 0) ++bits;  // keys 0 .. V
+    sa.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
+    sa.bits = (bits + sa.passes - 1) / sa.passes;
+    if (sa.bits < 2) sa.bits = 2;
+    sa.err = reinterpret_cast<uint32_t*>(base + kWsErrOffset);
+    sa.invalid = reinterpret_cast<uint32_t*>(base + kWsInvalidOffset);
+    uint2* a = reinterpret_cast<uint2*>(base + w.a);
+    uint2* b = reinterpret_cast<uint2*>(base + w.b);
+    sa.a = a;
+    sa.b = b;
+    sa.used = accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + w.used);
+    if (launch_sort(sa, s) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (N == 0 && accumulate) return CE_OK;
+
+    GradArgs ga;
+    ga.ent = (sa.passes & 1) ? b : a;
+    ga.invalid = sa.invalid;
+    ga.N = sa.N;
+    ga.V = sa.V;
+    ga.H = H;
+    ga.g = static_cast<const char*>(grad_out);
+    ga.gs = grad_out_stride * es;
+    ga.dw = static_cast<char*>(grad_weight);
+    ga.dws = grad_weight_stride * wes;
+    ga.part = reinterpret_cast<float*>(base + w.part);
+    ga.used = sa.used;
+    ga.R = w.R;
+    ga.chunks = w.chunks;
+    ga.accumulate = accumulate ? 1 : 0;
+    ga.scale = scale;
+    // a vector of the gradient is VEC floats of a float32 dW: both on their grids
+    const uint64_t vals[] = {(uint64_t)(uintptr_t)grad_out, (uint64_t)(N > 1 ? ga.gs : 0), (uint64_t)H * es,
+                             (uint64_t)(uintptr_t)grad_weight, (uint64_t)(V > 1 ? ga.dws : 0)};
+    const int vb = common_vector_bytes(vals, 5, es);
+    cudaError_t e = dtype == CE_F32    ? launch_grad_t<float>(ga, true, vb, s)
+                    : dtype == CE_BF16 ? launch_grad_t<__nv_bfloat16>(ga, grad_dtype == CE_F32, vb, s)
+                                       : launch_grad_t<__half>(ga, grad_dtype == CE_F32, vb, s);
+    return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
+}

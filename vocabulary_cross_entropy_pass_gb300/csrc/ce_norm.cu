@@ -1,0 +1,704 @@
+// ce_norm.cu -- the residual's addition and the root-mean-square norm, and
+// their gradients.
+//
+//   h = x + r                      (r optional; stored rounded to the input type)
+//   y_j = h_j rstd w_j,            rstd = 1 / sqrt(mean_j h_j^2 + eps)
+//   8 bits: for each group of columns  s = max(max|y_j| / top, 2^-126),
+//           q_j = round(y_j / s) saturated at +-top (448 for e4m3, 57344 for e5m2)
+//
+// y comes from the unrounded float32 h, so the stored h and y each carry one
+// rounding.  Backward, from the stored h with n_j = h_j rstd, c = mean_j(g_j w_j n_j):
+//   dx_j = rstd (g_j w_j - n_j c) + dh_j,     dw_j = sum over rows of g_j n_j
+// where dh is the gradient that reaches h from the residual stream; x and r
+// share dx.  rstd is computed again from h (the row is in registers anyway),
+// so the forward saves nothing but h.
+//
+// Bound by HBM: forward reads x, r and writes h, y; backward reads h, g, dh and
+// writes dx.  A row's elements stay in registers between the statistics and
+// the output.
+#include <cuda_fp8.h>
+
+#include "ce_device.cuh"
+#include "ce_internal.h"
+#include "ce_pack.cuh"
+
+namespace gbce {
+namespace {
+
+constexpr float kTinyScale = 1.17549435e-38f;  // 2^-126: 1 / scale stays finite
+
+struct NormFwdArgs {
+    const char* x;
+    const char* r;         // or NULL
+    const char* w;
+    char* y;
+    char* h;               // or NULL
+    float* scales;         // [N][groups]
+    int64_t N, H;
+    int64_t xs, rs, ys, hs;  // row strides in bytes
+    float eps, inv_h, top;
+    int w32;               // the weight is float32
+    int group, groups;     // columns per scale and scales per row (8 bits)
+    int kind;              // 1 e4m3, 2 e5m2
+};
+
+// Sum over the CTA; every thread gets it.  `red` holds a float per warp, twice
+// (two calls in a row use alternate halves, so one barrier each is enough).
+__device__ __forceinline__ float cta_sum(float v, float* red) {
+    v = warp_allsum(v);
+    const int nw = blockDim.x >> 5;
+    if (nw == 1) return v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const float t = (threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.f;
+    return warp_allsum(t);
+}
+__device__ __forceinline__ float cta_max(float v, float* red) {
+    v = warp_allmax(v);
+    const int nw = blockDim.x >> 5;
+    if (nw == 1) return v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const float t = (threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.f;
+    return warp_allmax(t);
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_q8(char* p, const float* y, float inv, int kind) {
+    Pack<uint8_t, VEC> o;
+    const __nv_fp8_interpretation_t k = kind == 1 ? __NV_E4M3 : __NV_E5M2;
+    if constexpr (VEC >= 2) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            const uint16_t two = __nv_cvt_float2_to_fp8x2(make_float2(y[i] * inv, y[i + 1] * inv), __NV_SATFINITE, k);
+            o.v[i] = (uint8_t)two;
+            o.v[i + 1] = (uint8_t)(two >> 8);
+        }
+    } else {
+        o.v[0] = __nv_cvt_float_to_fp8(y[0] * inv, __NV_SATFINITE, k);
+    }
+    o.store(p);
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void load_w(const NormFwdArgs& p, int64_t col, float* w) {
+    if (p.w32) {
+        const float* q = reinterpret_cast<const float*>(p.w) + col;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w[i] = __ldg(q + i);
+    } else {
+        Pack<T, VEC> t;
+        t.load_nc(p.w + col * (int64_t)sizeof(T));
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) w[i] = t.f(i);
+    }
+}
+
+// One CTA per row, VPT vectors of VEC elements per thread in registers.
+template <typename T, int VEC, int VPT, bool Q8>
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(const __grid_constant__ NormFwdArgs p) {
+    constexpr int ES = sizeof(T);
+    __shared__ float red[64];
+    extern __shared__ uint32_t gmax[];  // Q8 with groups wider than a warp's vectors
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x, TH = blockDim.x;
+    const int nv = (int)(p.H / VEC);
+    const char* x = p.x + row * p.xs;
+    const char* r = p.r ? p.r + row * p.rs : nullptr;
+
+    float h[VPT][VEC];
+    {
+        Pack<T, VEC> a[VPT], b[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = tid + k * TH;
+            a[k].zero();
+            if (v < nv) a[k].load_cs(x + (int64_t)v * VEC * ES);
+        }
+        if (r) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = tid + k * TH;
+                b[k].zero();
+                if (v < nv) b[k].load_cs(r + (int64_t)v * VEC * ES);
+            }
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) h[k][i] = a[k].f(i) + b[k].f(i);
+        } else {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) h[k][i] = a[k].f(i);
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) ss = fmaf(h[k][i], h[k][i], ss);
+    if (p.h) {
+        char* ho = p.h + row * p.hs;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = tid + k * TH;
+            Pack<T, VEC> o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o.set(i, h[k][i]);
+            if (v < nv) o.store(ho + (int64_t)v * VEC * ES);
+        }
+    }
+    ss = cta_sum(ss, red);
+    const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int v = tid + k * TH;
+        float w[VEC];
+        if (v < nv) {
+            load_w<T, VEC>(p, (int64_t)v * VEC, w);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) h[k][i] *= rstd * w[i];
+        }
+    }
+    char* y = p.y + row * p.ys;
+    if constexpr (!Q8) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = tid + k * TH;
+            Pack<T, VEC> o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o.set(i, h[k][i]);
+            if (v < nv) o.store(y + (int64_t)v * VEC * ES);
+        }
+    } else {
+        float am[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            am[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) am[k] = fmaxf(am[k], fabsf(h[k][i]));
+            if (tid + k * TH >= nv) am[k] = 0.f;
+        }
+        float* sc = p.scales + row * (int64_t)p.groups;
+        const int gl = p.group / VEC;  // vectors (lanes) per group
+        if (p.groups == 1) {
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) m = fmaxf(m, am[k]);
+            m = cta_max(m, red + 32);
+            const float s = fmaxf(m / p.top, kTinyScale);
+            if (tid == 0) sc[0] = s;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) am[k] = s;
+        } else if (gl <= 32) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                for (int o = gl >> 1; o > 0; o >>= 1) am[k] = fmaxf(am[k], __shfl_xor_sync(kFull, am[k], o));
+                am[k] = fmaxf(am[k] / p.top, kTinyScale);
+                const int v = tid + k * TH;
+                if (v < nv && v % gl == 0) sc[v / gl] = am[k];
+            }
+        } else {
+            // a group spans several warps: its maximum through shared memory
+            // (non-negative floats compare as integers, in any order)
+            for (int g = tid; g < p.groups; g += TH) gmax[g] = 0u;
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = tid + k * TH;
+                const float m = warp_allmax(am[k]);
+                if ((tid & 31) == 0 && v < nv) atomicMax(&gmax[v / gl], __float_as_uint(m));
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = tid + k * TH;
+                if (v < nv) {
+                    am[k] = fmaxf(__uint_as_float(gmax[v / gl]) / p.top, kTinyScale);
+                    if (v % gl == 0) sc[v / gl] = am[k];
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = tid + k * TH;
+            if (v < nv) store_q8<VEC>(y + (int64_t)v * VEC, h[k], 1.f / am[k], p.kind);
+        }
+    }
+}
+
+// Rows too wide for registers: two passes (three with 8 bits) over the row,
+// the later ones from L2.  h and y are written in the last pass only, each
+// element by the thread that has just read it, so they may replace x or r.
+template <typename T, int VEC, bool Q8>
+__global__ void __launch_bounds__(512) ce_rmsnorm_fwd_wide_kernel(const __grid_constant__ NormFwdArgs p) {
+    constexpr int ES = sizeof(T);
+    __shared__ float red[64];
+    extern __shared__ uint32_t gmax[];
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x, TH = blockDim.x;
+    const int64_t nv = p.H / VEC;
+    const char* x = p.x + row * p.xs;
+    const char* r = p.r ? p.r + row * p.rs : nullptr;
+    auto get = [&](int64_t v, float* h) {
+        Pack<T, VEC> a, b;
+        a.load(x + v * VEC * ES);
+        if (r) b.load(r + v * VEC * ES);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) h[i] = r ? a.f(i) + b.f(i) : a.f(i);
+    };
+    float ss = 0.f;
+#pragma unroll 4
+    for (int64_t v = tid; v < nv; v += TH) {
+        float h[VEC];
+        get(v, h);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) ss = fmaf(h[i], h[i], ss);
+    }
+    ss = cta_sum(ss, red);
+    const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
+    float* sc = p.scales + row * (int64_t)p.groups;
+    if constexpr (Q8) {
+        for (int g = tid; g < p.groups; g += TH) gmax[g] = 0u;
+        __syncthreads();
+        for (int64_t v0 = 0; v0 < nv; v0 += TH) {
+            const int64_t v = v0 + tid;
+            float m = 0.f;
+            if (v < nv) {
+                float h[VEC], w[VEC];
+                get(v, h);
+                load_w<T, VEC>(p, v * VEC, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(h[i] * (rstd * w[i])));
+                atomicMax(&gmax[v * VEC / p.group], __float_as_uint(m));
+            }
+        }
+        __syncthreads();
+        for (int g = tid; g < p.groups; g += TH) sc[g] = fmaxf(__uint_as_float(gmax[g]) / p.top, kTinyScale);
+    }
+    char* y = p.y + row * p.ys;
+    char* ho = p.h ? p.h + row * p.hs : nullptr;
+#pragma unroll 2
+    for (int64_t v = tid; v < nv; v += TH) {
+        float h[VEC], w[VEC];
+        get(v, h);
+        load_w<T, VEC>(p, v * VEC, w);
+        Pack<T, VEC> o;
+        if (ho) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o.set(i, h[i]);
+            o.store(ho + v * VEC * ES);
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) h[i] *= rstd * w[i];
+        if constexpr (Q8) {
+            const float s = fmaxf(__uint_as_float(gmax[v * VEC / p.group]) / p.top, kTinyScale);
+            store_q8<VEC>(y + v * VEC, h, 1.f / s, p.kind);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) o.set(i, h[i]);
+            o.store(y + v * VEC * ES);
+        }
+    }
+}
+
+template <typename T, int VEC, bool Q8>
+cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
+    const int64_t nv = a.H / VEC;
+    const size_t smem = Q8 ? (size_t)a.groups * 4 : 0;
+    constexpr int MAXV = VEC >= 8 ? 4 : (VEC == 4 ? 8 : 16);  // 512 threads hold 512 * MAXV vectors
+    if (nv > 512 * MAXV) {
+        auto* k = ce_rmsnorm_fwd_wide_kernel<T, VEC, Q8>;
+        if (smem > 48 * 1024) {
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+        }
+        k<<<(unsigned)a.N, 512, smem, s>>>(a);
+        return cudaGetLastError();
+    }
+    if (nv <= 256 || (a.N <= 304 && nv <= 1024)) {
+        const int th = (int)((nv + 31) / 32 * 32);
+        ce_rmsnorm_fwd_kernel<T, VEC, 1, Q8><<<(unsigned)a.N, th, smem, s>>>(a);
+    } else if (nv <= 2048) {
+        const int th = (int)((nv + 127) / 128 * 32);
+        ce_rmsnorm_fwd_kernel<T, VEC, 4, Q8><<<(unsigned)a.N, th, smem, s>>>(a);
+    } else {
+        const int th = (int)((nv + 32 * MAXV - 1) / (32 * MAXV) * 32);
+        ce_rmsnorm_fwd_kernel<T, VEC, MAXV, Q8><<<(unsigned)a.N, th, smem, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_fwd_t(const NormFwdArgs& a, int vb, cudaStream_t s) {
+    constexpr int ES = sizeof(T);
+    const bool q = a.kind != 0;
+    if (vb == 16) return q ? launch_fwd<T, 16 / ES, true>(a, s) : launch_fwd<T, 16 / ES, false>(a, s);
+    if constexpr (ES == 2)
+        if (vb == 4) return q ? launch_fwd<T, 2, true>(a, s) : launch_fwd<T, 2, false>(a, s);
+    return q ? launch_fwd<T, 1, true>(a, s) : launch_fwd<T, 1, false>(a, s);
+}
+
+// ----------------------------------------------------------------- backward
+struct NormBwdArgs {
+    const char* g;
+    const char* h;
+    const char* w;
+    const char* dh;        // or NULL
+    char* dx;
+    float* part;           // [gridDim.x][H] partial sums of dw, or NULL
+    int64_t N, H;
+    int64_t gs, hs, dhs, dxs;  // row strides in bytes
+    float eps, inv_h;
+    int w32;
+};
+
+// A persistent grid over the rows; a thread keeps its columns' dw sums in
+// registers over all rows of its CTA and writes them once.
+template <typename T, int VEC, int VPT>
+__global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_constant__ NormBwdArgs p) {
+    constexpr int ES = sizeof(T);
+    __shared__ float2 red[2][32];
+    const int tid = threadIdx.x, TH = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = TH >> 5;
+    const int nv = (int)(p.H / VEC);
+    float w[VPT][VEC], dw[VPT][VEC];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int v = tid + k * TH;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            dw[k][i] = 0.f;
+            w[k][i] = 0.f;
+            if (v < nv)
+                w[k][i] = p.w32 ? __ldg(reinterpret_cast<const float*>(p.w) + (int64_t)v * VEC + i)
+                                : to_f32(reinterpret_cast<const T*>(p.w)[(int64_t)v * VEC + i]);
+        }
+    }
+    int flip = 0;
+    for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, flip ^= 1) {
+        const char* gp = p.g + row * p.gs;
+        const char* hp = p.h + row * p.hs;
+        Pack<T, VEC> g[VPT], h[VPT], d[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = tid + k * TH;
+            g[k].zero();
+            h[k].zero();
+            if (v < nv) {
+                g[k].load_cs(gp + (int64_t)v * VEC * ES);
+                h[k].load_cs(hp + (int64_t)v * VEC * ES);
+            }
+        }
+        if (p.dh) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = tid + k * TH;
+                if (v < nv) d[k].load_cs(p.dh + row * p.dhs + (int64_t)v * VEC * ES);
+            }
+        }
+        float ss = 0.f, c = 0.f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float hv = h[k].f(i);
+                ss = fmaf(hv, hv, ss);
+                c = fmaf(g[k].f(i) * w[k][i], hv, c);
+            }
+        ss = warp_allsum(ss);
+        c = warp_allsum(c);
+        if (nw > 1) {
+            if (lane == 0) red[flip][warp] = make_float2(ss, c);
+            __syncthreads();
+            const float2 t = lane < nw ? red[flip][lane] : make_float2(0.f, 0.f);
+            ss = warp_allsum(t.x);
+            c = warp_allsum(t.y);
+        }
+        const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
+        const float cc = c * rstd * p.inv_h;  // mean of g w n
+        char* xp = p.dx + row * p.dxs;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = tid + k * TH;
+            Pack<T, VEC> o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float n = h[k].f(i) * rstd, gv = g[k].f(i);
+                dw[k][i] = fmaf(gv, n, dw[k][i]);
+                float t = rstd * fmaf(-n, cc, gv * w[k][i]);
+                if (p.dh) t += d[k].f(i);
+                o.set(i, t);
+            }
+            if (v < nv) o.store(xp + (int64_t)v * VEC * ES);
+        }
+    }
+    if (p.part) {
+        float* out = p.part + (int64_t)blockIdx.x * p.H;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = tid + k * TH;
+            if (v < nv)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) out[(int64_t)v * VEC + i] = dw[k][i];
+        }
+    }
+}
+
+// Rows too wide for registers: two passes over each row, dw summed in this
+// CTA's own partial row.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(512) ce_rmsnorm_bwd_wide_kernel(const __grid_constant__ NormBwdArgs p) {
+    constexpr int ES = sizeof(T);
+    __shared__ float2 red[2][32];
+    const int tid = threadIdx.x, TH = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = TH >> 5;
+    const int64_t nv = p.H / VEC;
+    float* out = p.part ? p.part + (int64_t)blockIdx.x * p.H : nullptr;
+    auto wat = [&](int64_t c) {
+        return p.w32 ? __ldg(reinterpret_cast<const float*>(p.w) + c) : to_f32(reinterpret_cast<const T*>(p.w)[c]);
+    };
+    int flip = 0;
+    bool first = true;
+    for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, flip ^= 1, first = false) {
+        const char* gp = p.g + row * p.gs;
+        const char* hp = p.h + row * p.hs;
+        float ss = 0.f, c = 0.f;
+#pragma unroll 2
+        for (int64_t v = tid; v < nv; v += TH) {
+            Pack<T, VEC> g, h;
+            g.load(gp + v * VEC * ES);
+            h.load(hp + v * VEC * ES);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float hv = h.f(i);
+                ss = fmaf(hv, hv, ss);
+                c = fmaf(g.f(i) * wat(v * VEC + i), hv, c);
+            }
+        }
+        ss = warp_allsum(ss);
+        c = warp_allsum(c);
+        if (lane == 0) red[flip][warp] = make_float2(ss, c);
+        __syncthreads();
+        const float2 t = lane < nw ? red[flip][lane] : make_float2(0.f, 0.f);
+        ss = warp_allsum(t.x);
+        c = warp_allsum(t.y);
+        const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
+        const float cc = c * rstd * p.inv_h;
+        char* xp = p.dx + row * p.dxs;
+        for (int64_t v = tid; v < nv; v += TH) {
+            Pack<T, VEC> g, h, d, o;
+            g.load(gp + v * VEC * ES);
+            h.load(hp + v * VEC * ES);
+            if (p.dh) d.load(p.dh + row * p.dhs + v * VEC * ES);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float n = h.f(i) * rstd, gv = g.f(i);
+                if (out) {
+                    float* q = out + v * VEC + i;
+                    *q = first ? gv * n : fmaf(gv, n, *q);
+                }
+                float t2 = rstd * fmaf(-n, cc, gv * wat(v * VEC + i));
+                if (p.dh) t2 += d.f(i);
+                o.set(i, t2);
+            }
+            o.store(xp + v * VEC * ES);
+        }
+    }
+}
+
+// dw_j = the partial rows' column sums, in a fixed order: 32 columns per CTA,
+// eight rows' worth of lanes each summing every eighth partial row.
+__global__ void __launch_bounds__(256) ce_rmsnorm_dw_kernel(const float* part, int64_t rows, int64_t H, float* dw) {
+    __shared__ float sh[8][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float acc = 0.f;
+    if (c < H) {
+#pragma unroll 8
+        for (int64_t r = warp; r < rows; r += 8) acc += part[r * H + c];
+    }
+    sh[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0 && c < H) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += sh[k][lane];
+        dw[c] = t;
+    }
+}
+
+// CTAs of the backward grid, from the sizes alone (the workspace holds a
+// partial row for each).
+constexpr int kBwdGrid = 152 * 3;
+int bwd_grid(int64_t N) { return (int)(N < kBwdGrid ? N : kBwdGrid); }
+
+template <typename T, int VEC>
+cudaError_t launch_bwd_k(const NormBwdArgs& a, cudaStream_t s) {
+    constexpr int MAXV = VEC >= 8 ? 4 : (VEC == 4 ? 8 : 16);
+    const int64_t nv = a.H / VEC;
+    const int grid = bwd_grid(a.N);
+    if (nv <= 256) {
+        ce_rmsnorm_bwd_kernel<T, VEC, 1><<<grid, (unsigned)((nv + 31) / 32 * 32), 0, s>>>(a);
+    } else if (nv <= 1024) {
+        ce_rmsnorm_bwd_kernel<T, VEC, 2><<<grid, (unsigned)((nv + 63) / 64 * 32), 0, s>>>(a);
+    } else if (nv <= 512 * MAXV) {
+        ce_rmsnorm_bwd_kernel<T, VEC, MAXV>
+            <<<grid, (unsigned)((nv + 32 * MAXV - 1) / (32 * MAXV) * 32), 0, s>>>(a);
+    } else {
+        ce_rmsnorm_bwd_wide_kernel<T, VEC><<<grid, 512, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_bwd_t(const NormBwdArgs& a, int vb, cudaStream_t s) {
+    constexpr int ES = sizeof(T);
+    if (vb == 16) return launch_bwd_k<T, 16 / ES>(a, s);
+    if constexpr (ES == 2)
+        if (vb == 4) return launch_bwd_k<T, 2>(a, s);
+    return launch_bwd_k<T, 1>(a, s);
+}
+
+constexpr int64_t kMaxWidth = 1 << 20;
+
+bool bad_dtype(int d) { return d < CE_F32 || d > CE_F16; }
+bool off_grid(const void* p, int es) { return reinterpret_cast<uintptr_t>(p) % es != 0; }
+
+}  // namespace
+}  // namespace gbce
+
+using namespace gbce;
+
+extern "C" ce_status ce_rmsnorm_fwd(const void* x, const void* residual, const void* weight, ce_dtype dtype,
+                                    ce_dtype weight_dtype, int64_t N, int64_t H, int64_t x_stride,
+                                    int64_t residual_stride, float eps, void* out, int64_t out_stride,
+                                    ce_quant quant, int group_size, float* scales, void* residual_out,
+                                    int64_t residual_out_stride, void* stream) {
+    if (bad_dtype(dtype) || (weight_dtype != dtype && weight_dtype != CE_F32)) return CE_ERR_UNSUPPORTED_DTYPE;
+    if (quant < CE_QUANT_NONE || quant > CE_QUANT_E5M2) return CE_ERR_UNSUPPORTED_DTYPE;
+    if (N < 0 || N > 0x7fffffffLL || H < 1 || H > kMaxWidth) return CE_ERR_INVALID_ARG;
+    if (!(eps >= 0.f && eps <= 3.4e38f)) return CE_ERR_INVALID_ARG;
+    if (quant && group_size != 0 && group_size != 32 && group_size != 64 && group_size != 128)
+        return CE_ERR_INVALID_ARG;
+    if (!quant && (group_size != 0 || scales)) return CE_ERR_INVALID_ARG;
+    if (N == 0) return CE_OK;
+    if (!x || !weight || !out || (quant && !scales)) return CE_ERR_INVALID_ARG;
+    if (residual && !residual_out) return CE_ERR_INVALID_ARG;
+    if (out == residual_out) return CE_ERR_INVALID_ARG;
+    const int es = elem_size(dtype);
+    if (off_grid(x, es) || off_grid(residual, es) || off_grid(weight, elem_size(weight_dtype)) ||
+        off_grid(residual_out, es) || (!quant && off_grid(out, es)) || off_grid(scales, 4))
+        return CE_ERR_INVALID_ARG;
+    // input rows may repeat (stride 0); output rows may not share memory
+    if (x_stride < 0 || residual_stride < 0) return CE_ERR_BAD_STRIDE;
+    if (N > 1 && (out_stride < H || (residual_out && residual_out_stride < H))) return CE_ERR_BAD_STRIDE;
+    if (quant && (out == x || out == residual)) return CE_ERR_INVALID_ARG;
+    // an output that replaces an input takes its strides
+    if (N > 1 && ((out == x && out_stride != x_stride) || (out == residual && out_stride != residual_stride) ||
+                  (residual_out && residual_out == x && residual_out_stride != x_stride) ||
+                  (residual_out && residual_out == residual && residual_out_stride != residual_stride)))
+        return CE_ERR_BAD_STRIDE;
+
+    NormFwdArgs a;
+    a.x = static_cast<const char*>(x);
+    a.r = static_cast<const char*>(residual);
+    a.w = static_cast<const char*>(weight);
+    a.y = static_cast<char*>(out);
+    a.h = static_cast<char*>(residual_out);
+    a.scales = scales;
+    a.N = N;
+    a.H = H;
+    const int ys = quant ? 1 : es;
+    a.xs = x_stride * es;
+    a.rs = residual_stride * es;
+    a.ys = out_stride * ys;
+    a.hs = residual_out_stride * es;
+    a.eps = eps;
+    a.inv_h = 1.f / (float)H;
+    a.w32 = weight_dtype == CE_F32 && dtype != CE_F32;
+    a.kind = quant;
+    a.top = quant == CE_QUANT_E5M2 ? 57344.f : 448.f;
+    a.group = quant ? (group_size ? group_size : (int)H) : (int)H;
+    a.groups = (int)((H + a.group - 1) / a.group);
+    const int q = es / ys;  // the output's bytes scaled to the input's vectors
+    const uint64_t vals[] = {(uint64_t)(uintptr_t)x, (uint64_t)(uintptr_t)residual,
+                             (uint64_t)(a.w32 ? 0 : (uintptr_t)weight),
+                             (uint64_t)(uintptr_t)out * (uint64_t)q, (uint64_t)(uintptr_t)residual_out,
+                             (uint64_t)(N > 1 ? a.xs : 0), (uint64_t)(N > 1 && residual ? a.rs : 0),
+                             (uint64_t)(N > 1 ? a.ys * q : 0), (uint64_t)(N > 1 && residual_out ? a.hs : 0),
+                             (uint64_t)H * es};
+    const int vb = common_vector_bytes(vals, 10, es);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = dtype == CE_F32    ? launch_fwd_t<float>(a, vb, s)
+                    : dtype == CE_BF16 ? launch_fwd_t<__nv_bfloat16>(a, vb, s)
+                                       : launch_fwd_t<__half>(a, vb, s);
+    return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
+}
+
+extern "C" size_t ce_rmsnorm_bwd_workspace_bytes(int64_t N, int64_t H) {
+    if (N < 0 || N > 0x7fffffffLL || H < 1 || H > kMaxWidth) return 0;
+    return kWsHeaderBytes + (size_t)bwd_grid(N) * (size_t)H * sizeof(float);
+}
+
+extern "C" ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const void* weight, const void* grad_h,
+                                    ce_dtype dtype, ce_dtype weight_dtype, int64_t N, int64_t H,
+                                    int64_t grad_out_stride, int64_t h_stride, int64_t grad_h_stride, float eps,
+                                    void* grad_x, int64_t grad_x_stride, float* grad_weight, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    if (bad_dtype(dtype) || (weight_dtype != dtype && weight_dtype != CE_F32)) return CE_ERR_UNSUPPORTED_DTYPE;
+    if (N < 0 || N > 0x7fffffffLL || H < 1 || H > kMaxWidth) return CE_ERR_INVALID_ARG;
+    if (!(eps >= 0.f && eps <= 3.4e38f)) return CE_ERR_INVALID_ARG;
+    const int es = elem_size(dtype);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (off_grid(grad_weight, 4)) return CE_ERR_INVALID_ARG;
+    if (N > 0) {
+        if (!grad_out || !h || !weight || !grad_x) return CE_ERR_INVALID_ARG;
+        if (off_grid(grad_out, es) || off_grid(h, es) || off_grid(grad_h, es) || off_grid(grad_x, es) ||
+            off_grid(weight, elem_size(weight_dtype)))
+            return CE_ERR_INVALID_ARG;
+        if (grad_out_stride < 0 || h_stride < 0 || grad_h_stride < 0) return CE_ERR_BAD_STRIDE;
+        if (N > 1 && grad_x_stride < H) return CE_ERR_BAD_STRIDE;
+        if (N > 1 && ((grad_x == grad_out && grad_x_stride != grad_out_stride) ||
+                      (grad_x == h && grad_x_stride != h_stride) ||
+                      (grad_x == grad_h && grad_x_stride != grad_h_stride)))
+            return CE_ERR_BAD_STRIDE;
+        if (grad_weight) {
+            if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16) return CE_ERR_INVALID_ARG;
+            if (workspace_bytes < ce_rmsnorm_bwd_workspace_bytes(N, H)) return CE_ERR_WORKSPACE_TOO_SMALL;
+        }
+    } else {
+        // no rows: the weight's gradient is an empty sum
+        if (grad_weight && cudaMemsetAsync(grad_weight, 0, (size_t)H * 4, s) != cudaSuccess) return CE_ERR_LAUNCH;
+        return CE_OK;
+    }
+    NormBwdArgs a;
+    a.g = static_cast<const char*>(grad_out);
+    a.h = static_cast<const char*>(h);
+    a.w = static_cast<const char*>(weight);
+    a.dh = static_cast<const char*>(grad_h);
+    a.dx = static_cast<char*>(grad_x);
+    a.part = grad_weight ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kWsHeaderBytes) : nullptr;
+    a.N = N;
+    a.H = H;
+    a.gs = grad_out_stride * es;
+    a.hs = h_stride * es;
+    a.dhs = grad_h_stride * es;
+    a.dxs = grad_x_stride * es;
+    a.eps = eps;
+    a.inv_h = 1.f / (float)H;
+    a.w32 = weight_dtype == CE_F32 && dtype != CE_F32;
+    const uint64_t vals[] = {(uint64_t)(uintptr_t)grad_out, (uint64_t)(uintptr_t)h, (uint64_t)(uintptr_t)grad_h,
+                             (uint64_t)(uintptr_t)grad_x, (uint64_t)(N > 1 ? a.gs : 0),
+                             (uint64_t)(N > 1 ? a.hs : 0), (uint64_t)(N > 1 && grad_h ? a.dhs : 0),
+                             (uint64_t)(N > 1 ? a.dxs : 0), (uint64_t)H * es};
+    const int vb = common_vector_bytes(vals, 9, es);
+    cudaError_t e = dtype == CE_F32    ? launch_bwd_t<float>(a, vb, s)
+                    : dtype == CE_BF16 ? launch_bwd_t<__nv_bfloat16>(a, vb, s)
+                                       : launch_bwd_t<__half>(a, vb, s);
+    if (e != cudaSuccess) return CE_ERR_LAUNCH;
+    if (grad_weight) {
+        ce_rmsnorm_dw_kernel<<<(unsigned)((H + 31) / 32), 256, 0, s>>>(a.part, bwd_grid(N), H, grad_weight);
+        if (cudaGetLastError() != cudaSuccess) return CE_ERR_LAUNCH;
+    }
+    return CE_OK;
+}
