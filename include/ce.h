@@ -490,21 +490,30 @@ typedef struct {
  * A token that is not allowed gives mask_value whatever its logit (NaN
  * included); a row that allows none is mask_value throughout.  ce_fwd_bwd on
  * the result needs a finite mask_value (say -3e4: its smoothing term sums the
- * logits).  out may be the logits themselves (same strides). */
+ * logits).  out may be the logits themselves (same strides).
+ *   workspace    at least ce_logits_workspace_bytes(dim0*dim1, V, dtype, history_max,
+ *                bias_max) bytes, 16-byte aligned, no initialisation; not shared
+ *                by calls that may overlap.  NULL where that is 0 (no
+ *                lists, or few columns in all). */
+size_t ce_logits_workspace_bytes(int64_t N, int64_t V, ce_dtype dtype, int64_t history_max,
+                                 int64_t bias_max);
 ce_status ce_logits_process(const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1,
                             int64_t V, const int64_t strides[3], const ce_logits_params* params,
-                            void* out, const int64_t out_strides[3], void* stream);
+                            void* out, const int64_t out_strides[3], void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 /* Gradient of ce_logits_process with respect to the logits:
  *   grad_j = allowed_j ? grad_out_j / temperature * (s_j ? (x_j > 0 ? 1 / repetition
  *                        : repetition) : 1) : 0
  * The logits are read where the history holds their token; the biases, the counts
- * and mask_value play no part.  grad may be grad_out (same strides), not the logits. */
+ * and mask_value play no part.  grad may be grad_out (same strides), not the
+ * logits.  workspace as for ce_logits_process. */
 ce_status ce_logits_process_bwd(const void* grad_out, const int64_t grad_out_strides[3],
                                 const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1,
                                 int64_t V, const int64_t strides[3],
                                 const ce_logits_params* params, void* grad,
-                                const int64_t grad_strides[3], void* stream);
+                                const int64_t grad_strides[3], void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /* Waits for `stream`, then copies the device error word of the last pass that
  * used `workspace` into *host_err (host pointer).  Returns CE_OK,

@@ -148,6 +148,33 @@ def test_wide_rows(N, V, L):
     check(pkg.ce_logits_process_bwd(go.to(DEV), xd, **dev(bwd_params(p))), x, p, go=go)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L,K", [(1, 0), (0, 1), (63, 0), (61, 20), (127, 2), (513, 0), (600, 301)])
+def test_tables_of_odd_sizes(L, K, dtype):
+    # many columns in all: a kernel of its own finds the touched ones
+    x, p = make(21, 50257, dtype, L + K, L, K, 0.3)
+    xd = x.to(DEV)
+    check(pkg.ce_logits_process(xd, **dev(p)), x, p)
+    if L:
+        go = torch.randn(21, 50257, generator=rng(L)).to(dtype)
+        check(pkg.ce_logits_process_bwd(go.to(DEV), xd, **dev(bwd_params(p))), x, p, go=go)
+    want = pkg.ce_logits_process(xd, **dev(p))
+    assert torch.equal(pkg.ce_logits_process(xd, out=xd, **dev(p)), want)
+
+
+@pytest.mark.parametrize("N,V,L,K", [(3, 400000, 9000, 3), (9, 128000, 70000, 0), (9, 128000, 1000, 3000),
+                                     (300, 4096, 5000, 0), (2, 1 << 20, 300, 40)])
+def test_long_lists(N, V, L, K):
+    x, p = make(N, V, torch.bfloat16, L, L, K, 0.5)
+    p["history_lengths"][0] = L
+    xd, pd = x.to(DEV), dev(p)
+    got = pkg.ce_logits_process(xd, **pd)
+    check(got, x, p)
+    assert torch.equal(pkg.ce_logits_process(xd, **pd), got)
+    go = torch.randn(N, V, generator=rng(V)).to(torch.bfloat16)
+    check(pkg.ce_logits_process_bwd(go.to(DEV), xd, **dev(bwd_params(p))), x, p, go=go)
+
+
 def test_penalties_alone_and_signs():
     V = 64
     x = torch.linspace(-4, 4, V).repeat(2, 1)

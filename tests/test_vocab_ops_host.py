@@ -150,7 +150,7 @@ def test_rmsnorm_bwd_refusals(lib):
 
 def logits(lib, params=None, bwd=False, **kw):
     a = dict(x=0x1000, g=0x2000, dt=1, d0=2, d1=3, V=4096, st=(3 * 4096, 4096, 1), gst=(3 * 4096, 4096, 1),
-             out=0x9000, ost=(3 * 4096, 4096, 1))
+             out=0x9000, ost=(3 * 4096, 4096, 1), wk=None, wkb=0)
     a.update(kw)
     p = _lib.ce_logits_params()
     for k, v in (params or {}).items():
@@ -158,9 +158,10 @@ def logits(lib, params=None, bwd=False, **kw):
     if bwd:
         return lib.ce_logits_process_bwd(VP(a["g"]), _lib.i64_array(a["gst"]), VP(a["x"]), a["dt"], a["d0"], a["d1"],
                                          a["V"], _lib.i64_array(a["st"]), ctypes.byref(p), VP(a["out"]),
-                                         _lib.i64_array(a["ost"]), None)
+                                         _lib.i64_array(a["ost"]), VP(a["wk"]), a["wkb"], None)
     return lib.ce_logits_process(VP(a["x"]), a["dt"], a["d0"], a["d1"], a["V"], _lib.i64_array(a["st"]),
-                                 ctypes.byref(p), VP(a["out"]), _lib.i64_array(a["ost"]), None)
+                                 ctypes.byref(p), VP(a["out"]), _lib.i64_array(a["ost"]), VP(a["wk"]), a["wkb"],
+                                 None)
 
 
 @pytest.mark.parametrize("bwd", [False, True])
@@ -184,8 +185,24 @@ def test_logits_refusals(lib, bwd):
     p = _lib.ce_logits_params()
     p.reserved[0] = 1
     assert lib.ce_logits_process(VP(0x1000), 1, 2, 3, 4096, _lib.i64_array((3 * 4096, 4096, 1)), ctypes.byref(p),
-                                 VP(0x9000), _lib.i64_array((3 * 4096, 4096, 1)), None) == 1
+                                 VP(0x9000), _lib.i64_array((3 * 4096, 4096, 1)), None, 0, None) == 1
     assert logits(lib, bwd=bwd, d1=0, x=0, out=0, g=0) == 0
+
+
+def test_logits_workspace_refusals(lib):
+    # few columns in all and no lists need none; else a table of touched columns a row
+    assert lib.ce_logits_workspace_bytes(6, 4096, 1, 5000, 0) == 0
+    assert lib.ce_logits_workspace_bytes(4096, 4096, 1, 0, 0) == 0
+    assert lib.ce_logits_workspace_bytes(4096, 0, 1, 900, 0) == 0
+    need = lib.ce_logits_workspace_bytes(4096, 4096, 1, 900, 0)
+    assert need >= 4096 * 900 * 8
+    one = (4096 * 4096, 4096, 1)
+    for bwd in (False, True):
+        p = dict(history=0x100, history_max=900, history_stride=900, repetition_penalty=0x200)
+        kw = dict(bwd=bwd, d0=1, d1=4096, st=one, gst=one, ost=one)
+        assert logits(lib, p, **kw) == 1
+        assert logits(lib, p, wk=0x4008, wkb=need, **kw) == 1
+        assert logits(lib, p, wk=0x4000, wkb=need - 1, **kw) == 4
 
 
 def test_logits_in_place_refusals(lib):

@@ -33,15 +33,15 @@ from ._lib import (CE_PATH_AUTO, CE_PATH_CLUSTER, CE_PATH_ROW, CE_PATH_STREAM,
                    CE_PATH_TWO_STAGE, CE_PATH_VECROW, CE_PATH_WARP, CEError, ce_options,
                    make_options)
 from .vocab_ops import (ce_embed_bwd, ce_embed_bwd_workspace_bytes, ce_embed_fwd, ce_logits_process,
-                        ce_logits_process_bwd, ce_rmsnorm_bwd, ce_rmsnorm_bwd_workspace_bytes,
-                        ce_rmsnorm_fwd, embedding, process_logits, rms_norm)
+                        ce_logits_process_bwd, ce_logits_workspace_bytes, ce_rmsnorm_bwd,
+                        ce_rmsnorm_bwd_workspace_bytes, ce_rmsnorm_fwd, embedding, process_logits, rms_norm)
 
 __all__ = ["ce_fwd_bwd", "ce_fwd_bwd_noalloc", "ce_fwd_only", "ce_bwd", "parallel_cross_entropy",
            "ce_vp_partials", "ce_vp_combine", "ce_vp_bwd", "vocab_parallel_cross_entropy",
            "ce_linear_fwd_bwd",
            "ce_embed_fwd", "ce_embed_bwd", "ce_embed_bwd_workspace_bytes", "embedding",
            "ce_rmsnorm_fwd", "ce_rmsnorm_bwd", "ce_rmsnorm_bwd_workspace_bytes", "rms_norm",
-           "ce_logits_process", "ce_logits_process_bwd", "process_logits",
+           "ce_logits_process", "ce_logits_process_bwd", "ce_logits_workspace_bytes", "process_logits",
            "ce_workspace_bytes", "ce_get_error", "ce_noalloc_get_error",
            "ce_status_string",
            "ce_wait_timeout_probe",

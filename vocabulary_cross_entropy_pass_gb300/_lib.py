@@ -39,7 +39,7 @@ EXPORTS = ("ce_workspace_bytes", "ce_fwd_bwd", "ce_fwd_only", "ce_get_error", "c
            "ce_vp_bwd", "ce_linear_workspace_bytes", "ce_linear_fwd_bwd", "ce_wait_timeout_probe",
            "ce_noalloc_get_error", "ce_embed_fwd", "ce_embed_bwd_workspace_bytes", "ce_embed_bwd",
            "ce_rmsnorm_fwd", "ce_rmsnorm_bwd_workspace_bytes", "ce_rmsnorm_bwd",
-           "ce_logits_process", "ce_logits_process_bwd")
+           "ce_logits_workspace_bytes", "ce_logits_process", "ce_logits_process_bwd")
 
 
 class ce_options(ctypes.Structure):
@@ -152,10 +152,12 @@ def load(path: str = LIB_PATH):
         lib.ce_rmsnorm_bwd.argtypes = [vp, vp, vp, vp, i32, i32, i64, i64, i64, i64, i64, f32, vp,
                                        i64, vp, vp, size, vp]
         lib.ce_logits_process.restype = i32
-        lib.ce_logits_process.argtypes = [vp, i32, i64, i64, i64, I64_3, lp, vp, I64_3, vp]
+        lib.ce_logits_workspace_bytes.restype = size
+        lib.ce_logits_workspace_bytes.argtypes = [i64, i64, i32, i64, i64]
+        lib.ce_logits_process.argtypes = [vp, i32, i64, i64, i64, I64_3, lp, vp, I64_3, vp, size, vp]
         lib.ce_logits_process_bwd.restype = i32
         lib.ce_logits_process_bwd.argtypes = [vp, I64_3, vp, i32, i64, i64, i64, I64_3, lp, vp,
-                                              I64_3, vp]
+                                              I64_3, vp, size, vp]
         lib.ce_wait_timeout_probe.restype = i32
         lib.ce_wait_timeout_probe.argtypes = [vp, ctypes.c_size_t, vp]
         lib.ce_get_error.restype = i32

@@ -414,7 +414,24 @@ def _match(t, like, name):
         raise ValueError(f"{name} must match the logits in shape and dtype, on the same device")
 
 
-def ce_logits_process(logits: torch.Tensor, out: torch.Tensor | None = None, stream=None, **params) -> torch.Tensor:
+def ce_logits_workspace_bytes(N: int, V: int, dtype: torch.dtype, history_max: int = 0, bias_max: int = 0) -> int:
+    """Bytes of workspace that ce_logits_process(_bwd) needs for N rows; 0 without lists and for few columns in all."""
+    return int(_lib.load().ce_logits_workspace_bytes(N, V, _DTYPE[dtype], history_max, bias_max))
+
+
+def _logits_workspace(workspace, p, N, V, dt, dev):
+    if workspace is None and (p.history_max or p.bias_max):
+        need = _lib.load().ce_logits_workspace_bytes(N, V, dt, p.history_max, p.bias_max)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is None:
+        return None, None, 0
+    _on(dev, workspace=workspace)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def ce_logits_process(logits: torch.Tensor, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                      stream=None, **params) -> torch.Tensor:
     """The logits a token is taken from: per row of the (N, V) or (dim0, dim1,
     V) ``logits`` (rows flattened to N in the parameters), in float32, rounded
     once,
@@ -423,7 +440,8 @@ def ce_logits_process(logits: torch.Tensor, out: torch.Tensor | None = None, str
       y = (z - frequency * count - presence * [count > 0] + bias) / temperature
       out = y where the mask allows the token, else mask_value
 
-    ``out`` (allocated when None) may be the logits themselves.  Parameters,
+    ``out`` (allocated when None) may be the logits themselves; ``workspace``:
+    ce_logits_workspace_bytes bytes (allocated when None).  Parameters,
     each optional: ``history`` int64 (N, L) with ``history_lengths`` int64 (N,)
     tokens in use, the first ``prompt_lengths`` int64 (N,) of them the prompt
     (no count); ``repetition_penalty``, ``frequency_penalty``,
@@ -446,15 +464,16 @@ def ce_logits_process(logits: torch.Tensor, out: torch.Tensor | None = None, str
     else:
         _match(out, logits, "out")
     ost = _logits_dims(out, "out")[3]
+    workspace, wp, wb = _logits_workspace(workspace, p, d0 * d1, V, dt, dev)
     rc = _lib.load().ce_logits_process(logits.data_ptr(), dt, d0, d1, V, _lib.i64_array(st), ctypes.byref(p),
-                                       out.data_ptr(), _lib.i64_array(ost), _stream(dev, stream))
+                                       out.data_ptr(), _lib.i64_array(ost), wp, wb, _stream(dev, stream))
     if rc:
         _raise(rc, "ce_logits_process")
     return out
 
 
 def ce_logits_process_bwd(grad_out: torch.Tensor, logits: torch.Tensor, grad: torch.Tensor | None = None,
-                          stream=None, **params) -> torch.Tensor:
+                          workspace: torch.Tensor | None = None, stream=None, **params) -> torch.Tensor:
     """Gradient of :func:`ce_logits_process` with respect to the logits, from
     the logits it was given and the same parameters (the biases, the frequency
     and presence penalties, the prompt lengths and mask_value change nothing
@@ -474,9 +493,10 @@ def ce_logits_process_bwd(grad_out: torch.Tensor, logits: torch.Tensor, grad: to
     else:
         _match(grad, logits, "grad")
     ost = _logits_dims(grad, "grad")[3]
+    workspace, wp, wb = _logits_workspace(workspace, p, d0 * d1, V, dt, dev)
     rc = _lib.load().ce_logits_process_bwd(grad_out.data_ptr(), _lib.i64_array(gst), logits.data_ptr(), dt, d0, d1, V,
                                            _lib.i64_array(st), ctypes.byref(p), grad.data_ptr(),
-                                           _lib.i64_array(ost), _stream(dev, stream))
+                                           _lib.i64_array(ost), wp, wb, _stream(dev, stream))
     if rc:
         _raise(rc, "ce_logits_process_bwd")
     return grad
