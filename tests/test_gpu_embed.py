@@ -167,6 +167,25 @@ def test_backward_long_and_skewed():
     run_bwd(N, V, 72, torch.bfloat16, t, scale=8.0)
 
 
+def test_backward_more_than_fits_on_chip():
+    N, V = 70001, 3001
+    run_bwd(N, V, 8, torch.float32, torch.randint(0, V, (N,), generator=rng(10)))
+
+
+@pytest.mark.parametrize("V,H", [(1, 3), (7, 1001), (4096, 8), (513, 16), (100, 33)])
+def test_backward_zeros_what_is_absent(V, H):
+    # contiguous, padded and odd rows, from a dirty buffer
+    g = rng(V)
+    t = torch.randint(0, V, (3,), generator=g)
+    for dtype in (torch.float32, torch.bfloat16):
+        go = torch.randn(3, H, generator=g).to(dtype)
+        for pad in (0, 1, 5):
+            big = torch.full((V, H + pad), 7.0, dtype=dtype, device=DEV)
+            pkg.ce_embed_bwd(go.to(DEV), t.to(DEV), V, grad_weight=big[:, :H])
+            check_bwd(big[:, :H], go, t, V, 1.0)
+            assert bool((big[:, H:] == 7).all())
+
+
 @pytest.mark.parametrize("V", [1023, 1024, 1025, (1 << 20) - 1, (1 << 20) + 3])
 def test_backward_digit_counts(V):
     # one, two and three digits of up to ten bits; the highest token

@@ -8,16 +8,18 @@
 //
 // Gradient: equal tokens meet, so the sum is taken over the tokens in sorted
 // order, which makes it the same on every run.
-//   1. ce_embed_sort_kernel: a stable radix sort of (token, position), one
-//      launch, one cluster of up to eight CTAs: each warp counts the digits of
-//      its own run of tokens in shared memory, the CTAs exchange their counts
-//      over distributed shared memory, each warp then writes its run in order.
-//      Ignored and out-of-range tokens become key V and sort to the end.
+//   1. ce_embed_sort_kernel: a stable radix sort of (token, position) by one
+//      cluster of up to eight CTAs: each warp counts the digits of its own run of
+//      tokens in shared memory, the CTAs exchange their counts over distributed
+//      shared memory, each warp then sends its run in order to the CTAs that hold
+//      the places (up to 65536 tokens stay on chip between the digits).
+//      Ignored and out-of-range tokens become key V and sort to the end.  The
+//      sort is a chain of latencies on eight SMs: the launch's other CTAs zero
+//      the gradient meanwhile, where it is to be written whole.
 //   2. ce_embed_grad_kernel: a CTA sums a fixed number of sorted entries over
 //      a slab of columns, in registers, a gradient row at a time; a token
 //      whose entries all lie in the chunk is written at once, one that crosses
-//      a chunk border leaves its float32 part in the workspace.  Further CTAs
-//      of the same launch zero the rows of tokens that do not occur.
+//      a chunk border leaves its float32 part in the workspace.
 //   3. ce_embed_join_kernel: the parts of tokens that cross chunk borders,
 //      added in chunk order.
 #include "ce_device.cuh"
@@ -84,11 +86,11 @@ __global__ void __launch_bounds__(128) ce_embed_fwd_kernel(const __grid_constant
 }
 
 // ----------------------------------------------------------------- sorted tokens
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = 32;
-constexpr int kMaxDigitBits = 10;
-constexpr int kMaxBins = 1 << kMaxDigitBits;
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = 16;
+constexpr int kMaxDigitBits = 9;         // one bin per thread
 constexpr int kSortCluster = 8;
+constexpr int kOnChip = 8192;            // entries a CTA holds in shared memory, at most
 constexpr size_t kWsInvalidOffset = 16;  // uint32 tokens without a gradient
 
 struct SortArgs {
@@ -98,11 +100,13 @@ struct SortArgs {
     uint32_t N, V;
     int64_t ignore;
     int passes, bits;      // digits of `bits` bits, least first
+    int on_chip;           // entries per CTA kept in shared memory between the digits, or 0: in a and b
     uint32_t* err;
     uint32_t* invalid;
-    uint2* a;              // (key, position); the sorted ones end in `a`
+    uint2* a;              // (key, position): the sorted ones end here
     uint2* b;
-    uint32_t* used;        // bit v: token v occurs; or NULL
+    char* zero;            // the gradient to be zeroed, or NULL
+    int64_t zrows, zstride, zbytes;  // its rows, their stride and bytes
 };
 
 __device__ __forceinline__ uint32_t ld_dsmem_u32(const uint32_t* local, uint32_t rank) {
@@ -111,86 +115,137 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(const uint32_t* local, uint32_t
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
     return v;
 }
+__device__ __forceinline__ void st_dsmem_u2(uint2* local, uint32_t rank, uint2 v) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(remote), "r"(v.x), "r"(v.y) : "memory");
+}
+
+// Zero rows r0, r0 + step, ...: 16-byte vectors between a head and a tail of
+// two-byte pieces (a warp per row).
+__device__ __forceinline__ void zero_rows(const SortArgs& p, int64_t r0, int64_t step) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t r = r0; r < p.zrows; r += step) {
+        char* row = p.zero + r * p.zstride;
+        int64_t head = (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u);
+        if (head > p.zbytes) head = p.zbytes;
+        const int64_t nv = (p.zbytes - head) / 16;
+        uint4* body = reinterpret_cast<uint4*>(row + head);
+#pragma unroll 4
+        for (int64_t v = lane; v < nv; v += 32) __stcs(body + v, make_uint4(0, 0, 0, 0));
+        const int64_t t0 = head + nv * 16;  // lanes 0..7 the head, 8..15 the tail
+        const int64_t at = lane < 8 ? lane * 2 : t0 + (lane - 8) * 2;
+        if (lane < 8 ? at < head : (lane < 16 && at < p.zbytes)) *reinterpret_cast<uint16_t*>(row + at) = 0;
+    }
+}
 
 __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __grid_constant__ SortArgs p) {
     extern __shared__ __align__(16) uint32_t sm[];
-    const int bins = 1 << p.bits;
-    uint32_t* hist = sm;                          // [32][bins]: a warp's digit counts, then its next places
-    uint32_t* total = sm + kSortWarps * bins;     // [bins]: this CTA's counts
-    uint32_t* wsum = total + bins;                // [32]
+    griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_ctarank(), nc = cluster_nctarank();
+    if (cluster_id_x() > 0) {
+        const int64_t w = ((int64_t)blockIdx.x - nc) * kSortWarps + warp;
+        zero_rows(p, w, ((int64_t)gridDim.x - nc) * kSortWarps);
+        return;
+    }
+    const int bins = 1 << p.bits;
+    uint32_t* hist = sm;                          // [16][bins]: a warp's digit counts, then its next places
+    uint32_t* total = sm + kSortWarps * bins;     // [bins + 1]: this CTA's counts, and its tokens without a gradient
+    uint32_t* start = total + bins + 4;           // [bins]: where this CTA's entries of the digit go
+    uint32_t* wsum = start + bins;                // [16]
+    uint2* here = reinterpret_cast<uint2*>(wsum + 16);  // [2][on_chip]
     const uint32_t mask = (uint32_t)bins - 1;
 
     // each warp owns a run of tokens, in order over warps and CTAs
-    const uint32_t per = (p.N + nc * kSortWarps * 32 - 1) / (nc * kSortWarps * 32) * 32;
-    const uint64_t first = (uint64_t)(rank * kSortWarps + warp) * per;
-    const uint32_t i0 = (uint32_t)(first < p.N ? first : p.N);
-    const uint32_t i1 = (uint32_t)(first + per < p.N ? first + per : p.N);
-
-    if (rank == 0 && tid == 0) {
-        *p.err = 0u;
-        *p.invalid = 0u;
-    }
-    if (p.used) {
-        const uint32_t words = (p.V + 31) / 32;
-        for (uint32_t i = rank * kSortThreads + tid; i < words; i += nc * kSortThreads) p.used[i] = 0u;
-    }
-    __threadfence();
-    cluster_sync();
+    const uint32_t per = (p.N + nc * kSortThreads - 1) / (nc * kSortThreads) * 32;
+    const uint64_t from = (uint64_t)(rank * kSortWarps + warp) * per;
+    const uint32_t i0 = (uint32_t)(from < p.N ? from : p.N);
+    const uint32_t i1 = (uint32_t)(from + per < p.N ? from + per : p.N);
+    const uint32_t mine0 = rank * kSortWarps * per;  // the CTA's first entry
+    // bits 0..: tokens without a gradient, top bit: one of them out of range
+    if (tid == 0) total[bins] = 0u;
 
     for (int pass = 0; pass < p.passes; ++pass) {
-        const uint2* src = (pass & 1) ? p.b : p.a;
-        uint2* dst = (pass & 1) ? p.a : p.b;
+        const bool last = pass + 1 == p.passes;
         const int shift = pass * p.bits;
+        // read from `src` at i: this CTA's shared memory, or b and a in turn (the
+        // last digit is written to a)
+        uint2* chip = here + (pass & 1 ? p.on_chip : 0);
+        uint2* next = here + (pass & 1 ? 0 : p.on_chip);
+        uint2* src = ((p.passes - pass) & 1) ? p.b : p.a;
+        uint2* dst = ((p.passes - pass) & 1) ? p.a : p.b;
+        auto entry = [&](uint32_t i) -> uint2 { return p.on_chip ? chip[i - mine0] : __ldcg(src + i); };
         for (int i = tid; i < kSortWarps * bins / 4; i += kSortThreads)
             reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         uint32_t* mine = hist + warp * bins;
-        for (uint32_t base = i0; base < i1; base += 32) {
-            const uint32_t i = base + lane;
-            const bool on = i < i1;
-            uint32_t key = 0;
-            if (pass == 0) {
-                bool ok = true;
-                if (on) {
-                    const int64_t t = token_at(p.tok, p.dim1, p.ts0, p.ts1, p.flat, i);
-                    ok = t >= 0 && t < (int64_t)p.V && t != p.ignore;
-                    key = ok ? (uint32_t)t : p.V;
-                    if (!ok && t != p.ignore) atomicOr(p.err, CE_DEVERR_TARGET_RANGE);
-                    if (ok && p.used) atomicOr(p.used + (key >> 5), 1u << (key & 31));
-                    p.a[i] = make_uint2(key, i);  // what this thread scatters below
+        if (pass == 0) {
+            uint32_t none = 0;
+            bool out = false;
+            for (uint32_t base = i0; base < i1; base += 128) {
+                int64_t t[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t i = base + u * 32 + lane;
+                    if (i < i1) t[u] = token_at(p.tok, p.dim1, p.ts0, p.ts1, p.flat, i);
                 }
-                const unsigned bad = __ballot_sync(kFull, !ok);
-                if (bad && lane == 0) atomicAdd(p.invalid, (uint32_t)__popc(bad));
-            } else if (on) {
-                key = __ldcg(src + i).x;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t i = base + u * 32 + lane;
+                    if (i < i1) {
+                        const bool ok = t[u] >= 0 && t[u] < (int64_t)p.V && t[u] != p.ignore;
+                        const uint32_t key = ok ? (uint32_t)t[u] : p.V;
+                        none += !ok;
+                        out |= !ok && t[u] != p.ignore;
+                        // what this thread sends on below
+                        if (p.on_chip) chip[i - mine0] = make_uint2(key, i);
+                        else src[i] = make_uint2(key, i);
+                        atomicAdd(&mine[key & mask], 1u);
+                    }
+                }
             }
-            const uint32_t d = on ? (key >> shift) & mask : 0xffffffffu;
-            const unsigned peers = __match_any_sync(kFull, d);
-            if (on && lane == __ffs(peers) - 1) mine[d] += __popc(peers);
-            __syncwarp();
+            if (none) atomicAdd(&total[bins], none);
+            if (out) atomicOr(&total[bins], 0x80000000u);
+        } else {
+            for (uint32_t i = i0 + lane; i < i1; i += 32) atomicAdd(&mine[(entry(i).x >> shift) & mask], 1u);
         }
         __syncthreads();
-        // each bin: exclusive prefix over the warps, then the CTA's total
-        for (int b = tid; b < bins; b += kSortThreads) {
-            uint32_t run = 0;
-#pragma unroll 8
+        // each bin (one per thread): exclusive prefix over the warps, the CTA's total
+        if (tid < bins) {
+            uint32_t c[kSortWarps], run = 0;
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) c[w] = hist[w * bins + tid];
+#pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t c = hist[w * bins + b];
-                hist[w * bins + b] = run;
-                run += c;
+                hist[w * bins + tid] = run;
+                run += c[w];
             }
-            total[b] = run;
+            total[tid] = run;
         }
-        cluster_sync();
-        uint32_t before = 0, all = 0;  // bins <= threads: one bin per thread
-        if (tid < bins)
-            for (uint32_t r = 0; r < nc; ++r) {
-                const uint32_t c = ld_dsmem_u32(total + tid, r);
-                if (r < rank) before += c;
-                all += c;
+        if (nc > 1) cluster_sync(); else __syncthreads();
+        uint32_t before = 0, all = 0;
+        if (tid < bins) {
+            uint32_t c[kSortCluster];
+#pragma unroll
+            for (uint32_t r = 0; r < kSortCluster; ++r) c[r] = r < nc ? ld_dsmem_u32(total + tid, r) : 0u;
+#pragma unroll
+            for (uint32_t r = 0; r < kSortCluster; ++r) {
+                if (r < rank) before += c[r];
+                all += c[r];
             }
+        }
+        if (pass == 0 && rank == 0 && tid < 32) {
+            uint32_t c = lane < (int)nc ? ld_dsmem_u32(total + bins, lane) : 0u;
+            const unsigned out = __ballot_sync(kFull, (c & 0x80000000u) != 0u);
+            c &= 0x7fffffffu;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(kFull, c, o);
+            if (lane == 0) {
+                *p.invalid = c;
+                *p.err = out ? CE_DEVERR_TARGET_RANGE : 0u;
+            }
+        }
         // exclusive scan of `all` over the bins
         uint32_t inc = all;
 #pragma unroll
@@ -200,35 +255,48 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
         }
         if (lane == 31) wsum[warp] = inc;
         __syncthreads();
-        uint32_t ws = wsum[lane];
+        uint32_t ws = lane < kSortWarps ? wsum[lane] : 0u;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
+        for (int o = 1; o < kSortWarps; o <<= 1) {
             const uint32_t u = __shfl_up_sync(kFull, ws, o);
             if (lane >= o) ws += u;
         }
         const uint32_t upto = __shfl_sync(kFull, ws, warp == 0 ? 0 : warp - 1);
-        const uint32_t start = (warp == 0 ? 0u : upto) + inc - all + before;
-        if (tid < bins)
-#pragma unroll 8
-            for (int w = 0; w < kSortWarps; ++w) hist[w * bins + tid] += start;
+        if (tid < bins) start[tid] = (warp == 0 ? 0u : upto) + inc - all + before;
+        // this CTA has read the others' counts: with the last digit it only
+        // has to stay until they have read its own
+        if (last && nc > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         __syncthreads();
         for (uint32_t base = i0; base < i1; base += 32) {
             const uint32_t i = base + lane;
             const bool on = i < i1;
-            uint2 e = make_uint2(0, 0);
-            if (on) e = __ldcg(src + i);
-            const uint32_t d = on ? (e.x >> shift) & mask : 0xffffffffu;
-            const unsigned peers = __match_any_sync(kFull, d);
+            const uint2 e = on ? entry(i) : make_uint2(0u, 0u);
+            const uint32_t d = (e.x >> shift) & mask;
+            // the lanes with the same digit, a bit of it at a time
+            unsigned peers = __ballot_sync(kFull, on);
+            for (int k = 0; k < p.bits; ++k) {
+                const unsigned one = __ballot_sync(kFull, (d >> k) & 1u);
+                peers &= (d >> k) & 1u ? one : ~one;
+            }
             uint32_t at = 0;
-            if (on) at = mine[d] + __popc(peers & ((1u << lane) - 1u));
+            if (on) at = start[d] + mine[d] + __popc(peers & ((1u << lane) - 1u));
             __syncwarp();
             if (on && lane == __ffs(peers) - 1) mine[d] += __popc(peers);
             __syncwarp();
-            if (on) dst[at] = e;
+            if (on) {
+                if (last || !p.on_chip) {
+                    dst[at] = e;
+                } else {
+                    const uint32_t to = at / (kSortWarps * per);
+                    st_dsmem_u2(next + (at - to * kSortWarps * per), to, e);
+                }
+            }
         }
-        __threadfence();
-        cluster_sync();  // the next pass reads what all CTAs wrote; no CTA leaves while its counts are read
+        if (last) break;
+        if (!p.on_chip) __threadfence();
+        if (nc > 1) cluster_sync(); else __syncthreads();  // the next pass reads what all CTAs wrote
     }
+    if (nc > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ----------------------------------------------------------------- sums of runs
@@ -242,11 +310,9 @@ struct GradArgs {
     char* dw;
     int64_t dws;           // in bytes
     float* part;           // [chunks][2][H]
-    const uint32_t* used;  // or NULL: rows of absent tokens stay as they are
     int nv;                // vectors per row
     int R;                 // entries per chunk
     int chunks;
-    int zero_ctas;         // CTAs per column slab that zero absent rows
     int accumulate;
     float scale;
 };
@@ -254,20 +320,29 @@ struct GradArgs {
 constexpr int kGradThreads = 128;
 constexpr int kMaxR = 64;
 
+// One run's sum.  Adding goes through L2's reductions: a row has one writer, so
+// the result does not depend on any order, and the thread does not wait for what
+// is there (a load in its place held every run's end up for an HBM latency).
+// L2 takes values below 2^-126 as zeros.
 template <typename TW, int VEC>
 __device__ __forceinline__ void write_row(char* row, int64_t col, const float* acc, float scale, int accumulate) {
     if constexpr (sizeof(TW) == 4) {
         float* q = reinterpret_cast<float*>(row) + col;
         float o[VEC];
-        if (accumulate) {
-            load_f32<VEC>(q, o);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = fmaf(acc[i], scale, o[i]);
+        for (int i = 0; i < VEC; ++i) o[i] = acc[i] * scale;
+        if (!accumulate) {
+            store_f32<VEC>(q, o);
+        } else if constexpr (VEC % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < VEC; i += 4)
+                asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(q + i), "f"(o[i]), "f"(o[i + 1]),
+                             "f"(o[i + 2]), "f"(o[i + 3])
+                             : "memory");
         } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = acc[i] * scale;
+            for (int i = 0; i < VEC; ++i) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(q + i), "f"(o[i]) : "memory");
         }
-        store_f32<VEC>(q, o);
     } else {
         Pack<TW, VEC> o;
 #pragma unroll
@@ -283,19 +358,9 @@ __global__ void __launch_bounds__(kGradThreads) ce_embed_grad_kernel(const __gri
     const int v = blockIdx.y * kGradThreads + threadIdx.x;
     const bool on = v < p.nv;
     const int64_t col = (int64_t)v * VEC;
-    if ((int)blockIdx.x >= p.chunks) {
-        // absent tokens' rows
-        if (!on) return;
-        float z[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) z[i] = 0.f;
-        for (uint32_t r = blockIdx.x - p.chunks; r < p.V; r += p.zero_ctas) {
-            if ((__ldg(p.used + (r >> 5)) >> (r & 31)) & 1u) continue;
-            write_row<TW, VEC>(p.dw + (int64_t)r * p.dws, col, z, 0.f, 0);
-        }
-        return;
-    }
     __shared__ uint2 ent[kMaxR + 2];  // the chunk's entries between its neighbours
+    griddep_wait();
+    griddep_launch_dependents();
     const uint32_t n = p.N - *p.invalid;
     const uint32_t c0 = blockIdx.x * (uint32_t)p.R;
     if (c0 >= n) return;
@@ -340,27 +405,46 @@ __global__ void __launch_bounds__(kGradThreads) ce_embed_grad_kernel(const __gri
     }
 }
 
-template <typename TW>
+// A run that crosses chunk borders begins in one chunk (its part is that chunk's
+// second) and fills whole chunks (their first parts) up to its last.
+template <typename TW, int VEC>
 __global__ void __launch_bounds__(kGradThreads) ce_embed_join_kernel(const __grid_constant__ GradArgs p) {
+    griddep_wait();
     const uint32_t n = p.N - *p.invalid;
     const uint64_t c0 = (uint64_t)blockIdx.x * p.R, c1 = c0 + p.R;
     if (c1 >= n) return;                        // the last chunk's last run ends there
-    const uint32_t key = p.ent[c1 - 1].x;
-    if (p.ent[c1].x != key) return;             // no run crosses this border
-    if (p.ent[c0].x == key && c0 > 0 && p.ent[c0 - 1].x == key) return;  // it began in an earlier chunk
-    // the run's end: first entry past it
-    uint32_t lo = (uint32_t)c1, hi = n;
-    while (lo < hi) {
-        const uint32_t m = lo + (hi - lo) / 2;
-        if (p.ent[m].x == key) lo = m + 1; else hi = m;
+    const uint32_t key = p.ent[c1 - 1].x, over = p.ent[c1].x;
+    const uint32_t at0 = p.ent[c0].x, prev = c0 > 0 ? p.ent[c0 - 1].x : 0xffffffffu;
+    if (over != key) return;                    // no run crosses this border
+    if (at0 == key && prev == key) return;      // it began in an earlier chunk
+    // the last chunk that begins with the token, 32 chunks at a look
+    const int lane = threadIdx.x & 31;
+    int64_t last = blockIdx.x + 1;
+    for (;;) {
+        const int64_t c = last + 1 + lane;
+        const uint64_t i = (uint64_t)c * p.R;
+        const unsigned same = __ballot_sync(kFull, i < n && p.ent[i < n ? i : 0].x == key);
+        const int k = same == kFull ? 32 : __ffs(~same) - 1;
+        last += k;
+        if (k < 32) break;
     }
-    const int64_t last = (lo - 1) / (uint32_t)p.R;  // chunk of its last entry
-    const int64_t col = (int64_t)blockIdx.y * kGradThreads + threadIdx.x;
+    const int64_t col = ((int64_t)blockIdx.y * kGradThreads + threadIdx.x) * VEC;
     if (col >= p.H) return;
-    float acc = p.part[((int64_t)blockIdx.x * 2 + 1) * p.H + col];
-#pragma unroll 8
-    for (int64_t c = blockIdx.x + 1; c <= last; ++c) acc += p.part[c * 2 * p.H + col];
-    write_row<TW, 1>(p.dw + (int64_t)key * p.dws, col, &acc, p.scale, p.accumulate);
+    constexpr int B = 8;
+    float acc[VEC];
+    load_f32<VEC>(p.part + ((int64_t)blockIdx.x * 2 + 1) * p.H + col, acc);
+    for (int64_t c = blockIdx.x + 1; c <= last; c += B) {
+        float v[B][VEC];
+#pragma unroll
+        for (int u = 0; u < B; ++u)
+            if (c + u <= last) load_f32<VEC>(p.part + (c + u) * 2 * p.H + col, v[u]);
+#pragma unroll
+        for (int u = 0; u < B; ++u)
+            if (c + u <= last)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) acc[i] += v[u][i];
+    }
+    write_row<TW, VEC>(p.dw + (int64_t)key * p.dws, col, acc, p.scale, p.accumulate);
 }
 
 // entries per chunk, from the sizes alone (the workspace holds two float32
@@ -368,17 +452,16 @@ __global__ void __launch_bounds__(kGradThreads) ce_embed_join_kernel(const __gri
 int chunk_entries(int64_t N) { return N >= 8192 ? 32 : (N >= 1024 ? 16 : 8); }
 
 struct EmbedWs {
-    size_t a, b, used, part, bytes;
+    size_t a, b, part, bytes;
     int R, chunks;
 };
-EmbedWs embed_ws(int64_t N, int64_t H, int64_t V) {
+EmbedWs embed_ws(int64_t N, int64_t H) {
     EmbedWs w;
     w.R = chunk_entries(N);
     w.chunks = (int)((N + w.R - 1) / w.R);
     w.a = kWsHeaderBytes;
     w.b = w.a + align_up((size_t)N * 8, 256);
-    w.used = w.b + align_up((size_t)N * 8, 256);
-    w.part = w.used + align_up((size_t)(V + 31) / 32 * 4, 256);
+    w.part = w.b + align_up((size_t)N * 8, 256);
     w.bytes = w.part + (size_t)w.chunks * 2 * (size_t)H * 4;
     return w;
 }
@@ -417,20 +500,30 @@ cudaError_t launch_fwd_t(EmbedFwdArgs& a, int64_t H, int vb, cudaStream_t s) {
     return launch_fwd<T, 1>(a, H, s);
 }
 
+// A kernel that may start while the one before it ends.
+template <typename K, typename A>
+cudaError_t launch_behind(K* k, dim3 grid, int threads, const A& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    set_pdl_attr(at);
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a);
+}
+
 template <typename T, typename TW, int VEC>
 cudaError_t launch_grad(GradArgs& a, cudaStream_t s) {
+    if (a.chunks == 0) return cudaSuccess;
     a.nv = (int)(a.H / VEC);
-    const unsigned slabs = (unsigned)((a.nv + kGradThreads - 1) / kGradThreads);
-    a.zero_ctas = a.used ? (int)(a.V < 2048 ? a.V : 2048) : 0;
-    ce_embed_grad_kernel<T, TW, VEC><<<dim3((unsigned)(a.chunks + a.zero_ctas), slabs), kGradThreads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (a.chunks > 1) {
-        const dim3 grid((unsigned)(a.chunks - 1), (unsigned)((a.H + kGradThreads - 1) / kGradThreads));
-        ce_embed_join_kernel<TW><<<grid, kGradThreads, 0, s>>>(a);
-        e = cudaGetLastError();
-    }
-    return e;
+    const dim3 grid((unsigned)a.chunks, (unsigned)((a.nv + kGradThreads - 1) / kGradThreads));
+    cudaError_t e = launch_behind(ce_embed_grad_kernel<T, TW, VEC>, grid, kGradThreads, a, s);
+    if (e != cudaSuccess || a.chunks == 1) return e;
+    constexpr int JV = VEC >= 4 ? 4 : 1;  // floats of the parts per thread
+    const dim3 join((unsigned)(a.chunks - 1), (unsigned)((a.H / JV + kGradThreads - 1) / kGradThreads));
+    return launch_behind(ce_embed_join_kernel<TW, JV>, join, kGradThreads, a, s);
 }
 template <typename T>
 cudaError_t launch_grad_t(GradArgs& a, bool w32, int vb, cudaStream_t s) {
@@ -449,16 +542,28 @@ cudaError_t launch_grad_t(GradArgs& a, bool w32, int vb, cudaStream_t s) {
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_sort(const SortArgs& a, cudaStream_t s) {
+cudaError_t launch_sort(SortArgs& a, cudaStream_t s) {
     const int bins = 1 << a.bits;
-    const size_t smem = (size_t)(kSortWarps * bins + bins + 32) * 4;
-    cudaError_t e = cudaFuncSetAttribute(ce_embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)((kSortWarps * kMaxBins + kMaxBins + 32) * 4));
-    if (e != cudaSuccess) return e;
     int nc = 1;
-    while (nc < kSortCluster && (int64_t)nc * 2048 < a.N) nc *= 2;
+    while (nc < kSortCluster && (int64_t)nc * 1024 < a.N) nc *= 2;
+    const int64_t each = ((int64_t)a.N + nc * kSortThreads - 1) / (nc * kSortThreads) * kSortThreads;
+    const size_t counts = (size_t)(kSortWarps * bins + 2 * bins + 20) * 4;
+    a.on_chip = each <= kOnChip && counts + (size_t)each * 16 <= 220 * 1024 ? (int)each : 0;
+    const size_t smem = counts + (size_t)a.on_chip * 16;
+    cudaError_t e;
+    if (smem > 48 * 1024 &&
+        (e = cudaFuncSetAttribute(ce_embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
+            cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(nc);
+    // a warp for every row to zero, up to two CTAs on each of the other SMs
+    int extra = 0;
+    if (a.zero) {
+        const int64_t want = (a.zrows + kSortWarps - 1) / kSortWarps;
+        extra = (int)(want < 288 ? want : 288);
+        extra = (extra + nc - 1) / nc * nc;
+    }
+    cfg.gridDim = dim3(nc + extra);
     cfg.blockDim = dim3(kSortThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -523,7 +628,7 @@ extern "C" ce_status ce_embed_fwd(const int64_t* tokens, int64_t dim0, int64_t d
 
 extern "C" size_t ce_embed_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V) {
     if (bad_sizes(N, H, V)) return 0;
-    return embed_ws(N, H, V).bytes;
+    return embed_ws(N, H).bytes;
 }
 
 extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t grad_out_stride,
@@ -544,7 +649,7 @@ extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t 
         if (!grad_out || !tokens || off_grid(grad_out, es) || off_grid(tokens, 8)) return CE_ERR_INVALID_ARG;
         if (token_strides[0] < 0 || token_strides[1] < 0 || grad_out_stride < 0) return CE_ERR_BAD_STRIDE;
     }
-    const EmbedWs w = embed_ws(N, H, V);
+    const EmbedWs w = embed_ws(N, H);
     if (workspace_bytes < w.bytes) return CE_ERR_WORKSPACE_TOO_SMALL;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* base = static_cast<char*>(workspace);
@@ -566,15 +671,25 @@ extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t 
     sa.err = reinterpret_cast<uint32_t*>(base + kWsErrOffset);
     sa.invalid = reinterpret_cast<uint32_t*>(base + kWsInvalidOffset);
     uint2* a = reinterpret_cast<uint2*>(base + w.a);
-    uint2* b = reinterpret_cast<uint2*>(base + w.b);
     sa.a = a;
-    sa.b = b;
-    sa.used = accumulate ? nullptr : reinterpret_cast<uint32_t*>(base + w.used);
+    sa.b = reinterpret_cast<uint2*>(base + w.b);
+    sa.zero = accumulate ? nullptr : static_cast<char*>(grad_weight);
+    sa.zrows = V;
+    sa.zstride = grad_weight_stride * wes;
+    sa.zbytes = H * wes;
+    if (sa.zero && (V == 1 || sa.zstride == sa.zbytes)) {
+        // one run of memory: rows of 16 KB
+        const int64_t all = V * sa.zbytes, row = 16384;
+        if (all % row == 0 || all < row) {
+            sa.zrows = all < row ? 1 : all / row;
+            sa.zstride = sa.zbytes = all < row ? all : row;
+        }
+    }
     if (launch_sort(sa, s) != cudaSuccess) return CE_ERR_LAUNCH;
-    if (N == 0 && accumulate) return CE_OK;
+    if (N == 0) return CE_OK;
 
     GradArgs ga;
-    ga.ent = (sa.passes & 1) ? b : a;
+    ga.ent = a;
     ga.invalid = sa.invalid;
     ga.N = sa.N;
     ga.V = sa.V;
@@ -584,7 +699,6 @@ extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t 
     ga.dw = static_cast<char*>(grad_weight);
     ga.dws = grad_weight_stride * wes;
     ga.part = reinterpret_cast<float*>(base + w.part);
-    ga.used = sa.used;
     ga.R = w.R;
     ga.chunks = w.chunks;
     ga.accumulate = accumulate ? 1 : 0;
