@@ -207,7 +207,7 @@ def test_backward(H, dtype):
         assert none is None and torch.equal(only, gx)
 
 
-@pytest.mark.parametrize("H", [72, 1001, 4096, 9001])
+@pytest.mark.parametrize("H", [72, 520, 1001, 1024, 2048, 4096, 9001])
 @pytest.mark.parametrize("N", [455, 457, 1500])
 def test_backward_many_rows(N, H):
     h, dh, w = make(N, H, torch.bfloat16, N)
@@ -236,6 +236,20 @@ def test_backward_strides_and_in_place(H, dtype):
     one = go[:1].expand(7, H)  # one gradient row for all
     gx, gw = pkg.ce_rmsnorm_bwd(one, h, w)
     check_bwd(gx, gw, one, h, w, None)
+
+
+@pytest.mark.parametrize("H", [1, 5, 1024, 4097, 8190])
+@pytest.mark.parametrize("N", [1, 2, 300, 1300])
+def test_backward_rows_off_the_grid(H, N):
+    # each tensor at its own offset from 16 bytes, the first and last rows at the storage's ends
+    g = rng(H + N)
+    flat = [torch.randn(N * H + 8, generator=g).to(torch.float16).to(DEV) for _ in range(3)]
+    go, h, dh = (f[k:k + N * H].view(N, H) for f, k in zip(flat, (1, 3, 6)))
+    w = torch.randn(H, generator=g).to(torch.float16).to(DEV)
+    gx, gw = pkg.ce_rmsnorm_bwd(go, h, w, grad_h=dh)
+    check_bwd(gx, gw, go, h, w, dh)
+    gx, gw = pkg.ce_rmsnorm_bwd(go, h, w)
+    check_bwd(gx, gw, go, h, w, None)
 
 
 def test_no_rows():

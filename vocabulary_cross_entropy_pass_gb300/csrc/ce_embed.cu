@@ -551,7 +551,7 @@ cudaError_t launch_sort(SortArgs& a, cudaStream_t s) {
     a.on_chip = each <= kOnChip && counts + (size_t)each * 16 <= 220 * 1024 ? (int)each : 0;
     const size_t smem = counts + (size_t)a.on_chip * 16;
     cudaError_t e;
-    if (smem > 48 * 1024 &&
+    if (smem > 40 * 1024 &&
         (e = cudaFuncSetAttribute(ce_embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) !=
             cudaSuccess)
         return e;

@@ -595,7 +595,7 @@ template <typename T, bool BWD>
 cudaError_t launch_logits_t(const LogitArgs& a, cudaStream_t s) {
     cudaError_t e;
     auto allow = [](auto* k, size_t smem) {
-        return smem > 48 * 1024 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
+        return smem > 40 * 1024 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
                                 : cudaSuccess;
     };
     const int64_t rows = a.N < 65535 ? a.N : 65535;

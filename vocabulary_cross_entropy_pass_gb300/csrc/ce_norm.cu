@@ -310,7 +310,7 @@ cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
     constexpr int MAXV = VEC >= 8 ? 4 : (VEC == 4 ? 8 : 16);  // 512 threads hold 512 * MAXV vectors
     if (nv > 512 * MAXV) {
         auto* k = ce_rmsnorm_fwd_wide_kernel<T, VEC, Q8>;
-        if (smem > 48 * 1024) {
+        if (smem > 40 * 1024) {
             cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess) return e;
         }
@@ -355,62 +355,176 @@ struct NormBwdArgs {
 };
 
 // A persistent grid over the rows; a thread keeps its columns' dw sums in
-// registers over all rows of its CTA and writes them once.
-template <typename T, int VEC, int VPT>
-__global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_constant__ NormBwdArgs p) {
+// registers over all rows of its CTA and writes them once.  The rows come in by
+// bulk copies (TMA) into a ring of `stages` row sets (g, h and dh): the next ones
+// are on their way while one is worked on, and both passes over a row read
+// shared memory.  A row off the 16-byte grid is copied from the boundary before
+// it to the boundary after it, as far as that stays between the tensor's first
+// and last element, the rest element by element.
+//   GRID: rows on the grid, VPT vectors of 16 bytes per thread; else VPT
+//   single elements per thread, TH apart.
+// One barrier per row: it hands the sums over, and past it the row before
+// has been read by all, so its place is filled again.  A copy that does not
+// arrive sets the workspace's error word, and every thread leaves at the row's barrier.
+struct RingArgs {
+    NormBwdArgs n;
+    uint32_t* err;         // the workspace's error word, or NULL
+    int stages, slot;      // bytes of one tensor's row in the ring (a multiple of 16)
+};
+
+template <int ES>
+struct RowSpan {           // what of a row the bulk copy takes
+    const char* from;
+    uint32_t bytes;        // 0: nothing
+    int at;                // byte of the slot where `from` lands; the row begins at byte `phase`
+    int phase;
+};
+template <int ES>
+__device__ __forceinline__ RowSpan<ES> row_span(const char* base, int64_t stride, int64_t row, int64_t rows, int64_t len) {
+    const char* a = base + row * stride;
+    const uintptr_t u = reinterpret_cast<uintptr_t>(a), e = u + (uintptr_t)len;
+    const uintptr_t first = reinterpret_cast<uintptr_t>(base);
+    const uintptr_t last = first + (uintptr_t)((rows - 1) * stride + len);  // past the last element
+    uintptr_t lo = u & ~(uintptr_t)15, hi = (e + 15) & ~(uintptr_t)15;
+    const int phase = (int)(u - lo);
+    if (lo < first) lo = (u + 15) & ~(uintptr_t)15;
+    if (hi > last) hi = e & ~(uintptr_t)15;
+    RowSpan<ES> s;
+    s.phase = phase;
+    s.from = reinterpret_cast<const char*>(lo);
+    s.bytes = hi > lo ? (uint32_t)(hi - lo) : 0u;
+    s.at = (int)(lo - (u - phase));
+    return s;
+}
+
+template <typename T, int VPT, bool GRID, bool RES>
+__global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_constant__ RingArgs q) {
     constexpr int ES = sizeof(T);
-    __shared__ float2 red[2][32];
+    constexpr int VEC = GRID ? 16 / ES : 1;
+    constexpr int NT = RES ? 3 : 2;            // tensors per row set
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ uint64_t full[16];
+    __shared__ float2 red[2][16];
+    __shared__ int gave_up;
+    const NormBwdArgs& p = q.n;
     const int tid = threadIdx.x, TH = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = TH >> 5;
     const int nv = (int)(p.H / VEC);
-    float w[VPT][VEC], dw[VPT][VEC];
+    const int64_t len = p.H * ES;
+    const uint64_t policy = l2_evict_first_policy();
+    if (tid == 0) {
+        for (int k = 0; k < q.stages; ++k) mbar_init(&full[k], 1);
+        gave_up = 0;
+        if (blockIdx.x == 0 && q.err) *q.err = 0u;
+        fence_barrier_init();
+    }
+    __syncthreads();
+
+    auto base_of = [&](int t) { return t == 0 ? p.g : (t == 1 ? p.h : p.dh); };
+    auto stride_of = [&](int t) { return t == 0 ? p.gs : (t == 1 ? p.hs : p.dhs); };
+    auto span_of = [&](int t, int64_t row) { return row_span<ES>(base_of(t), stride_of(t), row, p.N, len); };
+    auto issue = [&](int64_t row, int stage) {  // one thread
+        unsigned char* at = ring + (size_t)stage * NT * q.slot;
+        if (GRID) {
+            mbar_arrive_expect_tx(&full[stage], (uint32_t)(NT * len));
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                tma_load_1d(at + t * q.slot, base_of(t) + row * stride_of(t), (uint32_t)len, &full[stage], policy);
+        } else {
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) bytes += span_of(t, row).bytes;
+            mbar_arrive_expect_tx(&full[stage], bytes);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const RowSpan<ES> s = span_of(t, row);
+                if (s.bytes) tma_load_1d(at + t * q.slot + s.at, s.from, s.bytes, &full[stage], policy);
+            }
+        }
+    };
+    if (tid == 0)
+        for (int k = 0; k < q.stages; ++k) {
+            const int64_t row = blockIdx.x + (int64_t)k * gridDim.x;
+            if (row < p.N) issue(row, k);
+        }
+
+    float w32[VPT][VEC], dw[VPT][VEC];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int v = tid + k * TH;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             dw[k][i] = 0.f;
-            w[k][i] = 0.f;
+            w32[k][i] = 0.f;
             if (v < nv)
-                w[k][i] = p.w32 ? __ldg(reinterpret_cast<const float*>(p.w) + (int64_t)v * VEC + i)
-                                : to_f32(reinterpret_cast<const T*>(p.w)[(int64_t)v * VEC + i]);
+                w32[k][i] = p.w32 ? __ldg(reinterpret_cast<const float*>(p.w) + (int64_t)v * VEC + i)
+                                   : to_f32(reinterpret_cast<const T*>(p.w)[(int64_t)v * VEC + i]);
         }
     }
-    int flip = 0;
+
+    int stage = 0, flip = 0;
+    uint32_t parity = 0;
+    int64_t done = -1;     // stage whose row all threads have read once they pass the next barrier
     for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, flip ^= 1) {
-        const char* gp = p.g + row * p.gs;
-        const char* hp = p.h + row * p.hs;
-        Pack<T, VEC> g[VPT], h[VPT], d[VPT];
+        const unsigned char* at = ring + (size_t)stage * NT * q.slot;
+        if (!mbar_wait_bounded(&full[stage], parity)) {
+            if (q.err) atomicOr(q.err, CE_DEVERR_TIMEOUT);
+            gave_up = 1;
+        }
+        int ph[3] = {0, 0, 0};
+        if (!GRID) {
+            // the elements that no copy could take (the tensor's first and last row)
+            bool some = false;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const RowSpan<ES> s = span_of(t, row);
+                ph[t] = s.phase;
+                // elements before the copy, and the first one after it
+                const int64_t head = min(p.H, s.at > s.phase ? (int64_t)((s.at - s.phase) / ES) : (int64_t)0);
+                const int64_t tail0 = s.bytes ? ((int64_t)s.at + s.bytes - s.phase) / ES : head;
+                const char* a = base_of(t) + row * stride_of(t);
+                T* to = reinterpret_cast<T*>(ring + (size_t)stage * NT * q.slot + t * q.slot + s.phase);
+                const bool part = head > 0 || tail0 < p.H;
+                some |= part;
+                if (part) {
+                    for (int64_t c = tid; c < head; c += TH) to[c] = reinterpret_cast<const T*>(a)[c];
+                    for (int64_t c = tail0 + tid; c < p.H; c += TH) to[c] = reinterpret_cast<const T*>(a)[c];
+                }
+            }
+            if (some) {
+                fence_proxy_async_smem();  // a later copy may land on these bytes
+                __syncthreads();
+            }
+        }
+        auto get = [&](int t, int v) {
+            Pack<T, VEC> x;
+            x.load(at + t * q.slot + ph[t] + (size_t)v * VEC * ES);
+            return x;
+        };
+        float ss = 0.f, c = 0.f;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int v = tid + k * TH;
-            g[k].zero();
-            h[k].zero();
             if (v < nv) {
-                g[k].load_cs(gp + (int64_t)v * VEC * ES);
-                h[k].load_cs(hp + (int64_t)v * VEC * ES);
+                const Pack<T, VEC> g = get(0, v), h = get(1, v);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float hv = h.f(i);
+                    ss = fmaf(hv, hv, ss);
+                    c = fmaf(g.f(i) * w32[k][i], hv, c);
+                }
             }
         }
-        if (p.dh) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int v = tid + k * TH;
-                if (v < nv) d[k].load_cs(p.dh + row * p.dhs + (int64_t)v * VEC * ES);
-            }
-        }
-        float ss = 0.f, c = 0.f;
-#pragma unroll
-        for (int k = 0; k < VPT; ++k)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float hv = h[k].f(i);
-                ss = fmaf(hv, hv, ss);
-                c = fmaf(g[k].f(i) * w[k][i], hv, c);
-            }
         ss = warp_allsum(ss);
         c = warp_allsum(c);
-        if (nw > 1) {
-            if (lane == 0) red[flip][warp] = make_float2(ss, c);
-            __syncthreads();
+        if (lane == 0) red[flip][warp] = make_float2(ss, c);
+        __syncthreads();
+        if (gave_up) break;
+        if (tid == 0 && done >= 0) {
+            // the row before this one has been read by all
+            const int64_t next = row + (int64_t)(q.stages - 1) * gridDim.x;
+            if (next < p.N) issue(next, (int)done);
+        }
+        {
             const float2 t = lane < nw ? red[flip][lane] : make_float2(0.f, 0.f);
             ss = warp_allsum(t.x);
             c = warp_allsum(t.y);
@@ -421,26 +535,40 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int v = tid + k * TH;
-            Pack<T, VEC> o;
+            if (v < nv) {
+                const Pack<T, VEC> g = get(0, v), h = get(1, v);
+                Pack<T, VEC> d, o;
+                if (RES) d = get(2, v);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float n = h[k].f(i) * rstd, gv = g[k].f(i);
-                dw[k][i] = fmaf(gv, n, dw[k][i]);
-                float t = rstd * fmaf(-n, cc, gv * w[k][i]);
-                if (p.dh) t += d[k].f(i);
-                o.set(i, t);
+                for (int i = 0; i < VEC; ++i) {
+                    const float n = h.f(i) * rstd, gv = g.f(i);
+                    dw[k][i] = fmaf(gv, n, dw[k][i]);
+                    float t = rstd * fmaf(-n, cc, gv * w32[k][i]);
+                    if (RES) t += d.f(i);
+                    o.set(i, t);
+                }
+                o.store_cs(xp + (int64_t)v * VEC * ES);
             }
-            if (v < nv) o.store(xp + (int64_t)v * VEC * ES);
         }
+        done = stage;
+        if (++stage == q.stages) {
+            stage = 0;
+            parity ^= 1u;
+        }
+    }
+    if (gave_up) {
+        // no copy may land after this CTA has left
+        if (tid == 0)
+            for (int k = 0; k < q.stages; ++k) mbar_wait_bounded(&full[k], k >= stage ? parity : parity ^ 1u);
+        __syncthreads();
+        return;
     }
     if (p.part) {
         float* out = p.part + (int64_t)blockIdx.x * p.H;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int v = tid + k * TH;
-            if (v < nv)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) out[(int64_t)v * VEC + i] = dw[k][i];
+            if (v < nv) store_f32<VEC>(out + (int64_t)v * VEC, dw[k]);
         }
     }
 }
@@ -506,57 +634,75 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_wide_kernel(const __grid_c
     }
 }
 
-// dw_j = the partial rows' column sums, in a fixed order: 32 columns per CTA,
-// eight rows' worth of lanes each summing every eighth partial row.
-__global__ void __launch_bounds__(256) ce_rmsnorm_dw_kernel(const float* part, int64_t rows, int64_t H, float* dw) {
-    __shared__ float sh[8][33];
+// dw_j = the partial rows' column sums, in a fixed order: 32 columns per CTA, a
+// warp to every 32nd partial row, then the warps' sums in order.
+__global__ void __launch_bounds__(1024) ce_rmsnorm_dw_kernel(const float* part, int rows, int64_t H, float* dw) {
+    __shared__ float sh[32][33];
+    griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float acc = 0.f;
     if (c < H) {
 #pragma unroll 8
-        for (int64_t r = warp; r < rows; r += 8) acc += part[r * H + c];
+        for (int r = warp; r < rows; r += 32) acc += __ldcg(part + r * H + c);
     }
     sh[warp][lane] = acc;
     __syncthreads();
-    if (warp == 0 && c < H) {
-        float t = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) t += sh[k][lane];
-        dw[c] = t;
-    }
+    // warp w adds column w's 32 sums pairwise, the same pairs on every run
+    const float t = warp_allsum(sh[lane][warp]);
+    const int64_t col = (int64_t)blockIdx.x * 32 + warp;
+    if (lane == 0 && col < H) dw[col] = t;
 }
 
 // CTAs of the backward grid, from the sizes alone (the workspace holds a
-// partial row for each).
-constexpr int kBwdGrid = 152 * 3;
-int bwd_grid(int64_t N) { return (int)(N < kBwdGrid ? N : kBwdGrid); }
+// partial row for each): two per SM, more for short rows.
+int bwd_per_sm(int64_t H) { return H >= 2048 ? 2 : (H >= 1024 ? 4 : 8); }
+int bwd_grid(int64_t N, int64_t H) {
+    const int64_t most = 152 * bwd_per_sm(H);
+    return (int)(N < most ? N : most);
+}
 
-template <typename T, int VEC>
-cudaError_t launch_bwd_k(const NormBwdArgs& a, cudaStream_t s) {
-    constexpr int MAXV = VEC >= 8 ? 4 : (VEC == 4 ? 8 : 16);
-    const int64_t nv = a.H / VEC;
-    const int grid = bwd_grid(a.N);
-    if (nv <= 256) {
-        ce_rmsnorm_bwd_kernel<T, VEC, 1><<<grid, (unsigned)((nv + 31) / 32 * 32), 0, s>>>(a);
-    } else if (nv <= 1024) {
-        ce_rmsnorm_bwd_kernel<T, VEC, 2><<<grid, (unsigned)((nv + 63) / 64 * 32), 0, s>>>(a);
-    } else if (nv <= 512 * MAXV) {
-        ce_rmsnorm_bwd_kernel<T, VEC, MAXV>
-            <<<grid, (unsigned)((nv + 32 * MAXV - 1) / (32 * MAXV) * 32), 0, s>>>(a);
-    } else {
-        ce_rmsnorm_bwd_wide_kernel<T, VEC><<<grid, 512, 0, s>>>(a);
+template <typename T, bool GRID, int VPT>
+cudaError_t launch_ring(RingArgs& q, int threads, size_t smem, cudaStream_t s) {
+    auto* k = q.n.dh ? ce_rmsnorm_bwd_kernel<T, VPT, GRID, true> : ce_rmsnorm_bwd_kernel<T, VPT, GRID, false>;
+    if (smem > 40 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
     }
+    k<<<bwd_grid(q.n.N, q.n.H), threads, smem, s>>>(q);
+    return cudaGetLastError();
+}
+
+// The widest row that the ring kernel takes: 512 threads' registers, and two row
+// sets in shared memory.
+template <typename T, bool GRID>
+cudaError_t launch_bwd_g(const NormBwdArgs& a, uint32_t* err, cudaStream_t s) {
+    constexpr int ES = sizeof(T);
+    constexpr int VEC = GRID ? 16 / ES : 1;
+    constexpr int M = GRID ? (VEC == 8 ? 1 : 2) : 4;  // a step of vectors per thread: 8 elements, 4 off the grid
+    const int64_t nv = a.H / VEC;
+    RingArgs q;
+    q.n = a;
+    q.err = err;
+    q.slot = (int)((a.H * ES + 15) / 16 * 16 + (GRID ? 0 : 16));
+    const int64_t set = (int64_t)q.slot * (a.dh ? 3 : 2);
+    int64_t room = 216 * 1024 / bwd_per_sm(a.H);
+    if (room < 3 * set) room = 216 * 1024;
+    q.stages = (int)(room / set < 8 ? room / set : 8);
+    if (q.stages >= 2 && nv <= 512 * 4 * M) {
+        const size_t smem = (size_t)q.stages * set;
+        const auto th = [&](int v) { return (int)((nv + 32 * v - 1) / (32 * v) * 32); };
+        if (nv <= 256 * M) return launch_ring<T, GRID, M>(q, th(M), smem, s);
+        if (nv <= 512 * M) return launch_ring<T, GRID, 2 * M>(q, th(2 * M), smem, s);
+        return launch_ring<T, GRID, 4 * M>(q, th(4 * M), smem, s);
+    }
+    ce_rmsnorm_bwd_wide_kernel<T, VEC><<<bwd_grid(a.N, a.H), 512, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_bwd_t(const NormBwdArgs& a, int vb, cudaStream_t s) {
-    constexpr int ES = sizeof(T);
-    if (vb == 16) return launch_bwd_k<T, 16 / ES>(a, s);
-    if constexpr (ES == 2)
-        if (vb == 4) return launch_bwd_k<T, 2>(a, s);
-    return launch_bwd_k<T, 1>(a, s);
+cudaError_t launch_bwd_t(const NormBwdArgs& a, int vb, uint32_t* err, cudaStream_t s) {
+    return vb == 16 ? launch_bwd_g<T, true>(a, err, s) : launch_bwd_g<T, false>(a, err, s);
 }
 
 constexpr int64_t kMaxWidth = 1 << 20;
@@ -637,7 +783,7 @@ extern "C" ce_status ce_rmsnorm_fwd(const void* x, const void* residual, const v
 
 extern "C" size_t ce_rmsnorm_bwd_workspace_bytes(int64_t N, int64_t H) {
     if (N < 0 || N > 0x7fffffffLL || H < 1 || H > kMaxWidth) return 0;
-    return kWsHeaderBytes + (size_t)bwd_grid(N) * (size_t)H * sizeof(float);
+    return kWsHeaderBytes + (size_t)bwd_grid(N, H) * (size_t)H * sizeof(float);
 }
 
 extern "C" ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const void* weight, const void* grad_h,
@@ -692,13 +838,23 @@ extern "C" ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const v
                              (uint64_t)(N > 1 ? a.hs : 0), (uint64_t)(N > 1 && grad_h ? a.dhs : 0),
                              (uint64_t)(N > 1 ? a.dxs : 0), (uint64_t)H * es};
     const int vb = common_vector_bytes(vals, 9, es);
-    cudaError_t e = dtype == CE_F32    ? launch_bwd_t<float>(a, vb, s)
-                    : dtype == CE_BF16 ? launch_bwd_t<__nv_bfloat16>(a, vb, s)
-                                       : launch_bwd_t<__half>(a, vb, s);
+    uint32_t* err = grad_weight ? reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kWsErrOffset) : nullptr;
+    cudaError_t e = dtype == CE_F32    ? launch_bwd_t<float>(a, vb, err, s)
+                    : dtype == CE_BF16 ? launch_bwd_t<__nv_bfloat16>(a, vb, err, s)
+                                       : launch_bwd_t<__half>(a, vb, err, s);
     if (e != cudaSuccess) return CE_ERR_LAUNCH;
     if (grad_weight) {
-        ce_rmsnorm_dw_kernel<<<(unsigned)((H + 31) / 32), 256, 0, s>>>(a.part, bwd_grid(N), H, grad_weight);
-        if (cudaGetLastError() != cudaSuccess) return CE_ERR_LAUNCH;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((H + 31) / 32));
+        cfg.blockDim = dim3(1024);
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
+        set_pdl_attr(at);
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, ce_rmsnorm_dw_kernel, (const float*)a.part, bwd_grid(N, H), H, grad_weight) !=
+            cudaSuccess)
+            return CE_ERR_LAUNCH;
     }
     return CE_OK;
 }
