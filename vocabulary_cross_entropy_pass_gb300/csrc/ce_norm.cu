@@ -95,33 +95,58 @@ __device__ __forceinline__ void load_w(const NormFwdArgs& p, int64_t col, float*
 }
 
 // One CTA per row, VPT vectors of VEC elements per thread in registers.
-template <typename T, int VEC, int VPT, bool Q8>
+// PHASED: the rows of x, r, y and h lie off the 16-byte grid, all at the same
+// offset: a thread's vectors are those of the grid, the row's first and last only
+// in part (element i of vector v is column v * VEC + i - sh).
+template <typename T, int VEC, int VPT, bool Q8, bool PHASED>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(const __grid_constant__ NormFwdArgs p) {
     constexpr int ES = sizeof(T);
     __shared__ float red[64];
     extern __shared__ uint32_t gmax[];  // Q8 with groups wider than a warp's vectors
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, TH = blockDim.x;
-    const int nv = (int)(p.H / VEC);
     const char* x = p.x + row * p.xs;
     const char* r = p.r ? p.r + row * p.rs : nullptr;
+    const int sh = PHASED ? (int)(reinterpret_cast<uintptr_t>(x) & 15u) / ES : 0;
+    const int nv = PHASED ? (int)((p.H + sh + VEC - 1) / VEC) : (int)(p.H / VEC);
+    auto edge = [&](int v) { return PHASED && (v == 0 || v == nv - 1); };
+    auto inside = [&](int v, int i) {
+        const int64_t c = (int64_t)v * VEC + i - sh;
+        return c >= 0 && c < p.H;
+    };
+    auto take = [&](const char* row_at, int v) {
+        Pack<T, VEC> a;
+        a.zero();
+        if (edge(v)) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (inside(v, i)) a.v[i] = reinterpret_cast<const T*>(row_at)[(int64_t)v * VEC + i - sh];
+        } else if (v < nv) {
+            a.load_cs(row_at + ((int64_t)v * VEC - sh) * ES);
+        }
+        return a;
+    };
+    auto give = [&](char* row_at, int v, const float* f) {
+        Pack<T, VEC> o;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o.set(i, f[i]);
+        if (edge(v)) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (inside(v, i)) reinterpret_cast<T*>(row_at)[(int64_t)v * VEC + i - sh] = o.v[i];
+        } else if (v < nv) {
+            o.store(row_at + ((int64_t)v * VEC - sh) * ES);
+        }
+    };
 
     float h[VPT][VEC];
     {
         Pack<T, VEC> a[VPT], b[VPT];
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = tid + k * TH;
-            a[k].zero();
-            if (v < nv) a[k].load_cs(x + (int64_t)v * VEC * ES);
-        }
+        for (int k = 0; k < VPT; ++k) a[k] = take(x, tid + k * TH);
         if (r) {
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int v = tid + k * TH;
-                b[k].zero();
-                if (v < nv) b[k].load_cs(r + (int64_t)v * VEC * ES);
-            }
+            for (int k = 0; k < VPT; ++k) b[k] = take(r, tid + k * TH);
 #pragma unroll
             for (int k = 0; k < VPT; ++k)
 #pragma unroll
@@ -139,15 +164,8 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
 #pragma unroll
         for (int i = 0; i < VEC; ++i) ss = fmaf(h[k][i], h[k][i], ss);
     if (p.h) {
-        char* ho = p.h + row * p.hs;
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = tid + k * TH;
-            Pack<T, VEC> o;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) o.set(i, h[k][i]);
-            if (v < nv) o.store(ho + (int64_t)v * VEC * ES);
-        }
+        for (int k = 0; k < VPT; ++k) give(p.h + row * p.hs, tid + k * TH, h[k]);
     }
     ss = cta_sum(ss, red);
     const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
@@ -156,7 +174,16 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
         const int v = tid + k * TH;
         float w[VEC];
         if (v < nv) {
-            load_w<T, VEC>(p, (int64_t)v * VEC, w);
+            if constexpr (PHASED) {
+                // the weight starts where it starts: element by element
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    w[i] = 0.f;
+                    if (!edge(v) || inside(v, i)) load_w<T, 1>(p, (int64_t)v * VEC + i - sh, w + i);
+                }
+            } else {
+                load_w<T, VEC>(p, (int64_t)v * VEC, w);
+            }
 #pragma unroll
             for (int i = 0; i < VEC; ++i) h[k][i] *= rstd * w[i];
         }
@@ -164,13 +191,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
     char* y = p.y + row * p.ys;
     if constexpr (!Q8) {
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = tid + k * TH;
-            Pack<T, VEC> o;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) o.set(i, h[k][i]);
-            if (v < nv) o.store(y + (int64_t)v * VEC * ES);
-        }
+        for (int k = 0; k < VPT; ++k) give(y, tid + k * TH, h[k]);
     } else {
         float am[VPT];
 #pragma unroll
@@ -303,13 +324,13 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_fwd_wide_kernel(const __grid_c
     }
 }
 
-template <typename T, int VEC, bool Q8>
+template <typename T, int VEC, bool Q8, bool PHASED = false>
 cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
-    const int64_t nv = a.H / VEC;
+    const int64_t nv = PHASED ? (a.H + VEC - 1 + VEC - 1) / VEC : a.H / VEC;
     const size_t smem = Q8 ? (size_t)a.groups * 4 : 0;
     constexpr int MAXV = VEC >= 8 ? 4 : (VEC == 4 ? 8 : 16);  // 512 threads hold 512 * MAXV vectors
     if (nv > 512 * MAXV) {
-        auto* k = ce_rmsnorm_fwd_wide_kernel<T, VEC, Q8>;
+        auto* k = ce_rmsnorm_fwd_wide_kernel<T, PHASED ? 1 : VEC, Q8>;
         if (smem > 40 * 1024) {
             cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess) return e;
@@ -319,13 +340,13 @@ cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
     }
     if (nv <= 256 || (a.N <= 304 && nv <= 1024)) {
         const int th = (int)((nv + 31) / 32 * 32);
-        ce_rmsnorm_fwd_kernel<T, VEC, 1, Q8><<<(unsigned)a.N, th, smem, s>>>(a);
+        ce_rmsnorm_fwd_kernel<T, VEC, 1, Q8, PHASED><<<(unsigned)a.N, th, smem, s>>>(a);
     } else if (nv <= 2048) {
         const int th = (int)((nv + 127) / 128 * 32);
-        ce_rmsnorm_fwd_kernel<T, VEC, 4, Q8><<<(unsigned)a.N, th, smem, s>>>(a);
+        ce_rmsnorm_fwd_kernel<T, VEC, 4, Q8, PHASED><<<(unsigned)a.N, th, smem, s>>>(a);
     } else {
         const int th = (int)((nv + 32 * MAXV - 1) / (32 * MAXV) * 32);
-        ce_rmsnorm_fwd_kernel<T, VEC, MAXV, Q8><<<(unsigned)a.N, th, smem, s>>>(a);
+        ce_rmsnorm_fwd_kernel<T, VEC, MAXV, Q8, PHASED><<<(unsigned)a.N, th, smem, s>>>(a);
     }
     return cudaGetLastError();
 }
@@ -335,6 +356,14 @@ cudaError_t launch_fwd_t(const NormFwdArgs& a, int vb, cudaStream_t s) {
     constexpr int ES = sizeof(T);
     const bool q = a.kind != 0;
     if (vb == 16) return q ? launch_fwd<T, 16 / ES, true>(a, s) : launch_fwd<T, 16 / ES, false>(a, s);
+    if (!q) {
+        auto at = [](const void* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u); };
+        bool phased = at(a.y) == at(a.x) && (!a.r || at(a.r) == at(a.x)) && (!a.h || at(a.h) == at(a.x));
+        if (a.N > 1)
+            phased = phased && (a.ys - a.xs) % 16 == 0 && (!a.r || (a.rs - a.xs) % 16 == 0) &&
+                     (!a.h || (a.hs - a.xs) % 16 == 0);
+        if (phased) return launch_fwd<T, 16 / ES, false, true>(a, s);
+    }
     if constexpr (ES == 2)
         if (vb == 4) return q ? launch_fwd<T, 2, true>(a, s) : launch_fwd<T, 2, false>(a, s);
     return q ? launch_fwd<T, 1, true>(a, s) : launch_fwd<T, 1, false>(a, s);
@@ -347,12 +376,15 @@ struct NormBwdArgs {
     const char* w;
     const char* dh;        // or NULL
     char* dx;
-    float* part;           // [gridDim.x][H] partial sums of dw, or NULL
+    float* part;           // [gridDim.x][part_pitch] partial sums of dw, or NULL
     int64_t N, H;
     int64_t gs, hs, dhs, dxs;  // row strides in bytes
     float eps, inv_h;
     int w32;
 };
+
+// Floats between the partial rows of dw.
+__host__ __device__ __forceinline__ int64_t part_pitch(int64_t H) { return (H + 15) / 4 * 4 + 4; }
 
 // A persistent grid over the rows; a thread keeps its columns' dw sums in
 // registers over all rows of its CTA and writes them once.  The rows come in by
@@ -361,11 +393,17 @@ struct NormBwdArgs {
 // shared memory.  A row off the 16-byte grid is copied from the boundary before
 // it to the boundary after it, as far as that stays between the tensor's first
 // and last element, the rest element by element.
-//   GRID: rows on the grid, VPT vectors of 16 bytes per thread; else VPT
-//   single elements per thread, TH apart.
+// MODE, by how the rows of g, h, dh and dx lie:
+//   kOnGrid  all on the 16-byte grid, a whole number of vectors each;
+//   kPhased  off it, but all at the same offset, row for row: a thread's
+//            vectors are those of the 16-byte grid, the row's first and last only
+//            in part.  Every row of a CTA has the same offset (the grid is a
+//            multiple of 8 CTAs), so a thread's columns stay its own;
+//   kLoose   anything else: single elements, TH apart.
 // One barrier per row: it hands the sums over, and past it the row before
 // has been read by all, so its place is filled again.  A copy that does not
 // arrive sets the workspace's error word, and every thread leaves at the row's barrier.
+constexpr int kOnGrid = 0, kPhased = 1, kLoose = 2;
 struct RingArgs {
     NormBwdArgs n;
     uint32_t* err;         // the workspace's error word, or NULL
@@ -397,10 +435,11 @@ __device__ __forceinline__ RowSpan<ES> row_span(const char* base, int64_t stride
     return s;
 }
 
-template <typename T, int VPT, bool GRID, bool RES>
+template <typename T, int VPT, int MODE, bool RES>
 __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_constant__ RingArgs q) {
     constexpr int ES = sizeof(T);
-    constexpr int VEC = GRID ? 16 / ES : 1;
+    constexpr bool GRID = MODE == kOnGrid;
+    constexpr int VEC = MODE == kLoose ? 1 : 16 / ES;
     constexpr int NT = RES ? 3 : 2;            // tensors per row set
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ uint64_t full[16];
@@ -408,8 +447,16 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_consta
     __shared__ int gave_up;
     const NormBwdArgs& p = q.n;
     const int tid = threadIdx.x, TH = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = TH >> 5;
-    const int nv = (int)(p.H / VEC);
     const int64_t len = p.H * ES;
+    // kPhased: the elements by which the CTA's rows lie past the grid; element i of
+    // vector v is column v * VEC + i - sh
+    const int sh = MODE == kPhased ? (int)((reinterpret_cast<uintptr_t>(p.h) + blockIdx.x * (uint64_t)p.hs) & 15u) / ES : 0;
+    const int nv = MODE == kPhased ? (int)((p.H + sh + VEC - 1) / VEC) : (int)(p.H / VEC);
+    auto edge = [&](int v) { return MODE == kPhased && (v == 0 || v == nv - 1); };
+    auto inside = [&](int v, int i) {
+        const int64_t c = (int64_t)v * VEC + i - sh;
+        return c >= 0 && c < p.H;
+    };
     const uint64_t policy = l2_evict_first_policy();
     if (tid == 0) {
         for (int k = 0; k < q.stages; ++k) mbar_init(&full[k], 1);
@@ -455,9 +502,9 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_consta
         for (int i = 0; i < VEC; ++i) {
             dw[k][i] = 0.f;
             w32[k][i] = 0.f;
-            if (v < nv)
-                w32[k][i] = p.w32 ? __ldg(reinterpret_cast<const float*>(p.w) + (int64_t)v * VEC + i)
-                                   : to_f32(reinterpret_cast<const T*>(p.w)[(int64_t)v * VEC + i]);
+            if (v < nv && (!edge(v) || inside(v, i)))
+                w32[k][i] = p.w32 ? __ldg(reinterpret_cast<const float*>(p.w) + (int64_t)v * VEC + i - sh)
+                                  : to_f32(reinterpret_cast<const T*>(p.w)[(int64_t)v * VEC + i - sh]);
         }
     }
 
@@ -497,7 +544,12 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_consta
         }
         auto get = [&](int t, int v) {
             Pack<T, VEC> x;
-            x.load(at + t * q.slot + ph[t] + (size_t)v * VEC * ES);
+            x.load(at + t * q.slot + (MODE == kLoose ? ph[t] : 0) + (size_t)v * VEC * ES);
+            if (edge(v)) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (!inside(v, i)) x.set(i, 0.f);
+            }
             return x;
         };
         float ss = 0.f, c = 0.f;
@@ -547,7 +599,13 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_consta
                     if (RES) t += d.f(i);
                     o.set(i, t);
                 }
-                o.store_cs(xp + (int64_t)v * VEC * ES);
+                if (edge(v)) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        if (inside(v, i)) reinterpret_cast<T*>(xp)[(int64_t)v * VEC + i - sh] = o.v[i];
+                } else {
+                    o.store_cs(xp + ((int64_t)v * VEC - sh) * ES);
+                }
             }
         }
         done = stage;
@@ -564,7 +622,8 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_consta
         return;
     }
     if (p.part) {
-        float* out = p.part + (int64_t)blockIdx.x * p.H;
+        // kPhased: shifted like the rows
+        float* out = p.part + (int64_t)blockIdx.x * part_pitch(p.H);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int v = tid + k * TH;
@@ -581,7 +640,7 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_wide_kernel(const __grid_c
     __shared__ float2 red[2][32];
     const int tid = threadIdx.x, TH = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = TH >> 5;
     const int64_t nv = p.H / VEC;
-    float* out = p.part ? p.part + (int64_t)blockIdx.x * p.H : nullptr;
+    float* out = p.part ? p.part + (int64_t)blockIdx.x * part_pitch(p.H) : nullptr;
     auto wat = [&](int64_t c) {
         return p.w32 ? __ldg(reinterpret_cast<const float*>(p.w) + c) : to_f32(reinterpret_cast<const T*>(p.w)[c]);
     };
@@ -636,7 +695,9 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_wide_kernel(const __grid_c
 
 // dw_j = the partial rows' column sums, in a fixed order: 32 columns per CTA, a
 // warp to every 32nd partial row, then the warps' sums in order.
-__global__ void __launch_bounds__(1024) ce_rmsnorm_dw_kernel(const float* part, int rows, int64_t H, float* dw) {
+// Partial row r lies (low + r * step) mod 16 bytes / es past its start.
+__global__ void __launch_bounds__(1024) ce_rmsnorm_dw_kernel(const float* part, int rows, int64_t H, float* dw,
+                                                             uint32_t low, uint32_t step, int es) {
     __shared__ float sh[32][33];
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -644,7 +705,7 @@ __global__ void __launch_bounds__(1024) ce_rmsnorm_dw_kernel(const float* part, 
     float acc = 0.f;
     if (c < H) {
 #pragma unroll 8
-        for (int r = warp; r < rows; r += 32) acc += __ldcg(part + r * H + c);
+        for (int r = warp; r < rows; r += 32) acc += __ldcg(part + r * part_pitch(H) + c + ((low + r * step) & 15u) / es);
     }
     sh[warp][lane] = acc;
     __syncthreads();
@@ -662,9 +723,9 @@ int bwd_grid(int64_t N, int64_t H) {
     return (int)(N < most ? N : most);
 }
 
-template <typename T, bool GRID, int VPT>
+template <typename T, int MODE, int VPT>
 cudaError_t launch_ring(RingArgs& q, int threads, size_t smem, cudaStream_t s) {
-    auto* k = q.n.dh ? ce_rmsnorm_bwd_kernel<T, VPT, GRID, true> : ce_rmsnorm_bwd_kernel<T, VPT, GRID, false>;
+    auto* k = q.n.dh ? ce_rmsnorm_bwd_kernel<T, VPT, MODE, true> : ce_rmsnorm_bwd_kernel<T, VPT, MODE, false>;
     if (smem > 40 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -675,34 +736,43 @@ cudaError_t launch_ring(RingArgs& q, int threads, size_t smem, cudaStream_t s) {
 
 // The widest row that the ring kernel takes: 512 threads' registers, and two row
 // sets in shared memory.
-template <typename T, bool GRID>
-cudaError_t launch_bwd_g(const NormBwdArgs& a, uint32_t* err, cudaStream_t s) {
+template <typename T, int MODE>
+cudaError_t launch_bwd_m(const NormBwdArgs& a, uint32_t* err, bool* shifted, cudaStream_t s) {
     constexpr int ES = sizeof(T);
-    constexpr int VEC = GRID ? 16 / ES : 1;
-    constexpr int M = GRID ? (VEC == 8 ? 1 : 2) : 4;  // a step of vectors per thread: 8 elements, 4 off the grid
-    const int64_t nv = a.H / VEC;
+    constexpr int VEC = MODE == kLoose ? 1 : 16 / ES;
+    constexpr int M = MODE == kLoose ? 4 : (VEC == 8 ? 1 : 2);  // a step of vectors per thread: 8 elements, 4 if loose
+    const int64_t nv = MODE == kPhased ? (a.H + VEC - 1 + VEC - 1) / VEC : a.H / VEC;
     RingArgs q;
     q.n = a;
     q.err = err;
-    q.slot = (int)((a.H * ES + 15) / 16 * 16 + (GRID ? 0 : 16));
+    q.slot = (int)((a.H * ES + 15) / 16 * 16 + (MODE == kOnGrid ? 0 : 16));
     const int64_t set = (int64_t)q.slot * (a.dh ? 3 : 2);
     int64_t room = 216 * 1024 / bwd_per_sm(a.H);
     if (room < 3 * set) room = 216 * 1024;
     q.stages = (int)(room / set < 8 ? room / set : 8);
     if (q.stages >= 2 && nv <= 512 * 4 * M) {
+        *shifted = MODE == kPhased;
         const size_t smem = (size_t)q.stages * set;
         const auto th = [&](int v) { return (int)((nv + 32 * v - 1) / (32 * v) * 32); };
-        if (nv <= 256 * M) return launch_ring<T, GRID, M>(q, th(M), smem, s);
-        if (nv <= 512 * M) return launch_ring<T, GRID, 2 * M>(q, th(2 * M), smem, s);
-        return launch_ring<T, GRID, 4 * M>(q, th(4 * M), smem, s);
+        if (nv <= 256 * M) return launch_ring<T, MODE, M>(q, th(M), smem, s);
+        if (nv <= 512 * M) return launch_ring<T, MODE, 2 * M>(q, th(2 * M), smem, s);
+        return launch_ring<T, MODE, 4 * M>(q, th(4 * M), smem, s);
     }
-    ce_rmsnorm_bwd_wide_kernel<T, VEC><<<bwd_grid(a.N, a.H), 512, 0, s>>>(a);
+    constexpr int WV = MODE == kOnGrid ? VEC : 1;
+    ce_rmsnorm_bwd_wide_kernel<T, WV><<<bwd_grid(a.N, a.H), 512, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_bwd_t(const NormBwdArgs& a, int vb, uint32_t* err, cudaStream_t s) {
-    return vb == 16 ? launch_bwd_g<T, true>(a, err, s) : launch_bwd_g<T, false>(a, err, s);
+cudaError_t launch_bwd_t(const NormBwdArgs& a, int vb, uint32_t* err, bool* shifted, cudaStream_t s) {
+    if (vb == 16) return launch_bwd_m<T, kOnGrid>(a, err, shifted, s);
+    auto at = [](const void* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u); };
+    const bool many = a.N > 1;
+    bool phased = at(a.g) == at(a.h) && at(a.dx) == at(a.h) && (!a.dh || at(a.dh) == at(a.h));
+    if (many)
+        phased = phased && (a.gs - a.hs) % 16 == 0 && (a.dxs - a.hs) % 16 == 0 && (!a.dh || (a.dhs - a.hs) % 16 == 0);
+    if (phased) return launch_bwd_m<T, kPhased>(a, err, shifted, s);
+    return launch_bwd_m<T, kLoose>(a, err, shifted, s);
 }
 
 constexpr int64_t kMaxWidth = 1 << 20;
@@ -783,7 +853,7 @@ extern "C" ce_status ce_rmsnorm_fwd(const void* x, const void* residual, const v
 
 extern "C" size_t ce_rmsnorm_bwd_workspace_bytes(int64_t N, int64_t H) {
     if (N < 0 || N > 0x7fffffffLL || H < 1 || H > kMaxWidth) return 0;
-    return kWsHeaderBytes + (size_t)bwd_grid(N, H) * (size_t)H * sizeof(float);
+    return kWsHeaderBytes + (size_t)bwd_grid(N, H) * (size_t)part_pitch(H) * sizeof(float);
 }
 
 extern "C" ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const void* weight, const void* grad_h,
@@ -839,9 +909,10 @@ extern "C" ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const v
                              (uint64_t)(N > 1 ? a.dxs : 0), (uint64_t)H * es};
     const int vb = common_vector_bytes(vals, 9, es);
     uint32_t* err = grad_weight ? reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kWsErrOffset) : nullptr;
-    cudaError_t e = dtype == CE_F32    ? launch_bwd_t<float>(a, vb, err, s)
-                    : dtype == CE_BF16 ? launch_bwd_t<__nv_bfloat16>(a, vb, err, s)
-                                       : launch_bwd_t<__half>(a, vb, err, s);
+    bool shifted = false;
+    cudaError_t e = dtype == CE_F32    ? launch_bwd_t<float>(a, vb, err, &shifted, s)
+                    : dtype == CE_BF16 ? launch_bwd_t<__nv_bfloat16>(a, vb, err, &shifted, s)
+                                       : launch_bwd_t<__half>(a, vb, err, &shifted, s);
     if (e != cudaSuccess) return CE_ERR_LAUNCH;
     if (grad_weight) {
         cudaLaunchConfig_t cfg = {};
@@ -852,8 +923,10 @@ extern "C" ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const v
         set_pdl_attr(at);
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, ce_rmsnorm_dw_kernel, (const float*)a.part, bwd_grid(N, H), H, grad_weight) !=
-            cudaSuccess)
+        const uint32_t low = shifted ? (uint32_t)(reinterpret_cast<uintptr_t>(h) & 15u) : 0u;
+        const uint32_t step = shifted && N > 1 ? (uint32_t)(a.hs & 15) : 0u;
+        if (cudaLaunchKernelEx(&cfg, ce_rmsnorm_dw_kernel, (const float*)a.part, bwd_grid(N, H), H, grad_weight, low,
+                               step, es) != cudaSuccess)
             return CE_ERR_LAUNCH;
     }
     return CE_OK;
