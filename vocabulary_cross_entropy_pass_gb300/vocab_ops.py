@@ -31,20 +31,37 @@ def _raise(st: int, what: str):
         raise _lib.CEError(st, what)
 
 
+# A call of a small decoding step takes longer on the host than on the GPU, so the
+# paths below ask torch for as little as they can: the current stream's handle
+# without a Stream object, one is_contiguous() before any stride.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(device, stream):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return stream.cuda_stream
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev} (there is no CPU path)")
+def _on(dev, t, name):
+    if t is not None and t.device != dev:
+        raise ValueError(f"{name} must be on {dev} (there is no CPU path)")
+
+
+def _cuda(t, name):
+    """(device, dtype code) of the tensor an operator goes by."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    dt = _DTYPE.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported {name} dtype {t.dtype}")
+    return t.device, dt
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _rows(t: torch.Tensor, H: int, name: str):
@@ -73,15 +90,25 @@ def _rows(t: torch.Tensor, H: int, name: str):
     return N, H if step is None else step
 
 
+def _stride(t: torch.Tensor, H: int, name: str) -> int:
+    """Stride between the rows of a (..., H) tensor."""
+    return H if t.is_contiguous() and t.shape[-1] == H else _rows(t, H, name)[1]
+
+
+_UNIT = _lib.i64_array((0, 1))  # strides of a contiguous run taken as one row
+
+
 def _tokens(tokens: torch.Tensor):
-    """(dim0, dim1, strides) of an int64 tensor of any shape."""
+    """(tokens, dim0, dim1, strides) of an int64 tensor of any shape."""
     if tokens.dtype != torch.int64:
         raise TypeError("tokens must be int64")
+    if tokens.is_contiguous():
+        return tokens, 1, tokens.numel(), _UNIT
     if tokens.dim() == 2:
-        return tokens, tokens.shape[0], tokens.shape[1], tokens.stride()
+        return tokens, tokens.shape[0], tokens.shape[1], _lib.i64_array(tokens.stride())
     if tokens.dim() != 1:
         tokens = tokens.reshape(-1)
-    return tokens, 1, tokens.shape[0], (tokens.shape[0] * tokens.stride(0), tokens.stride(0))
+    return tokens, 1, tokens.shape[0], _lib.i64_array((0, tokens.stride(0)))
 
 
 # ---------------------------------------------------------------- embedding
@@ -92,27 +119,24 @@ def ce_embed_fwd(tokens: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
     H)``, computed in float32 and rounded once.  ``ignore_idx`` gives a row of
     zeros, any other token outside [0, V) a row of NaN (and, with a
     ``workspace`` of 256 bytes, the error word that ce_get_error reads)."""
-    if not weight.is_cuda:
-        raise ValueError("weight must be a CUDA tensor (there is no CPU path)")
-    dt = _DTYPE.get(weight.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported weight dtype {weight.dtype}")
+    dev, dt = _cuda(weight, "weight")
     if weight.dim() != 2:
         raise ValueError("weight must be (V, H)")
-    dev = weight.device
-    _on(dev, tokens=tokens, out=out, workspace=workspace)
     V, H = weight.shape
-    _, ws = _rows(weight, H, "weight")
+    _on(dev, tokens, "tokens")
     flat, d0, d1, ts = _tokens(tokens)
     if out is None:
-        out = torch.empty(*tokens.shape, H, dtype=weight.dtype, device=dev)
-    elif out.dtype != weight.dtype or tuple(out.shape) != (*tokens.shape, H):
-        raise ValueError("out must be (*tokens.shape, H) in the weight's dtype")
-    _, os = _rows(out, H, "out")
-    rc = _lib.load().ce_embed_fwd(flat.data_ptr(), d0, d1, _lib.i64_array(ts), weight.data_ptr(), dt, V, H, ws,
-                                  scale, ignore_idx, out.data_ptr(), os, _ptr(workspace),
-                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                  _stream(dev, stream))
+        out = torch.empty((*tokens.shape, H), dtype=weight.dtype, device=dev)
+        os = H
+    else:
+        _on(dev, out, "out")
+        if out.dtype != weight.dtype or tuple(out.shape) != (*tokens.shape, H):
+            raise ValueError("out must be (*tokens.shape, H) in the weight's dtype")
+        os = _stride(out, H, "out")
+    _on(dev, workspace, "workspace")
+    rc = _lib.load().ce_embed_fwd(flat.data_ptr(), d0, d1, ts, weight.data_ptr(), dt, V, H,
+                                  _stride(weight, H, "weight"), scale, ignore_idx, out.data_ptr(), os,
+                                  _ptr(workspace), _bytes(workspace), _stream(dev, stream))
     if rc:
         _raise(rc, "ce_embed_fwd")
     return out
@@ -132,38 +156,37 @@ def ce_embed_bwd(grad_out: torch.Tensor, tokens: torch.Tensor, num_embeddings: i
     ``grad_out``'s dtype and written whole; with ``accumulate`` (float32 only)
     it is added to, as ce_linear_fwd_bwd adds to the gradient of the same,
     tied matrix.  ``workspace``: ce_embed_bwd_workspace_bytes bytes."""
-    if not grad_out.is_cuda:
-        raise ValueError("grad_out must be a CUDA tensor (there is no CPU path)")
-    dt = _DTYPE.get(grad_out.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported grad_out dtype {grad_out.dtype}")
-    dev = grad_out.device
-    _on(dev, tokens=tokens, grad_weight=grad_weight, workspace=workspace)
-    if tuple(grad_out.shape[:-1]) != tuple(tokens.shape):
+    dev, dt = _cuda(grad_out, "grad_out")
+    _on(dev, tokens, "tokens")
+    if grad_out.shape[:-1] != tokens.shape:
         raise ValueError(f"grad_out {tuple(grad_out.shape)} does not match tokens {tuple(tokens.shape)}")
     H = grad_out.shape[-1]
     flat, d0, d1, ts = _tokens(tokens)
-    _, gs = _rows(grad_out, H, "grad_out")
     if grad_weight is None:
         if accumulate:
             raise ValueError("accumulate needs the grad_weight to add to")
-        grad_weight = torch.empty(num_embeddings, H, dtype=grad_dtype, device=dev)
-    elif tuple(grad_weight.shape) != (num_embeddings, H):
-        raise ValueError("grad_weight must be (num_embeddings, H)")
+        grad_weight = torch.empty((num_embeddings, H), dtype=grad_dtype, device=dev)
+        wst = H
+    else:
+        _on(dev, grad_weight, "grad_weight")
+        if tuple(grad_weight.shape) != (num_embeddings, H):
+            raise ValueError("grad_weight must be (num_embeddings, H)")
+        wst = _stride(grad_weight, H, "grad_weight")
     wdt = _DTYPE.get(grad_weight.dtype)
     if wdt is None or (wdt != _lib.CE_F32 and wdt != dt):
         raise TypeError("grad_weight must be float32 or of grad_out's dtype")
     if accumulate and wdt != _lib.CE_F32:
         raise TypeError("grad_weight accumulates in float32")
-    _, wst = _rows(grad_weight, H, "grad_weight")
     lib = _lib.load()
     if workspace is None:
-        workspace = torch.empty(lib.ce_embed_bwd_workspace_bytes(d0 * d1, H, num_embeddings), dtype=torch.uint8,
-                                device=dev)
-    rc = lib.ce_embed_bwd(grad_out.data_ptr(), dt, gs, flat.data_ptr(), d0, d1, _lib.i64_array(ts),
+        need = lib.ce_embed_bwd_workspace_bytes(d0 * d1, H, num_embeddings)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _on(dev, workspace, "workspace")
+        need = _bytes(workspace)
+    rc = lib.ce_embed_bwd(grad_out.data_ptr(), dt, _stride(grad_out, H, "grad_out"), flat.data_ptr(), d0, d1, ts,
                           num_embeddings, H, scale, ignore_idx, grad_weight.data_ptr(), wdt, wst,
-                          int(accumulate), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                          _stream(dev, stream))
+                          1 if accumulate else 0, workspace.data_ptr(), need, _stream(dev, stream))
     if rc:
         _raise(rc, "ce_embed_bwd")
     return grad_weight
@@ -214,52 +237,59 @@ def ce_rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor
     group_size))`` with ``y = q * scale`` and group_size 32, 64, 128 or 0 (the
     row).  ``weight``: H elements of x's dtype or float32.  ``residual_out`` may
     be x or residual, ``out`` (without quant) too."""
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor (there is no CPU path)")
-    dt = _DTYPE.get(x.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {x.dtype}")
-    dev = x.device
-    if x.dim() == 0:
+    dev, dt = _cuda(x, "x")
+    shape, dtype = x.shape, x.dtype
+    if not shape:
         raise ValueError("x must be (..., H)")
-    H = x.shape[-1]
-    _on(dev, weight=weight, residual=residual, out=out, residual_out=residual_out, scales_out=scales_out)
-    if weight.dtype != x.dtype and weight.dtype != torch.float32:
+    H = shape[-1]
+    N = x.numel() // H if H else 0
+    _on(dev, weight, "weight")
+    wdt = _DTYPE.get(weight.dtype)
+    if wdt != dt and wdt != _lib.CE_F32:
         raise TypeError("weight must be of x's dtype or float32")
-    if tuple(weight.shape) != (H,) or not weight.is_contiguous():
+    if weight.shape != (H,) or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous vector of H elements")
-    if quant not in _QUANT:
-        raise TypeError(f"quant must be torch.float8_e4m3fn, torch.float8_e5m2 or None, not {quant}")
-    N, xs = _rows(x, H, "x")
     rs = hs = 0
     if residual is not None:
-        if residual.shape != x.shape or residual.dtype != x.dtype:
+        _on(dev, residual, "residual")
+        if residual.shape != shape or residual.dtype != dtype:
             raise ValueError("residual must match x in shape and dtype")
-        _, rs = _rows(residual, H, "residual")
+        rs = _stride(residual, H, "residual")
         if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            residual_out = torch.empty(shape, dtype=dtype, device=dev)
     if residual_out is not None:
-        if residual_out.shape != x.shape or residual_out.dtype != x.dtype:
+        _on(dev, residual_out, "residual_out")
+        if residual_out.shape != shape or residual_out.dtype != dtype:
             raise ValueError("residual_out must match x in shape and dtype")
-        _, hs = _rows(residual_out, H, "residual_out")
-    if out is None:
-        out = torch.empty(x.shape, dtype=quant or x.dtype, device=dev)
-    elif out.shape != x.shape or out.dtype != (quant or x.dtype):
-        raise ValueError("out must match x in shape, in x's dtype or quant's")
-    _, os = _rows(out, H, "out")
-    if quant is not None:
+        hs = _stride(residual_out, H, "residual_out")
+    if quant is None:
+        code = 0
+        if group_size or scales_out is not None:
+            raise ValueError("group_size and scales_out go with quant")
+    else:
+        code = _QUANT.get(quant)
+        if code is None:
+            raise TypeError(f"quant must be torch.float8_e4m3fn, torch.float8_e5m2 or None, not {quant}")
         if group_size not in (0, 32, 64, 128):
             raise ValueError("group_size must be 0, 32, 64 or 128")
         G = 1 if group_size == 0 else -(-H // group_size)
         if scales_out is None:
-            scales_out = torch.empty(N, G, dtype=torch.float32, device=dev)
+            scales_out = torch.empty((N, G), dtype=torch.float32, device=dev)
         elif scales_out.dtype != torch.float32 or scales_out.numel() != N * G or not scales_out.is_contiguous():
             raise ValueError("scales_out must be contiguous float32 (rows, groups)")
-    elif group_size or scales_out is not None:
-        raise ValueError("group_size and scales_out go with quant")
-    rc = _lib.load().ce_rmsnorm_fwd(x.data_ptr(), _ptr(residual), weight.data_ptr(), dt, _DTYPE[weight.dtype], N, H,
-                                    xs, rs, eps, out.data_ptr(), os, _QUANT[quant], group_size, _ptr(scales_out),
-                                    _ptr(residual_out), hs, _stream(dev, stream))
+        _on(dev, scales_out, "scales_out")
+        dtype = quant
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+        os = H
+    else:
+        _on(dev, out, "out")
+        if out.shape != shape or out.dtype != dtype:
+            raise ValueError("out must match x in shape, in x's dtype or quant's")
+        os = _stride(out, H, "out")
+    rc = _lib.load().ce_rmsnorm_fwd(x.data_ptr(), _ptr(residual), weight.data_ptr(), dt, wdt, N, H,
+                                    _stride(x, H, "x"), rs, eps, out.data_ptr(), os, code, group_size,
+                                    _ptr(scales_out), _ptr(residual_out), hs, _stream(dev, stream))
     if rc:
         _raise(rc, "ce_rmsnorm_fwd")
     return out, x if residual_out is None else residual_out, scales_out
@@ -277,43 +307,45 @@ def ce_rmsnorm_bwd(grad_out: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
     what reaches h from the residual stream.  Returns ``(grad_x,
     grad_weight)``: grad_x (x's and the residual's alike) in h's dtype, may be
     given as grad_out, h or grad_h; grad_weight float32, None to skip it."""
-    if not h.is_cuda:
-        raise ValueError("h must be a CUDA tensor (there is no CPU path)")
-    dt = _DTYPE.get(h.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported dtype {h.dtype}")
-    if h.dim() == 0:
+    dev, dt = _cuda(h, "h")
+    shape, dtype = h.shape, h.dtype
+    if not shape:
         raise ValueError("h must be (..., H)")
-    dev, H = h.device, h.shape[-1]
-    gw = grad_weight if isinstance(grad_weight, torch.Tensor) else None
-    _on(dev, grad_out=grad_out, weight=weight, grad_h=grad_h, grad_x=grad_x, grad_weight=gw, workspace=workspace)
-    if weight.dtype != h.dtype and weight.dtype != torch.float32:
+    H = shape[-1]
+    N = h.numel() // H if H else 0
+    _on(dev, weight, "weight")
+    wdt = _DTYPE.get(weight.dtype)
+    if wdt != dt and wdt != _lib.CE_F32:
         raise TypeError("weight must be of h's dtype or float32")
-    if tuple(weight.shape) != (H,) or not weight.is_contiguous():
+    if weight.shape != (H,) or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous vector of H elements")
-    N, hs = _rows(h, H, "h")
     if grad_x is None:
-        grad_x = torch.empty(h.shape, dtype=h.dtype, device=dev)
+        grad_x = torch.empty(shape, dtype=dtype, device=dev)
     dhs = 0
     for t, name in ((grad_out, "grad_out"), (grad_h, "grad_h"), (grad_x, "grad_x")):
-        if t is not None and (t.shape != h.shape or t.dtype != h.dtype):
-            raise ValueError(f"{name} must match h in shape and dtype")
-    _, gs = _rows(grad_out, H, "grad_out")
-    _, xs = _rows(grad_x, H, "grad_x")
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.device != dev):
+            raise ValueError(f"{name} must match h in shape, dtype and device")
     if grad_h is not None:
-        _, dhs = _rows(grad_h, H, "grad_h")
+        dhs = _stride(grad_h, H, "grad_h")
     lib = _lib.load()
+    gw, need = None, 0
     if grad_weight is True:
         gw = torch.empty(H, dtype=torch.float32, device=dev)
-    if gw is not None:
-        if gw.dtype != torch.float32 or tuple(gw.shape) != (H,) or not gw.is_contiguous():
+    elif isinstance(grad_weight, torch.Tensor):
+        gw = grad_weight
+        _on(dev, gw, "grad_weight")
+        if gw.dtype != torch.float32 or gw.shape != (H,) or not gw.is_contiguous():
             raise TypeError("grad_weight must be a contiguous float32 vector of H elements")
+    if gw is not None:
         if workspace is None:
-            workspace = torch.empty(lib.ce_rmsnorm_bwd_workspace_bytes(N, H), dtype=torch.uint8, device=dev)
-    rc = lib.ce_rmsnorm_bwd(grad_out.data_ptr(), h.data_ptr(), weight.data_ptr(), _ptr(grad_h), dt,
-                            _DTYPE[weight.dtype], N, H, gs, hs, dhs, eps, grad_x.data_ptr(), xs, _ptr(gw),
-                            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                            _stream(dev, stream))
+            need = lib.ce_rmsnorm_bwd_workspace_bytes(N, H)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _on(dev, workspace, "workspace")
+            need = _bytes(workspace)
+    rc = lib.ce_rmsnorm_bwd(grad_out.data_ptr(), h.data_ptr(), weight.data_ptr(), _ptr(grad_h), dt, wdt, N, H,
+                            _stride(grad_out, H, "grad_out"), _stride(h, H, "h"), dhs, eps, grad_x.data_ptr(),
+                            _stride(grad_x, H, "grad_x"), _ptr(gw), _ptr(workspace), need, _stream(dev, stream))
     if rc:
         _raise(rc, "ce_rmsnorm_bwd")
     return grad_x, gw
@@ -347,54 +379,63 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
 
 
 # ---------------------------------------------------------------- logits
+_I64x3 = ctypes.c_int64 * 3
+
+
 def _logits_dims(t: torch.Tensor, name: str):
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    """(dim0, dim1, V, strides) of (N, V) or (dim0, dim1, V) logits."""
+    s, n = t.stride(), t.shape
+    if s and s[-1] != 1 and n[-1] > 1:
         raise ValueError(f"the vocabulary dimension of {name} must be contiguous (call .contiguous())")
-    s = t.stride()
-    if t.dim() == 3:
-        return t.shape[0], t.shape[1], t.shape[2], (s[0], s[1], 1)
-    if t.dim() == 2:
-        return 1, t.shape[0], t.shape[1], (t.shape[0] * s[0], s[0], 1)
+    if len(n) == 2:
+        return 1, n[0], n[1], _I64x3(n[0] * s[0], s[0], 1)
+    if len(n) == 3:
+        return n[0], n[1], n[2], _I64x3(s[0], s[1], 1)
     raise ValueError(f"{name} must be (dim0, dim1, V) or (N, V)")
 
 
-def _per_row(t, N, dtype, dev, name):
-    if t is None:
-        return None
-    if t.dtype != dtype or t.device != dev or t.numel() != N or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor with one value per row")
-    return t.data_ptr()
+_PER_ROW = (("history_lengths", torch.int64), ("prompt_lengths", torch.int64), ("repetition_penalty", torch.float32),
+            ("frequency_penalty", torch.float32), ("presence_penalty", torch.float32), ("temperature", torch.float32))
+_LOGITS_PARAMS = {name for name, _ in _PER_ROW} | {"history", "bias_tokens", "bias_values", "mask", "mask_value"}
 
 
 def _list(t, N, dtype, dev, name):
     """(pointer, stride between rows, entries per row) of an (N, L) list."""
     if t.dtype != dtype or t.device != dev or t.dim() != 2 or t.shape[0] != N:
         raise TypeError(f"{name} must be {dtype} on the logits' device, one row of entries per row of logits")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    L = t.shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), L, L
+    if L > 1 and t.stride(1) != 1:
         raise ValueError(f"the entries of {name} must be contiguous (call .contiguous())")
-    return t.data_ptr(), t.stride(0), t.shape[1]
+    return t.data_ptr(), t.stride(0), L
 
 
-def _logits_params(N, V, dev, history=None, history_lengths=None, prompt_lengths=None, repetition_penalty=None,
-                   frequency_penalty=None, presence_penalty=None, bias_tokens=None, bias_values=None, mask=None,
-                   temperature=None, mask_value=-math.inf):
+def _logits_params(N, V, dev, given):
     p = _lib.ce_logits_params()
+    if not _LOGITS_PARAMS.issuperset(given):
+        raise TypeError(f"unknown parameters {sorted(set(given) - _LOGITS_PARAMS)}")
+    get = given.get
+    for name, dtype in _PER_ROW:
+        t = get(name)
+        if t is not None:
+            if t.dtype != dtype or t.device != dev or t.numel() != N or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor with one value per row")
+            setattr(p, name, t.data_ptr())
+    history = get("history")
     if history is not None:
         p.history, p.history_stride, p.history_max = _list(history, N, torch.int64, dev, "history")
-        p.history_lengths = _per_row(history_lengths, N, torch.int64, dev, "history_lengths")
-        p.prompt_lengths = _per_row(prompt_lengths, N, torch.int64, dev, "prompt_lengths")
-        p.repetition_penalty = _per_row(repetition_penalty, N, torch.float32, dev, "repetition_penalty")
-        p.frequency_penalty = _per_row(frequency_penalty, N, torch.float32, dev, "frequency_penalty")
-        p.presence_penalty = _per_row(presence_penalty, N, torch.float32, dev, "presence_penalty")
-    elif not (history_lengths is prompt_lengths is repetition_penalty is frequency_penalty is presence_penalty is None):
+    elif p.history_lengths or p.prompt_lengths or p.repetition_penalty or p.frequency_penalty or p.presence_penalty:
         raise ValueError("the penalties and lengths need a history")
-    if (bias_tokens is None) != (bias_values is None):
+    tokens, values = get("bias_tokens"), get("bias_values")
+    if (tokens is None) != (values is None):
         raise ValueError("bias_tokens and bias_values go together")
-    if bias_tokens is not None:
-        p.bias_tokens, p.bias_tokens_stride, p.bias_max = _list(bias_tokens, N, torch.int64, dev, "bias_tokens")
-        p.bias_values, p.bias_values_stride, n = _list(bias_values, N, torch.float32, dev, "bias_values")
+    if tokens is not None:
+        p.bias_tokens, p.bias_tokens_stride, p.bias_max = _list(tokens, N, torch.int64, dev, "bias_tokens")
+        p.bias_values, p.bias_values_stride, n = _list(values, N, torch.float32, dev, "bias_values")
         if n != p.bias_max:
             raise ValueError("bias_tokens and bias_values must have the same shape")
+    mask = get("mask")
     if mask is not None:
         words = (V + 31) // 32
         if mask.dtype != torch.int32 or mask.device != dev or mask.shape[-1] != words:
@@ -404,8 +445,7 @@ def _logits_params(N, V, dev, history=None, history_lengths=None, prompt_lengths
             raise ValueError("mask must be (words,) for all rows or (N, words), its words contiguous")
         p.mask = mask.data_ptr()
         p.mask_stride = mask.stride(0) if mask.dim() == 2 and mask.shape[0] == N and N > 1 else 0
-    p.temperature = _per_row(temperature, N, torch.float32, dev, "temperature")
-    p.mask_value = mask_value
+    p.mask_value = get("mask_value", -math.inf)
     return p
 
 
@@ -426,8 +466,8 @@ def _logits_workspace(workspace, p, N, V, dt, dev):
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is None:
         return None, None, 0
-    _on(dev, workspace=workspace)
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _on(dev, workspace, "workspace")
+    return workspace, workspace.data_ptr(), _bytes(workspace)
 
 
 def ce_logits_process(logits: torch.Tensor, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
@@ -451,22 +491,16 @@ def ce_logits_process(logits: torch.Tensor, out: torch.Tensor | None = None, wor
     ``mask_value`` (default -inf; the cross-entropy pass needs a finite one,
     say -3e4).  Tokens outside [0, V) are skipped; a row whose mask allows
     nothing is mask_value throughout."""
-    if not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor (there is no CPU path)")
-    dt = _DTYPE.get(logits.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported logits dtype {logits.dtype}")
+    dev, dt = _cuda(logits, "logits")
     d0, d1, V, st = _logits_dims(logits, "logits")
-    dev = logits.device
-    p = _logits_params(d0 * d1, V, dev, **params)
+    p = _logits_params(d0 * d1, V, dev, params)
     if out is None:
         out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
     else:
         _match(out, logits, "out")
     ost = _logits_dims(out, "out")[3]
     workspace, wp, wb = _logits_workspace(workspace, p, d0 * d1, V, dt, dev)
-    rc = _lib.load().ce_logits_process(logits.data_ptr(), dt, d0, d1, V, _lib.i64_array(st), ctypes.byref(p),
-                                       out.data_ptr(), _lib.i64_array(ost), wp, wb, _stream(dev, stream))
+    rc = _lib.load().ce_logits_process(logits.data_ptr(), dt, d0, d1, V, st, ctypes.byref(p), out.data_ptr(), ost, wp, wb, _stream(dev, stream))
     if rc:
         _raise(rc, "ce_logits_process")
     return out
@@ -478,15 +512,10 @@ def ce_logits_process_bwd(grad_out: torch.Tensor, logits: torch.Tensor, grad: to
     the logits it was given and the same parameters (the biases, the frequency
     and presence penalties, the prompt lengths and mask_value change nothing
     and may be left out).  ``grad`` may be ``grad_out`` itself."""
-    if not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor (there is no CPU path)")
-    dt = _DTYPE.get(logits.dtype)
-    if dt is None:
-        raise TypeError(f"unsupported logits dtype {logits.dtype}")
+    dev, dt = _cuda(logits, "logits")
     d0, d1, V, st = _logits_dims(logits, "logits")
-    dev = logits.device
     _match(grad_out, logits, "grad_out")
-    p = _logits_params(d0 * d1, V, dev, **params)
+    p = _logits_params(d0 * d1, V, dev, params)
     gst = _logits_dims(grad_out, "grad_out")[3]
     if grad is None:
         grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
@@ -494,9 +523,8 @@ def ce_logits_process_bwd(grad_out: torch.Tensor, logits: torch.Tensor, grad: to
         _match(grad, logits, "grad")
     ost = _logits_dims(grad, "grad")[3]
     workspace, wp, wb = _logits_workspace(workspace, p, d0 * d1, V, dt, dev)
-    rc = _lib.load().ce_logits_process_bwd(grad_out.data_ptr(), _lib.i64_array(gst), logits.data_ptr(), dt, d0, d1, V,
-                                           _lib.i64_array(st), ctypes.byref(p), grad.data_ptr(),
-                                           _lib.i64_array(ost), wp, wb, _stream(dev, stream))
+    rc = _lib.load().ce_logits_process_bwd(grad_out.data_ptr(), gst, logits.data_ptr(), dt, d0, d1, V, st,
+                                           ctypes.byref(p), grad.data_ptr(), ost, wp, wb, _stream(dev, stream))
     if rc:
         _raise(rc, "ce_logits_process_bwd")
     return grad
