@@ -87,23 +87,6 @@ __device__ __forceinline__ float special(float v, float x, uint32_t word, float 
     return z + bias;
 }
 
-// A row whose outputs start at another offset from 16 bytes than its inputs: the
-// vector that starts `ph` bytes into the two 16-byte vectors a, b.
-__device__ __forceinline__ uint4 shift_bytes(uint4 a, uint4 b, uint32_t ph) {
-    uint32_t r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (ph & 8u) {
-#pragma unroll
-        for (int k = 0; k < 6; ++k) r[k] = r[k + 2];
-    }
-    if (ph & 4u) {
-#pragma unroll
-        for (int k = 0; k < 5; ++k) r[k] = r[k + 1];
-    }
-    const uint32_t s = (ph & 3u) * 8u;
-    return make_uint4(__funnelshift_r(r[0], r[1], s), __funnelshift_r(r[1], r[2], s),
-                      __funnelshift_r(r[2], r[3], s), __funnelshift_r(r[3], r[4], s));
-}
-
 // One row's pointers at column c0.
 struct RowPtrs {
     const char* x;

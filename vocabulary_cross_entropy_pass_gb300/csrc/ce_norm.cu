@@ -102,7 +102,9 @@ template <typename T, int VEC, int VPT, bool Q8, bool PHASED>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(const __grid_constant__ NormFwdArgs p) {
     constexpr int ES = sizeof(T);
     __shared__ float red[64];
-    extern __shared__ uint32_t gmax[];  // Q8 with groups wider than a warp's vectors
+    extern __shared__ float stage[];  // STAGED: the row's y
+    // 8-bit groups go by columns: lanes of vectors hold them whole on the grid only
+    constexpr bool STAGED = Q8 && (PHASED || VEC == 1);
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, TH = blockDim.x;
     const char* x = p.x + row * p.xs;
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
     };
     auto take = [&](const char* row_at, int v) {
         Pack<T, VEC> a;
-        a.zero();
+        if (edge(v) || v >= nv) a.zero();
         if (edge(v)) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
@@ -169,17 +171,26 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
     }
     ss = cta_sum(ss, red);
     const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
+    const bool w_grid = PHASED && !p.w32 && (reinterpret_cast<uintptr_t>(p.w) & 15u) == 0;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int v = tid + k * TH;
         float w[VEC];
         if (v < nv) {
             if constexpr (PHASED) {
-                // the weight starts where it starts: element by element
+                if (w_grid && v > 0 && (int64_t)(v + 1) * VEC <= p.H) {
+                    // the weight's own vectors v - 1 and v hold these columns
+                    const uint4* q = reinterpret_cast<const uint4*>(p.w) + v;
+                    Pack<T, VEC> t;
+                    t.raw = sh ? shift_bytes(__ldg(q - 1), __ldg(q), 16u - (uint32_t)sh * ES) : __ldg(q);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    w[i] = 0.f;
-                    if (!edge(v) || inside(v, i)) load_w<T, 1>(p, (int64_t)v * VEC + i - sh, w + i);
+                    for (int i = 0; i < VEC; ++i) w[i] = t.f(i);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        w[i] = 0.f;
+                        if (!edge(v) || inside(v, i)) load_w<T, 1>(p, (int64_t)v * VEC + i - sh, w + i);
+                    }
                 }
             } else {
                 load_w<T, VEC>(p, (int64_t)v * VEC, w);
@@ -202,49 +213,66 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
             if (tid + k * TH >= nv) am[k] = 0.f;
         }
         float* sc = p.scales + row * (int64_t)p.groups;
-        const int gl = p.group / VEC;  // vectors (lanes) per group
+        float whole = 0.f;  // the scale of all columns, where there is one
         if (p.groups == 1) {
             float m = 0.f;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) m = fmaxf(m, am[k]);
-            m = cta_max(m, red + 32);
-            const float s = fmaxf(m / p.top, kTinyScale);
-            if (tid == 0) sc[0] = s;
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) am[k] = s;
-        } else if (gl <= 32) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                for (int o = gl >> 1; o > 0; o >>= 1) am[k] = fmaxf(am[k], __shfl_xor_sync(kFull, am[k], o));
-                am[k] = fmaxf(am[k] / p.top, kTinyScale);
-                const int v = tid + k * TH;
-                if (v < nv && v % gl == 0) sc[v / gl] = am[k];
-            }
-        } else {
-            // a group spans several warps: its maximum through shared memory
-            // (non-negative floats compare as integers, in any order)
-            for (int g = tid; g < p.groups; g += TH) gmax[g] = 0u;
-            __syncthreads();
+            whole = fmaxf(cta_max(m, red + 32) / p.top, kTinyScale);
+            if (tid == 0) sc[0] = whole;
+        }
+        if constexpr (STAGED) {
+            // the row's float32 y in shared memory; then a warp to each group of
+            // columns, lanes side by side
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int v = tid + k * TH;
-                const float m = warp_allmax(am[k]);
-                if ((tid & 31) == 0 && v < nv) atomicMax(&gmax[v / gl], __float_as_uint(m));
+                if (v < nv)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        if (!edge(v) || inside(v, i)) stage[(int64_t)v * VEC + i - sh] = h[k][i];
             }
             __syncthreads();
+            const int lane = tid & 31, nw = TH >> 5;
+            const int per = p.groups == 1 ? 4 : p.group / 32, run = per * 32;
+            const bool four = per == 4 && (reinterpret_cast<uintptr_t>(y) & 3u) == 0;
+            for (int g = tid >> 5; (int64_t)g * run < p.H; g += nw) {
+                const int64_t c0 = (int64_t)g * run + lane * per;
+                float f[4];
+                float m = 0.f;
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int v = tid + k * TH;
-                if (v < nv) {
-                    am[k] = fmaxf(__uint_as_float(gmax[v / gl]) / p.top, kTinyScale);
-                    if (v % gl == 0) sc[v / gl] = am[k];
+                for (int i = 0; i < 4; ++i) {
+                    f[i] = i < per && c0 + i < p.H ? stage[c0 + i] : 0.f;
+                    m = fmaxf(m, fabsf(f[i]));
+                }
+                float s = whole;
+                if (p.groups > 1) {
+                    s = fmaxf(warp_allmax(m) / p.top, kTinyScale);
+                    if (lane == 0) sc[g] = s;
+                }
+                const float inv = 1.f / s;
+                if (four && c0 + 4 <= p.H) {
+                    store_q8<4>(y + c0, f, inv, p.kind);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < per && c0 + i < p.H) store_q8<1>(y + c0 + i, f + i, inv, p.kind);
                 }
             }
-        }
+        } else {
+            const int gl = p.group / VEC;  // vectors (lanes) per group: at most 32
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = tid + k * TH;
-            if (v < nv) store_q8<VEC>(y + (int64_t)v * VEC, h[k], 1.f / am[k], p.kind);
+            for (int k = 0; k < VPT; ++k) {
+                const int v = tid + k * TH;
+                if (p.groups > 1) {
+                    for (int o = gl >> 1; o > 0; o >>= 1) am[k] = fmaxf(am[k], __shfl_xor_sync(kFull, am[k], o));
+                    am[k] = fmaxf(am[k] / p.top, kTinyScale);
+                    if (v < nv && v % gl == 0) sc[v / gl] = am[k];
+                } else {
+                    am[k] = whole;
+                }
+                if (v < nv) store_q8<VEC>(y + (int64_t)v * VEC, h[k], 1.f / am[k], p.kind);
+            }
         }
     }
 }
@@ -327,7 +355,7 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_fwd_wide_kernel(const __grid_c
 template <typename T, int VEC, bool Q8, bool PHASED = false>
 cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
     const int64_t nv = PHASED ? (a.H + VEC - 1 + VEC - 1) / VEC : a.H / VEC;
-    const size_t smem = Q8 ? (size_t)a.groups * 4 : 0;
+    size_t smem = Q8 ? (size_t)a.groups * 4 : 0;  // the wide kernel's maxima
     constexpr int MAXV = VEC >= 8 ? 4 : (VEC == 4 ? 8 : 16);  // 512 threads hold 512 * MAXV vectors
     if (nv > 512 * MAXV) {
         auto* k = ce_rmsnorm_fwd_wide_kernel<T, PHASED ? 1 : VEC, Q8>;
@@ -338,17 +366,19 @@ cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
         k<<<(unsigned)a.N, 512, smem, s>>>(a);
         return cudaGetLastError();
     }
-    if (nv <= 256 || (a.N <= 304 && nv <= 1024)) {
-        const int th = (int)((nv + 31) / 32 * 32);
-        ce_rmsnorm_fwd_kernel<T, VEC, 1, Q8, PHASED><<<(unsigned)a.N, th, smem, s>>>(a);
-    } else if (nv <= 2048) {
-        const int th = (int)((nv + 127) / 128 * 32);
-        ce_rmsnorm_fwd_kernel<T, VEC, 4, Q8, PHASED><<<(unsigned)a.N, th, smem, s>>>(a);
-    } else {
-        const int th = (int)((nv + 32 * MAXV - 1) / (32 * MAXV) * 32);
-        ce_rmsnorm_fwd_kernel<T, VEC, MAXV, Q8, PHASED><<<(unsigned)a.N, th, smem, s>>>(a);
-    }
-    return cudaGetLastError();
+    smem = Q8 && (PHASED || VEC == 1) ? (size_t)a.H * 4 : 0;
+    auto go = [&](auto* k, int th) {
+        if (smem > 40 * 1024) {
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+        }
+        k<<<(unsigned)a.N, th, smem, s>>>(a);
+        return cudaGetLastError();
+    };
+    const auto th = [&](int v) { return (int)((nv + 32 * v - 1) / (32 * v) * 32); };
+    if (nv <= 256 || (a.N <= 304 && nv <= 1024)) return go(ce_rmsnorm_fwd_kernel<T, VEC, 1, Q8, PHASED>, th(1));
+    if (nv <= 2048) return go(ce_rmsnorm_fwd_kernel<T, VEC, 4, Q8, PHASED>, th(4));
+    return go(ce_rmsnorm_fwd_kernel<T, VEC, MAXV, Q8, PHASED>, th(MAXV));
 }
 
 template <typename T>
@@ -356,16 +386,14 @@ cudaError_t launch_fwd_t(const NormFwdArgs& a, int vb, cudaStream_t s) {
     constexpr int ES = sizeof(T);
     const bool q = a.kind != 0;
     if (vb == 16) return q ? launch_fwd<T, 16 / ES, true>(a, s) : launch_fwd<T, 16 / ES, false>(a, s);
-    if (!q) {
-        auto at = [](const void* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u); };
-        bool phased = at(a.y) == at(a.x) && (!a.r || at(a.r) == at(a.x)) && (!a.h || at(a.h) == at(a.x));
-        if (a.N > 1)
-            phased = phased && (a.ys - a.xs) % 16 == 0 && (!a.r || (a.rs - a.xs) % 16 == 0) &&
-                     (!a.h || (a.hs - a.xs) % 16 == 0);
-        if (phased) return launch_fwd<T, 16 / ES, false, true>(a, s);
-    }
+    auto at = [](const void* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u); };
+    bool phased = (q || at(a.y) == at(a.x)) && (!a.r || at(a.r) == at(a.x)) && (!a.h || at(a.h) == at(a.x));
+    if (a.N > 1)
+        phased = phased && (q || (a.ys - a.xs) % 16 == 0) && (!a.r || (a.rs - a.xs) % 16 == 0) &&
+                 (!a.h || (a.hs - a.xs) % 16 == 0);
+    if (phased) return q ? launch_fwd<T, 16 / ES, true, true>(a, s) : launch_fwd<T, 16 / ES, false, true>(a, s);
     if constexpr (ES == 2)
-        if (vb == 4) return q ? launch_fwd<T, 2, true>(a, s) : launch_fwd<T, 2, false>(a, s);
+        if (vb == 4 && !q) return launch_fwd<T, 2, false>(a, s);
     return q ? launch_fwd<T, 1, true>(a, s) : launch_fwd<T, 1, false>(a, s);
 }
 

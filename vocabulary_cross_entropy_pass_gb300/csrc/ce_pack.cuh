@@ -71,6 +71,23 @@ __device__ __forceinline__ void load_f32(const float* p, float* x) {
     }
 }
 
+// The 16 bytes that start `ph` bytes into the two 16-byte vectors a, b (rows that
+// lie at different offsets from 16 bytes).
+__device__ __forceinline__ uint4 shift_bytes(uint4 a, uint4 b, uint32_t ph) {
+    uint32_t r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (ph & 8u) {
+#pragma unroll
+        for (int k = 0; k < 6; ++k) r[k] = r[k + 2];
+    }
+    if (ph & 4u) {
+#pragma unroll
+        for (int k = 0; k < 5; ++k) r[k] = r[k + 1];
+    }
+    const uint32_t s = (ph & 3u) * 8u;
+    return make_uint4(__funnelshift_r(r[0], r[1], s), __funnelshift_r(r[1], r[2], s),
+                      __funnelshift_r(r[2], r[3], s), __funnelshift_r(r[3], r[4], s));
+}
+
 // Widest run of elements (in bytes) that divides every given address or byte stride.
 inline int common_vector_bytes(const uint64_t* vals, int n, int es) {
     uint64_t all = 0;
