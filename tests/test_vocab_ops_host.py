@@ -212,7 +212,7 @@ def test_logits_in_place_refusals(lib):
     assert logits(lib, bwd=True, g=0) == 1
 
 
-def test_python_refuses_cpu_tensors_and_types():
+def test_python_refuses_cpu_tensors_and_types(lib):
     x = torch.zeros(4, 64)
     t = torch.zeros(4, dtype=torch.int64)
     with pytest.raises(ValueError):
@@ -229,21 +229,29 @@ def test_python_refuses_cpu_tensors_and_types():
         pkg.ce_logits_process_bwd(x, x)
 
 
-def test_row_strides_of_views():
-    from vocabulary_cross_entropy_pass_gb300.vocab_ops import _rows
+def test_row_strides_of_views(lib):
+    from vocabulary_cross_entropy_pass_gb300.vocab_ops import _load
+    stride = _load().row_stride
     x = torch.zeros(6, 5, 16)
-    assert _rows(x, 16, "x") == (30, 16)
-    assert _rows(x[:, :, :8], 8, "x") == (30, 16)
-    assert _rows(x[:, 2], 16, "x") == (6, 80)
-    assert _rows(x[:, :1], 16, "x") == (6, 80)
-    assert _rows(x[0, 0], 16, "x") == (1, 16)
-    assert _rows(x[:0], 16, "x") == (0, 16)
-    assert _rows(torch.zeros(16).expand(3, 2, 16), 16, "x") == (6, 0)
-    with pytest.raises(ValueError):
-        _rows(x[:, :4], 16, "x")           # rows unevenly spaced
-    with pytest.raises(ValueError):
-        _rows(x.transpose(0, 1), 16, "x")
-    with pytest.raises(ValueError):
-        _rows(x[:, :, ::2], 8, "x")
-    with pytest.raises(ValueError):
-        _rows(x, 8, "x")
+    assert stride(x) == 16
+    assert stride(x[:, :, :8]) == 16
+    assert stride(x[:, 2]) == 80
+    assert stride(x[:, :1]) == 80
+    assert stride(x[0, 0]) == 16
+    assert stride(x[:0]) == 16
+    assert stride(torch.zeros(16).expand(3, 2, 16)) == 0
+    for bad in (x[:, :4], x.transpose(0, 1), x[:, :, ::2]):
+        with pytest.raises(ValueError):
+            stride(bad)
+
+
+def test_python_refuses_what_is_no_tensor(lib):
+    x = torch.zeros(4, 64)
+    with pytest.raises(TypeError):
+        pkg.ce_embed_fwd([1, 2], x)
+    with pytest.raises(TypeError):
+        pkg.ce_rmsnorm_fwd(x, None)
+    with pytest.raises(TypeError):
+        pkg.ce_rmsnorm_fwd(x, x[0], quant=torch.int8)
+    with pytest.raises(TypeError):
+        pkg.ce_logits_process("logits")

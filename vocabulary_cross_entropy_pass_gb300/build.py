@@ -1,20 +1,25 @@
-"""Build libgbce.so (the CUDA kernels and the C ABI) in-tree with nvcc.
+"""Build libgbce.so (the CUDA kernels and the C ABI) in-tree with nvcc, and
+_gbce_torch.so (torch tensors into that ABI) with g++.
 
 Each translation unit is compiled for sm_103a in its own nvcc process, in
-parallel, then linked into vocabulary_cross_entropy_pass_gb300/libgbce.so.
+parallel, then linked into vocabulary_cross_entropy_pass_gb300/libgbce.so; the
+host module is compiled beside them and linked against it.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libgbce.so")
+EXT = os.path.join(HERE, "_gbce_torch.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["ce_api.cu", "ce_aux.cu", "ce_bwd.cu", "ce_fused.cu", "ce_rows.cu", "ce_split.cu",
            "ce_vecrow.cu", "ce_linear.cu", "ce_lmhead.cu", "ce_stream.cu", "ce_stream_geo.cu",
@@ -37,10 +42,36 @@ def _deps() -> list[str]:
     return out
 
 
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _compile_ext(obj: str) -> None:
+    """Compile csrc/ce_torch.cpp against the installed torch's headers."""
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", os.path.join(CSRC, "ce_torch.cpp"), "-o", obj,
+           f"-I{inc}", f"-I{inc}/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}", f"-I{cuda}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on ce_torch.cpp:\n{res.stdout}\n{res.stderr}")
+
+
+def _link_ext(obj: str) -> None:
+    lib = os.path.join(_torch_dir(), "lib")
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", obj, "-o", tmp, f"-L{HERE}", "-l:libgbce.so", f"-L{lib}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, EXT)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -61,14 +92,18 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(res.stdout + res.stderr)
         return obj
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    ext_obj = os.path.join(BUILD_DIR, "ce_torch.o")
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        ext = ex.submit(_compile_ext, ext_obj)
         objs = list(ex.map(compile_one, SOURCES))
+        ext.result()
     tmp = LIB + f".tmp{os.getpid()}"
     res = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcublas"], capture_output=True,
                          text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _link_ext(ext_obj)
     return LIB
 
 
