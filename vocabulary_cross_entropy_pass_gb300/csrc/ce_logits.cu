@@ -50,7 +50,7 @@ struct LogitArgs {
     int cols, runs;        // a CTA's run of columns (a multiple of 128) and the runs of a row
     int listed;            // the history or the biases touch columns
     int in_place;
-    uint2* table;          // [N][parts][entries] touched (column in the part, count and flags), by column; or NULL
+    uint2* table;          // [N][parts][entries] touched (column in its run, count and flags), by column; or NULL
     float* tbias;          // [N][parts][entries] their summed biases
     uint32_t* start;       // [N][runs][2] a run's first and last + 1 entry of its part's table
     int parts, part_runs;  // parts of a row with a table each (one but for the longest lists), runs in a part
@@ -124,9 +124,10 @@ __device__ __forceinline__ RowScalars row_scalars(const LogitArgs& p, int64_t ro
 }
 
 // A token's column in the run that starts at c0, or at least 2^31.
+// (c0 < 2^31: a token's upper half is zero or the token lies nowhere.)
 __device__ __forceinline__ uint32_t column_of(int64_t t, int64_t c0) {
-    const uint64_t d = (uint64_t)(t - c0);
-    return (d >> 31) ? 0xffffffffu : (uint32_t)d;
+    const uint32_t lo = (uint32_t)t, hi = (uint32_t)((uint64_t)t >> 32);
+    return hi == 0u && lo >= (uint32_t)c0 ? lo - (uint32_t)c0 : 0xffffffffu;
 }
 
 // The listed columns of this run: col[0 .. returned count), each one's output in
@@ -232,7 +233,10 @@ __device__ __forceinline__ void stream_run(const LogitArgs& p, const RowPtrs& rp
     constexpr int VEC = VT::kElems;
     constexpr int ES = sizeof(T);
     constexpr int TH = kThreads;
-    constexpr int U = 4;
+    // vectors per thread and batch: with a mask, two dependent loads each and few
+    // bytes, more CTAs count for more (512 x 128000 with lists 83 -> 77 us, 4096
+    // x 50257 205 -> 179 us; without a mask 66 -> 72 us)
+    constexpr int U = MASK ? 2 : 4;
     constexpr uint32_t ALL = (1u << VEC) - 1u;
     const int tid = threadIdx.x;
     const float blocked = BWD ? 0.f : p.mask_value;
@@ -274,7 +278,10 @@ __device__ __forceinline__ void stream_run(const LogitArgs& p, const RowPtrs& rp
         uint4 raw[U];
         uint32_t on[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) on[u] = v0 + u * TH >= nv ? 0u : (MASK ? bits_of(v0 + u * TH) : ALL);
+        for (int u = 0; u < U; ++u) {
+            const int v = v0 + u * TH;
+            on[u] = v >= nv ? 0u : (MASK ? bits_of(v) : ALL);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (on[u]) raw[u] = load(v0 + u * TH);
@@ -299,7 +306,7 @@ __device__ __forceinline__ void stream_run(const LogitArgs& p, const RowPtrs& rp
 }
 
 template <typename T, bool BWD, bool MASK>
-__global__ void __launch_bounds__(kThreads, 6) ce_logits_kernel(const __grid_constant__ LogitArgs p) {
+__global__ void __launch_bounds__(kThreads, MASK ? 8 : 6) ce_logits_kernel(const __grid_constant__ LogitArgs p) {
     using VT = Vec<T>;
     constexpr int ES = sizeof(T);
     extern __shared__ __align__(16) uint32_t sm[];
@@ -321,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, 6) ce_logits_kernel(const __grid_con
         if (p.in_place) __syncthreads();
     }
     const int64_t t0 = (row * p.parts + run / p.part_runs) * p.entries;
-    const int back = run % p.part_runs * p.cols;  // columns of the part before this run
     auto bias_of = [&](uint32_t e, uint32_t word) {
         return !BWD && (word & kBiased) ? __ldcg(p.tbias + t0 + e) : 0.f;
     };
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 6) ce_logits_kernel(const __grid_con
         // what the logits give is taken before the stream replaces them
         for (uint32_t e = range.x + tid; e < range.y; e += kThreads) {
             const uint2 t = __ldcg(p.table + t0 + e);
-            p.table[t0 + e].y = __float_as_uint(output(e, (int)t.x - back, t.y));
+            p.table[t0 + e].y = __float_as_uint(output(e, (int)t.x, t.y));
         }
         __syncthreads();
     }
@@ -345,16 +351,19 @@ __global__ void __launch_bounds__(kThreads, 6) ce_logits_kernel(const __grid_con
     float xv = 0.f, v = 0.f, bv = 0.f;
     bool ok = false;
     const bool have = range.x + tid < range.y;
+    auto gather = [&](int c) {
+        xv = VT::load1(rp.x + c * ES);
+        v = BWD ? VT::load1(rp.src + c * ES) : xv;
+    };
     auto fetch = [&](int step) {
         if (!have) return;
         if (step == 0) {
             mine = __ldcg(p.table + t0 + range.x + tid);
         } else if (!p.in_place) {
-            const int c = (int)mine.x - back;
-            xv = VT::load1(rp.x + c * ES);
-            v = BWD ? VT::load1(rp.src + c * ES) : xv;
+            const int c = (int)mine.x;
             ok = allowed(rp.mask, c);
             bv = bias_of(range.x + tid, mine.y);
+            if (!MASK) gather(c);
         }
     };
     const Span16 sp = span16<ES>(rp.out, 0, n);
@@ -363,16 +372,17 @@ __global__ void __launch_bounds__(kThreads, 6) ce_logits_kernel(const __grid_con
     else
         stream_run<T, BWD, true, MASK>(p, rp, c0, n, sp, fetch);
     if (range.x < range.y) {
+        if (MASK && have && ok && !p.in_place) gather((int)mine.x);  // a forbidden logit's line may never have been read
         __syncthreads();
         if (have) {
             const float o = p.in_place ? __uint_as_float(mine.y)
                             : ok       ? special<BWD>(v, xv, mine.y, bv, rs) * rp.inv_temp
                                        : (BWD ? 0.f : p.mask_value);
-            VT::store1(rp.out + ((int)mine.x - back) * ES, o);
+            VT::store1(rp.out + (int)mine.x * ES, o);
         }
         for (uint32_t e = range.x + tid + kThreads; e < range.y; e += kThreads) {
             const uint2 t = __ldcg(p.table + t0 + e);
-            const int c = (int)t.x - back;
+            const int c = (int)t.x;
             VT::store1(rp.out + c * ES, p.in_place ? __uint_as_float(t.y) : output(e, c, t.y));
         }
     } else if (l.n > 0) {
@@ -385,7 +395,8 @@ __global__ void __launch_bounds__(kThreads, 6) ce_logits_kernel(const __grid_con
 // The table of one part of a row.  Shared memory: bits[words] (a whole number of
 // 16-byte vectors), cnt[entries], keys[slots] and sums[slots] of the biased
 // entries, first[words] (entries before each word: 16 bits, a part has at most
-// 65535).
+// 65535), col[entries] (columns in their runs: 16 bits, a run is a power of two
+// of at most 65536).
 template <int TH, int U>
 __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __grid_constant__ LogitArgs p) {
     extern __shared__ __align__(16) uint32_t sm[];
@@ -401,23 +412,27 @@ __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __
     uint32_t* keys = cnt + p.entries;
     float* sums = reinterpret_cast<float*>(keys + p.slots);
     uint16_t* first = reinterpret_cast<uint16_t*>(sums + p.slots);
+    uint16_t* col = first + words;
+    const uint32_t in_run = (uint32_t)p.cols - 1;
     const int64_t t0 = (row * p.parts + blockIdx.x) * p.entries;
     uint2* table = p.table + t0;
     const int64_t* h = p.hist + row * p.hist_stride;
     const int64_t* bt = p.btok + row * p.btok_stride;
     const float* bv = p.bval + row * p.bval_stride;
 
+    const int hist_max = (int)p.hist_max;
     uint32_t tc[U];  // this thread's first tokens, as columns of the part
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t k = u * TH + tid;
-        tc[u] = k < p.hist_max ? column_of(__ldg(h + k), c0) : 0xffffffffu;
+        const int k = u * TH + tid;
+        tc[u] = k < hist_max ? column_of(__ldg(h + k), c0) : 0xffffffffu;
     }
-    int64_t len = 0, prompt = 0;
-    if (p.hist_max > 0) {
-        len = p.hist_len ? __ldg(p.hist_len + row) : p.hist_max;
-        len = len < 0 ? 0 : (len > p.hist_max ? p.hist_max : len);
-        prompt = p.prompt_len ? __ldg(p.prompt_len + row) : 0;
+    int len = 0, prompt = 0;
+    if (hist_max > 0) {
+        const int64_t l = p.hist_len ? __ldg(p.hist_len + row) : hist_max;
+        const int64_t q = p.prompt_len ? __ldg(p.prompt_len + row) : 0;
+        len = l < 0 ? 0 : (l > hist_max ? hist_max : (int)l);
+        prompt = q < 0 ? 0 : (q > hist_max ? hist_max : (int)q);
     }
     for (int k = tid; k < words / 4; k += TH) reinterpret_cast<uint4*>(bits)[k] = make_uint4(0, 0, 0, 0);
     if (p.bias_max > 0)
@@ -425,16 +440,19 @@ __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __
             keys[k] = 0xffffffffu;
             sums[k] = 0.f;
         }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (u * TH + tid >= len) tc[u] = 0xffffffffu;
     __syncthreads();
     auto each = [&](auto f) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (u * TH + tid < len && tc[u] < (uint32_t)n) f(tc[u], u * TH + tid < prompt);
-        for (int64_t k0 = (int64_t)U * TH; k0 < len; k0 += TH * 4) {
+            if (tc[u] < (uint32_t)n) f(tc[u], u * TH + tid < prompt);
+        for (int k0 = U * TH; k0 < len; k0 += TH * 4) {
             uint32_t c[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int64_t k = k0 + u * TH + tid;
+                const int k = k0 + u * TH + tid;
                 c[u] = k < len ? column_of(__ldg(h + k), c0) : 0xffffffffu;
             }
 #pragma unroll
@@ -497,7 +515,7 @@ __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __
     each([&](uint32_t c, bool in_prompt) {
         const uint32_t e = place(c);
         const uint32_t old = in_prompt ? atomicOr(&cnt[e], kSeen) : atomicAdd(&cnt[e], 1u);
-        if (old == 0u) table[e].x = c;
+        if (old == 0u) col[e] = (uint16_t)(c & in_run);
     });
     if (p.bias_max > 0 && warp == TH / 32 - 1) {
         for (int64_t k0 = 0; k0 < p.bias_max; k0 += 32) {
@@ -530,14 +548,14 @@ __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __
             }
             if (lead) {
                 sums[slot] = sum;
-                if (atomicOr(&cnt[e], kBiased) == 0u) table[e].x = c;
+                if (atomicOr(&cnt[e], kBiased) == 0u) col[e] = (uint16_t)(c & in_run);
             }
             __syncwarp();
         }
     }
     griddep_launch_dependents();  // earlier the waiting stream takes the place of lists not yet begun
     __syncthreads();
-    for (int e = tid; e < ne; e += TH) table[e].y = cnt[e];
+    for (int e = tid; e < ne; e += TH) table[e] = make_uint2(col[e], cnt[e]);
     if (p.bias_max > 0)
         for (int k = tid; k < p.slots; k += TH)
             if (keys[k] != 0xffffffffu) p.tbias[t0 + keys[k]] = sums[k];
@@ -546,7 +564,7 @@ __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __
 // Words of shared memory of the list kernel.
 size_t list_bytes(const LogitArgs& a) {
     const int64_t words = (int64_t)a.part_runs * a.cols / 32;
-    return (size_t)(words + a.entries + 2 * a.slots) * 4 + (size_t)words * 2;
+    return (size_t)(words + a.entries + 2 * a.slots) * 4 + (size_t)(words + a.entries) * 2;
 }
 
 // The runs of columns and, for many columns in all, the tables.
@@ -555,7 +573,11 @@ bool plan_logits(LogitArgs& a, int es) {
     const int64_t list = a.hist_max + a.bias_max;
     a.listed = list > 0;
     const bool tables = list > 0 && a.N * a.V > kFusedColumns;
-    a.cols = list > 0 && !tables ? kFusedCols : kThreads * 8 * 16 / es;  // eight vectors a thread
+    // a run of eight vectors a thread; sixteen where that still fills the GPU's 912
+    // places six times over (4096 rows of 50257 columns 219 -> 204 us; 512 of
+    // 128000, 2.2 times, 83 -> 86 us)
+    a.cols = list > 0 && !tables ? kFusedCols : kThreads * 8 * 16 / es;
+    if (a.N * ((a.V + 2 * a.cols - 1) / (2 * a.cols)) >= 6 * 912 && a.cols != kFusedCols) a.cols *= 2;
     // few columns in all: shorter runs on more SMs
     while (a.cols > 1024 && a.N * ((a.V + a.cols - 1) / a.cols) < 304) a.cols /= 2;
     a.runs = (int)((a.V + a.cols - 1) / a.cols);
@@ -643,7 +665,8 @@ ce_status logits_common(const void* grad, const int64_t* grad_strides, const voi
     const int64_t N = dim0 * dim1;
     for (int k = 0; k < 2; ++k)
         if (q->reserved[k] != 0) return CE_ERR_INVALID_ARG;
-    if (q->history_max < 0 || q->bias_max < 0) return CE_ERR_INVALID_ARG;
+    if (q->history_max < 0 || q->bias_max < 0 || q->history_max > 0x40000000LL || q->bias_max > 0x40000000LL)
+        return CE_ERR_INVALID_ARG;
     if (N > 0) {
         if (!logits || !out || (bwd && !grad)) return CE_ERR_INVALID_ARG;
         const uintptr_t all = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(out) |
