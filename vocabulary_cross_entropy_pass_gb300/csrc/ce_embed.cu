@@ -91,7 +91,6 @@ constexpr int kSortWarps = 16;
 constexpr int kMaxDigitBits = 9;         // one bin per thread
 constexpr int kSortCluster = 8;
 constexpr int kOnChip = 8192;            // entries a CTA holds in shared memory, at most
-constexpr size_t kWsInvalidOffset = 16;  // uint32 tokens without a gradient
 
 struct SortArgs {
     const int64_t* tok;
@@ -102,7 +101,6 @@ struct SortArgs {
     int passes, bits;      // digits of `bits` bits, least first
     int on_chip;           // entries per CTA kept in shared memory between the digits, or 0: in a and b
     uint32_t* err;
-    uint32_t* invalid;
     uint2* a;              // (key, position): the sorted ones end here
     uint2* b;
     char* zero;            // the gradient to be zeroed, or NULL
@@ -151,7 +149,7 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
     }
     const int bins = 1 << p.bits;
     uint32_t* hist = sm;                          // [16][bins]: a warp's digit counts, then its next places
-    uint32_t* total = sm + kSortWarps * bins;     // [bins + 1]: this CTA's counts, and its tokens without a gradient
+    uint32_t* total = sm + kSortWarps * bins;     // [bins + 1]: this CTA's counts, and whether a token is out of range
     uint32_t* start = total + bins + 4;           // [bins]: where this CTA's entries of the digit go
     uint32_t* wsum = start + bins;                // [16]
     uint2* here = reinterpret_cast<uint2*>(wsum + 16);  // [2][on_chip]
@@ -163,7 +161,6 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
     const uint32_t i0 = (uint32_t)(from < p.N ? from : p.N);
     const uint32_t i1 = (uint32_t)(from + per < p.N ? from + per : p.N);
     const uint32_t mine0 = rank * kSortWarps * per;  // the CTA's first entry
-    // bits 0..: tokens without a gradient, top bit: one of them out of range
     if (tid == 0) total[bins] = 0u;
 
     for (int pass = 0; pass < p.passes; ++pass) {
@@ -181,7 +178,6 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
         __syncthreads();
         uint32_t* mine = hist + warp * bins;
         if (pass == 0) {
-            uint32_t none = 0;
             bool out = false;
             for (uint32_t base = i0; base < i1; base += 128) {
                 int64_t t[4];
@@ -196,7 +192,6 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
                     if (i < i1) {
                         const bool ok = t[u] >= 0 && t[u] < (int64_t)p.V && t[u] != p.ignore;
                         const uint32_t key = ok ? (uint32_t)t[u] : p.V;
-                        none += !ok;
                         out |= !ok && t[u] != p.ignore;
                         // what this thread sends on below
                         if (p.on_chip) chip[i - mine0] = make_uint2(key, i);
@@ -205,8 +200,7 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
                     }
                 }
             }
-            if (none) atomicAdd(&total[bins], none);
-            if (out) atomicOr(&total[bins], 0x80000000u);
+            if (out) total[bins] = 1u;
         } else {
             for (uint32_t i = i0 + lane; i < i1; i += 32) atomicAdd(&mine[(entry(i).x >> shift) & mask], 1u);
         }
@@ -236,15 +230,9 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
             }
         }
         if (pass == 0 && rank == 0 && tid < 32) {
-            uint32_t c = lane < (int)nc ? ld_dsmem_u32(total + bins, lane) : 0u;
-            const unsigned out = __ballot_sync(kFull, (c & 0x80000000u) != 0u);
-            c &= 0x7fffffffu;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(kFull, c, o);
-            if (lane == 0) {
-                *p.invalid = c;
-                *p.err = out ? CE_DEVERR_TARGET_RANGE : 0u;
-            }
+            const bool out = lane < (int)nc && ld_dsmem_u32(total + bins, lane) != 0u;
+            const bool any = __any_sync(kFull, out);
+            if (lane == 0) *p.err = any ? CE_DEVERR_TARGET_RANGE : 0u;
         }
         // exclusive scan of `all` over the bins
         uint32_t inc = all;
@@ -302,7 +290,6 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
 // ----------------------------------------------------------------- sums of runs
 struct GradArgs {
     const uint2* ent;      // sorted (token, position)
-    const uint32_t* invalid;
     uint32_t N, V;
     int64_t H;
     const char* g;
@@ -361,15 +348,19 @@ __global__ void __launch_bounds__(kGradThreads) ce_embed_grad_kernel(const __gri
     __shared__ uint2 ent[kMaxR + 2];  // the chunk's entries between its neighbours
     griddep_wait();
     griddep_launch_dependents();
-    const uint32_t n = p.N - *p.invalid;
+    // tokens without a gradient have key V and lie at the end: no chunk's run
+    // reaches into them
     const uint32_t c0 = blockIdx.x * (uint32_t)p.R;
-    if (c0 >= n) return;
-    const int len = (int)min((uint32_t)p.R, n - c0);
-    for (int i = threadIdx.x; i < len + 2; i += kGradThreads) {
-        const int64_t at = (int64_t)c0 + i - 1;
-        ent[i] = (at >= 0 && at < (int64_t)n) ? p.ent[at] : make_uint2(0xffffffffu, 0u);
+    int mine = 0;
+    if ((int)threadIdx.x < p.R + 2) {
+        const int64_t at = (int64_t)c0 + threadIdx.x - 1;
+        uint2 e = make_uint2(0xffffffffu, 0u);
+        if (at >= 0 && at < (int64_t)p.N) e = p.ent[at];
+        if (e.x >= p.V) e.x = 0xffffffffu;
+        ent[threadIdx.x] = e;
+        mine = threadIdx.x >= 1 && (int)threadIdx.x <= p.R && e.x != 0xffffffffu;
     }
-    __syncthreads();
+    const int len = __syncthreads_count(mine);
     if (!on) return;
     const char* g = p.g + col * ES;
     float acc[VEC];
@@ -410,12 +401,12 @@ __global__ void __launch_bounds__(kGradThreads) ce_embed_grad_kernel(const __gri
 template <typename TW, int VEC>
 __global__ void __launch_bounds__(kGradThreads) ce_embed_join_kernel(const __grid_constant__ GradArgs p) {
     griddep_wait();
-    const uint32_t n = p.N - *p.invalid;
+    const uint32_t n = p.N;
     const uint64_t c0 = (uint64_t)blockIdx.x * p.R, c1 = c0 + p.R;
     if (c1 >= n) return;                        // the last chunk's last run ends there
     const uint32_t key = p.ent[c1 - 1].x, over = p.ent[c1].x;
     const uint32_t at0 = p.ent[c0].x, prev = c0 > 0 ? p.ent[c0 - 1].x : 0xffffffffu;
-    if (over != key) return;                    // no run crosses this border
+    if (over != key || key >= p.V) return;      // no run crosses this border
     if (at0 == key && prev == key) return;      // it began in an earlier chunk
     // the last chunk that begins with the token, 32 chunks at a look
     const int lane = threadIdx.x & 31;
@@ -669,7 +660,6 @@ extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t 
     sa.bits = (bits + sa.passes - 1) / sa.passes;
     if (sa.bits < 2) sa.bits = 2;
     sa.err = reinterpret_cast<uint32_t*>(base + kWsErrOffset);
-    sa.invalid = reinterpret_cast<uint32_t*>(base + kWsInvalidOffset);
     uint2* a = reinterpret_cast<uint2*>(base + w.a);
     sa.a = a;
     sa.b = reinterpret_cast<uint2*>(base + w.b);
@@ -690,7 +680,6 @@ extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t 
 
     GradArgs ga;
     ga.ent = a;
-    ga.invalid = sa.invalid;
     ga.N = sa.N;
     ga.V = sa.V;
     ga.H = H;
