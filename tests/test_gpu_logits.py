@@ -341,7 +341,7 @@ def test_policy_log_probabilities():
     ref, _, _ = reference(x, p)
     ref = torch.where(allowed, ref, -3e4).requires_grad_()
     want = torch.nn.functional.cross_entropy(ref, t, reduction="none")
-    assert float((loss[0].detach().double().cpu() - want).abs().max()) <= 1e-4
+    assert float((loss[0].detach().double().cpu() - want.detach()).abs().max()) <= 1e-4
     want.sum().backward()
     gref, _, _ = reference(x, p, go=ref.grad)
     gref = torch.where(allowed, gref, 0.0)

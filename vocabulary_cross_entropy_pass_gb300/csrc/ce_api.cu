@@ -23,6 +23,14 @@ namespace gbce {
 
 int elem_size(int dtype) { return dtype == CE_F32 ? 4 : 2; }
 
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+    if (bytes <= 16 * 1024) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess || bytes <= 40 * 1024) return e;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 namespace {
 
 constexpr int kMaxCluster = 16;

@@ -158,6 +158,10 @@ struct VpCombineProblem {
 };
 
 int elem_size(int dtype);
+// A kernel's dynamic shared memory past the default limit, from an SM configured
+// for as much as there is: by its own choice the driver may leave room for fewer
+// CTAs than fit (five row sets of 20 KB: one CTA per SM in place of two).
+cudaError_t allow_smem(const void* kernel, size_t bytes);
 bool fused_aligned(const Problem& p);
 int fused_capacity(int dtype, int threads);  // elements one CTA can hold
 int split_auto_chunks(int64_t V);

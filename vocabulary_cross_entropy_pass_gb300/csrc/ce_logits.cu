@@ -599,10 +599,7 @@ bool plan_logits(LogitArgs& a, int es) {
 template <typename T, bool BWD>
 cudaError_t launch_logits_t(const LogitArgs& a, cudaStream_t s) {
     cudaError_t e;
-    auto allow = [](auto* k, size_t smem) {
-        return smem > 40 * 1024 ? cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)
-                                : cudaSuccess;
-    };
+    auto allow = [](auto* k, size_t smem) { return allow_smem(reinterpret_cast<const void*>(k), smem); };
     const int64_t rows = a.N < 65535 ? a.N : 65535;
     const unsigned deep = (unsigned)((a.N + rows - 1) / rows);
     cudaLaunchAttribute at[1];

@@ -547,25 +547,27 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_consta
         }
         int ph[3] = {0, 0, 0};
         if (!GRID) {
-            // the elements that no copy could take (the tensor's first and last row)
-            bool some = false;
+            // rows within 16 bytes of a tensor's ends may have elements that no copy
+            // could take
+            bool ends = false;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const RowSpan<ES> s = span_of(t, row);
-                ph[t] = s.phase;
-                // elements before the copy, and the first one after it
-                const int64_t head = min(p.H, s.at > s.phase ? (int64_t)((s.at - s.phase) / ES) : (int64_t)0);
-                const int64_t tail0 = s.bytes ? ((int64_t)s.at + s.bytes - s.phase) / ES : head;
-                const char* a = base_of(t) + row * stride_of(t);
-                T* to = reinterpret_cast<T*>(ring + (size_t)stage * NT * q.slot + t * q.slot + s.phase);
-                const bool part = head > 0 || tail0 < p.H;
-                some |= part;
-                if (part) {
-                    for (int64_t c = tid; c < head; c += TH) to[c] = reinterpret_cast<const T*>(a)[c];
-                    for (int64_t c = tail0 + tid; c < p.H; c += TH) to[c] = reinterpret_cast<const T*>(a)[c];
-                }
+                const int64_t off = row * stride_of(t);
+                ends |= off < 16 || (p.N - 1 - row) * stride_of(t) < 16;
+                ph[t] = (int)((reinterpret_cast<uintptr_t>(base_of(t)) + (uintptr_t)off) & 15u);
             }
-            if (some) {
+            if (ends) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const RowSpan<ES> s = span_of(t, row);
+                    // elements before the copy, and the first one after it
+                    const int64_t head = min(p.H, s.at > s.phase ? (int64_t)((s.at - s.phase) / ES) : (int64_t)0);
+                    const int64_t tail0 = s.bytes ? ((int64_t)s.at + s.bytes - s.phase) / ES : head;
+                    const T* a = reinterpret_cast<const T*>(base_of(t) + row * stride_of(t));
+                    T* to = reinterpret_cast<T*>(ring + (size_t)stage * NT * q.slot + t * q.slot + s.phase);
+                    for (int64_t c = tid; c < head; c += TH) to[c] = a[c];
+                    for (int64_t c = tail0 + tid; c < p.H; c += TH) to[c] = a[c];
+                }
                 fence_proxy_async_smem();  // a later copy may land on these bytes
                 __syncthreads();
             }
@@ -744,8 +746,11 @@ __global__ void __launch_bounds__(1024) ce_rmsnorm_dw_kernel(const float* part, 
 }
 
 // CTAs of the backward grid, from the sizes alone (the workspace holds a
-// partial row for each): two per SM, more for short rows.
-int bwd_per_sm(int64_t H) { return H >= 2048 ? 2 : (H >= 1024 ? 4 : 8); }
+// partial row for each): two per SM, more for short rows, whose barrier each is
+// paid over fewer bytes (bf16, 32768 rows, GB/s of algorithmic bytes with two /
+// four / eight per SM: 2048 wide 5290 / 5840, 1024 wide with four / eight 4820 /
+// 5330; 4096 wide with two / three 6000 / 5840).
+int bwd_per_sm(int64_t H) { return H >= 4096 ? 2 : (H >= 2048 ? 4 : (H >= 1024 ? 8 : 16)); }
 int bwd_grid(int64_t N, int64_t H) {
     const int64_t most = 152 * bwd_per_sm(H);
     return (int)(N < most ? N : most);
@@ -754,10 +759,7 @@ int bwd_grid(int64_t N, int64_t H) {
 template <typename T, int MODE, int VPT>
 cudaError_t launch_ring(RingArgs& q, int threads, size_t smem, cudaStream_t s) {
     auto* k = q.n.dh ? ce_rmsnorm_bwd_kernel<T, VPT, MODE, true> : ce_rmsnorm_bwd_kernel<T, VPT, MODE, false>;
-    if (smem > 40 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem); e != cudaSuccess) return e;
     k<<<bwd_grid(q.n.N, q.n.H), threads, smem, s>>>(q);
     return cudaGetLastError();
 }
@@ -783,7 +785,7 @@ cudaError_t launch_bwd_m(const NormBwdArgs& a, uint32_t* err, bool* shifted, cud
         const size_t smem = (size_t)q.stages * set;
         const auto th = [&](int v) { return (int)((nv + 32 * v - 1) / (32 * v) * 32); };
         if (nv <= 256 * M) return launch_ring<T, MODE, M>(q, th(M), smem, s);
-        if (nv <= 512 * M) return launch_ring<T, MODE, 2 * M>(q, th(2 * M), smem, s);
+        if (nv <= 1024 * M) return launch_ring<T, MODE, 2 * M>(q, th(2 * M), smem, s);
         return launch_ring<T, MODE, 4 * M>(q, th(4 * M), smem, s);
     }
     constexpr int WV = MODE == kOnGrid ? VEC : 1;
