@@ -25,6 +25,7 @@
 #include "ce_device.cuh"
 #include "ce_internal.h"
 #include "ce_pack.cuh"
+#include "ce_span.cuh"
 
 namespace gbce {
 namespace {
@@ -36,8 +37,7 @@ struct EmbedFwdArgs {
     const char* w;
     char* out;
     int64_t ws, os;        // row strides in bytes
-    int64_t V, ignore;
-    int nv;                // vectors per row
+    int64_t V, H, ignore;
     float scale;
     uint32_t* err;         // or NULL
 };
@@ -49,39 +49,71 @@ __device__ __forceinline__ int64_t token_at(const int64_t* tok, int64_t dim1, in
     return __ldg(tok + a * ts0 + (i - a * dim1) * ts1);
 }
 
-// One CTA per token and slab of 128 * U vectors.
-template <typename T, int VEC, int U>
+// One CTA (128 threads) or, for rows of at most 128 vectors, one warp per token
+// and slab of U vectors of 16 bytes a thread.  SHIFT: rows off
+// the 16-byte grid (odd widths, views): the output's vectors, each cut out of
+// the two vectors of the matrix's row that hold it, the elements around them one
+// per thread.
+template <typename T, int U, bool SHIFT>
 __global__ void __launch_bounds__(128) ce_embed_fwd_kernel(const __grid_constant__ EmbedFwdArgs p) {
     constexpr int ES = sizeof(T);
-    const int64_t row = blockIdx.x;
-    const int v0 = blockIdx.y * (128 * U) + threadIdx.x;
+    constexpr int VEC = 16 / ES;
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (row >= p.N) return;
+    const int TX = blockDim.x;
+    const int v0 = blockIdx.y * (TX * U) + threadIdx.x;
     const int64_t t = token_at(p.tok, p.dim1, p.ts0, p.ts1, p.flat, row);
     char* out = p.out + row * p.os;
     const bool in = t >= 0 && t < p.V && t != p.ignore;
-    if (!in) {
-        const float fill = t == p.ignore ? 0.f : __int_as_float(0x7fc00000);
-        Pack<T, VEC> o;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) o.set(i, fill);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v0 + u * 128 < p.nv) o.store(out + (int64_t)(v0 + u * 128) * VEC * ES);
-        if (t != p.ignore && p.err && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.err, CE_DEVERR_TARGET_RANGE);
-        return;
+    const float fill = t == p.ignore ? 0.f : __int_as_float(0x7fc00000);
+    if (!in && t != p.ignore && p.err && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(p.err, CE_DEVERR_TARGET_RANGE);
+    const char* src = p.w + (in ? t : 0) * p.ws;
+    int nv = (int)(p.H / VEC);
+    int safe0 = 0, safe1 = nv;
+    uint32_t ph = 0;
+    if (SHIFT) {
+        const Span16 sp = span16<ES>(out, 0, p.H);
+        nv = (int)sp.nv;
+        const int64_t e = span16_edge(sp, 0, p.H, threadIdx.x);
+        if (e >= 0 && blockIdx.y == 0) {
+            T o;
+            from_f32(o, in ? to_f32(reinterpret_cast<const T*>(src)[e]) * p.scale : fill);
+            reinterpret_cast<T*>(out)[e] = o;
+        }
+        const int64_t at = sp.h1 * ES;
+        out += at;
+        ph = (uint32_t)(reinterpret_cast<uintptr_t>(src + at) & 15u);
+        src += at - ph;
+        // a shifted vector's two lie inside the row: not before its first element,
+        // not past its last
+        safe0 = at < (int64_t)ph ? 1 : 0;
+        const int64_t room = (p.H * ES - at + ph) / 16 - (ph ? 1 : 0);
+        safe1 = (int)(room < nv ? room : nv);
     }
-    const char* src = p.w + t * p.ws;
     Pack<T, VEC> a[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (v0 + u * 128 < p.nv) a[u].load_nc(src + (int64_t)(v0 + u * 128) * VEC * ES);
+    for (int u = 0; u < U; ++u) {
+        const int v = v0 + u * TX;
+        if (!in || v >= nv) continue;
+        const uint4* q = reinterpret_cast<const uint4*>(src) + v;
+        if (!SHIFT || (ph == 0u && v < safe1)) {
+            a[u].raw = __ldg(q);
+        } else if (v >= safe0 && v < safe1) {
+            a[u].raw = shift_bytes(__ldg(q), __ldg(q + 1), ph);
+        } else {
+            const T* x = reinterpret_cast<const T*>(src + ph) + (int64_t)v * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) a[u].v[i] = x[i];
+        }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (v0 + u * 128 < p.nv) {
-            Pack<T, VEC> o;
+        const int v = v0 + u * TX;
+        if (v >= nv) continue;
+        Pack<T, VEC> o;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o.set(i, a[u].f(i) * p.scale);
-            o.store(out + (int64_t)(v0 + u * 128) * VEC * ES);
-        }
+        for (int i = 0; i < VEC; ++i) o.set(i, in ? a[u].f(i) * p.scale : fill);
+        o.store(out + (int64_t)v * 16);
     }
 }
 
@@ -469,26 +501,21 @@ int64_t count_of(int64_t d0, int64_t d1) {
 }
 bool tokens_flat(int64_t d0, int64_t d1, const int64_t* ts) { return d0 == 1 || ts[0] == d1 * ts[1]; }
 
-template <typename T, int VEC>
-cudaError_t launch_fwd(EmbedFwdArgs& a, int64_t H, cudaStream_t s) {
-    a.nv = (int)(H / VEC);
+template <typename T, bool SHIFT>
+cudaError_t launch_fwd(const EmbedFwdArgs& a, cudaStream_t s) {
+    const int64_t nv = (a.H * (int64_t)sizeof(T) + 15) / 16;
     // few tokens: a vector a thread over more CTAs
-    if (a.N * ((a.nv + 511) / 512) < 1024) {
-        const dim3 grid((unsigned)a.N, (unsigned)((a.nv + 127) / 128));
-        ce_embed_fwd_kernel<T, VEC, 1><<<grid, 128, 0, s>>>(a);
-    } else {
-        const dim3 grid((unsigned)a.N, (unsigned)((a.nv + 511) / 512));
-        ce_embed_fwd_kernel<T, VEC, 4><<<grid, 128, 0, s>>>(a);
-    }
+    if (a.N * ((nv + 511) / 512) < 1024)
+        ce_embed_fwd_kernel<T, 1, SHIFT><<<dim3((unsigned)a.N, (unsigned)((nv + 127) / 128)), 128, 0, s>>>(a);
+    else if (nv <= 128)
+        ce_embed_fwd_kernel<T, 4, SHIFT><<<(unsigned)((a.N + 3) / 4), dim3(32, 4), 0, s>>>(a);
+    else
+        ce_embed_fwd_kernel<T, 4, SHIFT><<<dim3((unsigned)a.N, (unsigned)((nv + 511) / 512)), 128, 0, s>>>(a);
     return cudaGetLastError();
 }
 template <typename T>
-cudaError_t launch_fwd_t(EmbedFwdArgs& a, int64_t H, int vb, cudaStream_t s) {
-    constexpr int ES = sizeof(T);
-    if (vb == 16) return launch_fwd<T, 16 / ES>(a, H, s);
-    if constexpr (ES == 2)
-        if (vb == 4) return launch_fwd<T, 2>(a, H, s);
-    return launch_fwd<T, 1>(a, H, s);
+cudaError_t launch_fwd_t(const EmbedFwdArgs& a, int vb, cudaStream_t s) {
+    return vb == 16 ? launch_fwd<T, false>(a, s) : launch_fwd<T, true>(a, s);
 }
 
 // A kernel that may start while the one before it ends.
@@ -606,14 +633,15 @@ extern "C" ce_status ce_embed_fwd(const int64_t* tokens, int64_t dim0, int64_t d
     a.ws = weight_stride * es;
     a.os = out_stride * es;
     a.V = V;
+    a.H = H;
     a.ignore = ignore_idx;
     a.scale = scale;
     const uint64_t vals[] = {(uint64_t)(uintptr_t)weight, (uint64_t)(uintptr_t)out, (uint64_t)(V > 1 ? a.ws : 0),
                              (uint64_t)(N > 1 ? a.os : 0), (uint64_t)H * es};
     const int vb = common_vector_bytes(vals, 5, es);
-    cudaError_t e = dtype == CE_F32    ? launch_fwd_t<float>(a, H, vb, s)
-                    : dtype == CE_BF16 ? launch_fwd_t<__nv_bfloat16>(a, H, vb, s)
-                                       : launch_fwd_t<__half>(a, H, vb, s);
+    cudaError_t e = dtype == CE_F32    ? launch_fwd_t<float>(a, vb, s)
+                    : dtype == CE_BF16 ? launch_fwd_t<__nv_bfloat16>(a, vb, s)
+                                       : launch_fwd_t<__half>(a, vb, s);
     return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
 }
 
