@@ -124,6 +124,23 @@ def test_rows_of_zeros(dtype):
     assert bool((gw == 0).all())
 
 
+@pytest.mark.parametrize("quant", [torch.float8_e4m3fn, torch.float8_e5m2])
+@pytest.mark.parametrize("H", [256, 259])
+def test_8_bits_of_the_smallest_values(H, quant):
+    # scales at and just above their least value: y of about 2^-126 times 448 and below
+    x, _, w = make(4, H, torch.float32, 9, residual=False)
+    x = (x.double() * torch.tensor([2.0 ** -118, 2.0 ** -124, 2.0 ** -128, 2.0 ** -112])[:, None]).float()
+    for group in (0, 32, 128):
+        y, _, s = pkg.ce_rmsnorm_fwd(d(x), d(w), eps=1.0, quant=quant, group_size=group)
+        top, rel, sub = FP8[quant]
+        _, yr = ref_fwd(x, None, w, 1.0)
+        full = s.double().cpu()[:, torch.arange(H) // (group or H)]
+        assert bool((s >= 2.0 ** -126).all())
+        # products below 2^-126 may be flushed or rounded by half the smallest float
+        bound = yr.abs() * (rel + 2 * F) + full * sub * (1 + F) + 2.0 ** -126 * 2.0 ** -20
+        assert bool(((y.float().double().cpu() * full - yr).abs() <= bound).all())
+
+
 def test_infinities_stay_in_their_row():
     x, r, w = make(4, 512, torch.float32, 3)
     x[1, 7] = float("inf")

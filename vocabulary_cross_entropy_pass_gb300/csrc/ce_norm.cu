@@ -197,8 +197,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
             } else {
                 load_w<T, VEC>(p, (int64_t)v * VEC, w);
             }
+            // 8 bits: y / rstd, and rstd goes into each group's factor
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) h[k][i] *= rstd * w[i];
+            for (int i = 0; i < VEC; ++i) h[k][i] *= Q8 ? w[i] : rstd * w[i];
         }
     }
     char* y = p.y + row * p.ys;
@@ -215,12 +216,23 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
             if (tid + k * TH >= nv) am[k] = 0.f;
         }
         float* sc = p.scales + row * (int64_t)p.groups;
+        // a group's scale from its largest |y / rstd|, and what y / rstd times gives q
+        // (the approximate reciprocal, off by 2^-23 of a value then rounded to 2^-4)
+        const float to_scale = rstd / p.top;
+        auto scale_of = [&](float m) { return fmaxf(m * to_scale, kTinyScale); };
+        auto factor_of = [&](float scale, float* v, int n) {
+            const float inv = __fdividef(1.f, scale), f = rstd * inv;
+            if (f <= 3.4e38f) return f;
+#pragma unroll
+            for (int i = 0; i < n; ++i) v[i] *= rstd;  // a scale near the least: in two steps
+            return inv;
+        };
         float whole = 0.f;  // the scale of all columns, where there is one
         if (p.groups == 1) {
             float m = 0.f;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) m = fmaxf(m, am[k]);
-            whole = fmaxf(cta_max(m, red + 32) / p.top, kTinyScale);
+            whole = scale_of(cta_max(m, red + 32));
             if (tid == 0) sc[0] = whole;
         }
         if constexpr (STAGED) {
@@ -249,10 +261,10 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
                 }
                 float s = whole;
                 if (p.groups > 1) {
-                    s = fmaxf(warp_allmax(m) / p.top, kTinyScale);
+                    s = scale_of(warp_allmax(m));
                     if (lane == 0) sc[g] = s;
                 }
-                const float inv = 1.f / s;
+                const float inv = factor_of(s, f, 4);
                 if (four && c0 + 4 <= p.H) {
                     store_q8<4>(y + c0, f, inv, p.kind);
                 } else {
@@ -268,12 +280,15 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
                 const int v = tid + k * TH;
                 if (p.groups > 1) {
                     for (int o = gl >> 1; o > 0; o >>= 1) am[k] = fmaxf(am[k], __shfl_xor_sync(kFull, am[k], o));
-                    am[k] = fmaxf(am[k] / p.top, kTinyScale);
-                    if (v < nv && v % gl == 0) sc[v / gl] = am[k];
+                    am[k] = scale_of(am[k]);
+                    if (v < nv && (v & (gl - 1)) == 0) sc[v / gl] = am[k];
                 } else {
                     am[k] = whole;
                 }
-                if (v < nv) store_q8<VEC>(y + (int64_t)v * VEC, h[k], 1.f / am[k], p.kind);
+                if (v < nv) {
+                    const float f = factor_of(am[k], h[k], VEC);
+                    store_q8<VEC>(y + (int64_t)v * VEC, h[k], f, p.kind);
+                }
             }
         }
     }
