@@ -568,14 +568,17 @@ size_t list_bytes(const LogitArgs& a) {
 }
 
 // The runs of columns and, for many columns in all, the tables.
-constexpr int64_t kFusedColumns = 1 << 20;
+// Up to 2^21 columns the CTAs read the lists themselves: 16 rows of 128000 under a
+// mask with histories of 1000 / 8000 tokens 6.8 / 11.8 us against 10.3 / 14.1
+// with tables; 30 rows 10.9 / 19.2 against 11.2 / 15.9.
+constexpr int64_t kFusedColumns = 1 << 21;
 bool plan_logits(LogitArgs& a, int es) {
     const int64_t list = a.hist_max + a.bias_max;
     a.listed = list > 0;
     const bool tables = list > 0 && a.N * a.V > kFusedColumns;
-    // a run of eight vectors a thread; sixteen where that still fills the GPU's 912
-    // places six times over (4096 rows of 50257 columns 219 -> 204 us; 512 of
-    // 128000, 2.2 times, 83 -> 86 us)
+    // a run of eight vectors a thread; sixteen where that still fills the GPU's
+    // places several times over (gradient of 4096 rows of 50257 columns 182 ->
+    // 179 us; 512 rows of 128000, twice, 77 -> 81 us)
     a.cols = list > 0 && !tables ? kFusedCols : kThreads * 8 * 16 / es;
     if (a.N * ((a.V + 2 * a.cols - 1) / (2 * a.cols)) >= 6 * 912 && a.cols != kFusedCols) a.cols *= 2;
     // few columns in all: shorter runs on more SMs
