@@ -15,7 +15,11 @@
 //
 // Bound by HBM: forward reads x, r and writes h, y; backward reads h, g, dh and
 // writes dx.  A row's elements stay in registers between the statistics and
-// the output.
+// the output.  Measured, of the GPU's 6.70 TB/s copy rate (bf16, GPU time of a call in
+// a graph): forward of 16384 x 4096 with a residual 80.4 us, 6.68 TB/s; to e4m3 with a
+// scale for 128 columns, 8192 x 8192, 81.4 us, 5.8 TB/s (its conversions keep the
+// schedulers at 76 %); gradients of 16384 x 4096 88 us, 6.1 TB/s.  Rows off the
+// 16-byte grid run at about half that.
 #include <cuda_fp8.h>
 
 #include "ce_device.cuh"
