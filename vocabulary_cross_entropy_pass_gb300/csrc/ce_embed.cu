@@ -197,7 +197,10 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
     const uint64_t from = (uint64_t)(rank * kSortWarps + warp) * per;
     const uint32_t i0 = (uint32_t)(from < p.N ? from : p.N);
     const uint32_t i1 = (uint32_t)(from + per < p.N ? from + per : p.N);
-    const uint32_t mine0 = rank * kSortWarps * per;  // the CTA's first entry
+    const uint32_t per_cta = kSortWarps * per, mine0 = rank * per_cta;  // its entries, the first one
+    // at / per_cta is the upper half of at times this: exact while at times the
+    // rounding (below per_cta) is below 2^32, and on chip both are at most 2^16
+    const uint32_t per_cta_inv = per_cta ? 0xffffffffu / per_cta + 1u : 0u;
     if (tid == 0) total[bins] = 0u;
 
     for (int pass = 0; pass < p.passes; ++pass) {
@@ -297,9 +300,11 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
             const bool on = i < i1;
             const uint2 e = on ? entry(i) : make_uint2(0u, 0u);
             const uint32_t d = (e.x >> shift) & mask;
-            // the lanes with the same digit, a bit of it at a time
+            // the lanes with the same digit, a bit of it at a time (bits past the
+            // digit's are zero everywhere)
             unsigned peers = __ballot_sync(kFull, on);
-            for (int k = 0; k < p.bits; ++k) {
+#pragma unroll
+            for (int k = 0; k < kMaxDigitBits; ++k) {
                 const unsigned one = __ballot_sync(kFull, (d >> k) & 1u);
                 peers &= (d >> k) & 1u ? one : ~one;
             }
@@ -312,8 +317,8 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
                 if (last || !p.on_chip) {
                     dst[at] = e;
                 } else {
-                    const uint32_t to = at / (kSortWarps * per);
-                    st_dsmem_u2(next + (at - to * kSortWarps * per), to, e);
+                    const uint32_t to = __umulhi(at, per_cta_inv);
+                    st_dsmem_u2(next + (at - to * per_cta), to, e);
                 }
             }
         }
