@@ -149,9 +149,32 @@ def test_backward(N, V, H, dtype):
     run_bwd(N, V, H, dtype, t, scale=float(torch.tensor(1.3)))
 
 
-@pytest.mark.parametrize("N", [15, 16, 17, 255, 1024, 5000, 9000])
+@pytest.mark.parametrize("N", [15, 16, 17, 255, 1024, 1025, 5000, 9000])
 def test_backward_one_token_takes_all(N):
     run_bwd(N, 77, 40, torch.bfloat16, torch.full((N,), 76))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,H", [(2, 256), (9, 257), (128, 4096), (129, 4096), (1000, 300), (1024, 512), (1023, 513)])
+def test_backward_on_both_sides_of_few_tokens(N, H, dtype):
+    # a kernel of its own below, the sort above; values seen once, often, and never
+    V = 3 * N + 5
+    g = rng(N + H)
+    t = torch.randint(0, V, (N,), generator=g)
+    t[torch.rand(N, generator=g) < 0.3] = V - 1
+    run_bwd(N, V, H, dtype, t, scale=2.0)
+
+
+def test_backward_few_tokens_strides_and_strangers():
+    g = rng(17)
+    go = torch.randn(6, 10, 40, generator=g).to(torch.bfloat16)
+    t = torch.randint(0, 9000, (6, 10), generator=g)
+    t[1, 1], t[2, 3], t[5, 9] = -100, 9000, -7
+    ws = torch.empty(pkg.ce_embed_bwd_workspace_bytes(60, 33, 9000), dtype=torch.uint8, device=DEV)
+    wide, td = go.to(DEV), t.t().contiguous().to(DEV).t()
+    got = pkg.ce_embed_bwd(wide[:, :, 2:35], td, 9000, workspace=ws)
+    check_bwd(got, go[:, :, 2:35], t, 9000, 1.0)
+    assert pkg.ce_get_error(ws) == (6, 1)
 
 
 @pytest.mark.parametrize("N,V", [(3000, 3000), (9000, 9001)])

@@ -24,6 +24,9 @@
 //      a chunk border leaves its float32 part in the workspace.
 //   3. ce_embed_join_kernel: the parts of tokens that cross chunk borders,
 //      added in chunk order.
+// Few tokens (those launches' latencies would be most of the time): one kernel in
+// which each token's CTA looks through all tokens, the first of each value sums
+// its rows in order, and further CTAs zero the rows of tokens that do not occur.
 // 16384 tokens of 4096 bf16 added to a 128000-row float32 gradient: 12.5 us of
 // sorting, 61 us of sums (360 MB, 0.88 of the copy rate), 10 us of joining (the most
 // frequent token's 29 parts), 88 us together.
@@ -156,22 +159,19 @@ __device__ __forceinline__ void st_dsmem_u2(uint2* local, uint32_t rank, uint2 v
     asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(remote), "r"(v.x), "r"(v.y) : "memory");
 }
 
-// Zero rows r0, r0 + step, ...: 16-byte vectors between a head and a tail of
-// two-byte pieces (a warp per row).
-__device__ __forceinline__ void zero_rows(const SortArgs& p, int64_t r0, int64_t step) {
+// Zero one row (a warp): 16-byte vectors between a head and a tail of two-byte
+// pieces.
+__device__ __forceinline__ void zero_row(char* row, int64_t bytes) {
     const int lane = threadIdx.x & 31;
-    for (int64_t r = r0; r < p.zrows; r += step) {
-        char* row = p.zero + r * p.zstride;
-        int64_t head = (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u);
-        if (head > p.zbytes) head = p.zbytes;
-        const int64_t nv = (p.zbytes - head) / 16;
-        uint4* body = reinterpret_cast<uint4*>(row + head);
+    int64_t head = (int64_t)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u);
+    if (head > bytes) head = bytes;
+    const int64_t nv = (bytes - head) / 16;
+    uint4* body = reinterpret_cast<uint4*>(row + head);
 #pragma unroll 4
-        for (int64_t v = lane; v < nv; v += 32) __stcs(body + v, make_uint4(0, 0, 0, 0));
-        const int64_t t0 = head + nv * 16;  // lanes 0..7 the head, 8..15 the tail
-        const int64_t at = lane < 8 ? lane * 2 : t0 + (lane - 8) * 2;
-        if (lane < 8 ? at < head : (lane < 16 && at < p.zbytes)) *reinterpret_cast<uint16_t*>(row + at) = 0;
-    }
+    for (int64_t v = lane; v < nv; v += 32) __stcs(body + v, make_uint4(0, 0, 0, 0));
+    const int64_t t0 = head + nv * 16;  // lanes 0..7 the head, 8..15 the tail
+    const int64_t at = lane < 8 ? lane * 2 : t0 + (lane - 8) * 2;
+    if (lane < 8 ? at < head : (lane < 16 && at < bytes)) *reinterpret_cast<uint16_t*>(row + at) = 0;
 }
 
 __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __grid_constant__ SortArgs p) {
@@ -180,8 +180,9 @@ __global__ void __launch_bounds__(kSortThreads) ce_embed_sort_kernel(const __gri
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_ctarank(), nc = cluster_nctarank();
     if (cluster_id_x() > 0) {
-        const int64_t w = ((int64_t)blockIdx.x - nc) * kSortWarps + warp;
-        zero_rows(p, w, ((int64_t)gridDim.x - nc) * kSortWarps);
+        const int64_t step = ((int64_t)gridDim.x - nc) * kSortWarps;
+        for (int64_t r = ((int64_t)blockIdx.x - nc) * kSortWarps + warp; r < p.zrows; r += step)
+            zero_row(p.zero + r * p.zstride, p.zbytes);
         return;
     }
     const int bins = 1 << p.bits;
@@ -480,9 +481,146 @@ __global__ void __launch_bounds__(kGradThreads) ce_embed_join_kernel(const __gri
     write_row<TW, VEC>(p.dw + (int64_t)key * p.dws, col, acc, p.scale, p.accumulate);
 }
 
+// ----------------------------------------------------------------- few tokens
+constexpr int kFewThreads = 256;
+constexpr int kFewTokens = 1024;         // at most
+constexpr int kFewCols = 256;            // columns of a CTA
+constexpr int kZeroRows = 4096;          // rows of a CTA that zeroes, at most
+
+struct FewArgs {
+    const int64_t* tok;
+    int64_t dim1, ts0, ts1;
+    int flat;
+    int N;
+    int64_t V, H, ignore;
+    const char* g;
+    int64_t gs;            // in bytes
+    char* dw;
+    int64_t dws, row_bytes;
+    uint32_t* err;
+    int zero_rows;         // rows of each zeroing CTA (blockIdx.x >= N)
+    int accumulate;
+    float scale;
+};
+
+// A CTA per token and 256 columns.  All but the first CTA of a value leave; it
+// lists the value's places in order, its eight warps take every eighth of
+// those rows, and the warps' sums are added in order.
+template <typename T, typename TW, int VEC>
+__global__ void __launch_bounds__(kFewThreads) ce_embed_few_kernel(const __grid_constant__ FewArgs p) {
+    constexpr int ES = sizeof(T);
+    constexpr int NW = kFewThreads / 32;
+    constexpr int NV = 8 / VEC;            // vectors of a lane: eight columns
+    constexpr int U = 4;
+    constexpr int IT = kFewTokens / kFewThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto token = [&](int k) { return token_at(p.tok, p.dim1, p.ts0, p.ts1, p.flat, k); };
+    if ((int)blockIdx.x >= p.N) {
+        if (blockIdx.y > 0) return;
+        __shared__ uint32_t used[kZeroRows / 32];
+        const int64_t r0 = (int64_t)(blockIdx.x - p.N) * p.zero_rows, r1 = min(p.V, r0 + p.zero_rows);
+        for (int k = tid; k < kZeroRows / 32; k += kFewThreads) used[k] = 0u;
+        __syncthreads();
+        for (int k = tid; k < p.N; k += kFewThreads) {
+            const int64_t t = token(k);
+            if (t >= r0 && t < r1 && t != p.ignore) atomicOr(&used[(t - r0) >> 5], 1u << ((t - r0) & 31));
+        }
+        __syncthreads();
+        for (int64_t r = r0 + warp; r < r1; r += NW)
+            if (!((used[(r - r0) >> 5] >> ((r - r0) & 31)) & 1u)) zero_row(p.dw + r * p.dws, p.row_bytes);
+        return;
+    }
+    __shared__ uint16_t place[kFewTokens];
+    __shared__ int count[IT * NW];
+    __shared__ float sums[NW][kFewCols];
+    const int i = blockIdx.x;
+    const int64_t mine = token(i);
+    int64_t t[IT];
+#pragma unroll
+    for (int q = 0; q < IT; ++q) {
+        const int k = q * kFewThreads + tid;
+        t[q] = k < p.N ? token(k) : p.ignore;
+    }
+    if (i == 0 && blockIdx.y == 0) {
+        bool out = false;
+#pragma unroll
+        for (int q = 0; q < IT; ++q) out |= t[q] != p.ignore && (t[q] < 0 || t[q] >= p.V);
+        const int any = __syncthreads_or(out);
+        if (tid == 0) *p.err = any ? CE_DEVERR_TARGET_RANGE : 0u;
+    }
+    if (mine == p.ignore || mine < 0 || mine >= p.V) return;
+    bool earlier = false;
+    unsigned same[IT];
+#pragma unroll
+    for (int q = 0; q < IT; ++q) {
+        const bool s = q * kFewThreads + tid < p.N && t[q] == mine;
+        earlier |= s && q * kFewThreads + tid < i;
+        same[q] = __ballot_sync(kFull, s);
+        if (lane == 0) count[q * NW + warp] = __popc(same[q]);
+    }
+    if (__syncthreads_or(earlier)) return;
+    // the value's places in order: token k is in row k / 256 of the loop, then by warp
+    int before = 0, m = 0;
+#pragma unroll
+    for (int q = 0; q < IT; ++q) {
+        for (int w = 0; w < NW; ++w) {
+            if (w == warp) before = m;
+            m += count[q * NW + w];
+        }
+        if ((same[q] >> lane) & 1u)
+            place[before + __popc(same[q] & ((1u << lane) - 1u))] = (uint16_t)(q * kFewThreads + tid);
+    }
+    __syncthreads();
+    float acc[NV][VEC];
+#pragma unroll
+    for (int e = 0; e < NV; ++e)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[e][k] = 0.f;
+    const int64_t c0 = (int64_t)blockIdx.y * kFewCols;
+    for (int j = warp; j < m; j += NW * U) {
+        Pack<T, VEC> x[U][NV];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (j + u * NW < m) {
+                const char* row = p.g + (int64_t)place[j + u * NW] * p.gs;
+#pragma unroll
+                for (int e = 0; e < NV; ++e) {
+                    const int64_t c = c0 + (e * 32 + lane) * VEC;
+                    x[u][e].zero();
+                    if (c < p.H) x[u][e].load_cs(row + c * ES);
+                }
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (j + u * NW < m)
+#pragma unroll
+                for (int e = 0; e < NV; ++e)
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) acc[e][k] += x[u][e].f(k);
+    }
+    const int warps = m < NW ? m : NW;     // warps that have a sum
+    if (warp < warps) {
+#pragma unroll
+        for (int e = 0; e < NV; ++e) store_f32<VEC>(&sums[warp][(e * 32 + lane) * VEC], acc[e]);
+    }
+    __syncthreads();
+    if (c0 + tid < p.H) {
+        float f = sums[0][tid];
+        for (int w = 1; w < warps; ++w) f += sums[w][tid];
+        write_row<TW, 1>(p.dw + mine * p.dws, c0 + tid, &f, p.scale, p.accumulate);
+    }
+}
+
 // entries per chunk, from the sizes alone (the workspace holds two float32
 // rows for each chunk)
 int chunk_entries(int64_t N) { return N >= 8192 ? 32 : (N >= 1024 ? 16 : 8); }
+
+// Whether one kernel takes all (every CTA looks through all tokens).  Added to a tied
+// gradient, few / sorted: 16 tokens of 4096 2.7 / 8.3 us, 100 of 4096 (1600 CTAs)
+// 5.9 / 9.3, 256 of 4096 (4096 CTAs) 11.2 / 9.9.
+bool few_tokens(int64_t N, int64_t H) {
+    return N > 0 && N <= kFewTokens && N * ((H + kFewCols - 1) / kFewCols) <= 2048;
+}
 
 struct EmbedWs {
     size_t a, b, part, bytes;
@@ -568,6 +706,25 @@ cudaError_t launch_grad_t(GradArgs& a, bool w32, int vb, cudaStream_t s) {
         return launch_grad<T, T, 1>(a, s);
     }
     return cudaErrorInvalidValue;
+}
+
+template <typename T, typename TW, int VEC>
+cudaError_t launch_few_v(const FewArgs& a, cudaStream_t s) {
+    const int64_t zero = a.zero_rows ? (a.V + a.zero_rows - 1) / a.zero_rows : 0;
+    // the zeroing CTAs go by the first slab alone
+    const unsigned slabs = (unsigned)((a.H + kFewCols - 1) / kFewCols);
+    ce_embed_few_kernel<T, TW, VEC><<<dim3((unsigned)(a.N + zero), slabs), kFewThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_few(const FewArgs& a, bool w32, int vb, cudaStream_t s) {
+    constexpr int ES = sizeof(T);
+    if constexpr (ES == 4) {
+        return vb == 16 ? launch_few_v<T, float, 4>(a, s) : launch_few_v<T, float, 1>(a, s);
+    } else {
+        if (w32) return vb == 16 ? launch_few_v<T, float, 8>(a, s) : launch_few_v<T, float, 1>(a, s);
+        return vb == 16 ? launch_few_v<T, T, 8>(a, s) : launch_few_v<T, T, 1>(a, s);
+    }
 }
 
 cudaError_t launch_sort(SortArgs& a, cudaStream_t s) {
@@ -682,6 +839,39 @@ extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t 
     if (workspace_bytes < w.bytes) return CE_ERR_WORKSPACE_TOO_SMALL;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* base = static_cast<char*>(workspace);
+    const uint64_t vals[] = {(uint64_t)(uintptr_t)grad_out, (uint64_t)(N > 1 ? grad_out_stride * es : 0),
+                             (uint64_t)H * es, (uint64_t)(uintptr_t)grad_weight,
+                             (uint64_t)(V > 1 ? grad_weight_stride * wes : 0)};
+    const int vb = common_vector_bytes(vals, 5, es);
+    const bool w32 = grad_dtype == CE_F32;
+
+    if (few_tokens(N, H)) {
+        FewArgs fa;
+        fa.tok = tokens;
+        fa.dim1 = dim1 > 0 ? dim1 : 1;
+        fa.ts0 = token_strides[0];
+        fa.ts1 = token_strides[1];
+        fa.flat = tokens_flat(dim0, dim1, token_strides);
+        fa.N = (int)N;
+        fa.V = V;
+        fa.H = H;
+        fa.ignore = ignore_idx;
+        fa.g = static_cast<const char*>(grad_out);
+        fa.gs = grad_out_stride * es;
+        fa.dw = static_cast<char*>(grad_weight);
+        fa.dws = grad_weight_stride * wes;
+        fa.row_bytes = H * wes;
+        fa.err = reinterpret_cast<uint32_t*>(base + kWsErrOffset);
+        // zeroing: about two CTAs on each SM, more for more rows than they take
+        const int64_t per = (V + 303) / 304;
+        fa.zero_rows = accumulate ? 0 : (int)(per < 8 ? 8 : (per > kZeroRows ? kZeroRows : per));
+        fa.accumulate = accumulate ? 1 : 0;
+        fa.scale = scale;
+        cudaError_t e = dtype == CE_F32    ? launch_few<float>(fa, true, vb, s)
+                        : dtype == CE_BF16 ? launch_few<__nv_bfloat16>(fa, w32, vb, s)
+                                           : launch_few<__half>(fa, w32, vb, s);
+        return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
+    }
 
     SortArgs sa;
     sa.tok = tokens;
@@ -730,12 +920,8 @@ extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t 
     ga.chunks = w.chunks;
     ga.accumulate = accumulate ? 1 : 0;
     ga.scale = scale;
-    // a vector of the gradient is VEC floats of a float32 dW: both on their grids
-    const uint64_t vals[] = {(uint64_t)(uintptr_t)grad_out, (uint64_t)(N > 1 ? ga.gs : 0), (uint64_t)H * es,
-                             (uint64_t)(uintptr_t)grad_weight, (uint64_t)(V > 1 ? ga.dws : 0)};
-    const int vb = common_vector_bytes(vals, 5, es);
     cudaError_t e = dtype == CE_F32    ? launch_grad_t<float>(ga, true, vb, s)
-                    : dtype == CE_BF16 ? launch_grad_t<__nv_bfloat16>(ga, grad_dtype == CE_F32, vb, s)
-                                       : launch_grad_t<__half>(ga, grad_dtype == CE_F32, vb, s);
+                    : dtype == CE_BF16 ? launch_grad_t<__nv_bfloat16>(ga, w32, vb, s)
+                                       : launch_grad_t<__half>(ga, w32, vb, s);
     return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
 }
