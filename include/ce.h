@@ -446,7 +446,10 @@ ce_status ce_rmsnorm_fwd(const void* x, const void* residual, const void* weight
  *   grad_x       the gradient of x and of the residual alike, rounded once;
  *                may replace grad_out, h or grad_h with the same strides.
  *   grad_weight  NULL to skip (no workspace needed then).
- *   workspace    ce_rmsnorm_bwd_workspace_bytes(N, H) bytes, 16-byte aligned. */
+ *   workspace    ce_rmsnorm_bwd_workspace_bytes(N, H) bytes, 16-byte aligned, no
+ *                initialisation; not shared by calls that may overlap.  Its error
+ *                word gets CE_DEVERR_TIMEOUT if a bounded wait inside the kernel
+ *                gave up (ce_get_error). */
 size_t ce_rmsnorm_bwd_workspace_bytes(int64_t N, int64_t H);
 ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const void* weight,
                          const void* grad_h, ce_dtype dtype, ce_dtype weight_dtype, int64_t N,

@@ -176,6 +176,19 @@ def test_long_lists(N, V, L, K):
     check(pkg.ce_logits_process_bwd(go.to(DEV), xd, **dev(bwd_params(p))), x, p, go=go)
 
 
+def test_more_rows_than_a_grid_dimension():
+    N, V = 70001, 64
+    g = rng(20)
+    x = torch.randn(N, V, generator=g).to(DEV)
+    p = dict(history=torch.randint(0, V, (N, 3), generator=g).to(DEV), frequency_penalty=torch.rand(N, generator=g).to(DEV),
+             mask=torch.randint(-2 ** 31, 2 ** 31, (N, 2), generator=g).to(torch.int32).to(DEV))
+    got = pkg.ce_logits_process(x, **p)
+    for rows in (slice(0, 40000), slice(40000, N)):
+        assert torch.equal(got[rows], pkg.ce_logits_process(x[rows], **{k: v[rows] for k, v in p.items()}))
+    some = torch.randint(0, N, (40,), generator=g)
+    check(got[some.to(DEV)], x[some.to(DEV)], {k: v.cpu()[some] for k, v in p.items()})
+
+
 def test_penalties_alone_and_signs():
     V = 64
     x = torch.linspace(-4, 4, V).repeat(2, 1)

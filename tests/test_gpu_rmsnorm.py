@@ -234,6 +234,7 @@ def test_backward_many_rows(N, H):
     ws = torch.full((pkg.ce_rmsnorm_bwd_workspace_bytes(N, H),), 171, dtype=torch.uint8, device=DEV)
     gx2, gw2 = pkg.ce_rmsnorm_bwd(d(go), d(h), d(w), grad_h=d(dh), workspace=ws)
     assert torch.equal(gx, gx2) and torch.equal(gw, gw2)
+    assert pkg.ce_get_error(ws) == (0, 0)
 
 
 @pytest.mark.parametrize("dtype", TYPES)

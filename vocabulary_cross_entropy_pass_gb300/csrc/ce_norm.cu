@@ -18,7 +18,7 @@
 // the output.  Measured, of the GPU's 6.70 TB/s copy rate (bf16, GPU time of a call in
 // a graph): forward of 16384 x 4096 with a residual 80.4 us, 6.68 TB/s; to e4m3 with a
 // scale for 128 columns, 8192 x 8192, 81.4 us, 5.8 TB/s (its conversions keep the
-// schedulers at 76 %); gradients of 16384 x 4096 88 us, 6.1 TB/s.  Rows off the
+// schedulers at 75 %); gradients of 16384 x 4096 88 us, 6.1 TB/s.  Rows off the
 // 16-byte grid run at about half that.
 #include <cuda_fp8.h>
 
@@ -439,6 +439,7 @@ struct NormBwdArgs {
     int64_t gs, hs, dhs, dxs;  // row strides in bytes
     float eps, inv_h;
     int w32;
+    uint32_t* err;         // the workspace's error word, or NULL
 };
 
 // Floats between the partial rows of dw.
@@ -464,7 +465,6 @@ __host__ __device__ __forceinline__ int64_t part_pitch(int64_t H) { return (H + 
 constexpr int kOnGrid = 0, kPhased = 1, kLoose = 2;
 struct RingArgs {
     NormBwdArgs n;
-    uint32_t* err;         // the workspace's error word, or NULL
     int stages, slot;      // bytes of one tensor's row in the ring (a multiple of 16)
 };
 
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_consta
     if (tid == 0) {
         for (int k = 0; k < q.stages; ++k) mbar_init(&full[k], 1);
         gave_up = 0;
-        if (blockIdx.x == 0 && q.err) *q.err = 0u;
+        if (blockIdx.x == 0 && p.err) *p.err = 0u;
         fence_barrier_init();
     }
     __syncthreads();
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_kernel(const __grid_consta
     for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x, flip ^= 1) {
         const unsigned char* at = ring + (size_t)stage * NT * q.slot;
         if (!mbar_wait_bounded(&full[stage], parity)) {
-            if (q.err) atomicOr(q.err, CE_DEVERR_TIMEOUT);
+            if (p.err) atomicOr(p.err, CE_DEVERR_TIMEOUT);
             gave_up = 1;
         }
         int ph[3] = {0, 0, 0};
@@ -701,6 +701,7 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_wide_kernel(const __grid_c
     const int tid = threadIdx.x, TH = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = TH >> 5;
     const int64_t nv = p.H / VEC;
     float* out = p.part ? p.part + (int64_t)blockIdx.x * part_pitch(p.H) : nullptr;
+    if (blockIdx.x == 0 && tid == 0 && p.err) *p.err = 0u;
     auto wat = [&](int64_t c) {
         return p.w32 ? __ldg(reinterpret_cast<const float*>(p.w) + c) : to_f32(reinterpret_cast<const T*>(p.w)[c]);
     };
@@ -797,14 +798,13 @@ cudaError_t launch_ring(RingArgs& q, int threads, size_t smem, cudaStream_t s) {
 // The widest row that the ring kernel takes: 512 threads' registers, and two row
 // sets in shared memory.
 template <typename T, int MODE>
-cudaError_t launch_bwd_m(const NormBwdArgs& a, uint32_t* err, bool* shifted, cudaStream_t s) {
+cudaError_t launch_bwd_m(const NormBwdArgs& a, bool* shifted, cudaStream_t s) {
     constexpr int ES = sizeof(T);
     constexpr int VEC = MODE == kLoose ? 1 : 16 / ES;
     constexpr int M = MODE == kLoose ? 4 : (VEC == 8 ? 1 : 2);  // a step of vectors per thread: 8 elements, 4 if loose
     const int64_t nv = MODE == kPhased ? (a.H + VEC - 1 + VEC - 1) / VEC : a.H / VEC;
     RingArgs q;
     q.n = a;
-    q.err = err;
     q.slot = (int)((a.H * ES + 15) / 16 * 16 + (MODE == kOnGrid ? 0 : 16));
     const int64_t set = (int64_t)q.slot * (a.dh ? 3 : 2);
     int64_t room = 216 * 1024 / bwd_per_sm(a.H);
@@ -824,15 +824,15 @@ cudaError_t launch_bwd_m(const NormBwdArgs& a, uint32_t* err, bool* shifted, cud
 }
 
 template <typename T>
-cudaError_t launch_bwd_t(const NormBwdArgs& a, int vb, uint32_t* err, bool* shifted, cudaStream_t s) {
-    if (vb == 16) return launch_bwd_m<T, kOnGrid>(a, err, shifted, s);
+cudaError_t launch_bwd_t(const NormBwdArgs& a, int vb, bool* shifted, cudaStream_t s) {
+    if (vb == 16) return launch_bwd_m<T, kOnGrid>(a, shifted, s);
     auto at = [](const void* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u); };
     const bool many = a.N > 1;
     bool phased = at(a.g) == at(a.h) && at(a.dx) == at(a.h) && (!a.dh || at(a.dh) == at(a.h));
     if (many)
         phased = phased && (a.gs - a.hs) % 16 == 0 && (a.dxs - a.hs) % 16 == 0 && (!a.dh || (a.dhs - a.hs) % 16 == 0);
-    if (phased) return launch_bwd_m<T, kPhased>(a, err, shifted, s);
-    return launch_bwd_m<T, kLoose>(a, err, shifted, s);
+    if (phased) return launch_bwd_m<T, kPhased>(a, shifted, s);
+    return launch_bwd_m<T, kLoose>(a, shifted, s);
 }
 
 constexpr int64_t kMaxWidth = 1 << 20;
@@ -968,11 +968,11 @@ extern "C" ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const v
                              (uint64_t)(N > 1 ? a.hs : 0), (uint64_t)(N > 1 && grad_h ? a.dhs : 0),
                              (uint64_t)(N > 1 ? a.dxs : 0), (uint64_t)H * es};
     const int vb = common_vector_bytes(vals, 9, es);
-    uint32_t* err = grad_weight ? reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kWsErrOffset) : nullptr;
+    a.err = grad_weight ? reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kWsErrOffset) : nullptr;
     bool shifted = false;
-    cudaError_t e = dtype == CE_F32    ? launch_bwd_t<float>(a, vb, err, &shifted, s)
-                    : dtype == CE_BF16 ? launch_bwd_t<__nv_bfloat16>(a, vb, err, &shifted, s)
-                                       : launch_bwd_t<__half>(a, vb, err, &shifted, s);
+    cudaError_t e = dtype == CE_F32    ? launch_bwd_t<float>(a, vb, &shifted, s)
+                    : dtype == CE_BF16 ? launch_bwd_t<__nv_bfloat16>(a, vb, &shifted, s)
+                                       : launch_bwd_t<__half>(a, vb, &shifted, s);
     if (e != cudaSuccess) return CE_ERR_LAUNCH;
     if (grad_weight) {
         cudaLaunchConfig_t cfg = {};
