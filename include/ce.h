@@ -392,7 +392,7 @@ ce_status ce_embed_fwd(const int64_t* tokens, int64_t dim0, int64_t dim1,
                        size_t workspace_bytes, void* stream);
 
 /* Gradient of ce_embed_fwd:  dW_v = scale * (sum of grad_out_i over tokens
- * i = v, in float32, in the order of the tokens sorted stably by value).
+ * i = v, in float32, in an order fixed by the tokens and the sizes).
  * Ignored and out-of-range tokens give nothing; the latter set
  * CE_DEVERR_TARGET_RANGE in the workspace.
  *   grad_out     N = dim0*dim1 rows in `dtype`, grad_out_stride apart (0 for
