@@ -238,6 +238,31 @@ def test_backward_many_rows(N, H):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H", [1, 40, 63, 128, 129, 130, 256, 257, 258, 396, 512, 513])
+@pytest.mark.parametrize("N", [1, 9, 10007])
+def test_backward_short_rows(N, H, dtype):
+    h, dh, w = make(N, H, dtype, H + N)
+    go = torch.randn(N, H, generator=rng(N + 5)).to(dtype)
+    gx, gw = pkg.ce_rmsnorm_bwd(d(go), d(h), d(w), grad_h=d(dh))
+    check_bwd(gx, gw, go, h, w, dh)
+    gx2, gw2 = pkg.ce_rmsnorm_bwd(d(go), d(h), d(w))
+    check_bwd(gx2, gw2, go, h, w, None)
+    assert torch.equal(gw, gw2)
+    # rows of a wider matrix, a row's end followed by numbers that must not count
+    wide = torch.full((3, N, H + 3), float("nan"), dtype=dtype, device=DEV)
+    for k, t in enumerate((go, h, dh)):
+        wide[k, :, :H] = d(t)
+    x3, w3 = pkg.ce_rmsnorm_bwd(wide[0, :, :H], wide[1, :, :H], d(w), grad_h=wide[2, :, :H])
+    check_bwd(x3, w3, go, h, w, dh)
+    # in place, and into a tensor of its own with the same strides (another stride may add in another order)
+    apart = torch.full_like(wide[0], float("nan"))[:, :H]
+    x4, w4 = pkg.ce_rmsnorm_bwd(wide[0, :, :H], wide[1, :, :H], d(w), grad_h=wide[2, :, :H], grad_x=apart)
+    x5, w5 = pkg.ce_rmsnorm_bwd(wide[0, :, :H], wide[1, :, :H], d(w), grad_h=wide[2, :, :H], grad_x=wide[0, :, :H])
+    check_bwd(x5, w5, go, h, w, dh)
+    assert torch.equal(x4, x5) and torch.equal(w4, w5) and bool(wide[0, :, H:].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("H", [64, 65, 66, 9001])
 def test_backward_strides_and_in_place(H, dtype):
     g = rng(H)

@@ -18,7 +18,7 @@
 // the output.  Measured, of the GPU's 6.70 TB/s copy rate (bf16, GPU time of a call in
 // a graph): forward of 16384 x 4096 with a residual 80.4 us, 6.68 TB/s; to e4m3 with a
 // scale for 128 columns, 8192 x 8192, 81.4 us, 5.8 TB/s (its conversions keep the
-// schedulers at 75 %); gradients of 16384 x 4096 88 us, 6.1 TB/s.  Rows off the
+// schedulers at 75 %); gradients of 16384 x 4096 89.5 us, 6.0 TB/s.  Rows off the
 // 16-byte grid run at about half that.
 #include <cuda_fp8.h>
 
@@ -754,6 +754,112 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_bwd_wide_kernel(const __grid_c
     }
 }
 
+// Rows of at most kShortWidth elements: a warp to each, straight into registers,
+// U rows at once, without barriers; a lane's columns' dw stay in its registers over
+// all of its warp's rows, and the CTA's eight warps are added in order at the end.
+// EPL: elements of a lane (32 * EPL is at least the width).
+// Against the ring above with a CTA to a row (bf16 with a residual, GPU us of a call,
+// here / ring): 262144 x 128 51 / 109, 32768 x 256 17 / 24, 131072 x 512 92 / 99; off
+// the grid 32768 x 511 47 / 66, 4708 x 396 8.6 / 17.4; 64 x 128 4.2 / 5.5.
+constexpr int64_t kShortWidth = 512;
+constexpr int kShortWarps = 8;
+// CTAs per SM, two / four: 262144 x 128 72 / 51 us, 262144 x 64 66 / 46; 32768 x 256
+// 16.8 / 19.6, 32768 x 512 25.7 / 28.6 (fewer partial rows of dw to write and add).
+// Three, six and eight were behind the better of these at nearly all sizes.
+constexpr int short_per_sm(int64_t H) { return H <= 128 ? 4 : 2; }
+template <typename T, int EPL, int VEC>
+__global__ void __launch_bounds__(kShortWarps * 32) ce_rmsnorm_bwd_short_kernel(const __grid_constant__ NormBwdArgs p) {
+    constexpr int ES = sizeof(T);
+    constexpr int VPT = EPL / VEC;
+    constexpr int U = EPL <= 8 ? 2 : 1;
+    __shared__ __align__(16) float sum[kShortWarps][EPL * 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int H = (int)p.H, nv = H / VEC;
+    if (blockIdx.x == 0 && tid == 0 && p.err) *p.err = 0u;
+    float w32[VPT][VEC], dw[VPT][VEC];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int v = lane + k * 32;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            dw[k][i] = 0.f;
+            w32[k][i] = 0.f;
+            if (v < nv)
+                w32[k][i] = p.w32 ? __ldg(reinterpret_cast<const float*>(p.w) + v * VEC + i)
+                                  : to_f32(reinterpret_cast<const T*>(p.w)[v * VEC + i]);
+        }
+    }
+    const int64_t step = (int64_t)gridDim.x * kShortWarps;
+    for (int64_t row = (int64_t)blockIdx.x * kShortWarps + warp; row < p.N; row += U * step) {
+        Pack<T, VEC> g[U][VPT], h[U][VPT], d[U][VPT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = row + u * step;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = lane + k * 32;
+                g[u][k].zero();
+                h[u][k].zero();
+                d[u][k].zero();
+                if (r < p.N && v < nv) {
+                    g[u][k].load_cs(p.g + r * p.gs + v * (VEC * ES));
+                    h[u][k].load_cs(p.h + r * p.hs + v * (VEC * ES));
+                    if (p.dh) d[u][k].load_cs(p.dh + r * p.dhs + v * (VEC * ES));
+                }
+            }
+        }
+        float ss[U], c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            ss[u] = c[u] = 0.f;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float hv = h[u][k].f(i);
+                    ss[u] = fmaf(hv, hv, ss[u]);
+                    c[u] = fmaf(g[u][k].f(i) * w32[k][i], hv, c[u]);
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            ss[u] = warp_allsum(ss[u]);
+            c[u] = warp_allsum(c[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = row + u * step;
+            if (r >= p.N) break;
+            const float rstd = rsqrtf(fmaf(ss[u], p.inv_h, p.eps));
+            const float cc = c[u] * rstd * p.inv_h;  // mean of g w n
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int v = lane + k * 32;
+                Pack<T, VEC> o;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float n = h[u][k].f(i) * rstd, gv = g[u][k].f(i);
+                    dw[k][i] = fmaf(gv, n, dw[k][i]);
+                    float t = rstd * fmaf(-n, cc, gv * w32[k][i]);
+                    if (p.dh) t += d[u][k].f(i);
+                    o.set(i, t);
+                }
+                if (v < nv) o.store_cs(p.dx + r * p.dxs + v * (VEC * ES));
+            }
+        }
+    }
+    if (!p.part) return;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) store_f32<VEC>(&sum[warp][(lane + k * 32) * VEC], dw[k]);
+    __syncthreads();
+    for (int c = tid; c < H; c += kShortWarps * 32) {
+        float t = sum[0][c];
+#pragma unroll
+        for (int w = 1; w < kShortWarps; ++w) t += sum[w][c];
+        p.part[(int64_t)blockIdx.x * part_pitch(p.H) + c] = t;
+    }
+}
+
 // dw_j = the partial rows' column sums, in a fixed order: 32 columns per CTA, a
 // warp to every 32nd partial row, then the warps' sums in order.
 // Partial row r lies (low + r * step) mod 16 bytes / es past its start.
@@ -783,6 +889,11 @@ __global__ void __launch_bounds__(1024) ce_rmsnorm_dw_kernel(const float* part, 
 // 5330; 4096 wide with two / three 6000 / 5840).
 int bwd_per_sm(int64_t H) { return H >= 4096 ? 2 : (H >= 2048 ? 4 : (H >= 1024 ? 8 : 16)); }
 int bwd_grid(int64_t N, int64_t H) {
+    if (H <= kShortWidth) {
+        const int64_t ctas = (N + kShortWarps - 1) / kShortWarps;
+        const int64_t full = 152 * short_per_sm(H);
+        return (int)(ctas < full ? ctas : full);
+    }
     const int64_t most = 152 * bwd_per_sm(H);
     return (int)(N < most ? N : most);
 }
@@ -823,8 +934,21 @@ cudaError_t launch_bwd_m(const NormBwdArgs& a, bool* shifted, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename T, int EPL>
+cudaError_t launch_short(const NormBwdArgs& a, int vb, cudaStream_t s) {
+    constexpr int FULL = 16 / (int)sizeof(T) < EPL ? 16 / (int)sizeof(T) : EPL;
+    auto* k = vb == 16                  ? ce_rmsnorm_bwd_short_kernel<T, EPL, FULL>
+              : vb == 4 && sizeof(T) == 2 ? ce_rmsnorm_bwd_short_kernel<T, EPL, sizeof(T) == 2 ? 2 : 1>
+                                          : ce_rmsnorm_bwd_short_kernel<T, EPL, 1>;
+    k<<<bwd_grid(a.N, a.H), kShortWarps * 32, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_bwd_t(const NormBwdArgs& a, int vb, bool* shifted, cudaStream_t s) {
+    if (a.H <= 128) return launch_short<T, 4>(a, vb, s);
+    if (a.H <= 256) return launch_short<T, 8>(a, vb, s);
+    if (a.H <= kShortWidth) return launch_short<T, 16>(a, vb, s);
     if (vb == 16) return launch_bwd_m<T, kOnGrid>(a, shifted, s);
     auto at = [](const void* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u); };
     const bool many = a.N > 1;
