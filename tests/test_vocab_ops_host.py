@@ -255,3 +255,12 @@ def test_python_refuses_what_is_no_tensor(lib):
         pkg.ce_rmsnorm_fwd(x, x[0], quant=torch.int8)
     with pytest.raises(TypeError):
         pkg.ce_logits_process("logits")
+
+
+@pytest.mark.parametrize("name", ["out", "workspace", "stream"])
+def test_process_logits_takes_no_buffers(lib, name):
+    # under autograd the logits are kept for the backward pass: an output over them would change its signs unseen
+    x = torch.zeros(4, 64, requires_grad=True)
+    for value in (x.detach(), None):
+        with pytest.raises(TypeError, match=name):
+            pkg.process_logits(x, **{name: value})

@@ -233,6 +233,11 @@ class _ProcessLogits(torch.autograd.Function):
 def process_logits(logits: torch.Tensor, **params) -> torch.Tensor:
     """:func:`ce_logits_process` with autograd: the gradient reaches the logits
     (a policy's log-probabilities under the distribution its tokens were drawn
-    from); the parameters are constants."""
+    from); the parameters are constants.  Takes no ``out``, ``workspace`` or
+    ``stream``: the logits are kept for the backward pass, which runs on the
+    forward's stream."""
+    for name in ("out", "workspace", "stream"):
+        if name in params:
+            raise TypeError(f"process_logits takes no {name} (ce_logits_process does)")
     x = logits if logits.stride(-1) == 1 else logits.contiguous()
     return _ProcessLogits.apply(x, params)
