@@ -133,20 +133,46 @@ std::pair<int64_t, int64_t> rows(const Tensor& t, int64_t H, const char* name) {
 }
 int64_t stride(const Tensor& t, int64_t H, const char* name) { return t.defined() ? rows(t, H, name).second : 0; }
 
-Tensor empty(at::IntArrayRef sizes, at::ScalarType t, const Tensor& like) {
-    return at::empty(sizes, like.options().dtype(t));
-}
+// Where a call runs: the stream handed in (an object with a cuda_stream) or the
+// current one, on the tensors' device.  A stream handed in is the current one for
+// as long as the call lasts: what is allocated here comes from its memory and goes
+// back there, behind the kernels that use it, and a copy of the tokens is made on it.
+class Launch {
+  public:
+    Launch(PyObject* given, const Tensor& like)
+        : on_(like.device()), before_(c10::cuda::getCurrentCUDAStream(like.device().index())),
+          stream(before_.stream()) {
+        if (given == Py_None) return;
+        PyObject* h = PyObject_GetAttrString(given, "cuda_stream");
+        if (!h) throw PythonError{};
+        const unsigned long long v = PyLong_AsUnsignedLongLong(h);
+        Py_DECREF(h);
+        if (PyErr_Occurred()) throw PythonError{};
+        stream = reinterpret_cast<void*>(static_cast<uintptr_t>(v));
+        if (stream == before_.stream()) return;
+        // the legacy default stream by its other name
+        const auto raw = stream == cudaStreamLegacy ? nullptr : static_cast<cudaStream_t>(stream);
+        other_.reset_stream(c10::cuda::getStreamFromExternal(raw, like.device().index()));
+    }
+    Tensor empty(at::IntArrayRef sizes, at::ScalarType t, const Tensor& like) const {
+        return at::empty(sizes, like.options().dtype(t));
+    }
+    // Of the other stream's memory too, but for the caller: not used again there
+    // before what the caller's own stream then does with it.
+    Tensor output(at::IntArrayRef sizes, at::ScalarType t, const Tensor& like) const {
+        Tensor r = empty(sizes, t, like);
+        if (other_.current_stream()) r.record_stream(before_.unwrap());
+        return r;
+    }
 
-// The stream handed in (a torch.cuda.Stream), or the current one.
-void* stream_of(PyObject* o, const Tensor& like) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(like.device().index()).stream();
-    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-    if (!h) throw PythonError{};
-    const unsigned long long v = PyLong_AsUnsignedLongLong(h);
-    Py_DECREF(h);
-    if (PyErr_Occurred()) throw PythonError{};
-    return reinterpret_cast<void*>(static_cast<uintptr_t>(v));
-}
+  private:
+    c10::cuda::CUDAGuard on_;
+    c10::cuda::CUDAStream before_;
+    c10::cuda::OptionalCUDAStreamGuard other_;
+
+  public:
+    void* stream;
+};
 
 struct Tokens {
     Tensor t;
@@ -172,13 +198,13 @@ PyObject* embed_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const ce_dtype dt = cuda(weight, "weight");
         if (weight.dim() != 2) value_error("weight must be (V, H)");
         const int64_t V = weight.size(0), H = weight.size(1);
+        const Launch on(a[6], weight);
         const Tokens t = tokens_of(tokens, weight);
         beside(ws, weight, "workspace");
         at::DimVector shape(tokens.sizes());
         shape.push_back(H);
-        const c10::cuda::CUDAGuard on(weight.device());
         if (!out.defined()) {
-            out = empty(shape, weight.scalar_type(), weight);
+            out = on.output(shape, weight.scalar_type(), weight);
         } else {
             beside(out, weight, "out");
             if (out.scalar_type() != weight.scalar_type() || !out.sizes().equals(shape))
@@ -186,7 +212,7 @@ PyObject* embed_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         done(ce_embed_fwd(t.t.const_data_ptr<int64_t>(), t.d0, t.d1, t.s, weight.data_ptr(), dt, V, H,
                           stride(weight, H, "weight"), number(a[2]), integer(a[3]), out.data_ptr(),
-                          stride(out, H, "out"), ptr(ws), bytes(ws), stream_of(a[6], weight)),
+                          stride(out, H, "out"), ptr(ws), bytes(ws), on.stream),
              "ce_embed_fwd");
         return THPVariable_Wrap(out);
     });
@@ -207,13 +233,13 @@ PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (nd == 0 || !g.sizes().slice(0, nd - 1).equals(tokens.sizes()))
             value_error("grad_out must be (*tokens.shape, H)");
         const int64_t H = g.size(nd - 1);
+        const Launch on(a[9], g);
         const Tokens t = tokens_of(tokens, g);
-        const c10::cuda::CUDAGuard on(g.device());
         if (!dw.defined()) {
             if (accumulate) value_error("accumulate needs the grad_weight to add to");
             const int64_t code = integer(a[7]);
             if (code != CE_F32 && code != dt) type_error("grad_dtype must be float32 or grad_out's dtype");
-            dw = empty({V, H}, code == CE_F32 ? at::kFloat : g.scalar_type(), g);
+            dw = on.output({V, H}, code == CE_F32 ? at::kFloat : g.scalar_type(), g);
         } else {
             beside(dw, g, "grad_weight");
             if (dw.dim() != 2 || dw.size(0) != V || dw.size(1) != H)
@@ -223,12 +249,12 @@ PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (wdt < 0 || (wdt != CE_F32 && wdt != dt)) type_error("grad_weight must be float32 or of grad_out's dtype");
         if (accumulate && wdt != CE_F32) type_error("grad_weight accumulates in float32");
         if (!ws.defined())
-            ws = empty({(int64_t)ce_embed_bwd_workspace_bytes(t.d0 * t.d1, H, V)}, at::kByte, g);
+            ws = on.empty({(int64_t)ce_embed_bwd_workspace_bytes(t.d0 * t.d1, H, V)}, at::kByte, g);
         else
             beside(ws, g, "workspace");
         done(ce_embed_bwd(g.data_ptr(), dt, stride(g, H, "grad_out"), t.t.const_data_ptr<int64_t>(), t.d0, t.d1, t.s,
                           V, H, number(a[3]), integer(a[4]), dw.data_ptr(), (ce_dtype)wdt,
-                          stride(dw, H, "grad_weight"), accumulate, ws.data_ptr(), bytes(ws), stream_of(a[9], g)),
+                          stride(dw, H, "grad_weight"), accumulate, ws.data_ptr(), bytes(ws), on.stream),
              "ce_embed_bwd");
         return THPVariable_Wrap(dw);
     });
@@ -259,8 +285,8 @@ PyObject* rmsnorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const auto [N, xs] = rows(x, H, "x");
         const ce_dtype wdt = weight_code(w, x, H, dt);
         matches(res, x, "residual");
-        const c10::cuda::CUDAGuard on(x.device());
-        if (res.defined() && !h.defined()) h = empty(x.sizes(), x.scalar_type(), x);
+        const Launch on(a[9], x);
+        if (res.defined() && !h.defined()) h = on.output(x.sizes(), x.scalar_type(), x);
         matches(h, x, "residual_out");
         at::ScalarType ot = x.scalar_type();
         if (quant == CE_QUANT_NONE) {
@@ -271,7 +297,7 @@ PyObject* rmsnorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 value_error("group_size must be 0, 32, 64 or 128");
             const int64_t G = group == 0 ? 1 : (H + group - 1) / group;
             if (!scales.defined()) {
-                scales = empty({N, G}, at::kFloat, x);
+                scales = on.output({N, G}, at::kFloat, x);
             } else {
                 beside(scales, x, "scales_out");
                 if (scales.scalar_type() != at::kFloat || scales.numel() != N * G || !scales.is_contiguous())
@@ -279,7 +305,7 @@ PyObject* rmsnorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
             }
         }
         if (!out.defined()) {
-            out = empty(x.sizes(), ot, x);
+            out = on.output(x.sizes(), ot, x);
         } else {
             beside(out, x, "out");
             if (out.scalar_type() != ot || !out.sizes().equals(x.sizes()))
@@ -288,7 +314,7 @@ PyObject* rmsnorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         done(ce_rmsnorm_fwd(x.data_ptr(), ptr(res), w.data_ptr(), dt, wdt, N, H, xs, stride(res, H, "residual"),
                             number(a[3]), out.data_ptr(), stride(out, H, "out"), quant, (int)group,
                             static_cast<float*>(ptr(scales)), ptr(h), stride(h, H, "residual_out"),
-                            stream_of(a[9], x)),
+                            on.stream),
              "ce_rmsnorm_fwd");
         PyObject* r = PyTuple_New(3);
         if (!r) throw PythonError{};
@@ -321,10 +347,10 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         matches(g, h, "grad_out");
         matches(dh, h, "grad_h");
         matches(dx, h, "grad_x");
-        const c10::cuda::CUDAGuard on(h.device());
-        if (!dx.defined()) dx = empty(h.sizes(), h.scalar_type(), h);
+        const Launch on(a[8], h);
+        if (!dx.defined()) dx = on.output(h.sizes(), h.scalar_type(), h);
         if (a[6] == Py_True) {
-            dw = empty({H}, at::kFloat, h);
+            dw = on.output({H}, at::kFloat, h);
         } else if (a[6] != Py_None && a[6] != Py_False) {
             dw = tensor(a[6], "grad_weight");
             beside(dw, h, "grad_weight");
@@ -332,10 +358,10 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 type_error("grad_weight must be a contiguous float32 vector of H elements");
         }
         beside(ws, h, "workspace");
-        if (dw.defined() && !ws.defined()) ws = empty({(int64_t)ce_rmsnorm_bwd_workspace_bytes(N, H)}, at::kByte, h);
+        if (dw.defined() && !ws.defined()) ws = on.empty({(int64_t)ce_rmsnorm_bwd_workspace_bytes(N, H)}, at::kByte, h);
         done(ce_rmsnorm_bwd(g.data_ptr(), h.data_ptr(), w.data_ptr(), ptr(dh), dt, wdt, N, H, stride(g, H, "grad_out"),
                             hs, stride(dh, H, "grad_h"), number(a[3]), dx.data_ptr(), stride(dx, H, "grad_x"),
-                            static_cast<float*>(ptr(dw)), ptr(ws), bytes(ws), stream_of(a[8], h)),
+                            static_cast<float*>(ptr(dw)), ptr(ws), bytes(ws), on.stream),
              "ce_rmsnorm_bwd");
         PyObject* r = PyTuple_New(2);
         if (!r) throw PythonError{};
@@ -436,14 +462,15 @@ ce_logits_params logits_params(PyObject* given, int64_t N, int64_t V, const Tens
     return p;
 }
 
-Tensor logits_workspace(const Tensor& given, const ce_logits_params& p, const Dims& d, ce_dtype dt, const Tensor& like) {
+Tensor logits_workspace(const Launch& on, const Tensor& given, const ce_logits_params& p, const Dims& d, ce_dtype dt,
+                        const Tensor& like) {
     if (given.defined()) {
         beside(given, like, "workspace");
         return given;
     }
     const size_t need =
         p.history_max || p.bias_max ? ce_logits_workspace_bytes(d.d0 * d.d1, d.V, dt, p.history_max, p.bias_max) : 0;
-    return need ? empty({(int64_t)need}, at::kByte, like) : Tensor();
+    return need ? on.empty({(int64_t)need}, at::kByte, like) : Tensor();
 }
 
 // ce_logits_process(logits, out, workspace, stream, params)
@@ -454,14 +481,14 @@ PyObject* logits_process(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Tensor out = maybe(a[1], "out");
         const ce_dtype dt = cuda(x, "logits");
         const Dims d = logits_dims(x, "logits");
-        const c10::cuda::CUDAGuard on(x.device());
+        const Launch on(a[3], x);
         const ce_logits_params p = logits_params(a[4], d.d0 * d.d1, d.V, x);
         matches(out, x, "out");
-        if (!out.defined()) out = empty(x.sizes(), x.scalar_type(), x);
+        if (!out.defined()) out = on.output(x.sizes(), x.scalar_type(), x);
         const Dims o = logits_dims(out, "out");
-        const Tensor ws = logits_workspace(maybe(a[2], "workspace"), p, d, dt, x);
+        const Tensor ws = logits_workspace(on, maybe(a[2], "workspace"), p, d, dt, x);
         done(ce_logits_process(x.data_ptr(), dt, d.d0, d.d1, d.V, d.s, &p, out.data_ptr(), o.s, ptr(ws), bytes(ws),
-                               stream_of(a[3], x)),
+                               on.stream),
              "ce_logits_process");
         return THPVariable_Wrap(out);
     });
@@ -478,14 +505,14 @@ PyObject* logits_process_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Dims d = logits_dims(x, "logits");
         matches(g, x, "grad_out");
         const Dims gd = logits_dims(g, "grad_out");
-        const c10::cuda::CUDAGuard on(x.device());
+        const Launch on(a[4], x);
         const ce_logits_params p = logits_params(a[5], d.d0 * d.d1, d.V, x);
         matches(out, x, "grad");
-        if (!out.defined()) out = empty(x.sizes(), x.scalar_type(), x);
+        if (!out.defined()) out = on.output(x.sizes(), x.scalar_type(), x);
         const Dims o = logits_dims(out, "grad");
-        const Tensor ws = logits_workspace(maybe(a[3], "workspace"), p, d, dt, x);
+        const Tensor ws = logits_workspace(on, maybe(a[3], "workspace"), p, d, dt, x);
         done(ce_logits_process_bwd(g.data_ptr(), gd.s, x.data_ptr(), dt, d.d0, d.d1, d.V, d.s, &p, out.data_ptr(), o.s,
-                                   ptr(ws), bytes(ws), stream_of(a[4], x)),
+                                   ptr(ws), bytes(ws), on.stream),
              "ce_logits_process_bwd");
         return THPVariable_Wrap(out);
     });

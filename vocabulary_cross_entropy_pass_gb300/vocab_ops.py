@@ -9,6 +9,9 @@ forms.
 
 The ce_* forms take and return plain tensors and can be captured into a CUDA
 graph (pass the outputs and the workspace, or allocate from the graph's pool).
+``stream``: a call runs on the current stream or on the one handed in, after what
+that stream holds; what the call allocates is of that stream's memory, and the
+caller waits for the stream before it reads the outputs on another.
 As with every torch.autograd graph, capture a backward only of a forward made
 on the capture's own stream, with no older graph of the same leaves alive.
 """
