@@ -34,34 +34,30 @@
 // of it the list kernel, which its shared-memory atomics and scans keep busy).
 #include "ce_device.cuh"
 #include "ce_internal.h"
+#include "ce_logits_plan.h"
 #include "ce_pack.cuh"
 #include "ce_span.cuh"
 
 namespace gbce {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kFusedCols = 4096;       // columns of a CTA that reads the lists itself, at most
+constexpr int kThreads = kLogitThreads;
 constexpr uint32_t kBiased = 0x40000000u;  // a bias is given for the column
 constexpr uint32_t kSeen = 0x80000000u;    // the token occurs; the low 30 bits count it in the answer
 
-struct LogitArgs {
+struct LogitArgs : LogitSizes {
     const char* x;         // logits (backward: read where the history touches them)
     const char* g;         // backward: the gradient of the outputs, else NULL
     char* out;
     int64_t xs0, xs1, gs0, gs1, os0, os1;  // in elements
-    int64_t dim1, N, V;
-    int cols, runs;        // a CTA's run of columns (a multiple of 128) and the runs of a row
+    int64_t dim1;
     int listed;            // the history or the biases touch columns
     int in_place;
     uint2* table;          // [N][parts][entries] touched (column in its run, count and flags), by column; or NULL
     float* tbias;          // [N][parts][entries] their summed biases
     uint32_t* start;       // [N][runs][2] a run's first and last + 1 entry of its part's table
-    int parts, part_runs;  // parts of a row with a table each (one but for the longest lists), runs in a part
-    int entries;           // room of a table: min(history + biases, the part's columns), a multiple of 4
-    int slots;             // list kernel: slots for biased entries, a power of two
     const int64_t* hist;
-    int64_t hist_stride, hist_max;
+    int64_t hist_stride;
     const int64_t* hist_len;
     const int64_t* prompt_len;
     const float* rep;
@@ -69,7 +65,7 @@ struct LogitArgs {
     const float* pres;
     const int64_t* btok;
     const float* bval;
-    int64_t btok_stride, bval_stride, bias_max;
+    int64_t btok_stride, bval_stride;
     const uint32_t* mask;
     int64_t mask_stride;
     const float* temp;
@@ -397,10 +393,10 @@ __global__ void __launch_bounds__(kThreads, MASK ? 8 : 6) ce_logits_kernel(const
 }
 
 // The table of one part of a row.  Shared memory: bits[words] (a whole number of
-// 16-byte vectors), cnt[entries], keys[slots] and sums[slots] of the biased
-// entries, first[words] (entries before each word: 16 bits, a part has at most
-// 65535), col[entries] (columns in their runs: 16 bits, a run is a power of two
-// of at most 65536).
+// 16-byte vectors), cnt[entries], keys[slots] and sums[sums] of the biased entries
+// (without slots a sum for each entry), first[words] (entries before each word:
+// 16 bits, a part has at most 65535), col[entries] (columns in their runs: 16 bits,
+// a run is a power of two of at most 65536).
 template <int TH, int U>
 __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __grid_constant__ LogitArgs p) {
     extern __shared__ __align__(16) uint32_t sm[];
@@ -415,7 +411,7 @@ __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __
     uint32_t* cnt = bits + words;
     uint32_t* keys = cnt + p.entries;
     float* sums = reinterpret_cast<float*>(keys + p.slots);
-    uint16_t* first = reinterpret_cast<uint16_t*>(sums + p.slots);
+    uint16_t* first = reinterpret_cast<uint16_t*>(sums + p.sums);
     uint16_t* col = first + words;
     const uint32_t in_run = (uint32_t)p.cols - 1;
     const int64_t t0 = (row * p.parts + blockIdx.x) * p.entries;
@@ -505,7 +501,10 @@ __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __
         before += __popc(b.w);
         *reinterpret_cast<ushort4*>(first + k) = f;
     }
-    for (int k = tid; k < ne; k += TH) cnt[k] = 0u;
+    for (int k = tid; k < ne; k += TH) {
+        cnt[k] = 0u;
+        if (p.bias_max > 0 && p.slots == 0) sums[k] = 0.f;
+    }
     __syncthreads();
     // where each run's entries are
     const int r0 = blockIdx.x * p.part_runs;
@@ -532,7 +531,9 @@ __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __
             const unsigned peers = __match_any_sync(kFull, e);
             const bool lead = in && lane == __ffs(peers) - 1;
             uint32_t slot = 0;
-            if (lead) {  // the entry's slot, a new one for its first bias
+            if (lead && p.slots == 0) {
+                slot = e;
+            } else if (lead) {  // the entry's slot, a new one for its first bias
                 slot = (e * 2654435761u) & (p.slots - 1);
                 for (;;) {
                     const uint32_t was = atomicCAS(&keys[slot], 0xffffffffu, e);
@@ -559,48 +560,13 @@ __global__ void __launch_bounds__(TH, 2048 / TH) ce_logits_lists_kernel(const __
     }
     griddep_launch_dependents();  // earlier the waiting stream takes the place of lists not yet begun
     __syncthreads();
-    for (int e = tid; e < ne; e += TH) table[e] = make_uint2(col[e], cnt[e]);
+    for (int e = tid; e < ne; e += TH) {
+        table[e] = make_uint2(col[e], cnt[e]);
+        if (p.bias_max > 0 && p.slots == 0 && (cnt[e] & kBiased)) p.tbias[t0 + e] = sums[e];
+    }
     if (p.bias_max > 0)
         for (int k = tid; k < p.slots; k += TH)
             if (keys[k] != 0xffffffffu) p.tbias[t0 + keys[k]] = sums[k];
-}
-
-// Words of shared memory of the list kernel.
-size_t list_bytes(const LogitArgs& a) {
-    const int64_t words = (int64_t)a.part_runs * a.cols / 32;
-    return (size_t)(words + a.entries + 2 * a.slots) * 4 + (size_t)(words + a.entries) * 2;
-}
-
-// The runs of columns and, for many columns in all, the tables.
-// Up to 2^21 columns the CTAs read the lists themselves: 16 rows of 128000 under a
-// mask with histories of 1000 / 8000 tokens 6.8 / 11.8 us against 10.3 / 14.1
-// with tables; 30 rows 10.9 / 19.2 against 11.2 / 15.9.
-constexpr int64_t kFusedColumns = 1 << 21;
-bool plan_logits(LogitArgs& a, int es) {
-    const int64_t list = a.hist_max + a.bias_max;
-    a.listed = list > 0;
-    const bool tables = list > 0 && a.N * a.V > kFusedColumns;
-    // a run of eight vectors a thread; sixteen where that still fills the GPU's
-    // places several times over (gradient of 4096 rows of 50257 columns 182 ->
-    // 179 us; 512 rows of 128000, twice, 77 -> 81 us)
-    a.cols = list > 0 && !tables ? kFusedCols : kThreads * 8 * 16 / es;
-    if (a.N * ((a.V + 2 * a.cols - 1) / (2 * a.cols)) >= 6 * 912 && a.cols != kFusedCols) a.cols *= 2;
-    // few columns in all: shorter runs on more SMs
-    while (a.cols > 1024 && a.N * ((a.V + a.cols - 1) / a.cols) < 304) a.cols /= 2;
-    a.runs = (int)((a.V + a.cols - 1) / a.cols);
-    if (!tables) return false;
-    a.slots = 32;
-    while (a.slots < 2 * a.bias_max && a.slots < (1 << 17)) a.slots *= 2;
-    // one table a row; parts of a row where that would not fit
-    for (int64_t per = a.runs;; per = (per + 1) / 2) {
-        a.part_runs = (int)per;
-        a.parts = (int)((a.runs + per - 1) / per);
-        const int64_t cols = per * a.cols;
-        a.entries = (int)((list < cols ? list : cols) + 3) / 4 * 4;  // what follows them holds vectors
-        while (a.slots > 32 && a.slots >= 4 * (int64_t)a.entries) a.slots /= 2;
-        if (per == 1 || (a.entries <= 65535 && list_bytes(a) <= 200 * 1024)) break;
-    }
-    return true;
 }
 
 template <typename T, bool BWD>
@@ -691,7 +657,7 @@ ce_status logits_common(const void* grad, const int64_t* grad_strides, const voi
         if (bwd && out == logits) return CE_ERR_INVALID_ARG;
     }
     if (N == 0) return CE_OK;
-    LogitArgs a;
+    LogitArgs a = {};
     a.x = static_cast<const char*>(logits);
     a.g = static_cast<const char*>(grad);
     a.out = static_cast<char*>(out);
@@ -752,8 +718,8 @@ ce_status logits_common(const void* grad, const int64_t* grad_strides, const voi
 extern "C" size_t ce_logits_workspace_bytes(int64_t N, int64_t V, ce_dtype dtype, int64_t history_max,
                                             int64_t bias_max) {
     using namespace gbce;
-    if (dtype < CE_F32 || dtype > CE_F16 || N < 0 || N > (int64_t)0x7fffffff * 0x7fffffff || V < 1 ||
-        V > 0x7fffffffLL || history_max < 0 || bias_max < 0)
+    if (dtype < CE_F32 || dtype > CE_F16 || N < 0 || N > 65535LL * 65535 || V < 1 || V > 0x7fffffffLL ||
+        history_max < 0 || bias_max < 0 || history_max > 0x40000000LL || bias_max > 0x40000000LL)
         return 0;
     LogitArgs a = {};
     a.N = N;
