@@ -355,14 +355,14 @@ ce_status run_pass(Problem& pb, const ce_options* o, float* loss_out, int64_t* n
         w + kWsHeaderBytes + align_up((size_t)pb.N * sizeof(float), 256));
     pb.loss_rows = pb.reduce ? rows : loss_out;
 
-    if (launch_count(pb, n_out, s) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (launch_count(pb, n_out, s) != cudaSuccess) return launch_failed();
     cudaEvent_t eb = o ? static_cast<cudaEvent_t>(o->event_begin) : nullptr;
     cudaEvent_t ee = o ? static_cast<cudaEvent_t>(o->event_end) : nullptr;
-    if (eb && cudaEventRecord(eb, s) != cudaSuccess) return CE_ERR_LAUNCH;
-    if (pb.N > 0 && launch_planned(pb, pl, parts, s) != cudaSuccess) return CE_ERR_LAUNCH;
-    if (ee && cudaEventRecord(ee, s) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (eb && cudaEventRecord(eb, s) != cudaSuccess) return launch_failed();
+    if (pb.N > 0 && launch_planned(pb, pl, parts, s) != cudaSuccess) return launch_failed();
+    if (ee && cudaEventRecord(ee, s) != cudaSuccess) return launch_failed();
     if (pb.reduce && !mean_in_kernel && launch_reduce_mean(pb, loss_out, s) != cudaSuccess)
-        return CE_ERR_LAUNCH;
+        return launch_failed();
     return CE_OK;
 }
 
@@ -457,7 +457,7 @@ ce_status bwd_common(const void* logits, int dtype, int64_t dim0, int64_t dim1, 
     bp.vec_ok = (reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(grad)) % 16 == 0 &&
                 ((strides[0] - grad_strides[0]) * es) % 16 == 0 &&
                 ((strides[1] - grad_strides[1]) * es) % 16 == 0;
-    if (launch_bwd(bp, stream) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (launch_bwd(bp, stream) != cudaSuccess) return launch_failed();
     return CE_OK;
 }
 
@@ -582,7 +582,7 @@ ce_status ce_vp_partials(const void* shard_logits, ce_dtype dtype, int64_t dim0,
     vp.ts1 = target_strides[1];
     vp.ignore_idx = ignore_idx;
     vp.part = reinterpret_cast<float4*>(partials);
-    if (launch_vp_partials(vp, static_cast<cudaStream_t>(stream)) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (launch_vp_partials(vp, static_cast<cudaStream_t>(stream)) != cudaSuccess) return launch_failed();
     return CE_OK;
 }
 
@@ -616,7 +616,7 @@ ce_status ce_vp_combine(const float* partials, int num_shards, const int64_t* sh
     pb.n_dev = reinterpret_cast<int64_t*>(w + kWsCountOffset);
     pb.ticket = reinterpret_cast<uint32_t*>(w + kWsTicketOffset);
     pb.loss_rows = reduce_loss ? reinterpret_cast<float*>(w + kWsHeaderBytes) : loss_out;
-    if (launch_count(pb, n_non_ignore_out, s) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (launch_count(pb, n_non_ignore_out, s) != cudaSuccess) return launch_failed();
     VpCombineProblem vc;
     vc.part = reinterpret_cast<const float4*>(partials);
     vc.R = num_shards;
@@ -630,8 +630,8 @@ ce_status ce_vp_combine(const float* partials, int num_shards, const int64_t* sh
     vc.a = label_smoothing;
     vc.loss = pb.loss_rows;
     vc.lse = lse_out;
-    if (launch_vp_combine(vc, s) != cudaSuccess) return CE_ERR_LAUNCH;
-    if (reduce_loss && launch_reduce_mean(pb, loss_out, s) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (launch_vp_combine(vc, s) != cudaSuccess) return launch_failed();
+    if (reduce_loss && launch_reduce_mean(pb, loss_out, s) != cudaSuccess) return launch_failed();
     return CE_OK;
 }
 
@@ -652,8 +652,8 @@ ce_status ce_get_error(const void* workspace, void* stream, uint32_t* host_err) 
     uint32_t v = 0;
     if (cudaMemcpyAsync(&v, static_cast<const char*>(workspace) + kWsErrOffset, sizeof v,
                         cudaMemcpyDeviceToHost, s) != cudaSuccess)
-        return CE_ERR_LAUNCH;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return CE_ERR_LAUNCH;
+        return launch_failed();
+    if (cudaStreamSynchronize(s) != cudaSuccess) return launch_failed();
     *host_err = v;
     if (v & CE_DEVERR_TIMEOUT) return CE_ERR_DEVICE_TIMEOUT;
     if (v & CE_DEVERR_TARGET_RANGE) return CE_ERR_TARGET_RANGE;
@@ -664,7 +664,7 @@ ce_status ce_wait_timeout_probe(void* workspace, size_t workspace_bytes, void* s
     if (!workspace || workspace_bytes < kWsHeaderBytes) return CE_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(workspace) % 16) return CE_ERR_INVALID_ARG;
     uint32_t* err = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kWsErrOffset);
-    if (launch_wait_probe(err, static_cast<cudaStream_t>(stream)) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (launch_wait_probe(err, static_cast<cudaStream_t>(stream)) != cudaSuccess) return launch_failed();
     return CE_OK;
 }
 
@@ -733,11 +733,11 @@ void* g_noalloc_device_ptr[kNoAllocMaxDevices];  // device address per device, s
 ce_status noalloc_scratch(void** out) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kNoAllocMaxDevices)
-        return CE_ERR_LAUNCH;
+        return launch_failed();
     std::lock_guard<std::mutex> lock(g_noalloc_mutex);
     if (!g_noalloc_device_ptr[dev]) {
         void* p = nullptr;
-        if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || !p) return CE_ERR_LAUNCH;
+        if (cudaGetSymbolAddress(&p, g_noalloc_scratch) != cudaSuccess || !p) return launch_failed();
         g_noalloc_device_ptr[dev] = p;
     }
     *out = g_noalloc_device_ptr[dev];

@@ -786,7 +786,7 @@ extern "C" ce_status ce_embed_fwd(const int64_t* tokens, int64_t dim0, int64_t d
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     EmbedFwdArgs a;
     a.err = workspace ? reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kWsErrOffset) : nullptr;
-    if (a.err && cudaMemsetAsync(a.err, 0, 4, s) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (a.err && cudaMemsetAsync(a.err, 0, 4, s) != cudaSuccess) return launch_failed();
     if (N == 0) return CE_OK;
     const int es = elem_size(dtype);
     a.tok = tokens;
@@ -809,7 +809,7 @@ extern "C" ce_status ce_embed_fwd(const int64_t* tokens, int64_t dim0, int64_t d
     cudaError_t e = dtype == CE_F32    ? launch_fwd_t<float>(a, vb, s)
                     : dtype == CE_BF16 ? launch_fwd_t<__nv_bfloat16>(a, vb, s)
                                        : launch_fwd_t<__half>(a, vb, s);
-    return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
+    return e == cudaSuccess ? CE_OK : launch_failed();
 }
 
 extern "C" size_t ce_embed_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V) {
@@ -870,7 +870,7 @@ extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t 
         cudaError_t e = dtype == CE_F32    ? launch_few<float>(fa, true, vb, s)
                         : dtype == CE_BF16 ? launch_few<__nv_bfloat16>(fa, w32, vb, s)
                                            : launch_few<__half>(fa, w32, vb, s);
-        return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
+        return e == cudaSuccess ? CE_OK : launch_failed();
     }
 
     SortArgs sa;
@@ -903,7 +903,7 @@ extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t 
             sa.zstride = sa.zbytes = all < row ? all : row;
         }
     }
-    if (launch_sort(sa, s) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (launch_sort(sa, s) != cudaSuccess) return launch_failed();
     if (N == 0) return CE_OK;
 
     GradArgs ga;
@@ -923,5 +923,5 @@ extern "C" ce_status ce_embed_bwd(const void* grad_out, ce_dtype dtype, int64_t 
     cudaError_t e = dtype == CE_F32    ? launch_grad_t<float>(ga, true, vb, s)
                     : dtype == CE_BF16 ? launch_grad_t<__nv_bfloat16>(ga, w32, vb, s)
                                        : launch_grad_t<__half>(ga, w32, vb, s);
-    return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
+    return e == cudaSuccess ? CE_OK : launch_failed();
 }

@@ -158,6 +158,12 @@ struct VpCombineProblem {
 };
 
 int elem_size(int dtype);
+// What an entry returns after a runtime call has failed.  The error is taken out of
+// the runtime, where the next launch's check would find it for its own.
+inline ce_status launch_failed() {
+    cudaGetLastError();
+    return CE_ERR_LAUNCH;
+}
 // A kernel's dynamic shared memory past the default limit, from an SM configured
 // for as much as there is: by its own choice the driver may leave room for fewer
 // CTAs than fit (five row sets of 20 KB: one CTA per SM in place of two).

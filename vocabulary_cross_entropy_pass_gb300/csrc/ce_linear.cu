@@ -135,19 +135,19 @@ ce_status ce_linear_fwd_bwd(const void* hidden, const void* weight, ce_dtype dty
     all.row_claim = reinterpret_cast<uint32_t*>(w + kWsRowClaimOffset);
     all.row_done = reinterpret_cast<uint32_t*>(w + kWsRowDoneOffset);
     all.loss_rows = reduce_loss ? reinterpret_cast<float*>(w + L.rows_off) : loss_out;
-    if (launch_count(all, n_non_ignore_out, s) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (launch_count(all, n_non_ignore_out, s) != cudaSuccess) return launch_failed();
     if (N == 0) {
-        if (reduce_loss && launch_reduce_mean(all, loss_out, s) != cudaSuccess) return CE_ERR_LAUNCH;
+        if (reduce_loss && launch_reduce_mean(all, loss_out, s) != cudaSuccess) return launch_failed();
         return CE_OK;
     }
 
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (cudaGetDevice(&dev) != cudaSuccess) return launch_failed();
     cublasHandle_t h = thread_handle(dev);
-    if (!h) return CE_ERR_LAUNCH;
-    if (cublasSetStream(h, s) != CUBLAS_STATUS_SUCCESS) return CE_ERR_LAUNCH;
+    if (!h) return launch_failed();
+    if (cublasSetStream(h, s) != CUBLAS_STATUS_SUCCESS) return launch_failed();
     if (cublasSetWorkspace(h, w + L.cublas_off, kCublasWorkspaceBytes) != CUBLAS_STATUS_SUCCESS)
-        return CE_ERR_LAUNCH;
+        return launch_failed();
     const cudaDataType_t ty = cuda_type(dtype);
     const float one = 1.f, zero = 0.f;
     char* chunk = w + L.chunk_off;
@@ -180,7 +180,7 @@ ce_status ce_linear_fwd_bwd(const void* hidden, const void* weight, ce_dtype dty
             lp.loss_rows = all.loss_rows + r0;
             lp.lse = reinterpret_cast<float*>(w + L.lse_off);
             lp.err = all.err;
-            if (launch_lmhead(lp, s) != cudaSuccess) return CE_ERR_LAUNCH;
+            if (launch_lmhead(lp, s) != cudaSuccess) return launch_failed();
             //    the gradient in place over the chunk's logits, from lse
             if (grads) {
                 BwdProblem bp;
@@ -207,18 +207,18 @@ ce_status ce_linear_fwd_bwd(const void* hidden, const void* weight, ce_dtype dty
                 bp.vec_ok = true;
                 bp.vocab_offset = 0;
                 bp.V_total = V;
-                if (launch_bwd(bp, s) != cudaSuccess) return CE_ERR_LAUNCH;
+                if (launch_bwd(bp, s) != cudaSuccess) return launch_failed();
             }
         } else {
             // 1. logits of the chunk, row-major (rows, V): column-major C[V, rows] = W^T-op . h
             if (cublasGemmEx(h, CUBLAS_OP_T, CUBLAS_OP_N, (int)V, (int)rows, (int)H, &one, weight, ty,
                              (int)H, hid + (size_t)r0 * H * es, ty, (int)H, &zero, chunk, ty, (int)V,
                              CUBLAS_COMPUTE_32F, CUBLAS_GEMM_DEFAULT) != CUBLAS_STATUS_SUCCESS)
-                return CE_ERR_LAUNCH;
+                return launch_failed();
             //    the cross-entropy pass over the chunk, gradient in place,
             //    after the GEMM has completed (see ce_order_kernel)
             ce_order_kernel<<<1, 32, 0, s>>>();
-            if (cudaGetLastError() != cudaSuccess) return CE_ERR_LAUNCH;
+            if (cudaGetLastError() != cudaSuccess) return launch_failed();
             const int64_t c_strides[3] = {rows * V, V, 1};
             const int64_t ct_strides[2] = {rows, 1};
             Problem pb;
@@ -234,7 +234,7 @@ ce_status ce_linear_fwd_bwd(const void* hidden, const void* weight, ce_dtype dty
             pb.grad = grads;
             if (launch_main_pass(pb, nullptr, reinterpret_cast<float4*>(w + L.part_off),
                                  L.cublas_off - L.part_off, s) != cudaSuccess)
-                return CE_ERR_LAUNCH;
+                return launch_failed();
         }
         // 2. gradients through the projection
         if (grad_hidden &&
@@ -242,15 +242,15 @@ ce_status ce_linear_fwd_bwd(const void* hidden, const void* weight, ce_dtype dty
                          (int)H, chunk, ty, (int)ld, &zero,
                          static_cast<char*>(grad_hidden) + (size_t)r0 * H * es, ty, (int)H,
                          CUBLAS_COMPUTE_32F, CUBLAS_GEMM_DEFAULT) != CUBLAS_STATUS_SUCCESS)
-            return CE_ERR_LAUNCH;
+            return launch_failed();
         if (grad_weight &&
             cublasGemmEx(h, CUBLAS_OP_N, CUBLAS_OP_T, (int)H, (int)V, (int)rows, &one,
                          hid + (size_t)r0 * H * es, ty, (int)H, chunk, ty, (int)ld, &one, grad_weight,
                          CUDA_R_32F, (int)H, CUBLAS_COMPUTE_32F,
                          CUBLAS_GEMM_DEFAULT) != CUBLAS_STATUS_SUCCESS)
-            return CE_ERR_LAUNCH;
+            return launch_failed();
     }
-    if (reduce_loss && launch_reduce_mean(all, loss_out, s) != cudaSuccess) return CE_ERR_LAUNCH;
+    if (reduce_loss && launch_reduce_mean(all, loss_out, s) != cudaSuccess) return launch_failed();
     return CE_OK;
 }
 

@@ -709,7 +709,7 @@ ce_status logits_common(const void* grad, const int64_t* grad_strides, const voi
     a.listed = a.hist_max + a.bias_max > 0;
     if (!a.listed) a.table = nullptr;
     cudaError_t e = bwd ? launch_logits<true>(a, dtype, s) : launch_logits<false>(a, dtype, s);
-    return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
+    return e == cudaSuccess ? CE_OK : launch_failed();
 }
 
 }  // namespace

@@ -1032,7 +1032,7 @@ extern "C" ce_status ce_rmsnorm_fwd(const void* x, const void* residual, const v
     cudaError_t e = dtype == CE_F32    ? launch_fwd_t<float>(a, vb, s)
                     : dtype == CE_BF16 ? launch_fwd_t<__nv_bfloat16>(a, vb, s)
                                        : launch_fwd_t<__half>(a, vb, s);
-    return e == cudaSuccess ? CE_OK : CE_ERR_LAUNCH;
+    return e == cudaSuccess ? CE_OK : launch_failed();
 }
 
 extern "C" size_t ce_rmsnorm_bwd_workspace_bytes(int64_t N, int64_t H) {
@@ -1068,7 +1068,7 @@ extern "C" ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const v
         }
     } else {
         // no rows: the weight's gradient is an empty sum
-        if (grad_weight && cudaMemsetAsync(grad_weight, 0, (size_t)H * 4, s) != cudaSuccess) return CE_ERR_LAUNCH;
+        if (grad_weight && cudaMemsetAsync(grad_weight, 0, (size_t)H * 4, s) != cudaSuccess) return launch_failed();
         return CE_OK;
     }
     NormBwdArgs a;
@@ -1097,7 +1097,7 @@ extern "C" ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const v
     cudaError_t e = dtype == CE_F32    ? launch_bwd_t<float>(a, vb, &shifted, s)
                     : dtype == CE_BF16 ? launch_bwd_t<__nv_bfloat16>(a, vb, &shifted, s)
                                        : launch_bwd_t<__half>(a, vb, &shifted, s);
-    if (e != cudaSuccess) return CE_ERR_LAUNCH;
+    if (e != cudaSuccess) return launch_failed();
     if (grad_weight) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)((H + 31) / 32));
@@ -1111,7 +1111,7 @@ extern "C" ce_status ce_rmsnorm_bwd(const void* grad_out, const void* h, const v
         const uint32_t step = shifted && N > 1 ? (uint32_t)(a.hs & 15) : 0u;
         if (cudaLaunchKernelEx(&cfg, ce_rmsnorm_dw_kernel, (const float*)a.part, bwd_grid(N, H), H, grad_weight, low,
                                step, es) != cudaSuccess)
-            return CE_ERR_LAUNCH;
+            return launch_failed();
     }
     return CE_OK;
 }
