@@ -3,7 +3,8 @@ _gbce_torch.so (torch tensors into that ABI) with g++.
 
 Each translation unit is compiled for sm_103a in its own nvcc process, in
 parallel, then linked into vocabulary_cross_entropy_pass_gb300/libgbce.so; the
-host module is compiled beside them and linked against it.
+host module is compiled beside them and linked against it.  The library needs
+nvcc alone: it is linked first, and without torch it is all there is to build.
 """
 from __future__ import annotations
 
@@ -42,8 +43,10 @@ def _deps() -> list[str]:
     return out
 
 
-def _torch_dir() -> str:
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+def _torch_dir() -> str | None:
+    """The installed torch's folder, or None."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec else None
 
 
 def _compile_ext(obj: str) -> None:
@@ -69,9 +72,10 @@ def _link_ext(obj: str) -> None:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(EXT):
+    made = [LIB, EXT] if _torch_dir() else [LIB]
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -94,16 +98,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
     ext_obj = os.path.join(BUILD_DIR, "ce_torch.o")
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        ext = ex.submit(_compile_ext, ext_obj)
+        ext = ex.submit(_compile_ext, ext_obj) if _torch_dir() else None
         objs = list(ex.map(compile_one, SOURCES))
-        ext.result()
     tmp = LIB + f".tmp{os.getpid()}"
     res = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcublas"], capture_output=True,
                          text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
-    _link_ext(ext_obj)
+    if ext is not None:
+        ext.result()
+        _link_ext(ext_obj)
     return LIB
 
 
