@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kFewThreads) ce_embed_few_kernel(const __grid_
     }
     __shared__ uint16_t place[kFewTokens];
     __shared__ int count[IT * NW];
-    __shared__ float sums[NW][kFewCols];
+    __shared__ __align__(16) float sums[NW][kFewCols];  // written as float4
     const int i = blockIdx.x;
     const int64_t mine = token(i);
     int64_t t[IT];
