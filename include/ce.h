@@ -465,7 +465,7 @@ typedef struct {
     const int64_t* history;         /* token k of row r at history[r*history_stride + k];
                                        tokens outside [0, V) count nowhere */
     int64_t history_stride;
-    int64_t history_max;            /* tokens a row has room for */
+    int64_t history_max;            /* tokens a row has room for, below 2^30 */
     const int64_t* history_lengths; /* [N] tokens in use (clamped to [0, history_max]);
                                        NULL: all */
     const int64_t* prompt_lengths;  /* [N] the first ones are the prompt: they count for

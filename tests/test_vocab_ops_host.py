@@ -264,3 +264,11 @@ def test_process_logits_takes_no_buffers(lib, name):
     for value in (x.detach(), None):
         with pytest.raises(TypeError, match=name):
             pkg.process_logits(x, **{name: value})
+
+
+def test_logits_history_fits_its_count(lib):
+    # a column's count has 30 bits beside its two flags
+    p = dict(history=0x100, history_max=1 << 30, history_stride=1 << 30, frequency_penalty=0x200)
+    for bwd in (False, True):
+        assert logits(lib, p, bwd=bwd) == 1
+        assert logits(lib, dict(p, history_max=(1 << 30) + 1), bwd=bwd) == 1

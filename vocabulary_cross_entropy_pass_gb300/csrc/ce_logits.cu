@@ -635,7 +635,7 @@ ce_status logits_common(const void* grad, const int64_t* grad_strides, const voi
     const int64_t N = dim0 * dim1;
     for (int k = 0; k < 2; ++k)
         if (q->reserved[k] != 0) return CE_ERR_INVALID_ARG;
-    if (q->history_max < 0 || q->bias_max < 0 || q->history_max > 0x40000000LL || q->bias_max > 0x40000000LL)
+    if (q->history_max < 0 || q->bias_max < 0 || q->history_max >= 0x40000000LL || q->bias_max > 0x40000000LL)
         return CE_ERR_INVALID_ARG;
     if (N > 0) {
         if (!logits || !out || (bwd && !grad)) return CE_ERR_INVALID_ARG;
