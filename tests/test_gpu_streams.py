@@ -116,3 +116,21 @@ def test_the_current_stream_handed_in_by_any_name():
     side.synchronize()
     assert same(got, want)
     assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+def test_a_workspace_is_one_run_of_memory():
+    # a view's elements say more than its memory holds
+    one = torch.zeros(1, dtype=torch.uint8, device=DEV)
+    spaced = torch.zeros(1 << 21, dtype=torch.uint8, device=DEV)
+    x, p, size = logits_inputs()
+    go, w = torch.zeros(60, 64, device=DEV), torch.ones(64, device=DEV)
+    t = torch.zeros(60, dtype=torch.int64, device=DEV)
+    many = 1 << 27
+    assert size < many
+    for ws in (one.expand(many), spaced[::2]):
+        for call in (lambda: pkg.ce_embed_fwd(t, go, workspace=ws), lambda: pkg.ce_embed_bwd(go, t, 60, workspace=ws),
+                     lambda: pkg.ce_rmsnorm_bwd(go, go, w, workspace=ws),
+                     lambda: pkg.ce_logits_process(x, workspace=ws, **p),
+                     lambda: pkg.ce_logits_process_bwd(x, x, workspace=ws, **p)):
+            with pytest.raises(ValueError, match="contiguous"):
+                call()

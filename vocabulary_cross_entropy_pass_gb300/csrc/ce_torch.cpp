@@ -109,6 +109,11 @@ void matches(const Tensor& t, const Tensor& like, const char* name) {
     if (t.scalar_type() != like.scalar_type() || !t.sizes().equals(like.sizes()))
         value_error(std::string(name) + " must match in shape and dtype");
 }
+// A workspace is one run of memory: its bytes are counted from its elements.
+void workspace(const Tensor& t, const Tensor& like) {
+    beside(t, like, "workspace");
+    if (t.defined() && !t.is_contiguous()) value_error("workspace must be contiguous");
+}
 size_t bytes(const Tensor& t) { return t.defined() ? t.numel() * t.element_size() : 0; }
 void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
@@ -200,7 +205,7 @@ PyObject* embed_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t V = weight.size(0), H = weight.size(1);
         const Launch on(a[6], weight);
         const Tokens t = tokens_of(tokens, weight);
-        beside(ws, weight, "workspace");
+        workspace(ws, weight);
         at::DimVector shape(tokens.sizes());
         shape.push_back(H);
         if (!out.defined()) {
@@ -251,7 +256,7 @@ PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!ws.defined())
             ws = on.empty({(int64_t)ce_embed_bwd_workspace_bytes(t.d0 * t.d1, H, V)}, at::kByte, g);
         else
-            beside(ws, g, "workspace");
+            workspace(ws, g);
         done(ce_embed_bwd(g.data_ptr(), dt, stride(g, H, "grad_out"), t.t.const_data_ptr<int64_t>(), t.d0, t.d1, t.s,
                           V, H, number(a[3]), integer(a[4]), dw.data_ptr(), (ce_dtype)wdt,
                           stride(dw, H, "grad_weight"), accumulate, ws.data_ptr(), bytes(ws), on.stream),
@@ -357,7 +362,7 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (dw.scalar_type() != at::kFloat || dw.dim() != 1 || dw.size(0) != H || !dw.is_contiguous())
                 type_error("grad_weight must be a contiguous float32 vector of H elements");
         }
-        beside(ws, h, "workspace");
+        workspace(ws, h);
         if (dw.defined() && !ws.defined()) ws = on.empty({(int64_t)ce_rmsnorm_bwd_workspace_bytes(N, H)}, at::kByte, h);
         done(ce_rmsnorm_bwd(g.data_ptr(), h.data_ptr(), w.data_ptr(), ptr(dh), dt, wdt, N, H, stride(g, H, "grad_out"),
                             hs, stride(dh, H, "grad_h"), number(a[3]), dx.data_ptr(), stride(dx, H, "grad_x"),
@@ -465,7 +470,7 @@ ce_logits_params logits_params(PyObject* given, int64_t N, int64_t V, const Tens
 Tensor logits_workspace(const Launch& on, const Tensor& given, const ce_logits_params& p, const Dims& d, ce_dtype dt,
                         const Tensor& like) {
     if (given.defined()) {
-        beside(given, like, "workspace");
+        workspace(given, like);
         return given;
     }
     const size_t need =
