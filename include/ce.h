@@ -490,7 +490,9 @@ typedef struct {
  *   z_j = s_j ? (x_j > 0 ? x_j / repetition : x_j * repetition) : x_j
  *   y_j = (z_j - frequency * c_j - presence * [c_j > 0] + b_j) / temperature
  *   out_j = allowed_j ? y_j : mask_value
- * A token that is not allowed gives mask_value whatever its logit (NaN
+ * In CE_F32 a quotient is rounded once; in the 16-bit types it is a product with
+ * the rounded reciprocal (at most 2^-23 of the value more, before the rounding to
+ * the type).  A token that is not allowed gives mask_value whatever its logit (NaN
  * included); a row that allows none is mask_value throughout.  ce_fwd_bwd on
  * the result needs a finite mask_value (say -3e4: its smoothing term sums the
  * logits).  out may be the logits themselves (same strides).
@@ -508,7 +510,7 @@ ce_status ce_logits_process(const void* logits, ce_dtype dtype, int64_t dim0, in
 /* Gradient of ce_logits_process with respect to the logits:
  *   grad_j = allowed_j ? grad_out_j / temperature * (s_j ? (x_j > 0 ? 1 / repetition
  *                        : repetition) : 1) : 0
- * The logits are read where the history holds their token; the biases, the counts
+ * with quotients as above.  The logits are read where the history holds their token; the biases, the counts
  * and mask_value play no part.  grad may be grad_out (same strides), not the
  * logits.  workspace as for ce_logits_process. */
 ce_status ce_logits_process_bwd(const void* grad_out, const int64_t grad_out_strides[3],

@@ -113,3 +113,24 @@ def test_many_biases_of_one_token():
         s = s + b
     one = {"bias_tokens": p["bias_tokens"], "bias_values": p["bias_values"]}
     assert float(pkg.ce_logits_process(x, **one)[0, 77]) == float(x[0, 77].cpu() + s)
+
+
+@pytest.mark.parametrize("N,V", [(3, 5000), (40, 70001)])
+def test_float32_quotients_are_rounded_once(N, V):
+    # the repetition penalty's and the temperature's division, bit for bit
+    x, p = make(N, V, 300, 0, torch.float32, N)
+    rep, temp = p["repetition_penalty"][:, None], p["temperature"][:, None]
+    inside = torch.arange(300, device=DEV)[None] < p["history_lengths"][:, None]
+    seen = spread(p["history"], inside.float(), V) > 0
+    q = {k: p[k] for k in ("history", "history_lengths", "repetition_penalty")}
+    z = torch.where(seen, torch.where(x > 0, x / rep, x * rep), x)
+    assert torch.equal(pkg.ce_logits_process(x, temperature=p["temperature"]), x / temp)
+    assert torch.equal(pkg.ce_logits_process(x, **q), z)
+    assert torch.equal(pkg.ce_logits_process(x, temperature=p["temperature"], **q), z / temp)
+    go = torch.randn_like(x)
+    g = torch.where(seen, torch.where(x > 0, go / rep, go * rep), go)
+    assert torch.equal(pkg.ce_logits_process_bwd(go, x, temperature=p["temperature"], **q), g / temp)
+    # values that a quotient takes out of the ordinary range, and an odd offset
+    x[0, :6] = torch.tensor([float("inf"), -float("inf"), 0.0, -0.0, 1e-40, 3e38])
+    assert torch.equal(pkg.ce_logits_process(x[:, 1:], temperature=p["temperature"]), x[:, 1:] / temp)
+    assert torch.equal(pkg.ce_logits_process(x, temperature=p["temperature"]), x / temp)
