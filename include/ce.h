@@ -402,7 +402,8 @@ ce_status ce_embed_fwd(const int64_t* tokens, int64_t dim0, int64_t dim1,
  *   accumulate   0: every element is written (zeros for tokens that do not
  *                occur).  1 (CE_F32 only): added to what is there, rows of
  *                tokens that do not occur are not touched -- the tied matrix's
- *                float32 gradient that ce_linear_fwd_bwd has added to.
+ *                float32 gradient that ce_linear_fwd_bwd has added to.  Values
+ *                below 2^-126, there or in a sum, are taken as zeros.
  *   workspace    ce_embed_bwd_workspace_bytes(N, H, V) bytes, 16-byte aligned,
  *                no initialisation; not shared by calls that may overlap. */
 size_t ce_embed_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V);
@@ -425,8 +426,11 @@ typedef enum { CE_QUANT_NONE = 0, CE_QUANT_E4M3 = 1, CE_QUANT_E5M2 = 2 } ce_quan
  *                (out_stride in bytes): y_j / scale rounded to nearest even and
  *                saturated, scale = max(max |y_j| / top, 2^-126) over each run of
  *                group_size columns (32, 64 or 128; 0: the row), top = 448
- *                (e4m3) or 57344 (e5m2).  A group that holds an infinity or a
- *                NaN has no finite values to give.
+ *                (e4m3) or 57344 (e5m2).  The quotient takes one rounding to
+ *                float32, from h_j weight_j and its group's maximum, before that to
+ *                8 bits; the scale's last bits go with the order of the row's sum
+ *                (its width and alignment).  A group that holds an infinity or a NaN
+ *                has no finite values to give.
  *   scales       with quant: float32 (N, ceil(H / group)) contiguous.
  *   residual_out h: N rows in `dtype`.  It may replace x or residual, and out (without
  *                quant) x or residual, with the same strides; other overlaps
@@ -510,9 +514,9 @@ ce_status ce_logits_process(const void* logits, ce_dtype dtype, int64_t dim0, in
 /* Gradient of ce_logits_process with respect to the logits:
  *   grad_j = allowed_j ? grad_out_j / temperature * (s_j ? (x_j > 0 ? 1 / repetition
  *                        : repetition) : 1) : 0
- * with quotients as above.  The logits are read where the history holds their token; the biases, the counts
- * and mask_value play no part.  grad may be grad_out (same strides), not the
- * logits.  workspace as for ce_logits_process. */
+ * with quotients as above.  The logits are read where the history holds their
+ * token; the biases, the counts and mask_value play no part.  grad may be grad_out
+ * (same strides), not the logits.  workspace as for ce_logits_process. */
 ce_status ce_logits_process_bwd(const void* grad_out, const int64_t grad_out_strides[3],
                                 const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1,
                                 int64_t V, const int64_t strides[3],

@@ -377,3 +377,26 @@ def test_rows_past_32_bits():
     go = y[at]
     gx, _ = pkg.ce_rmsnorm_bwd(y, x, w, grad_x=y)
     check_bwd(gx[at], None, go, x[at], w, None)
+
+
+@pytest.mark.parametrize("quant,least,bits", [(torch.float8_e4m3fn, -6, 3), (torch.float8_e5m2, -14, 2)])
+@pytest.mark.parametrize("N,H,group", [(1000, 1024, 128), (200, 8192, 0), (1000, 1003, 64), (100, 20480, 32)])
+def test_8_bits_on_rounding_borders(N, H, group, quant, least, bits):
+    """q_j is t_j top / max|t| (t = h w in float32) with one rounding of 2^-24 before
+    that to 8 bits: within half a step and 2^-23 of it, and half-way values, which
+    a float holds, go to the even neighbour."""
+    top = FP8[quant][0]
+    x, r, w = make(N, H, torch.bfloat16, N + H)
+    y, _, _ = pkg.ce_rmsnorm_fwd(d(x), d(w), residual=d(r), quant=quant, group_size=group)
+    t = (x.float() + r.float()) * w.float()
+    cols = torch.arange(H) // (group or H)
+    m = torch.zeros(N, int(cols[-1]) + 1).scatter_reduce_(1, cols[None].expand(N, -1), t.abs(), "amax")
+    v = t.double() * top / m.double()[:, cols]
+    powers = 2.0 ** torch.arange(-40, 40, dtype=torch.float64)
+    step = powers[(torch.frexp(v.abs())[1] - 1).clamp(min=least) - bits + 40]
+    even = torch.round(v / step) * step
+    half = (v / step).abs() % 1 == 0.5
+    got = y.float().double().cpu()
+    assert int(half.sum()) > 10
+    assert torch.equal(got[half], even[half])
+    assert bool(((got - v).abs() <= step / 2 + v.abs() * 2.0 ** -23).all())

@@ -17,7 +17,7 @@
 // writes dx.  A row's elements stay in registers between the statistics and
 // the output.  Measured, of the GPU's 6.70 TB/s copy rate (bf16, GPU time of a call in
 // a graph): forward of 16384 x 4096 with a residual 80.4 us, 6.68 TB/s; to e4m3 with a
-// scale for 128 columns, 8192 x 8192, 81.4 us, 5.8 TB/s (its conversions keep the
+// scale for 128 columns, 8192 x 8192, 81.9 us, 5.8 TB/s (its conversions keep the
 // schedulers at 75 %); gradients of 16384 x 4096 89.5 us, 6.0 TB/s.  Rows off the
 // 16-byte grid run at about half that.
 #include <cuda_fp8.h>
@@ -67,19 +67,50 @@ __device__ __forceinline__ float cta_max(float v, float* red) {
     return warp_allmax(t);
 }
 
-template <int VEC>
-__device__ __forceinline__ void store_q8(char* p, const float* y, float inv, int kind) {
+// 8-bit values of a group, from t_j = h_j w_j (y_j = t_j rstd): with m = max|t| the
+// scale is m / top rstd and q_j = t_j top / m.  The factor top / m is kept as a
+// float and what that leaves (hi + lo), so q_j takes one rounding before that to 8
+// bits and a value on a rounding border goes to the definition's side (34 million
+// values of bf16 rows in groups of 128: none off the rounded definition; with a
+// factor of one float 11 of a million, and 80.1 us for 8192 x 8192 against 81.9).
+// A scale at its least value, or an m whose reciprocal may not be finite: y_j times
+// 1 / scale.
+struct Group {
+    float hi, lo, scale;
+    bool direct;           // t_j is taken, not y_j
+};
+__device__ __forceinline__ Group group_of(float m, float to_scale, float top) {
+    Group g;
+    g.scale = fmaxf(m * to_scale, kTinyScale);
+    g.direct = g.scale > kTinyScale && m > 0x1p-100f && m < 0x1p100f;
+    const float d = g.direct ? m : g.scale, n = g.direct ? top : 1.f;
+    const float inv = __fdividef(1.f, d);
+    g.hi = n * inv;
+    g.lo = fmaf(-g.hi, d, n) * inv;
+    return g;
+}
+// PAIRS: two values to an instruction (in the wide kernel they took more than they
+// gave: 2048 x 20480 in float32 150 -> 162 us).
+template <int VEC, bool PAIRS = true>
+__device__ __forceinline__ void store_q8(char* p, float* t, const Group& g, float rstd, int kind) {
     Pack<uint8_t, VEC> o;
+    if (!g.direct) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) t[i] *= rstd;
+    }
     const __nv_fp8_interpretation_t k = kind == 1 ? __NV_E4M3 : __NV_E5M2;
     if constexpr (VEC >= 2) {
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) {
-            const uint16_t two = __nv_cvt_float2_to_fp8x2(make_float2(y[i] * inv, y[i + 1] * inv), __NV_SATFINITE, k);
+            const float2 f = make_float2(t[i], t[i + 1]);
+            const float2 q = PAIRS ? __ffma2_rn(f, make_float2(g.hi, g.hi), __fmul2_rn(f, make_float2(g.lo, g.lo)))
+                                   : make_float2(fmaf(f.x, g.hi, f.x * g.lo), fmaf(f.y, g.hi, f.y * g.lo));
+            const uint16_t two = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, k);
             o.v[i] = (uint8_t)two;
             o.v[i + 1] = (uint8_t)(two >> 8);
         }
     } else {
-        o.v[0] = __nv_cvt_float_to_fp8(y[0] * inv, __NV_SATFINITE, k);
+        o.v[0] = __nv_cvt_float_to_fp8(fmaf(t[0], g.hi, t[0] * g.lo), __NV_SATFINITE, k);
     }
     o.store(p);
 }
@@ -201,9 +232,18 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
             } else {
                 load_w<T, VEC>(p, (int64_t)v * VEC, w);
             }
-            // 8 bits: y / rstd, and rstd goes into each group's factor
+            // 8 bits: t, and rstd goes into the scales
+            if constexpr (Q8 && VEC % 2 == 0) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) h[k][i] *= Q8 ? w[i] : rstd * w[i];
+                for (int i = 0; i < VEC; i += 2) {
+                    const float2 t = __fmul2_rn(make_float2(h[k][i], h[k][i + 1]), make_float2(w[i], w[i + 1]));
+                    h[k][i] = t.x;
+                    h[k][i + 1] = t.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) h[k][i] *= Q8 ? w[i] : rstd * w[i];
+            }
         }
     }
     char* y = p.y + row * p.ys;
@@ -220,27 +260,17 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
             if (tid + k * TH >= nv) am[k] = 0.f;
         }
         float* sc = p.scales + row * (int64_t)p.groups;
-        // a group's scale from its largest |y / rstd|, and what y / rstd times gives q
-        // (the approximate reciprocal, off by 2^-23 of a value then rounded to 2^-4)
         const float to_scale = rstd / p.top;
-        auto scale_of = [&](float m) { return fmaxf(m * to_scale, kTinyScale); };
-        auto factor_of = [&](float scale, float* v, int n) {
-            const float inv = __fdividef(1.f, scale), f = rstd * inv;
-            if (f <= 3.4e38f) return f;
-#pragma unroll
-            for (int i = 0; i < n; ++i) v[i] *= rstd;  // a scale near the least: in two steps
-            return inv;
-        };
-        float whole = 0.f;  // the scale of all columns, where there is one
+        Group whole = {};  // of all columns, where there is one group
         if (p.groups == 1) {
             float m = 0.f;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) m = fmaxf(m, am[k]);
-            whole = scale_of(cta_max(m, red + 32));
-            if (tid == 0) sc[0] = whole;
+            whole = group_of(cta_max(m, red + 32), to_scale, p.top);
+            if (tid == 0) sc[0] = whole.scale;
         }
         if constexpr (STAGED) {
-            // the row's float32 y in shared memory; then a warp to each group of
+            // the row's float32 t in shared memory; then a warp to each group of
             // columns, lanes side by side
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
@@ -263,18 +293,17 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
                     f[i] = i < per && c0 + i < p.H ? stage[c0 + i] : 0.f;
                     m = fmaxf(m, fabsf(f[i]));
                 }
-                float s = whole;
+                Group s = whole;
                 if (p.groups > 1) {
-                    s = scale_of(warp_allmax(m));
-                    if (lane == 0) sc[g] = s;
+                    s = group_of(warp_allmax(m), to_scale, p.top);
+                    if (lane == 0) sc[g] = s.scale;
                 }
-                const float inv = factor_of(s, f, 4);
                 if (four && c0 + 4 <= p.H) {
-                    store_q8<4>(y + c0, f, inv, p.kind);
+                    store_q8<4>(y + c0, f, s, rstd, p.kind);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (i < per && c0 + i < p.H) store_q8<1>(y + c0 + i, f + i, inv, p.kind);
+                        if (i < per && c0 + i < p.H) store_q8<1>(y + c0 + i, f + i, s, rstd, p.kind);
                 }
             }
         } else {
@@ -282,17 +311,13 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) ce_rmsnorm_fwd_kernel(c
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int v = tid + k * TH;
+                Group s = whole;
                 if (p.groups > 1) {
                     for (int o = gl >> 1; o > 0; o >>= 1) am[k] = fmaxf(am[k], __shfl_xor_sync(kFull, am[k], o));
-                    am[k] = scale_of(am[k]);
-                    if (v < nv && (v & (gl - 1)) == 0) sc[v / gl] = am[k];
-                } else {
-                    am[k] = whole;
+                    s = group_of(am[k], to_scale, p.top);
+                    if (v < nv && (v & (gl - 1)) == 0) sc[v / gl] = s.scale;
                 }
-                if (v < nv) {
-                    const float f = factor_of(am[k], h[k], VEC);
-                    store_q8<VEC>(y + (int64_t)v * VEC, h[k], f, p.kind);
-                }
+                if (v < nv) store_q8<VEC>(y + (int64_t)v * VEC, h[k], s, rstd, p.kind);
             }
         }
     }
@@ -329,6 +354,7 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_fwd_wide_kernel(const __grid_c
     ss = cta_sum(ss, red);
     const float rstd = rsqrtf(fmaf(ss, p.inv_h, p.eps));
     float* sc = p.scales + row * (int64_t)p.groups;
+    const float to_scale = rstd / p.top;
     if constexpr (Q8) {
         for (int g = tid; g < p.groups; g += TH) gmax[g] = 0u;
         __syncthreads();
@@ -340,12 +366,12 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_fwd_wide_kernel(const __grid_c
                 get(v, h);
                 load_w<T, VEC>(p, v * VEC, w);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(h[i] * (rstd * w[i])));
+                for (int i = 0; i < VEC; ++i) m = fmaxf(m, fabsf(h[i] * w[i]));
                 atomicMax(&gmax[v * VEC / p.group], __float_as_uint(m));
             }
         }
         __syncthreads();
-        for (int g = tid; g < p.groups; g += TH) sc[g] = fmaxf(__uint_as_float(gmax[g]) / p.top, kTinyScale);
+        for (int g = tid; g < p.groups; g += TH) sc[g] = group_of(__uint_as_float(gmax[g]), to_scale, p.top).scale;
     }
     char* y = p.y + row * p.ys;
     char* ho = p.h ? p.h + row * p.hs : nullptr;
@@ -361,10 +387,10 @@ __global__ void __launch_bounds__(512) ce_rmsnorm_fwd_wide_kernel(const __grid_c
             o.store(ho + v * VEC * ES);
         }
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) h[i] *= rstd * w[i];
+        for (int i = 0; i < VEC; ++i) h[i] *= Q8 ? w[i] : rstd * w[i];
         if constexpr (Q8) {
-            const float s = fmaxf(__uint_as_float(gmax[v * VEC / p.group]) / p.top, kTinyScale);
-            store_q8<VEC>(y + v * VEC, h, 1.f / s, p.kind);
+            store_q8<VEC, false>(y + v * VEC, h, group_of(__uint_as_float(gmax[v * VEC / p.group]), to_scale, p.top),
+                                 rstd, p.kind);
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) o.set(i, h[i]);
