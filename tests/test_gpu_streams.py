@@ -134,3 +134,52 @@ def test_a_workspace_is_one_run_of_memory():
                      lambda: pkg.ce_logits_process_bwd(x, x, workspace=ws, **p)):
             with pytest.raises(ValueError, match="contiguous"):
                 call()
+
+
+def pass_calls():
+    """The cross-entropy passes, each with its inputs twice (one overwrites them)."""
+    g = rng(7)
+    N, V, H = 64, 50257, 72
+    x = torch.randn(1, N, V, generator=g).to(torch.bfloat16).to(DEV)
+    t = torch.randint(0, V, (1, N), generator=g).to(DEV)
+    lse = torch.empty(N, device=DEV)
+    n = torch.empty(1, dtype=torch.int64, device=DEV)
+    pkg.ce_fwd_only(x, t, reduce_loss=True, lse_out=lse, n_non_ignore_out=n)
+    part = pkg.ce_vp_partials(x, t, 0).unsqueeze(0).repeat(1, 1, 2)[:, :, :4]  # not contiguous
+    hidden = torch.randn(N, 2 * H, generator=g).to(torch.bfloat16).to(DEV)[:, ::2]
+    weight = torch.randn(900, H, generator=g).to(torch.bfloat16).to(DEV)
+    few = t[0] % 900
+    twice = [x.clone(), x.clone()]
+
+    def in_place(**kw):
+        y = twice.pop()
+        return pkg.ce_fwd_bwd(y, t, reduce_loss=True, **kw), y
+
+    size = pkg.ce_workspace_bytes(1, N, V, torch.bfloat16)
+    return {
+        "loss": (lambda **kw: pkg.ce_fwd_only(x, t, reduce_loss=True, **kw), [size]),
+        "loss and gradient": (in_place, [size]),
+        "gradient": (lambda **kw: pkg.ce_bwd(x, t, lse, reduce_loss=True, n_non_ignore=n, **kw), []),
+        "partials": (lambda **kw: pkg.ce_vp_partials(x, t, 0, **kw), []),
+        "combined": (lambda **kw: pkg.ce_vp_combine(part, [0, V], t, reduce_loss=True, **kw), [size, N * 16]),
+        "shard's gradient": (lambda **kw: pkg.ce_vp_bwd(x, t, 0, V, lse, **kw), []),
+        "lm_head": (lambda **kw: pkg.ce_linear_fwd_bwd(hidden, weight, few, reduce_loss=True, **kw),
+                    [N * H * 2, 900 * H * 4]),
+    }
+
+
+@pytest.mark.parametrize("name", ["loss", "loss and gradient", "gradient", "partials", "combined", "shard's gradient",
+                                  "lm_head"])
+def test_the_passes_memory_belongs_to_the_stream_handed_in(name):
+    call, sizes = pass_calls()[name]
+    want = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(WAIT)
+    got = call(stream=side)
+    junk = [torch.full((n,), 171, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(4)]
+    side.synchronize()
+    assert same(got, want)
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    del junk

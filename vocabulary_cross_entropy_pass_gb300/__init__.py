@@ -25,6 +25,8 @@ raises if it is missing.  There is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 
 import torch
 
@@ -128,12 +130,41 @@ def _workspace(workspace, d0, d1, V, dtype, opts, device):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _on_its_stream(fn):
+    """``fn``, whose ``stream`` is the current one for as long as the call lasts: what
+    it allocates, copies or zeroes is of that stream, and the tensors it returns are
+    recorded for the caller's own."""
+    names = list(inspect.signature(fn).parameters)
+    at = names.index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        dev = getattr(args[0] if args else kw.get(names[0]), "device", None)
+        if stream is None or dev is None or dev.type != "cuda":
+            return fn(*args, **kw)
+        before = torch.cuda.current_stream(dev)
+        if stream.cuda_stream == before.cuda_stream:
+            return fn(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=dev)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kw)
+        for t in out if isinstance(out, tuple) else (out,):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(before)
+        return out
+
+    return call
+
+
 def _stream(device, stream):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+@_on_its_stream
 def ce_fwd_bwd(logits: torch.Tensor, targets: torch.Tensor, label_smoothing: float = 0.0,
                ignore_idx: int = -100, reduce_loss: bool = False, dloss: torch.Tensor | None = None,
                layout: str = "bsv", loss_out: torch.Tensor | None = None,
@@ -172,6 +203,7 @@ def ce_fwd_bwd(logits: torch.Tensor, targets: torch.Tensor, label_smoothing: flo
     return loss_out
 
 
+@_on_its_stream
 def ce_fwd_only(logits: torch.Tensor, targets: torch.Tensor, label_smoothing: float = 0.0,
                 ignore_idx: int = -100, reduce_loss: bool = False, layout: str = "bsv",
                 loss_out: torch.Tensor | None = None, lse_out: torch.Tensor | None = None,
@@ -268,6 +300,7 @@ def ce_status_string(status: int) -> str:
 
 
 
+@_on_its_stream
 def ce_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
            label_smoothing: float = 0.0, ignore_idx: int = -100, reduce_loss: bool = False,
            dloss: torch.Tensor | None = None, n_non_ignore: torch.Tensor | None = None,
@@ -345,6 +378,7 @@ def parallel_cross_entropy(inp: torch.Tensor, target: torch.Tensor, label_smooth
 
 
 # ---------------------------------------------------------------- vocabulary parallel
+@_on_its_stream
 def ce_vp_partials(shard: torch.Tensor, targets: torch.Tensor, vocab_offset: int,
                    partials: torch.Tensor | None = None, ignore_idx: int = -100,
                    stream=None) -> torch.Tensor:
@@ -364,6 +398,7 @@ def ce_vp_partials(shard: torch.Tensor, targets: torch.Tensor, vocab_offset: int
     return partials
 
 
+@_on_its_stream
 def ce_vp_combine(partials: torch.Tensor, shard_offsets, targets: torch.Tensor,
                   label_smoothing: float = 0.0, ignore_idx: int = -100, reduce_loss: bool = False,
                   loss_out: torch.Tensor | None = None, lse_out: torch.Tensor | None = None,
@@ -395,6 +430,7 @@ def ce_vp_combine(partials: torch.Tensor, shard_offsets, targets: torch.Tensor,
     return loss_out, lse_out
 
 
+@_on_its_stream
 def ce_vp_bwd(shard: torch.Tensor, targets: torch.Tensor, vocab_offset: int, V_total: int,
               lse: torch.Tensor, label_smoothing: float = 0.0, ignore_idx: int = -100,
               reduce_loss: bool = False, dloss: torch.Tensor | None = None,
@@ -445,6 +481,7 @@ def vocab_parallel_cross_entropy(shards, targets: torch.Tensor, label_smoothing:
 
 
 # ---------------------------------------------------------------- lm_head + cross-entropy
+@_on_its_stream
 def ce_linear_fwd_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                       label_smoothing: float = 0.0, ignore_idx: int = -100,
                       reduce_loss: bool = False, dloss: torch.Tensor | None = None,
