@@ -29,7 +29,8 @@
 // its rows in order, and further CTAs zero the rows of tokens that do not occur.
 // 16384 tokens of 4096 bf16 added to a 128000-row float32 gradient: 12.5 us of
 // sorting, 61 us of sums (360 MB, 0.88 of the copy rate), 10 us of joining (the most
-// frequent token's 29 parts), 88 us together.
+// frequent token's 29 parts), 88 us together; 65536 tokens 253 us, 131072 (sorted
+// through global memory) 464, 0.69 of the copy rate.
 #include "ce_device.cuh"
 #include "ce_internal.h"
 #include "ce_pack.cuh"

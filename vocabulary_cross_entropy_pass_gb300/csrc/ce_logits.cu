@@ -28,9 +28,9 @@
 //           logits of its columns again while L2 still holds them (read by the
 //           first kernel they came from HBM a second time, 64 bytes for each).
 // Biases of one column are added in list order by one warp.
-// bf16, 512 rows of 128000 columns: 39.6 us without lists and mask (6.6 TB/s, 0.99
-// of the copy rate), 41.4 us under masks of which one row of four is free (235 MB in
-// 128-byte lines: 35 us), 77 us with histories of 4096 and 64 biases as well (17.6 us
+// bf16, 512 rows of 128000 columns: 40.6 us without lists and mask (6.5 TB/s, 0.97
+// of the copy rate), 41.5 us under masks of which one row of four is free (235 MB in
+// 128-byte lines: 35 us), 77 us with histories of 4096 and 64 biases as well (17.1 us
 // of it the list kernel, which its shared-memory atomics and scans keep busy).
 #include "ce_device.cuh"
 #include "ce_internal.h"

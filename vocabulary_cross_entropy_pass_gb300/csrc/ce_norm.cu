@@ -17,9 +17,12 @@
 // writes dx.  A row's elements stay in registers between the statistics and
 // the output.  Measured, of the GPU's 6.70 TB/s copy rate (bf16, GPU time of a call in
 // a graph): forward of 16384 x 4096 with a residual 80.4 us, 6.68 TB/s; to e4m3 with a
-// scale for 128 columns, 8192 x 8192, 81.9 us, 5.8 TB/s (its conversions keep the
-// schedulers at 75 %); gradients of 16384 x 4096 89.5 us, 6.0 TB/s.  Rows off the
-// 16-byte grid run at about half that.
+// scale for 128 columns, 8192 x 8192, 83.2 us, 5.7 TB/s (its conversions keep the
+// schedulers at 75 %); gradients of 16384 x 4096 88.1 us, 6.1 TB/s.  Rows off the
+// 16-byte grid, 16384 x 4097: forward 154 us (0.52 of the copy rate), gradients 133
+// (0.60), e4m3 230 (0.30); short ones, 32768 x 511 and 777, 0.3 to 0.5.  A float32
+// weight under 16-bit rows, which is loaded an element at a time: forward of 16384 x
+// 4096 92 us, gradients 89.7.
 #include <cuda_fp8.h>
 
 #include "ce_device.cuh"
@@ -72,7 +75,8 @@ __device__ __forceinline__ float cta_max(float v, float* red) {
 // float and what that leaves (hi + lo), so q_j takes one rounding before that to 8
 // bits and a value on a rounding border goes to the definition's side (34 million
 // values of bf16 rows in groups of 128: none off the rounded definition; with a
-// factor of one float 11 of a million, and 80.1 us for 8192 x 8192 against 81.9).
+// factor of one float 11 of a million, and 80.1 us for 8192 x 8192, its outputs given,
+// against 81.9).
 // A scale at its least value, or an m whose reciprocal may not be finite: y_j times
 // 1 / scale.
 struct Group {
@@ -912,7 +916,11 @@ __global__ void __launch_bounds__(1024) ce_rmsnorm_dw_kernel(const float* part, 
 // partial row for each): two per SM, more for short rows, whose barrier each is
 // paid over fewer bytes (bf16, 32768 rows, GB/s of algorithmic bytes with two /
 // four / eight per SM: 2048 wide 5290 / 5840, 1024 wide with four / eight 4820 /
-// 5330; 4096 wide with two / three 6000 / 5840).
+// 5330; 4096 wide with two / three 6000 / 5840).  A ring has up to eight row
+// sets in such a share of the SM's shared memory.  Where fewer than three fit (bf16
+// with a residual: 776 to 1023, 1544 to 2047, 3080 to 4095 and more than 6144
+// columns), it takes up to eight from all of it; fewer CTAs than these are then
+// resident, and the grid runs in waves.
 int bwd_per_sm(int64_t H) { return H >= 4096 ? 2 : (H >= 2048 ? 4 : (H >= 1024 ? 8 : 16)); }
 int bwd_grid(int64_t N, int64_t H) {
     if (H <= kShortWidth) {
