@@ -524,6 +524,108 @@ ce_status ce_logits_process_bwd(const void* grad_out, const int64_t grad_out_str
                                 const int64_t grad_strides[3], void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A row's log-probabilities: given tokens', the entropy, the likeliest tokens';
+ * and the divergence from a teacher's.  The conventions above hold; rows are rows
+ * of logits as for ce_fwd_bwd, flattened r = i*dim1 + j (dim0*dim1 below 2^31).
+ * Lists of tokens are int64 (dim0, dim1, n), element (i, j, k) at
+ * tokens[i*strides[0] + j*strides[1] + k*strides[2]], strides not negative.
+ * Arithmetic is float32 on differences from the row's maximum; sums are taken in
+ * an order fixed by the sizes.
+ */
+
+/* With lp_j = x_j - logsumexp(x):
+ *   logprobs       float32 [N][given]: lp of the given tokens (at most 1024 a row).
+ *                  A token equal to ignore_idx gives 0; any other outside [0, V) NaN
+ *                  and CE_DEVERR_TARGET_RANGE in the workspace's error word.
+ *   entropy        float32 [N] or NULL: -sum_j exp(lp_j) lp_j.
+ *   top_k          0 to min(256, V): the k largest logits, in falling order, equal
+ *                  ones the lower column first (-0 is 0):
+ *   top_tokens     int64 [N][top_k], top_logprobs float32 [N][top_k].
+ *   stats          float32 [N][4], 16-byte aligned, or NULL: {max, log sum exp(x - max),
+ *                  entropy, 0} for ce_logprobs_bwd.
+ *   workspace      ce_logprobs_workspace_bytes(dim0*dim1, V, dtype, top_k) bytes, 16-byte
+ *                  aligned, no initialisation; not shared by calls that may overlap.
+ * A row whose given tokens (one at least) are all ignore_idx is not read: zeros, and
+ * ignore_idx for its top tokens.  A row of -inf throughout (a mask that allows
+ * nothing) has log-probabilities of -inf, entropy 0 and top tokens 0, 1, 2, ...  A NaN
+ * or +inf in a row makes its log-probabilities and its entropy NaN; a NaN is never
+ * among the top tokens (-1 where no others are left). */
+size_t ce_logprobs_workspace_bytes(int64_t N, int64_t V, ce_dtype dtype, int top_k);
+ce_status ce_logprobs_fwd(const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1, int64_t V,
+                          const int64_t strides[3], const int64_t* tokens,
+                          const int64_t token_strides[3], int64_t given, int64_t ignore_idx,
+                          float* logprobs, float* entropy, int top_k, int64_t* top_tokens,
+                          float* top_logprobs, float* stats, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Gradient of ce_logprobs_fwd's log-probabilities and entropy H with respect to the
+ * logits, from the stats it left (p_j = exp(lp_j)):
+ *   grad_j = sum_k g_k [t_k = j] - p_j sum_k g_k - h p_j (lp_j + H)
+ *   grad_logprobs  float32 [N][given] g, or NULL;  grad_entropy  float32 [N] h, or NULL.
+ *   grad           in the logits' dtype with its own strides: the logits themselves
+ *                  (same strides) or memory that does not overlap them.
+ * Zeros for a row that was not read and for one of -inf throughout; ignored and
+ * out-of-range tokens give nothing; a token given twice gets both. */
+ce_status ce_logprobs_bwd(const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1, int64_t V,
+                          const int64_t strides[3], const int64_t* tokens,
+                          const int64_t token_strides[3], int64_t given, int64_t ignore_idx,
+                          const float* stats, const float* grad_logprobs,
+                          const float* grad_entropy, void* grad, const int64_t grad_strides[3],
+                          void* stream);
+
+/* Distillation from a teacher's top logits, forward and backward in one pass.  With
+ * s = 1/temperature, p = softmax(s x) over the vocabulary and q_k the teacher's
+ * probability of its token t_k (k < K, 1 <= K <= 1024),
+ *   q_k = exp(s z_k) / sum_k exp(s z_k)  (normalize), or exp(s z_k) as it is
+ *   loss = temperature^2 sum_k q_k (log q_k - log p_{t_k})
+ *   grad_j = dloss temperature (p_j sum_k q_k - sum_k q_k [t_k = j])
+ *   teacher_tokens  int64 (dim0, dim1, K).  A row whose first token is ignore_idx is
+ *                   ignored: loss 0, zero gradient, not counted.  A later ignore_idx
+ *                   leaves that entry out (its logit is not read).  Any other token
+ *                   outside [0, V): loss NaN, zero gradient, CE_DEVERR_TARGET_RANGE.
+ *   teacher_logits  (dim0, dim1, K) z in teacher_dtype with strides not negative; -inf
+ *                   gives q_k = 0.  Without normalize: log-probabilities, those of
+ *                   ce_logprobs_fwd, say (temperature 1); the tokens that are not
+ *                   listed then take no part.
+ *   temperature     1e-4 to 1e4.
+ *   dloss, reduce_loss, loss_out, n_non_ignore_out: as for ce_fwd_bwd.
+ *   grad            as for ce_logprobs_bwd.
+ *   workspace       ce_distill_workspace_bytes(dim0*dim1, V, dtype) bytes, 16-byte
+ *                   aligned, no initialisation; not shared by calls that may overlap.
+ * Tokens listed twice are two entries.  A row of logits of -inf throughout has p = 0:
+ * loss +inf where some q_k > 0, zero gradient. */
+size_t ce_distill_workspace_bytes(int64_t N, int64_t V, ce_dtype dtype);
+ce_status ce_distill_fwd_bwd(const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1,
+                             int64_t V, const int64_t strides[3], const int64_t* teacher_tokens,
+                             const int64_t teacher_token_strides[3], const void* teacher_logits,
+                             ce_dtype teacher_dtype, const int64_t teacher_strides[3], int64_t K,
+                             float temperature, int normalize, int64_t ignore_idx, int reduce_loss,
+                             const float* dloss, float* loss_out, void* grad,
+                             const int64_t grad_strides[3], int64_t* n_non_ignore_out,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Forward only.  stats: float32 [N][4], 16-byte aligned, or NULL: {max of the logits, log sum
+ * exp(s (x - max)), max of the teacher's logits, log sum exp(s (z - max))} for
+ * ce_distill_bwd; an ignored row's are {-inf, 0, -inf, 0}. */
+ce_status ce_distill_fwd(const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1, int64_t V,
+                         const int64_t strides[3], const int64_t* teacher_tokens,
+                         const int64_t teacher_token_strides[3], const void* teacher_logits,
+                         ce_dtype teacher_dtype, const int64_t teacher_strides[3], int64_t K,
+                         float temperature, int normalize, int64_t ignore_idx, int reduce_loss,
+                         float* loss_out, float* stats, int64_t* n_non_ignore_out, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Backward only, from ce_distill_fwd's stats (and its n_non_ignore_out with
+ * reduce_loss); no workspace. */
+ce_status ce_distill_bwd(const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1, int64_t V,
+                         const int64_t strides[3], const int64_t* teacher_tokens,
+                         const int64_t teacher_token_strides[3], const void* teacher_logits,
+                         ce_dtype teacher_dtype, const int64_t teacher_strides[3], int64_t K,
+                         float temperature, int normalize, int64_t ignore_idx, int reduce_loss,
+                         const float* stats, const float* dloss, const int64_t* n_non_ignore,
+                         void* grad, const int64_t grad_strides[3], void* stream);
+
 /* Waits for `stream`, then copies the device error word of the last pass that
  * used `workspace` into *host_err (host pointer).  Returns CE_OK,
  * CE_ERR_TARGET_RANGE or CE_ERR_DEVICE_TIMEOUT from its bits, CE_ERR_LAUNCH if

@@ -17,7 +17,10 @@ torch.autograd.Function with that interface's argument list.  Around the pass
 (vocab_ops.py): ce_embed_* (rows of the vocabulary matrix and their gradient),
 ce_rmsnorm_* (residual + root-mean-square norm) and ce_logits_process*
 (penalties, biases, masks, temperature), with their autograd forms
-``embedding``, ``rms_norm`` and ``process_logits``.
+``embedding``, ``rms_norm`` and ``process_logits``; beside it (logprob_ops.py):
+ce_logprobs_* (tokens' log-probabilities, entropy, likeliest tokens) and
+ce_distill_* (the divergence from a teacher's top logits), with
+``token_logprobs`` and ``distillation_loss``.
 
 Importing the package does not load the library; the first call does, and
 raises if it is missing.  There is no CPU fallback.
@@ -34,6 +37,9 @@ from . import _lib
 from ._lib import (CE_PATH_AUTO, CE_PATH_CLUSTER, CE_PATH_ROW, CE_PATH_STREAM,
                    CE_PATH_TWO_STAGE, CE_PATH_VECROW, CE_PATH_WARP, CEError, ce_options,
                    make_options)
+from .logprob_ops import (ce_distill_bwd, ce_distill_fwd, ce_distill_fwd_bwd, ce_distill_workspace_bytes,
+                          ce_logprobs_bwd, ce_logprobs_fwd, ce_logprobs_workspace_bytes, distillation_loss,
+                          token_logprobs)
 from .vocab_ops import (ce_embed_bwd, ce_embed_bwd_workspace_bytes, ce_embed_fwd, ce_logits_process,
                         ce_logits_process_bwd, ce_logits_workspace_bytes, ce_rmsnorm_bwd,
                         ce_rmsnorm_bwd_workspace_bytes, ce_rmsnorm_fwd, embedding, process_logits, rms_norm)
@@ -44,6 +50,8 @@ __all__ = ["ce_fwd_bwd", "ce_fwd_bwd_noalloc", "ce_fwd_only", "ce_bwd", "paralle
            "ce_embed_fwd", "ce_embed_bwd", "ce_embed_bwd_workspace_bytes", "embedding",
            "ce_rmsnorm_fwd", "ce_rmsnorm_bwd", "ce_rmsnorm_bwd_workspace_bytes", "rms_norm",
            "ce_logits_process", "ce_logits_process_bwd", "ce_logits_workspace_bytes", "process_logits",
+           "ce_logprobs_fwd", "ce_logprobs_bwd", "ce_logprobs_workspace_bytes", "token_logprobs",
+           "ce_distill_fwd_bwd", "ce_distill_fwd", "ce_distill_bwd", "ce_distill_workspace_bytes", "distillation_loss",
            "ce_workspace_bytes", "ce_get_error", "ce_noalloc_get_error",
            "ce_status_string",
            "ce_wait_timeout_probe",

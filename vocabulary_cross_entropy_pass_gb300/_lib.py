@@ -39,7 +39,9 @@ EXPORTS = ("ce_workspace_bytes", "ce_fwd_bwd", "ce_fwd_only", "ce_get_error", "c
            "ce_vp_bwd", "ce_linear_workspace_bytes", "ce_linear_fwd_bwd", "ce_wait_timeout_probe",
            "ce_noalloc_get_error", "ce_embed_fwd", "ce_embed_bwd_workspace_bytes", "ce_embed_bwd",
            "ce_rmsnorm_fwd", "ce_rmsnorm_bwd_workspace_bytes", "ce_rmsnorm_bwd",
-           "ce_logits_workspace_bytes", "ce_logits_process", "ce_logits_process_bwd")
+           "ce_logits_workspace_bytes", "ce_logits_process", "ce_logits_process_bwd",
+           "ce_logprobs_workspace_bytes", "ce_logprobs_fwd", "ce_logprobs_bwd", "ce_distill_workspace_bytes",
+           "ce_distill_fwd_bwd", "ce_distill_fwd", "ce_distill_bwd")
 
 
 class ce_options(ctypes.Structure):
@@ -160,6 +162,22 @@ def load(path: str = LIB_PATH):
         lib.ce_logits_process_bwd.restype = i32
         lib.ce_logits_process_bwd.argtypes = [vp, I64_3, vp, i32, i64, i64, i64, I64_3, lp, vp,
                                               I64_3, vp, size, vp]
+        lib.ce_logprobs_workspace_bytes.restype = size
+        lib.ce_logprobs_workspace_bytes.argtypes = [i64, i64, i32, i32]
+        rows = [vp, i32, i64, i64, i64, I64_3]
+        lib.ce_logprobs_fwd.restype = i32
+        lib.ce_logprobs_fwd.argtypes = rows + [vp, I64_3, i64, i64, vp, vp, i32, vp, vp, vp, vp, size, vp]
+        lib.ce_logprobs_bwd.restype = i32
+        lib.ce_logprobs_bwd.argtypes = rows + [vp, I64_3, i64, i64, vp, vp, vp, vp, I64_3, vp]
+        lib.ce_distill_workspace_bytes.restype = size
+        lib.ce_distill_workspace_bytes.argtypes = [i64, i64, i32]
+        teacher = [vp, I64_3, vp, i32, I64_3, i64, f32, i32, i64, i32]
+        lib.ce_distill_fwd_bwd.restype = i32
+        lib.ce_distill_fwd_bwd.argtypes = rows + teacher + [vp, vp, vp, I64_3, vp, vp, size, vp]
+        lib.ce_distill_fwd.restype = i32
+        lib.ce_distill_fwd.argtypes = rows + teacher + [vp, vp, vp, vp, size, vp]
+        lib.ce_distill_bwd.restype = i32
+        lib.ce_distill_bwd.argtypes = rows + teacher + [vp, vp, vp, vp, I64_3, vp]
         lib.ce_wait_timeout_probe.restype = i32
         lib.ce_wait_timeout_probe.argtypes = [vp, ctypes.c_size_t, vp]
         lib.ce_get_error.restype = i32

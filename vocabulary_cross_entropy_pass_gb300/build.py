@@ -24,7 +24,8 @@ EXT = os.path.join(HERE, "_gbce_torch.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["ce_api.cu", "ce_aux.cu", "ce_bwd.cu", "ce_fused.cu", "ce_rows.cu", "ce_split.cu",
            "ce_vecrow.cu", "ce_linear.cu", "ce_lmhead.cu", "ce_stream.cu", "ce_stream_geo.cu",
-           "ce_vp.cu", "ce_embed.cu", "ce_norm.cu", "ce_logits.cu"]
+           "ce_vp.cu", "ce_embed.cu", "ce_norm.cu", "ce_logits.cu", "ce_logprobs.cu",
+           "ce_softgrad.cu", "ce_distill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", f"-I{os.path.join(ROOT, 'include')}"]

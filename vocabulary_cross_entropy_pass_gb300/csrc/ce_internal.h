@@ -169,6 +169,8 @@ inline ce_status launch_failed() {
 // CTAs than fit (five row sets of 20 KB: one CTA per SM in place of two).
 cudaError_t allow_smem(const void* kernel, size_t bytes);
 bool fused_aligned(const Problem& p);
+// Whether rows of V elements at (i * s[0] + j * s[1]) share none.
+bool rows_apart(int64_t d0, int64_t d1, int64_t V, const int64_t* s);
 int fused_capacity(int dtype, int threads);  // elements one CTA can hold
 int split_auto_chunks(int64_t V);
 

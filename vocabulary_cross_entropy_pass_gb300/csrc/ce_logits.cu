@@ -633,7 +633,8 @@ size_t logits_workspace(const LogitArgs& a) {
     return start_bytes(a) + table_bytes(a) + (a.bias_max > 0 ? table_bytes(a) / 2 : 0);
 }
 
-// Rows at (i * s0 + j * s1) that share no element.
+}  // namespace
+
 bool rows_apart(int64_t d0, int64_t d1, int64_t V, const int64_t* s) {
     int64_t in_s = s[1], in_n = d1, out_s = s[0], out_n = d0;
     if (in_n <= 1 || (out_n > 1 && s[0] < s[1])) {
@@ -643,6 +644,8 @@ bool rows_apart(int64_t d0, int64_t d1, int64_t V, const int64_t* s) {
     if (out_n > 1 && out_s < (in_n > 1 ? in_s * in_n : V)) return false;
     return true;
 }
+
+namespace {
 
 ce_status logits_common(const void* grad, const int64_t* grad_strides, const void* logits, ce_dtype dtype,
                         int64_t dim0, int64_t dim1, int64_t V, const int64_t* strides,

@@ -1,11 +1,11 @@
 // ce_torch.cpp -- torch tensors into the C ABI for the operators around the
-// cross-entropy pass (embedding, norm, logits): a CPython module of fast calls.
+// cross-entropy pass (embedding, norm, logits, log-probabilities, distillation): a CPython module of fast calls.
 //
 // These operators run at every decoding step, where a call through ctypes took
 // two to four times as long on the host (16 us for a norm) as its kernel on the
 // GPU.  The module checks its arguments, allocates the outputs that are not given
 // and enqueues; it holds no arithmetic.  Argument lists, semantics and documentation
-// are those of the functions of the same names in vocab_ops.py, which call
+// are those of the functions of the same names in vocab_ops.py and logprob_ops.py, which call
 // these with every argument by position.
 #include <Python.h>
 
@@ -523,6 +523,238 @@ PyObject* logits_process_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// A list of tokens for each row of logits: (rows), one token each, or (rows, n).
+struct Listed {
+    Tensor t;
+    int64_t n = 0, s[3] = {0, 0, 0};
+};
+Listed listed_of(const Tensor& t, const Tensor& logits, const char* name) {
+    Listed l;
+    if (!t.defined()) return l;
+    beside(t, logits, name);
+    const int64_t lead = logits.dim() - 1;
+    if ((t.dim() != lead && t.dim() != lead + 1) || !t.sizes().slice(0, lead).equals(logits.sizes().slice(0, lead)))
+        value_error(std::string(name) + " must be one value, or a list of them, for each row of logits");
+    l.t = t;
+    const auto st = t.strides();
+    l.n = t.dim() == lead ? 1 : t.size(lead);
+    l.s[2] = t.dim() == lead ? 0 : st[lead];
+    l.s[1] = st[lead - 1];
+    l.s[0] = lead == 2 ? st[0] : 0;
+    return l;
+}
+const int64_t* token_ptr(const Listed& l) {
+    if (!l.t.defined()) return nullptr;
+    if (l.t.scalar_type() != at::kLong) type_error("tokens must be int64");
+    return l.t.const_data_ptr<int64_t>();
+}
+// A float32 tensor of `numel` values, in order.
+float* floats(const Tensor& t, const Tensor& like, int64_t numel, const char* name) {
+    if (!t.defined()) return nullptr;
+    beside(t, like, name);
+    if (t.scalar_type() != at::kFloat || t.numel() != numel || !t.is_contiguous())
+        type_error(std::string(name) + " must be contiguous float32 with " + std::to_string(numel) + " values");
+    return static_cast<float*>(t.data_ptr());
+}
+int64_t* count_ptr(const Tensor& t, const Tensor& like, const char* name) {
+    if (!t.defined()) return nullptr;
+    beside(t, like, name);
+    if (t.scalar_type() != at::kLong || t.numel() != 1) type_error(std::string(name) + " must be one int64");
+    return static_cast<int64_t*>(t.data_ptr());
+}
+void put(PyObject* tuple, int k, const Tensor& t) {
+    PyObject* o = Py_None;
+    if (t.defined()) {
+        o = THPVariable_Wrap(t);
+        if (!o) throw PythonError{};
+    } else {
+        Py_INCREF(o);
+    }
+    PyTuple_SET_ITEM(tuple, k, o);
+}
+struct Tuple {  // released where it was not handed out
+    PyObject* o;
+    explicit Tuple(Py_ssize_t n) : o(PyTuple_New(n)) {
+        if (!o) throw PythonError{};
+    }
+    ~Tuple() { Py_XDECREF(o); }
+    PyObject* out() {
+        PyObject* r = o;
+        o = nullptr;
+        return r;
+    }
+};
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PythonError{};
+    return v != 0;
+}
+
+// ce_logprobs_fwd(logits, tokens, top_k, entropy, stats, ignore_idx, workspace, stream)
+PyObject* logprobs_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        arity(n, 8);
+        const Tensor& x = tensor(a[0], "logits");
+        const ce_dtype dt = cuda(x, "logits");
+        const Dims d = logits_dims(x, "logits");
+        const Listed l = listed_of(maybe(a[1], "tokens"), x, "tokens");
+        const int64_t* tokens = token_ptr(l);
+        const int64_t top_k = integer(a[2]), N = d.d0 * d.d1;
+        const bool want_entropy = truth(a[3]), want_stats = truth(a[4]);
+        Tensor ws = maybe(a[6], "workspace");
+        workspace(ws, x);
+        if (top_k < 0 || top_k > 256 || top_k > d.V) value_error("top_k must be between 0 and min(256, V)");
+        if (l.n == 0 && top_k == 0 && !want_entropy && !want_stats)
+            value_error("nothing asked for: tokens, top_k, entropy or stats");
+        const Launch on(a[7], x);
+        Tensor lp, ent, top, top_lp, stats;
+        at::DimVector shape(x.sizes().slice(0, x.dim() - 1));
+        if (l.t.defined()) lp = on.output(l.t.sizes(), at::kFloat, x);
+        if (want_entropy) ent = on.output(shape, at::kFloat, x);
+        if (want_stats) stats = on.output({N, 4}, at::kFloat, x);
+        if (top_k) {
+            shape.push_back(top_k);
+            top = on.output(shape, at::kLong, x);
+            top_lp = on.output(shape, at::kFloat, x);
+        }
+        if (!ws.defined()) ws = on.empty({(int64_t)ce_logprobs_workspace_bytes(N, d.V, dt, (int)top_k)}, at::kByte, x);
+        done(ce_logprobs_fwd(x.data_ptr(), dt, d.d0, d.d1, d.V, d.s, tokens, l.s, l.n, integer(a[5]),
+                             static_cast<float*>(ptr(lp)), static_cast<float*>(ptr(ent)), (int)top_k,
+                             static_cast<int64_t*>(ptr(top)), static_cast<float*>(ptr(top_lp)),
+                             static_cast<float*>(ptr(stats)), ptr(ws), bytes(ws), on.stream),
+             "ce_logprobs_fwd");
+        Tuple r(5);
+        put(r.o, 0, lp);
+        put(r.o, 1, ent);
+        put(r.o, 2, top);
+        put(r.o, 3, top_lp);
+        put(r.o, 4, stats);
+        return r.out();
+    });
+}
+
+// The gradient's tensor, allocated when none is given.
+Tensor grad_of(const Tensor& given, const Tensor& x, const Launch& on) {
+    matches(given, x, "grad");
+    return given.defined() ? given : on.output(x.sizes(), x.scalar_type(), x);
+}
+
+// ce_logprobs_bwd(logits, stats, tokens, grad_logprobs, grad_entropy, ignore_idx, grad, stream)
+PyObject* logprobs_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        arity(n, 8);
+        const Tensor& x = tensor(a[0], "logits");
+        const ce_dtype dt = cuda(x, "logits");
+        const Dims d = logits_dims(x, "logits");
+        const int64_t N = d.d0 * d.d1;
+        const Tensor stats = tensor(a[1], "stats");
+        const Listed l = listed_of(maybe(a[2], "tokens"), x, "tokens");
+        const int64_t* tokens = token_ptr(l);
+        const Tensor gl = maybe(a[3], "grad_logprobs"), ge = maybe(a[4], "grad_entropy");
+        if (gl.defined() && l.n == 0) value_error("grad_logprobs goes with tokens");
+        const float* st = floats(stats, x, N * 4, "stats");
+        const float* g = floats(gl, x, N * l.n, "grad_logprobs");
+        const float* h = floats(ge, x, N, "grad_entropy");
+        const Launch on(a[7], x);
+        const Tensor grad = grad_of(maybe(a[6], "grad"), x, on);
+        const Dims o = logits_dims(grad, "grad");
+        done(ce_logprobs_bwd(x.data_ptr(), dt, d.d0, d.d1, d.V, d.s, tokens, l.s, l.n, integer(a[5]), st, g, h,
+                             grad.data_ptr(), o.s, on.stream),
+             "ce_logprobs_bwd");
+        return THPVariable_Wrap(grad);
+    });
+}
+
+// The teacher's tokens and logits.
+struct Taught {
+    Listed tokens, logits;
+    const int64_t* t;
+    ce_dtype dt;
+};
+Taught taught(PyObject* tokens, PyObject* logits, const Tensor& x) {
+    Taught r;
+    r.tokens = listed_of(tensor(tokens, "teacher_tokens"), x, "teacher_tokens");
+    r.logits = listed_of(tensor(logits, "teacher_logits"), x, "teacher_logits");
+    r.t = token_ptr(r.tokens);
+    r.dt = cuda(r.logits.t, "teacher_logits");
+    if (!r.tokens.t.sizes().equals(r.logits.t.sizes()))
+        value_error("teacher_tokens and teacher_logits must have the same shape");
+    return r;
+}
+
+// ce_distill_fwd(_bwd)(logits, teacher_tokens, teacher_logits, temperature, normalize, ignore_idx, reduce_loss, dloss,
+//                      grad (False: forward only, None, or a tensor), stats, loss_out, n_non_ignore_out, workspace,
+//                      stream)
+PyObject* distill_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        arity(n, 14);
+        const Tensor& x = tensor(a[0], "logits");
+        const ce_dtype dt = cuda(x, "logits");
+        const Dims d = logits_dims(x, "logits");
+        const int64_t N = d.d0 * d.d1, ignore = integer(a[5]);
+        const Taught t = taught(a[1], a[2], x);
+        const float tau = number(a[3]);
+        const int normalize = truth(a[4]), reduce = truth(a[6]);
+        const bool backward = a[8] != Py_False, want_stats = truth(a[9]);
+        Tensor loss = maybe(a[10], "loss_out"), ws = maybe(a[12], "workspace"), grad, stats;
+        const Tensor dloss = maybe(a[7], "dloss");
+        const float* g = floats(dloss, x, reduce ? 1 : N, "dloss");
+        floats(loss, x, reduce ? 1 : N, "loss_out");
+        int64_t* count = count_ptr(maybe(a[11], "n_non_ignore_out"), x, "n_non_ignore_out");
+        workspace(ws, x);
+        const Launch on(a[13], x);
+        if (!loss.defined()) loss = on.output({reduce ? 1 : N}, at::kFloat, x);
+        if (!ws.defined()) ws = on.empty({(int64_t)ce_distill_workspace_bytes(N, d.V, dt)}, at::kByte, x);
+        int status;
+        if (backward) {
+            grad = grad_of(maybe(a[8], "grad"), x, on);
+            const Dims o = logits_dims(grad, "grad");
+            status = ce_distill_fwd_bwd(x.data_ptr(), dt, d.d0, d.d1, d.V, d.s, t.t, t.tokens.s, t.logits.t.data_ptr(),
+                                        t.dt, t.logits.s, t.tokens.n, tau, normalize, ignore, reduce, g,
+                                        static_cast<float*>(loss.data_ptr()), grad.data_ptr(), o.s, count, ptr(ws),
+                                        bytes(ws), on.stream);
+        } else {
+            if (want_stats) stats = on.output({N, 4}, at::kFloat, x);
+            status = ce_distill_fwd(x.data_ptr(), dt, d.d0, d.d1, d.V, d.s, t.t, t.tokens.s, t.logits.t.data_ptr(),
+                                    t.dt, t.logits.s, t.tokens.n, tau, normalize, ignore, reduce,
+                                    static_cast<float*>(loss.data_ptr()), static_cast<float*>(ptr(stats)), count,
+                                    ptr(ws), bytes(ws), on.stream);
+        }
+        done(status, backward ? "ce_distill_fwd_bwd" : "ce_distill_fwd");
+        Tuple r(2);
+        put(r.o, 0, loss);
+        put(r.o, 1, backward ? grad : stats);
+        return r.out();
+    });
+}
+
+// ce_distill_bwd(logits, teacher_tokens, teacher_logits, stats, temperature, normalize, ignore_idx, reduce_loss, dloss,
+//                n_non_ignore, grad, stream)
+PyObject* distill_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&] {
+        arity(n, 12);
+        const Tensor& x = tensor(a[0], "logits");
+        const ce_dtype dt = cuda(x, "logits");
+        const Dims d = logits_dims(x, "logits");
+        const int64_t N = d.d0 * d.d1;
+        const Taught t = taught(a[1], a[2], x);
+        const float* stats = floats(tensor(a[3], "stats"), x, N * 4, "stats");
+        const int reduce = truth(a[7]);
+        const Tensor dloss = maybe(a[8], "dloss");
+        const float* g = floats(dloss, x, reduce ? 1 : N, "dloss");
+        const int64_t* count = count_ptr(maybe(a[9], "n_non_ignore"), x, "n_non_ignore");
+        if (reduce && !count) value_error("reduce_loss needs the forward's n_non_ignore");
+        const Launch on(a[11], x);
+        const Tensor grad = grad_of(maybe(a[10], "grad"), x, on);
+        const Dims o = logits_dims(grad, "grad");
+        done(ce_distill_bwd(x.data_ptr(), dt, d.d0, d.d1, d.V, d.s, t.t, t.tokens.s, t.logits.t.data_ptr(), t.dt,
+                            t.logits.s, t.tokens.n, number(a[4]), truth(a[5]), integer(a[6]), reduce, stats, g, count,
+                            grad.data_ptr(), o.s, on.stream),
+             "ce_distill_bwd");
+        return THPVariable_Wrap(grad);
+    });
+}
+
 // row_stride(t): the stride between a tensor's rows, ValueError where they are not evenly spaced.
 PyObject* row_stride(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&] {
@@ -546,6 +778,10 @@ PyMethodDef methods[] = {{"embed_fwd", FAST(embed_fwd), "ce_embed_fwd"},
                          {"rmsnorm_bwd", FAST(rmsnorm_bwd), "ce_rmsnorm_bwd"},
                          {"logits_process", FAST(logits_process), "ce_logits_process"},
                          {"logits_process_bwd", FAST(logits_process_bwd), "ce_logits_process_bwd"},
+                         {"logprobs_fwd", FAST(logprobs_fwd), "ce_logprobs_fwd"},
+                         {"logprobs_bwd", FAST(logprobs_bwd), "ce_logprobs_bwd"},
+                         {"distill_fwd", FAST(distill_fwd), "ce_distill_fwd and ce_distill_fwd_bwd"},
+                         {"distill_bwd", FAST(distill_bwd), "ce_distill_bwd"},
                          {"row_stride", FAST(row_stride), "stride between a tensor's rows"},
                          {"set_error", set_error, METH_O, "the class of library errors"},
                          {nullptr, nullptr, 0, nullptr}};
