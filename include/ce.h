@@ -582,7 +582,7 @@ ce_status ce_logprobs_bwd(const void* logits, ce_dtype dtype, int64_t dim0, int6
  *   grad_j = dloss temperature (p_j sum_k q_k - sum_k q_k [t_k = j])
  *   teacher_tokens  int64 (dim0, dim1, K).  A row whose first token is ignore_idx is
  *                   ignored: loss 0, zero gradient, not counted.  A later ignore_idx
- *                   leaves that entry out (its logit is not read).  Any other token
+ *                   leaves that entry out, whatever its logit.  Any other token
  *                   outside [0, V): loss NaN, zero gradient, CE_DEVERR_TARGET_RANGE.
  *   teacher_logits  (dim0, dim1, K) z in teacher_dtype with strides not negative; -inf
  *                   gives q_k = 0.  Without normalize: log-probabilities, those of

@@ -4,9 +4,11 @@
 //   lp_j = x_j - logsumexp(x),   H = -sum_j exp(lp_j) lp_j,
 //   top: the K largest x in falling order (ties: the lower column first), with lp
 //
-// Bound by HBM: every logit is read once.  ce_scan_kernel reads a segment of a row in
-// tiles of 16 KB, sums its statistics and selects its candidates (ce_rowscan.cuh);
-// a row in one piece is finished by the CTA that read it, a row in segments by
+// Bound by HBM: every logit is read once.  ce_scan_kernel is a persistent grid, two CTAs
+// per SM; a warp of each keeps a ring of 16 KB tiles filled with bulk copies, segment
+// after segment and row after row, and eight warps take them out, sum the statistics and
+// select candidates (ce_rowscan.cuh), so the copies go on while a row is finished.  A
+// row in one piece is finished by the CTA that read it, a row in segments by
 // ce_join_kernel from their partial results.
 #include <math.h>
 
@@ -18,9 +20,9 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Whether row r is left out.  All scanning threads; a barrier where a row has several tokens.
-__device__ __forceinline__ bool row_skipped(const RowTokens& t, int64_t r, bool first) {
+__device__ __forceinline__ bool row_skipped(const RowTokens& t, int64_t r) {
     if (t.n == 0) return false;
-    if (first || t.n == 1) return t.at(r, 0) == t.ignore_idx;
+    if (t.n == 1) return t.at(r, 0) == t.ignore_idx;
     bool keep = false;
     for (int k = threadIdx.x; k < t.n; k += kScanThreads) keep |= t.at(r, k) != t.ignore_idx;
     return scan_count(keep) == 0;
@@ -76,61 +78,145 @@ __device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const S
     }
 }
 
+// Shared memory: the ring, its barriers, the candidates.
+constexpr int kTileBytes = kScanTileVecs * 16;
+constexpr int scan_stages(bool top) { return top ? 4 : 6; }  // two CTAs of 228 KB
+constexpr size_t scan_smem(bool top) {
+    return (size_t)scan_stages(top) * kTileBytes + (top ? sizeof(TopSmem) : 0);
+}
+
+struct Segment {
+    const char* x;     // the row
+    Span16 sp;
+    int64_t v0, v1;    // its vectors of the body
+    bool first, last;
+};
+template <int ES>
+__device__ __forceinline__ Segment segment(const ScanArgs& p, int64_t r, int seg) {
+    Segment g;
+    g.x = p.x + p.row.at(r) * ES;
+    g.sp = span16<ES>(g.x, 0, p.V);
+    g.first = seg == 0;
+    g.last = seg == p.segs - 1;
+    g.v0 = min(g.sp.nv, seg * p.per);
+    g.v1 = g.last ? g.sp.nv : min(g.sp.nv, g.v0 + p.per);
+    return g;
+}
+
 template <typename T, bool TOP, bool ENT>
-__global__ void __launch_bounds__(kScanThreads) ce_scan_kernel(const __grid_constant__ ScanArgs p) {
+__global__ void __launch_bounds__(kScanThreads + 32, 2) ce_scan_kernel(const __grid_constant__ ScanArgs p) {
     using VT = Vec<T>;
-    constexpr int VEC = VT::kElems, ES = sizeof(T);
-    extern __shared__ __align__(16) unsigned char sm[];
+    constexpr int VEC = VT::kElems, ES = sizeof(T), STAGES = scan_stages(TOP);
+    extern __shared__ __align__(128) unsigned char sm[];
+    __shared__ RingBars bars;
     __shared__ float4 red[kScanThreads / 32];
-    TopSmem& top = *reinterpret_cast<TopSmem*>(sm);
-    const int tid = threadIdx.x;
-    for (int64_t item = blockIdx.x; item < p.N * p.segs; item += gridDim.x) {
-        const int64_t r = item / p.segs;
-        const int seg = (int)(item - r * p.segs);
-        if (row_skipped(p.tokens, r, p.skip_first)) {
+    unsigned char* ring = sm;
+    TopSmem& top = *reinterpret_cast<TopSmem*>(sm + (size_t)STAGES * kTileBytes);
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid == 0) ring_init(bars, STAGES);
+    __syncthreads();
+    const int64_t items = p.N * p.segs;
+    auto row_of = [&](int64_t item) { return p.segs == 1 ? item : item / p.segs; };
+
+    if (tid >= kScanThreads) {  // the copying warp
+        const uint64_t policy = l2_evict_first_policy();
+        RingAt at;
+        uint32_t issued = 0;
+        const bool lists = p.tokens.n > 1;
+        int64_t y = p.tokens.n == 1 && blockIdx.x < items ? p.tokens.at(row_of(blockIdx.x), 0) : 0;
+        for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+            const int64_t r = row_of(item), next = item + gridDim.x;
+            bool skip = p.tokens.n == 1 && y == p.tokens.ignore_idx;
+            if (p.tokens.n == 1 && next < items) y = p.tokens.at(row_of(next), 0);
+            if (lists) {
+                bool keep = false;
+                for (int k = lane; k < p.tokens.n; k += 32) keep |= p.tokens.at(r, k) != p.tokens.ignore_idx;
+                skip = !__any_sync(kFull, keep);
+            }
+            if (skip) continue;
+            bool ok = true;
+            if (lane == 0) {
+                const Segment g = segment<ES>(p, r, (int)(item - r * p.segs));
+                const char* body = g.x + g.sp.h1 * ES;
+                for (int64_t f = g.v0; ok && f < g.v1; f += kScanTileVecs)
+                    ok = ring_put(bars, at, issued, STAGES, ring, kTileBytes, body + f * 16,
+                                  (uint32_t)min((int64_t)kScanTileVecs, g.v1 - f) * 16u, policy);
+                if (!ok) ring_drain(bars, issued, STAGES);
+            }
+            if (!__shfl_sync(kFull, ok, 0)) break;
+        }
+        return;
+    }
+
+    RingAt at;
+    int64_t y = p.tokens.n == 1 && blockIdx.x < items ? p.tokens.at(row_of(blockIdx.x), 0) : 0;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t r = row_of(item), next = item + gridDim.x;
+        bool skip = p.tokens.n == 1 && y == p.tokens.ignore_idx;
+        if (p.tokens.n == 1 && next < items) y = p.tokens.at(row_of(next), 0);
+        if (p.tokens.n > 1) skip = row_skipped(p.tokens, r);
+        if (skip) {
             if (!p.part) write_skipped(p, r);
             continue;
         }
-        const char* x = p.x + p.row.at(r) * ES;
-        const Span16 sp = span16<ES>(x, 0, p.V);
-        const int64_t v0 = min(sp.nv, seg * p.per), v1 = seg == p.segs - 1 ? sp.nv : min(sp.nv, v0 + p.per);
-        const T* body = reinterpret_cast<const T*>(x + sp.h1 * ES);
+        const Segment g = segment<ES>(p, r, (int)(item - r * p.segs));
         // the elements before the body go with the first segment, those after it with the last
-        const bool head = seg == 0 && tid < sp.h1;
-        const bool tail = seg == p.segs - 1 && sp.t0 + tid < p.V;
-        const float xh = head ? VT::load1(x + tid * ES) : -INFINITY;
-        const float xt = tail ? VT::load1(x + (sp.t0 + tid) * ES) : -INFINITY;
+        const bool head = g.first && tid < g.sp.h1;
+        const bool tail = g.last && g.sp.t0 + tid < p.V;
+        const float xh = head ? VT::load1(g.x + tid * ES) : -INFINITY;
+        const float xt = tail ? VT::load1(g.x + (g.sp.t0 + tid) * ES) : -INFINITY;
         Stat st = stat_identity();
-        if (head) stat_add(st, xh, p.L);
-        if (tail) stat_add(st, xt, p.L);
         TopState ts = {};
-        const int64_t ntiles = (v1 - v0 + kScanTileVecs - 1) / kScanTileVecs;
-        for (int64_t t = 0; t < ntiles || t == 0; ++t) {
-            const int64_t f = v0 + t * kScanTileVecs;
-            const int n = (int)min((int64_t)kScanTileVecs, v1 - f);
-            const T* tile = body + f * VEC;
+        typename VT::Max gm[kScanVecs];
+        int has = 0;
+        if constexpr (TOP) {
+            ts = top_start(top, p.top_k);
+#pragma unroll
+            for (int i = 0; i < kScanVecs; ++i) gm[i] = VT::max_init();
+            if (head) has = 1;
+        }
+        const int ntiles = (int)((g.v1 - g.v0 + kScanTileVecs - 1) / kScanTileVecs);
+        for (int t = 0; t < ntiles || t == 0; ++t) {
+            const int64_t f = g.v0 + (int64_t)t * kScanTileVecs;
+            const int n = (int)min((int64_t)kScanTileVecs, g.v1 - f);
+            const T* tile = reinterpret_cast<const T*>(ring + (size_t)at.s * kTileBytes);
             uint4 raw[kScanVecs];
             bool have[kScanVecs];
+            if (ntiles > 0) ring_wait(bars, at);
 #pragma unroll
             for (int i = 0; i < kScanVecs; ++i) {
                 have[i] = tid + i * kScanThreads < n;
-                if (have[i]) raw[i] = __ldg(reinterpret_cast<const uint4*>(tile) + tid + i * kScanThreads);
+                if (have[i]) raw[i] = reinterpret_cast<const uint4*>(tile)[tid + i * kScanThreads];
             }
-            float mx = stat_tile<T, kScanVecs, ENT>(st, raw, have, p.L);
+            float mx = stat_tile<T, kScanVecs, ENT, TOP>(st, raw, have, p.L, gm);
             if constexpr (TOP) {
                 const bool edge = t == 0 && head;
+                bool raised = false;
                 if (edge) mx = fmaxf(mx, xh);
-                if (t == 0) ts = top_start(top, p.top_k, have[0] || edge, mx);
-                top_tile<T>(top, ts, have[0] || edge, mx, tile, n, (uint32_t)(sp.h1 + f * VEC), edge, xh, tid);
-                if (t == 0 && !ts.all) ts.strict = true;
+                if (t == 0) {
+#pragma unroll
+                    for (int i = 0; i < kScanVecs; ++i) has |= have[i] ? 1 << i : 0;
+                }
+                if ((t & (t + 1)) == 0) raised = top_raise<T, kScanVecs>(top, ts, gm, has, edge ? xh : -INFINITY);
+                top_tile<T>(top, ts, have[0] || edge, mx, tile, n, (uint32_t)(g.sp.h1 + f * VEC), edge, xh, tid);
+                if (t == 0) ts.recount(top);
+                else if (raised) ts.strict = true;
             }
+            if (ntiles > 0) ring_release(bars, at, STAGES);
         }
+        if (head) stat_add(st, xh, p.L);
+        if (tail) stat_add(st, xt, p.L);
         int c = 0;
         if constexpr (TOP) {
             const bool more = tail && ts.takes(xt);
             if (scan_count(more) > 0) {
                 if (ts.bound + VEC > kTopCap) ts.compact(top);
-                if (more && ts.takes(xt)) top_push_one(top, xt, (uint32_t)(sp.t0 + tid));
+                if (more && ts.takes(xt)) top_push_one(top, xt, (uint32_t)(g.sp.t0 + tid));
+            }
+            ts.recount(top);
+            if (ts.bound > 2 * p.top_k + 32) {
+                top_raise<T, kScanVecs>(top, ts, gm, has, -INFINITY);
+                top_prune(top, ts);
             }
             ts.compact(top);
             c = ts.bound;
@@ -144,6 +230,7 @@ __global__ void __launch_bounds__(kScanThreads) ce_scan_kernel(const __grid_cons
         }
         scan_sync();
     }
+    if (tid == 0 && bars.gone) atomicOr(p.err, CE_DEVERR_TIMEOUT);
 }
 
 // A row's segments put together.
@@ -154,7 +241,7 @@ __global__ void __launch_bounds__(kScanThreads) ce_join_kernel(const __grid_cons
     TopSmem& top = *reinterpret_cast<TopSmem*>(sm);
     const int tid = threadIdx.x;
     const int64_t r = blockIdx.x;
-    if (row_skipped(p.tokens, r, p.skip_first)) {
+    if (row_skipped(p.tokens, r)) {
         write_skipped(p, r);
         return;
     }
@@ -188,12 +275,13 @@ __global__ void __launch_bounds__(kScanThreads) ce_join_kernel(const __grid_cons
 
 template <typename T, bool TOP, bool ENT>
 cudaError_t launch_scan_t(const ScanArgs& a, cudaStream_t s) {
-    const size_t smem = TOP ? sizeof(TopSmem) : 0;
+    constexpr size_t smem = scan_smem(TOP);
     auto* k = ce_scan_kernel<T, TOP, ENT>;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
     if (e != cudaSuccess) return e;
-    const int64_t items = a.N * a.segs;
-    k<<<(unsigned)(items < (1 << 30) ? items : (1 << 30)), kScanThreads, smem, s>>>(a);
+    int64_t grid = a.N * a.segs;
+    if (grid > kScanSlots) grid = kScanSlots;
+    k<<<(unsigned)grid, kScanThreads + 32, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -213,15 +301,15 @@ cudaError_t launch_join(const ScanArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-size_t part_bytes(int64_t N, int segs) { return align_up((size_t)N * segs * sizeof(float4), 256); }
-
-}  // namespace
-
 cudaError_t launch_scan(const ScanArgs& a, int dtype, bool entropy, cudaStream_t s) {
     if (dtype == CE_F32) return launch_scan_type<float>(a, entropy, s);
     if (dtype == CE_BF16) return launch_scan_type<__nv_bfloat16>(a, entropy, s);
     return launch_scan_type<__half>(a, entropy, s);
 }
+
+size_t part_bytes(int64_t N, int segs) { return align_up((size_t)N * segs * sizeof(float4), 256); }
+
+}  // namespace
 
 // What every entry over rows of logits refuses (sizes, types, strides).
 ce_status check_rows(const void* logits, int dtype, int64_t dim0, int64_t dim1, int64_t V, const int64_t* strides) {

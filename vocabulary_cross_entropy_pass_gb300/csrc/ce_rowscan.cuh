@@ -10,12 +10,12 @@
 //
 // Selection of the K largest, ties to the lowest column: a candidate is the key
 // (value, ~column), so keys differ and their order is the answer's.  A threshold T
-// under which no logit can be among the K largest keeps nearly all logits out:
-//   first tile   of the maxima of 64 or 256 groups of its logits the K-th largest:
-//                at least K logits are not below it;
-//   later tiles  only what is above T counts, since K logits not below T lie in
-//                columns before it; when the buffer fills, it is sorted, K stay and
-//                T rises to the K-th.
+// under which no logit can be among the K largest keeps nearly all logits out: the
+// K-th largest of the maxima of 256 (K over 64: 1024) groups of the logits read so
+// far, which K logits at least are not below.  It is taken in the first tile and
+// again in tiles 1, 3, 7, ..., so of random logits about K (1 + ln 2) come in at
+// each and 1.2 K to 1.4 K are left at the end; in between only what is above T
+// counts, since K logits not below it lie in columns before.
 // A tile that could overfill the buffer (equal or rising logits) is taken vector by
 // vector with the buffer sorted in between, so any row is exact in bounded time.
 #pragma once
@@ -65,15 +65,20 @@ __device__ __forceinline__ void stat_add(Stat& a, float x, float L) {
     a = stat_combine(a, b, L);
 }
 
-// The vectors of one tile that a thread holds: n of them are there.  ENT: s as well.
-template <typename T, int NV, bool ENT>
-__device__ __forceinline__ float stat_tile(Stat& a, const uint4 (&raw)[NV], const bool (&have)[NV], float L) {
+// The vectors of one tile that a thread holds (have: those that are there).  ENT: s as
+// well.  GM: the running maxima of the thread's vector places, kept packed.
+template <typename T, int NV, bool ENT, bool GM>
+__device__ __forceinline__ float stat_tile(Stat& a, const uint4 (&raw)[NV], const bool (&have)[NV], float L,
+                                           typename Vec<T>::Max (&gm)[NV]) {
     using VT = Vec<T>;
     constexpr int PP = VT::kElems / 2;
     typename VT::Max tm = VT::max_init();
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (have[i]) tm = VT::max_acc(tm, raw[i]);
+    for (int i = 0; i < NV; ++i) {
+        if (!have[i]) continue;
+        tm = VT::max_acc(tm, raw[i]);
+        if (GM) gm[i] = VT::max_acc(gm[i], raw[i]);
+    }
     const float top = VT::max_done(tm);
     if (top > a.m) {
         const float y = fmaxf((a.m - top) * L, kFarBelow), f = ex2_approx(y);
@@ -108,16 +113,22 @@ __device__ __forceinline__ float stat_tile(Stat& a, const uint4 (&raw)[NV], cons
 }
 
 // ----------------------------------------------------------------- barriers
-// Over the kScanThreads threads that read tiles (others may belong to the CTA).
+// Over the kScanThreads threads that read tiles (others may belong to the CTA).  Not the
+// aligned form (bar.sync): that one says that the warp's lanes arrive together, and
+// where they do not (after a lane's own work or a wait that lanes leave one by one)
+// a later __syncwarp is taken for done and lane 0 hands a slot back before the others
+// have read it.
 __device__ __forceinline__ void scan_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(kScanThreads) : "memory");
+    __syncwarp();
+    asm volatile("barrier.sync 1, %0;" ::"n"(kScanThreads) : "memory");
 }
 __device__ __forceinline__ int scan_count(bool v) {  // how many threads passed true
     uint32_t n;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.popc.u32 %0, 1, %2, p;\n\t}"
+        "barrier.red.popc.u32 %0, 1, %2, p;\n\t}"
         : "=r"(n)
         : "r"((uint32_t)v), "n"(kScanThreads)
         : "memory");
@@ -172,10 +183,41 @@ __device__ __forceinline__ uint32_t key_column(uint64_t k) { return 0xffffffffu 
 
 struct TopSmem {
     uint64_t buf[kTopCap];
-    float gm[kScanThreads];
-    float T;
+    int cnt[16];
     int count;
 };
+
+// The largest 16-bit head of an ordered value that at least K of the groups' maxima
+// reach, where each thread brings n of them (v); as the value it stands for, rounded
+// down.  False: there are fewer than K groups (a group without logits is no group).
+template <int NG>
+__device__ __forceinline__ bool kth_group(TopSmem& s, const uint32_t (&v)[NG], int K, float& T) {
+    uint32_t head = 0;
+    if (NG > 1) {
+        if (threadIdx.x < 16) s.cnt[threadIdx.x] = 0;
+        scan_sync();
+    }
+    for (int b = 15; b >= 0; --b) {
+        const uint32_t cand = head | (1u << b);
+        int n;
+        if (NG == 1) {
+            n = scan_count(v[0] >= cand);
+        } else {
+            int own = 0;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) own += v[i] >= cand;
+            own = (int)__reduce_add_sync(kFull, (unsigned)own);
+            if ((threadIdx.x & 31) == 0) atomicAdd(&s.cnt[b], own);
+            scan_sync();
+            n = s.cnt[b];
+        }
+        if (n >= K) head = cand;
+        if (n == K) break;
+    }
+    T = head <= 0x007fu ? -INFINITY : key_value((uint64_t)head << 48);
+    return head != 0;
+}
+__device__ __forceinline__ uint32_t value_head(float x) { return (uint32_t)(top_key(x, 0) >> 48); }
 
 // The first c keys of buf in falling order.  All threads, between barriers.
 __device__ __forceinline__ void top_sort(TopSmem& s, int c) {
@@ -273,44 +315,75 @@ __device__ __forceinline__ void top_push_one(TopSmem& s, float x, uint32_t colum
     s.buf[atomicAdd(&s.count, 1)] = top_key(x, column);
 }
 
-// Starts a selection with the maxima of the threads' logits in the first tile
-// (has: the thread has any, top: their maximum).
-__device__ __forceinline__ TopState top_start(TopSmem& s, int K, bool has, float top) {
-    const int tid = threadIdx.x;
+__device__ __forceinline__ TopState top_start(TopSmem& s, int K) {
     TopState st;
     st.K = K;
     st.bound = 0;
     st.T = -INFINITY;
+    st.all = true;
     st.strict = false;
-    if (tid == 0) s.count = 0;
-    // few candidates beyond the K need at least three groups for each
-    const int G = K <= 21 ? 64 : kScanThreads;
-    if (G == 64) {
-        float g = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-        g = fmaxf(g, __shfl_xor_sync(kFull, g, 2));
-        if ((tid & 3) == 0) s.gm[tid >> 2] = g;
+    if (threadIdx.x == 0) s.count = 0;
+    return st;
+}
+
+// Raises the threshold from the groups' running maxima (has: the thread's group i has a
+// logit).  What is held and not below the new threshold was let in by the old one; the
+// present tile is to be taken with `takes` as it is then.
+template <typename T, int NV>
+__device__ __forceinline__ bool top_raise(TopSmem& s, TopState& st, const typename Vec<T>::Max (&gm)[NV], int has,
+                                          float edge) {
+    using VT = Vec<T>;
+    float t;
+    bool ok;
+    if (st.K <= 64) {
+        float f = edge;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) f = fmaxf(f, VT::max_done(gm[i]));
+        const uint32_t v[1] = {has ? value_head(f) : 0u};
+        ok = kth_group<1>(s, v, st.K, t);
     } else {
-        s.gm[tid] = top;
-    }
-    const bool any = G == 64 ? (__ballot_sync(kFull, has) >> (tid & 28)) & 15u : has;
-    const int groups = scan_count(any && (G != 64 || (tid & 3) == 0));
-    st.all = groups < K;
-    if (st.all) return st;
-    if (tid < G) {
-        const float own = s.gm[tid];
-        int r = 0;
-        for (int k = 0; k < G; k += 4) {
-            const float4 g = *reinterpret_cast<const float4*>(&s.gm[k]);
-            r += g.x > own || (g.x == own && k < tid);
-            r += g.y > own || (g.y == own && k + 1 < tid);
-            r += g.z > own || (g.z == own && k + 2 < tid);
-            r += g.w > own || (g.w == own && k + 3 < tid);
+        uint32_t v[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const float f = VT::max_done(gm[i]);
+            v[i] = (has >> i) & 1 ? value_head(i == 0 ? fmaxf(f, edge) : f) : 0u;
         }
-        if (r == K - 1) s.T = own;
+        ok = kth_group<NV>(s, v, st.K, t);
+    }
+    const bool up = ok && (st.all || t > st.T);
+    if (up) {
+        st.T = t;
+        st.all = false;
+        st.strict = false;
+    }
+    return up;
+}
+
+// Drops what is held below the threshold.
+__device__ __forceinline__ void top_prune(TopSmem& s, TopState& st) {
+    constexpr int EACH = kTopCap / kScanThreads;
+    const int lane = threadIdx.x & 31;
+    scan_sync();
+    const int c = s.count;
+    uint64_t k[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int at = i * kScanThreads + threadIdx.x;
+        k[i] = at < c ? s.buf[at] : 0;
     }
     scan_sync();
-    st.T = s.T;
-    return st;
+    if (threadIdx.x == 0) s.count = 0;
+    scan_sync();
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        if (i * kScanThreads >= c) break;
+        const bool ok = k[i] != 0 && (st.all || key_value(k[i]) >= st.T);
+        const unsigned m = __ballot_sync(kFull, ok);
+        int base = 0;
+        if (lane == 0 && m) base = atomicAdd(&s.count, __popc(m));
+        base = __shfl_sync(kFull, base, 0);
+        if (ok) s.buf[base + __popc(m & ((1u << lane) - 1u))] = k[i];
+    }
 }
 
 // A tile's candidates.  top: the maximum of the thread's logits in it (and of
@@ -345,6 +418,65 @@ __device__ __forceinline__ void top_tile(TopSmem& s, TopState& st, bool has, flo
         top_push<T>(s, st, hit, tile, nvec, col0, i, i + 1);
     }
     st.recount(s);
+}
+
+// ----------------------------------------------------------------- the ring
+// Tiles of a row's 16-byte aligned body, copied into a ring of shared memory by one
+// thread of a warp of its own (1-D bulk copies).  full[s] completes when the tile in slot
+// s has landed, empty[s] when every reading warp is done with it.  Every wait is
+// bounded: one that gives up raises `gone` and the error word; the copying thread then
+// issues no more, waits (bounded) for what it has issued and leaves, and the readers
+// run through their rows without waiting.
+constexpr int kRingMost = 12;
+struct RingBars {
+    uint64_t full[kRingMost], empty[kRingMost];
+    volatile int gone;
+};
+struct RingAt {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == stages) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+};
+__device__ __forceinline__ void ring_init(RingBars& b, int stages) {
+    for (int s = 0; s < stages; ++s) {
+        mbar_init(&b.full[s], 1);
+        mbar_init(&b.empty[s], kScanThreads / 32);
+    }
+    b.gone = 0;
+    fence_barrier_init();
+}
+// The copying thread: `bytes` (a multiple of 16, not 0) of src into the next slot.
+__device__ __forceinline__ bool ring_put(RingBars& b, RingAt& at, uint32_t& issued, int stages, unsigned char* ring,
+                                         int slot_bytes, const void* src, uint32_t bytes, uint64_t policy) {
+    if (!mbar_wait_bounded(&b.empty[at.s], at.ph ^ 1u)) {
+        b.gone = 1;
+        return false;
+    }
+    mbar_arrive_expect_tx(&b.full[at.s], bytes);
+    tma_load_1d(ring + (size_t)at.s * slot_bytes, src, bytes, &b.full[at.s], policy);
+    at.next(stages);
+    ++issued;
+    return true;
+}
+// Before the copying thread leaves early: every copy issued lands.
+__device__ __forceinline__ void ring_drain(RingBars& b, uint32_t issued, int stages) {
+    for (int s = 0; s < stages; ++s)
+        if (issued > (uint32_t)s)
+            (void)mbar_wait_bounded(&b.full[s], ((issued - 1u - (uint32_t)s) / (uint32_t)stages) & 1u);
+}
+// A reading thread: the slot `at` has landed (or the ring is gone).
+__device__ __forceinline__ void ring_wait(RingBars& b, const RingAt& at) {
+    if (!b.gone && !mbar_wait_bounded(&b.full[at.s], at.ph)) b.gone = 1;
+}
+__device__ __forceinline__ void ring_release(RingBars& b, RingAt& at, int stages) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&b.empty[at.s]);
+    at.next(stages);
 }
 
 // ----------------------------------------------------------------- rows

@@ -16,7 +16,6 @@ struct ScanArgs {
     int segs;              // segments of a row, `per` vectors of its body in each
     int64_t per;
     RowTokens tokens;
-    int skip_first;        // a row is left out when its first token is ignore_idx, else when all are
     float4* part;          // [N][segs] {m, d, s, candidates}, or NULL: one segment, finished in place
     uint64_t* cand;        // [N][segs][top_k]
     int top_k;
@@ -27,8 +26,6 @@ struct ScanArgs {
     float4* stats;         // [N] {m, log d, entropy, 0}
     uint32_t* err;
 };
-cudaError_t launch_scan(const ScanArgs& a, int dtype, bool entropy, cudaStream_t s);
-
 // The gradient p_j (a + b lp_j) of every row, and what its listed tokens get.
 struct SoftGradArgs {
     const char* x;

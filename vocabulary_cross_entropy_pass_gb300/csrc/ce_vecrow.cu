@@ -72,12 +72,6 @@ __device__ __forceinline__ uint4 ldg128_keep(const uint4* p, uint64_t pol) {
                  : "l"(p), "l"(pol));
     return v;
 }
-__device__ __forceinline__ uint64_t l2_evict_last_policy() {
-    uint64_t pol;
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
-    return pol;
-}
-
 // WARPROW: each warp takes its own rows (kVrThreads below is then the 32
 // lanes of a row's group, tid the lane); otherwise the whole CTA takes a row.
 template <typename T, bool GRAD, int THREADS, bool WARPROW>
