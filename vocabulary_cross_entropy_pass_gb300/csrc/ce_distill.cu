@@ -7,14 +7,15 @@
 //   loss = temperature^2 sum_k q_k (log q_k - log p_{t_k})
 //   grad_j = dloss temperature (Q p_j - sum_k q_k [t_k = j]),   Q = sum_k q_k
 //
-// Bound by HBM: a logit read, a gradient written.  ce_distill_kernel is a persistent
-// grid whose CTAs own whole rows.  A warp keeps a ring of tiles filled with bulk copies;
-// eight warps take them out: the row's statistics (ce_rowscan.cuh) in a first pass, the
-// gradient in a second, whose tiles come from L2, which the first was asked to keep
-// them in.  The row's list is worked on before its tiles: the teacher's softmax, the
-// student's logits of its tokens, and a hash table that finds tokens listed twice;
-// their columns are written again after the second pass.
+// Bound by HBM: a logit read, a gradient written.  ce_distill_kernel streams whole rows
+// (ce_rowscan.cuh): the statistics in a first pass, the gradient in a second, whose tiles
+// come from L2, which the first was asked to keep them in.  The side warps work on the
+// list of the row to come: the teacher's softmax, the student's logits of its tokens, and a
+// hash table that finds tokens listed twice; then on the loss of the row before and, once
+// its gradient is stored, on its listed columns again.
 #include <math.h>
+
+#include <type_traits>
 
 #include "ce_rowscan.h"
 
@@ -43,74 +44,48 @@ struct DistillArgs {
     const int64_t* n_dev;    // n_count for the mean's gradient, else NULL
     float* mean_out;         // or NULL
     uint32_t* ticket;        // CTAs done
+    uint32_t* claim;         // rows handed out beyond each CTA's first two
     int stages, slots;
 };
 
-// The teacher's table: its tokens and probabilities, and the slots of a hash table.
-inline int teacher_slots(int K) {
+// A row's list in shared memory: the present row's and the next one's.
+constexpr int kLists = 2;
+struct ListEntry {
+    float q, lq;  // the teacher's probability and its log
+    float x;      // the student's logit
+    int col;      // -1: left out; below: token -2 - col, listed before (counts for the loss alone)
+};
+struct ListRow {
+    float Q;          // the summed probability
+    float zm, logs;   // the teacher's maximum, log of its sum
+    float em, ed;     // statistics of the student's logits around the body
+    int bad, again;   // a token out of range; a token listed twice
+};
+inline int list_slots(int K) {
     int n = 64;
     while (n < 2 * K) n *= 2;
     return n;
 }
-struct TeacherSmem {
-    float* q;       // [K]
-    int* token;     // [K], -1: left out
-    int* key;       // [slots] token or -1
-    int* first;     // [slots] the lowest k of that token
-    int slots;
-};
 
-template <typename T, int NV, bool GRAD, int KE>  // KE: listed tokens a thread takes
-__global__ void __launch_bounds__(kScanThreads + 32, NV == 4 ? 2 : 1)
-ce_distill_kernel(const __grid_constant__ DistillArgs p) {
+template <typename T, int NV, bool GRAD>
+__global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kernel(const __grid_constant__ DistillArgs p) {
     using VT = Vec<T>;
     constexpr int ES = sizeof(T), PP = VT::kElems / 2;
-    constexpr int TILE = kScanThreads * NV;  // vectors
+    constexpr int TILE = kMainThreads * NV;  // vectors
     extern __shared__ __align__(128) unsigned char sm[];
-    __shared__ RingBars bars;
-    __shared__ float4 red4[kScanThreads / 32];
-    __shared__ float red[3][kScanThreads / 32];
+    __shared__ RowBars bars;
+    __shared__ ListRow lists[kLists];
+    __shared__ float red[4][kSideThreads / 32];
+    __shared__ double dred[kSideThreads / 32];
     __shared__ int last;
     unsigned char* ring = sm;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int K = p.tokens.n;
-    if (tid == 0) ring_init(bars, p.stages);
+    const int lane = threadIdx.x & 31, K = p.tokens.n;
+    ListEntry* entries = reinterpret_cast<ListEntry*>(sm + (size_t)p.stages * TILE * 16);
+    if (threadIdx.x == 0) row_bars_init(bars);
     __syncthreads();
 
-    if (tid >= kScanThreads) {  // the copying warp
-        if (lane == 0) {
-            // the first pass asks L2 to keep the row for the second
-            const uint64_t keep = GRAD ? l2_evict_last_policy() : l2_evict_first_policy();
-            const uint64_t drop = l2_evict_first_policy();
-            RingAt at;
-            uint32_t issued = 0;
-            bool ok = true;
-            int64_t y = p.tokens.at(blockIdx.x, 0);
-            for (int64_t r = blockIdx.x; ok && r < p.N; r += gridDim.x) {
-                const bool skip = y == p.tokens.ignore_idx;
-                if (r + gridDim.x < p.N) y = p.tokens.at(r + gridDim.x, 0);
-                if (skip) continue;
-                const char* x = p.x + p.row.at(r) * ES;
-                const Span16 sp = span16<ES>(x, 0, p.V);
-                for (int pass = 0; ok && pass < (GRAD ? 2 : 1); ++pass)
-                    for (int64_t f = 0; ok && f < sp.nv; f += TILE)
-                        ok = ring_put(bars, at, issued, p.stages, ring, TILE * 16, x + sp.h1 * ES + f * 16,
-                                      (uint32_t)min((int64_t)TILE, sp.nv - f) * 16u, pass == 0 ? keep : drop);
-            }
-            if (!ok) ring_drain(bars, issued, p.stages);
-        }
-        return;
-    }
-
-    TeacherSmem ts;
-    ts.slots = p.slots;
-    ts.q = reinterpret_cast<float*>(sm + (size_t)p.stages * TILE * 16);
-    ts.token = reinterpret_cast<int*>(ts.q + K);
-    ts.key = ts.token + K;
-    ts.first = ts.key + p.slots;
-    RingAt at;
-    // the row count and the error word come from the kernel before this one, which
-    // may still run: they are waited for where the first row needs them
+    // The row count and the error word come from the kernel before this one, which may
+    // still run: a thread waits for it where it first needs them.
     bool counted = false;
     float g_mean = 1.f;
     auto need_count = [&]() {
@@ -119,223 +94,343 @@ ce_distill_kernel(const __grid_constant__ DistillArgs p) {
         if (p.n_dev) g_mean = (p.dloss ? __ldg(p.dloss) : 1.f) / (float)(*p.n_dev);
         counted = true;
     };
-    // a row's first token and list are loaded one row ahead
-    int64_t y0 = p.tokens.at(blockIdx.x, 0), y[KE];
-    float z[KE];
-    auto fetch = [&](int64_t r) {
-#pragma unroll
-        for (int i = 0; i < KE; ++i) {
-            const int k = tid + i * kScanThreads;
-            y[i] = k < K ? p.tokens.at(r, k) : p.tokens.ignore_idx;
-            z[i] = k < K ? teacher_at(p.teacher, p.teacher_dtype, p.trow.at(r) + k * p.tstep) : -INFINITY;
-        }
+    auto row_scale = [&](int64_t r) {
+        need_count();
+        return (p.n_dev ? g_mean : (p.dloss ? __ldg(p.dloss + r) : 1.f)) * p.tau;
     };
-    fetch(blockIdx.x);
-    for (int64_t r = blockIdx.x; r < p.N; r += gridDim.x) {
-        const char* x = p.x + p.row.at(r) * ES;
-        char* out = GRAD ? p.out + p.orow.at(r) * ES : nullptr;
-        const Span16 sp = span16<ES>(x, 0, p.V);
-        const int64_t edge = span16_edge(sp, 0, p.V, tid);
-        const int64_t next = r + gridDim.x;
-        const bool skip = y0 == p.tokens.ignore_idx;
-        if (next < p.N) y0 = p.tokens.at(next, 0);
-        if (skip) {
-            if (GRAD) {
-                uint4* to = reinterpret_cast<uint4*>(out + sp.h1 * ES);
-                for (int64_t v = tid; v < sp.nv; v += kScanThreads) stg128_stream(to + v, make_uint4(0, 0, 0, 0));
-                if (edge >= 0) VT::store1(out + edge * ES, 0.f);
+
+    if (threadIdx.x < kMainThreads) {
+        const int tid = threadIdx.x;
+        Turn at, q;
+        for (int par = 0;; q.next(kQueue), par ^= 1) {
+            if (!row_wait(bars, &bars.ready[q.s], q.ph)) return;
+            const RowItem& it = bars.item[q.s];
+            const int64_t r = it.row, nv = it.nv;
+            if (r < 0) return;
+            uint4* to = GRAD ? reinterpret_cast<uint4*>(it.out + it.h1 * ES) + tid : nullptr;
+            if (it.skip) {
+                warp_arrive(&bars.done[q.s]);
+                if (GRAD) {
+                    for (int64_t v = tid; v < nv; v += kMainThreads, to += kMainThreads)
+                        stg128_stream(to, make_uint4(0, 0, 0, 0));
+                    warp_arrive(&bars.stored[q.s]);
+                }
+                warp_arrive(&bars.free_[q.s]);
+                continue;
             }
+            if (!main_stats<T, NV, false, 0>(bars, at, p.stages, ring, q.s, nv, p.L, nullptr)) return;
+            if constexpr (GRAD) {
+                if (!row_wait(bars, &bars.done[q.s], q.ph) || !row_wait(bars, &bars.prep[q.s], q.ph)) return;
+                const ListRow& l = lists[par];
+                Stat st = stat_identity();
+                if (lane < kMainThreads / 32) st = Stat{bars.part[q.s][lane].x, bars.part[q.s][lane].y, 0.f};
+                else if (lane == kMainThreads / 32) st = Stat{l.em, l.ed, 0.f};
+                st = stat_warp<false>(st, p.L);
+                const bool zero = l.bad || stat_none(st.m, st.d);
+                const float a = row_scale(r) * l.Q;
+                // p = 2^(x L + R) in one fused step for outputs in 16 bits (rounding R costs 2^-24 of it in the
+                // exponent, 3e-6 of p at most); else from the difference
+                const float logd2 = stat_logd(st, p.L) * kLog2e, M = stat_ref(st.m, p.L);
+                const bool fused = ES == 2 && fabsf(M) < 64.f;
+                const float R = fused ? -(M + logd2) : 0.f;
+                const float2 NM = make_float2(-st.m, -st.m), LL = make_float2(p.L, p.L);
+                const float2 SH = fused ? make_float2(R, R) : make_float2(-logd2, -logd2), A = make_float2(a, a);
+                auto vector = [&](uint4 raw, auto one) {
+                    float2 v[PP];
+                    VT::unpack2(raw, v);
+#pragma unroll
+                    for (int k = 0; k < PP; ++k) {
+                        const float2 e = __ffma2_rn(decltype(one)::value ? v[k] : __fadd2_rn(v[k], NM), LL, SH);
+                        v[k] = __fmul2_rn(make_float2(ex2_approx(e.x), ex2_approx(e.y)), A);
+                    }
+                    return VT::pack2(v);
+                };
+                for (int64_t f = 0; f < nv; f += TILE, to += TILE) {
+                    const uint4* tile = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16) + tid;
+                    if (!row_wait(bars, &bars.full[at.s], at.ph)) return;
+                    const int64_t n = nv - f - tid;  // vectors from this thread's first on
+                    if (fused && !zero && nv - f >= TILE) {
+                        uint4 raw[NV];
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) raw[i] = tile[i * kMainThreads];
+#pragma unroll
+                        for (int i = 0; i < NV; ++i)
+                            stg128_stream(to + i * kMainThreads, vector(raw[i], std::true_type()));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < NV; ++i) {
+                            if (i * kMainThreads >= n) break;
+                            const uint4 raw = tile[i * kMainThreads];
+                            uint4 o = fused ? vector(raw, std::true_type()) : vector(raw, std::false_type());
+                            if (zero) o = make_uint4(0, 0, 0, 0);
+                            stg128_stream(to + i * kMainThreads, o);
+                        }
+                    }
+                    warp_arrive(&bars.empty[at.s]);
+                    at.next(p.stages);
+                }
+                warp_arrive(&bars.stored[q.s]);
+            }
+            warp_arrive(&bars.free_[q.s]);
+        }
+    }
+
+    if (threadIdx.x < kMainThreads + 32) {  // the copying warp
+        if (lane == 0) {
+            // the first pass asks L2 to keep the row for the second
+            const uint64_t keep = GRAD ? l2_evict_last_policy() : l2_evict_first_policy();
+            const uint64_t drop = l2_evict_first_policy();
+            Turn at, q;
+            uint32_t issued = 0;
+            bool ok = true, started = false;
+            // rows: the CTA's first two, then the next that no CTA has claimed; each is known two ahead and in
+            // the queue one ahead of its copies, so the side warps work on its list meanwhile
+            auto token = [&](int64_t r) { return r < p.N ? p.tokens.at(r, 0) : 0; };
+            auto publish = [&](int64_t r, int64_t y) {
+                ok = ok && row_wait(bars, &bars.free_[q.s], q.ph ^ 1u);
+                if (!ok) return;
+                RowItem& it = bars.item[q.s];
+                it.row = r < p.N ? r : -1;
+                if (r < p.N) {
+                    const char* x = p.x + p.row.at(r) * ES;
+                    const Span16 sp = span16<ES>(x, 0, p.V);
+                    it.x = x;
+                    it.out = GRAD ? p.out + p.orow.at(r) * ES : nullptr;
+                    it.v0 = 0;
+                    it.nv = sp.nv;
+                    it.h1 = it.head = (int)sp.h1;
+                    it.tail = (int)sp.t0;
+                    it.tails = (int)(p.V - sp.t0);
+                    it.skip = y == p.tokens.ignore_idx;
+                }
+                mbar_arrive(&bars.ready[q.s]);
+                q.next(kQueue);
+            };
+            int64_t r = blockIdx.x, r1 = r + gridDim.x, r2 = 0;
+            int64_t y = token(r), y1 = token(r1), y2 = 0;
+            auto claim = [&]() {
+                if (r1 >= p.N) return;
+                if (!started) griddep_wait();  // the kernel before zeroes the counter
+                started = true;
+                r2 = 2 * (int64_t)gridDim.x + atomicAdd(p.claim, 1u);
+                y2 = token(r2);
+            };
+            publish(r, y);
+            while (ok && r < p.N) {
+                publish(r1, y1);
+                const bool skip = y == p.tokens.ignore_idx;
+                const char* x = p.x + p.row.at(r) * ES;
+                const Span16 sp = span16<ES>(x, 0, p.V);
+                const char* body = x + sp.h1 * ES;
+                auto pass = [&](uint64_t policy) {
+                    for (int64_t f = 0; ok && f < sp.nv; f += TILE)
+                        ok = ring_put(bars, at, issued, p.stages, ring, TILE * 16, body + f * 16,
+                                      (uint32_t)min((int64_t)TILE, sp.nv - f) * 16u, policy);
+                };
+                const bool early = started;
+                if (early) claim();
+                if (!skip) pass(keep);
+                if (!early) claim();
+                if (!skip && GRAD) pass(drop);
+                r = r1;
+                y = y1;
+                r1 = r2;
+                y1 = y2;
+            }
+            if (!ok) ring_drain(bars, issued, p.stages);
+        }
+        return;
+    }
+
+    const int tid = threadIdx.x - kMainThreads - 32;
+    int* key = reinterpret_cast<int*>(entries + kLists * K);  // [slots] a token, or -1
+    int* first = key + p.slots;                               // [slots] its first entry
+    // the row whose loss is still to come
+    bool pending = false;
+    float xe = 0.f;
+    int64_t ce = -1;
+    Turn qf;
+    int par = 0;  // the list of the row at hand; the other one is the pending row's
+    auto finish = [&]() -> bool {
+        if (!pending) return true;
+        pending = false;
+        const RowItem& it = bars.item[qf.s];
+        ListRow& l = lists[par ^ 1];
+        const ListEntry* e = entries + (par ^ 1) * K;
+        const int64_t r = it.row;
+        if (side_any(!row_wait(bars, &bars.done[qf.s], qf.ph))) return false;
+        if (!it.skip) {
+            const Stat st = row_stats<false>(bars.part[qf.s], ce >= 0, xe, p.L);
+            const bool none = stat_none(st.m, st.d);
+            const float logd = none ? 0.f : stat_logd(st, p.L);
+            float loss = 0.f;
+            for (int k = tid; k < K; k += kSideThreads) {
+                if (e[k].q == 0.f) continue;
+                const float lp = none ? -INFINITY : (e[k].x - st.m) * p.scale - logd;
+                loss += e[k].q * (e[k].lq - lp);
+            }
+            loss = side_sum(loss, red[2], tid);
+            need_count();
+            if (tid == 0) {
+                if (l.bad) atomicOr(p.err, CE_DEVERR_TARGET_RANGE);
+                p.loss[r] = l.bad ? NAN : p.tau * p.tau * loss;
+                if (p.stats) p.stats[r] = make_float4(st.m, logd, l.zm, l.logs);
+            }
+            if constexpr (GRAD) {
+                const float gt = row_scale(r), a = gt * l.Q, shift = -logd * kLog2e, nm = -st.m;
+                const bool zero = l.bad || none;
+                auto grad = [&](float v) { return ex2_approx(fmaf(v + nm, p.L, shift)) * a; };
+                if (tid < 32 && ce >= 0) VT::store1(it.out + ce * ES, zero ? 0.f : grad(xe));
+                if (side_any(!row_wait(bars, &bars.stored[qf.s], qf.ph))) return false;
+                for (int k = tid; k < K && !zero; k += kSideThreads) {
+                    const int col = e[k].col;
+                    if (col < 0) continue;
+                    float c = e[k].q;
+                    if (l.again) {  // in list order
+                        c = 0.f;
+                        for (int j = 0; j < K; ++j)
+                            if (e[j].col == col || e[j].col == -2 - col) c += e[j].q;
+                    }
+                    VT::store1(it.out + (int64_t)col * ES, fmaf(-gt, c, grad(e[k].x)));
+                }
+            }
+        } else {
             if (tid == 0) {
                 p.loss[r] = 0.f;
                 if (p.stats) p.stats[r] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
             }
-            if (next < p.N) fetch(next);
-            continue;
-        }
-        // the list: the student's logits, the teacher's softmax
-        float xv[KE], q[KE], lq[KE];
-        int col[KE];
-        bool bad = false;
-        float zm = -INFINITY;
-        const float xe = edge >= 0 ? VT::load1(x + edge * ES) : -INFINITY;
-#pragma unroll
-        for (int i = 0; i < KE; ++i) {
-            const bool there = y[i] != p.tokens.ignore_idx;
-            const bool in = there && y[i] >= 0 && y[i] < p.V;
-            bad |= there && !in;
-            col[i] = in ? (int)y[i] : -1;
-            xv[i] = in ? VT::load1(x + y[i] * ES) : 0.f;
-            lq[i] = in ? z[i] : -INFINITY;
-            zm = fmaxf(zm, lq[i]);
-        }
-        if (next < p.N) fetch(next);
-        zm = scan_max(zm, red[0]);
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < KE; ++i)
-            if (lq[i] != -INFINITY) sum += ex2_approx((lq[i] - zm) * p.L);
-        sum = scan_sum(sum, red[1]);
-        const bool nothing = zm == -INFINITY && sum == 0.f;  // no token has any probability
-        const float logs = nothing ? 0.f : logf(sum);
-        const float Q = nothing       ? 0.f
-                        : sum != sum  ? sum
-                        : p.normalize ? 1.f
-                                      : ex2_approx((zm * p.scale + logs) * kLog2e);
-#pragma unroll
-        for (int i = 0; i < KE; ++i) {
-            const int k = tid + i * kScanThreads;
-            q[i] = 0.f;
-            if (lq[i] != -INFINITY) {
-                lq[i] = p.normalize ? (lq[i] - zm) * p.scale - logs : lq[i] * p.scale;
-                q[i] = ex2_approx(lq[i] * kLog2e);
-            }
-            if (GRAD && k < K) {
-                ts.q[k] = q[i];
-                ts.token[k] = col[i];
+            if constexpr (GRAD) {
+                if (tid < 32 && ce >= 0) VT::store1(it.out + ce * ES, 0.f);
+                if (side_any(!row_wait(bars, &bars.stored[qf.s], qf.ph))) return false;
             }
         }
-        // tokens listed twice: the first entry of each speaks for all
-        if (GRAD) {
-            for (int k = tid; k < ts.slots; k += kScanThreads) {
-                ts.key[k] = -1;
-                ts.first[k] = 0x7fffffff;
-            }
-            scan_sync();
-            int slot[KE];
-#pragma unroll
-            for (int i = 0; i < KE; ++i) {
-                slot[i] = -1;
-                if (col[i] < 0) continue;
-                uint32_t h = ((uint32_t)col[i] * 2654435761u) >> 7;
-                for (;; ++h) {
-                    h &= (uint32_t)ts.slots - 1u;
-                    const int was = atomicCAS(&ts.key[h], -1, col[i]);
-                    if (was == -1 || was == col[i]) break;
-                }
-                slot[i] = (int)h;
-                atomicMin(&ts.first[h], tid + i * kScanThreads);
-            }
-            scan_sync();
-            bool again = false;
-#pragma unroll
-            for (int i = 0; i < KE; ++i)
-                if (slot[i] >= 0 && ts.first[slot[i]] != tid + i * kScanThreads) {
-                    again = true;
-                    slot[i] = -1;
-                    col[i] = -2 - col[i];  // counts for the loss alone
-                }
-            if (scan_count(again) > 0) {
-#pragma unroll
-                for (int i = 0; i < KE; ++i) {
-                    if (slot[i] < 0) continue;
-                    float c = 0.f;
-                    for (int k = 0; k < K; ++k)
-                        if (ts.token[k] == col[i]) c += ts.q[k];
-                    ts.q[tid + i * kScanThreads] = c;  // read by no other: its token is this thread's
-                }
-            }
+        side_sync();
+        if (tid == 0) mbar_arrive(&bars.free_[qf.s]);
+        qf.next(kQueue);
+        return true;
+    };
+    Turn q;
+    bool fine = true;
+    for (;; q.next(kQueue)) {
+        if (side_any(!row_wait(bars, &bars.ready[q.s], q.ph))) {
+            fine = false;
+            break;
         }
-
-        // first pass: the row's statistics
-        Stat st = stat_identity();
-        typename VT::Max gm[NV];
-        for (int64_t f = 0; f < sp.nv; f += TILE) {
-            const int n = (int)min((int64_t)TILE, sp.nv - f);
-            const uint4* tile = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16);
-            ring_wait(bars, at);
-            uint4 raw[NV];
-            bool have[NV];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                have[i] = tid + i * kScanThreads < n;
-                if (have[i]) raw[i] = tile[tid + i * kScanThreads];
-            }
-            stat_tile<T, NV, false, false>(st, raw, have, p.L, gm);
-            ring_release(bars, at, p.stages);
-        }
-        if (edge >= 0) stat_add(st, xe, p.L);
-        st = stat_block(st, p.L, red4);
-        const bool none = stat_none(st.m, st.d);
-        const float logd = none ? 0.f : logf(st.d);
-        float loss = 0.f;
-#pragma unroll
-        for (int i = 0; i < KE; ++i) {
-            const float lp = none ? -INFINITY : (xv[i] - st.m) * p.scale - logd;
-            loss += q[i] == 0.f ? 0.f : q[i] * (lq[i] - lp);
-        }
-        loss = scan_sum(loss, red[2]);
-        const bool wrong = scan_count(bad) > 0;
-        need_count();
-        if (tid == 0) {
-            if (wrong) atomicOr(p.err, CE_DEVERR_TARGET_RANGE);
-            p.loss[r] = wrong ? NAN : p.tau * p.tau * loss;
-            if (p.stats) p.stats[r] = make_float4(st.m, logd, zm, logs);
-        }
-        if constexpr (GRAD) {
-            // second pass: p_j dloss temperature Q, and at the listed columns that less q
-            const float gt = (p.n_dev ? g_mean : (p.dloss ? __ldg(p.dloss + r) : 1.f)) * p.tau;
-            const bool zero = wrong || none;
-            const float a = gt * Q, shift = -logd * kLog2e, nm = -st.m;
-            const float2 NM = make_float2(nm, nm), LL = make_float2(p.L, p.L), SH = make_float2(shift, shift);
-            const float2 A = make_float2(a, a);
-            for (int64_t f = 0; f < sp.nv; f += TILE) {
-                const int n = (int)min((int64_t)TILE, sp.nv - f);
-                const uint4* tile = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16);
-                uint4* to = reinterpret_cast<uint4*>(out + sp.h1 * ES) + f;
-                ring_wait(bars, at);
-                uint4 raw[NV];
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (tid + i * kScanThreads < n) raw[i] = tile[tid + i * kScanThreads];
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    if (tid + i * kScanThreads >= n) continue;
-                    float2 v[PP];
-                    VT::unpack2(raw[i], v);
-#pragma unroll
-                    for (int k = 0; k < PP; ++k) {
-                        const float2 e = __ffma2_rn(__fadd2_rn(v[k], NM), LL, SH);
-                        v[k] = __fmul2_rn(make_float2(ex2_approx(e.x), ex2_approx(e.y)), A);
+        const RowItem& it = bars.item[q.s];
+        const int64_t r = it.row;
+        if (r < 0) break;
+        ListRow& l = lists[par];
+        ListEntry* e = entries + par * K;
+        const int64_t cnew = edge_column(it);
+        float xnew = -INFINITY;
+        if (cnew >= 0) xnew = VT::load1(it.x + cnew * ES);
+        if (!it.skip) {
+            bool bad = false;
+            float zm = -INFINITY;
+            for (int k = tid; k < K; k += kSideThreads) {
+                const int64_t y = p.tokens.at(r, k);
+                const float z = teacher_at(p.teacher, p.teacher_dtype, p.trow.at(r) + k * p.tstep);
+                ListEntry n{0.f, -INFINITY, 0.f, -1};
+                if (y != p.tokens.ignore_idx) {
+                    if (y < 0 || y >= p.V) {
+                        bad = true;
+                    } else {
+                        n.lq = z;
+                        n.x = VT::load1(it.x + y * ES);
+                        n.col = (int)y;
                     }
-                    stg128_stream(to + tid + i * kScanThreads, zero ? make_uint4(0, 0, 0, 0) : VT::pack2(v));
                 }
-                ring_release(bars, at, p.stages);
+                e[k] = n;
+                zm = fmaxf(zm, n.lq);
             }
-            auto grad = [&](float v) { return ex2_approx(fmaf(v + nm, p.L, shift)) * a; };
-            if (edge >= 0) VT::store1(out + edge * ES, zero ? 0.f : grad(xe));
-            scan_sync();
-            if (!zero) {
-#pragma unroll
-                for (int i = 0; i < KE; ++i)
-                    if (col[i] >= 0)
-                        VT::store1(out + (int64_t)col[i] * ES,
-                                   fmaf(-gt, ts.q[tid + i * kScanThreads], grad(xv[i])));
+            zm = side_max(zm, red[0], tid);
+            float sum = 0.f;
+            for (int k = tid; k < K; k += kSideThreads)
+                if (e[k].lq != -INFINITY) sum += ex2_approx((e[k].lq - zm) * p.L);
+            sum = side_sum(sum, red[1], tid);
+            const bool nothing = zm == -INFINITY && sum == 0.f;  // no token has any probability
+            const float logs = nothing ? 0.f : logf(sum);
+            for (int k = tid; k < K; k += kSideThreads) {
+                if (e[k].lq == -INFINITY) continue;
+                const float lq = p.normalize ? (e[k].lq - zm) * p.scale - logs : e[k].lq * p.scale;
+                e[k].lq = lq;
+                e[k].q = ex2_approx(lq * kLog2e);
             }
-            scan_sync();
+            // tokens listed twice: the first entry of each writes for all
+            bool again = false;
+            if (GRAD) {
+                for (int k = tid; k < p.slots; k += kSideThreads) {
+                    key[k] = -1;
+                    first[k] = 0x7fffffff;
+                }
+                side_sync();
+                auto slot_of = [&](int col, bool insert) {
+                    uint32_t h = ((uint32_t)col * 2654435761u) >> 7;
+                    for (;; ++h) {
+                        h &= (uint32_t)p.slots - 1u;
+                        const int was = insert ? atomicCAS(&key[h], -1, col) : key[h];
+                        if (was == col || (insert && was == -1)) return (int)h;
+                    }
+                };
+                for (int k = tid; k < K; k += kSideThreads)
+                    if (e[k].col >= 0) atomicMin(&first[slot_of(e[k].col, true)], k);
+                side_sync();
+                for (int k = tid; k < K; k += kSideThreads)
+                    if (e[k].col >= 0 && first[slot_of(e[k].col, false)] != k) {
+                        again = true;
+                        e[k].col = -2 - e[k].col;
+                    }
+            }
+            const bool any_bad = side_any(bad), any_again = side_any(again);
+            if (tid < 32) {
+                Stat st = stat_identity();
+                if (cnew >= 0) stat_add(st, xnew, p.L);
+                st = stat_warp<false>(st, p.L);
+                if (tid == 0) {
+                    l.Q = nothing       ? 0.f
+                          : sum != sum  ? sum
+                          : p.normalize ? 1.f
+                                        : ex2_approx((zm * p.scale + logs) * kLog2e);
+                    l.zm = zm;
+                    l.logs = logs;
+                    l.em = st.m;
+                    l.ed = st.d;
+                    l.bad = any_bad;
+                    l.again = any_again;
+                }
+            }
         }
+        side_sync();
+        if (tid == 0) mbar_arrive(&bars.prep[q.s]);
+        if (!(fine = finish())) break;
+        pending = true;
+        xe = xnew;
+        ce = cnew;
+        qf = q;
+        par ^= 1;
     }
+    if (fine) finish();
     need_count();
     if (tid == 0 && bars.gone) atomicOr(p.err, CE_DEVERR_TIMEOUT);
     // the mean: the last CTA to finish sums the rows' losses in a fixed order
     if (p.mean_out) {
         __threadfence();
-        scan_sync();
+        side_sync();
         if (tid == 0) {
             __threadfence();
             last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
         }
-        scan_sync();
+        side_sync();
         if (!last) return;
         __threadfence();
-        __shared__ double dred[kScanThreads / 32];
-        double acc = strided_sum_fixed(p.loss, p.N, tid, kScanThreads);
+        double acc = strided_sum_fixed(p.loss, p.N, tid, kSideThreads);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(kFull, acc, off);
-        if (lane == 0) dred[warp] = acc;
-        scan_sync();
+        if (lane == 0) dred[tid >> 5] = acc;
+        side_sync();
         if (tid == 0) {
             double t = 0.0;
-            for (int w = 0; w < kScanThreads / 32; ++w) t += dred[w];
+            for (int w = 0; w < kSideThreads / 32; ++w) t += dred[w];
             p.mean_out[0] = (float)(t / (double)(*p.n_count));  // NaN when every row is ignored
         }
     }
@@ -354,23 +449,24 @@ Layout layout(int64_t N) {
     return l;
 }
 
-template <typename T, int NV, bool GRAD, int KE>
+template <typename T, int NV, bool GRAD>
 cudaError_t launch_distill_k(DistillArgs a, cudaStream_t s) {
-    auto* k = ce_distill_kernel<T, NV, GRAD, KE>;
-    a.slots = GRAD ? teacher_slots(a.tokens.n) : 0;
-    const size_t list = GRAD ? (size_t)a.tokens.n * 8 + (size_t)a.slots * 8 : 0;
-    // six tiles; five where a long list would cost an SM its second CTA
-    a.stages = NV == 4 && list > 8 * 1024 ? 5 : 6;
-    const size_t smem = (size_t)a.stages * kScanThreads * NV * 16 + list;
+    auto* k = ce_distill_kernel<T, NV, GRAD>;
+    a.slots = GRAD ? list_slots(a.tokens.n) : 0;
+    const size_t list = (size_t)kLists * a.tokens.n * sizeof(ListEntry) + (size_t)a.slots * 8;
+    constexpr size_t tile = kMainThreads * NV * 16, room = (NV == 4 ? 111 : 222) * 1024;
+    a.stages = (int)((room - list) / tile);
+    if (a.stages > kRingMost) a.stages = kRingMost;
+    const size_t smem = a.stages * tile + list;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
     if (e != cudaSuccess) return e;
-    int64_t grid = NV == 4 ? kScanSlots : kScanSlots / 2;
+    int64_t grid = NV == 4 ? kScanSlots : kSMs;
     if (grid > a.N) grid = a.N;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     set_pdl_attr(&attr[0]);
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kScanThreads + 32);
+    cfg.blockDim = dim3(kRowThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -380,13 +476,10 @@ cudaError_t launch_distill_k(DistillArgs a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_distill_t(const DistillArgs& a, cudaStream_t s) {
-    const bool brief = a.tokens.n <= kScanThreads;
-    if (!a.out) return brief ? launch_distill_k<T, 4, false, 1>(a, s) : launch_distill_k<T, 4, false, 4>(a, s);
+    if (!a.out) return launch_distill_k<T, 4, false>(a, s);
     // rows over 128 KB: one CTA per SM with tiles of 32 KB, so fewer rows wait in L2 for
     // their second pass
-    if (a.V * (int64_t)sizeof(T) > 128 * 1024)
-        return brief ? launch_distill_k<T, 8, true, 1>(a, s) : launch_distill_k<T, 8, true, 4>(a, s);
-    return brief ? launch_distill_k<T, 4, true, 1>(a, s) : launch_distill_k<T, 4, true, 4>(a, s);
+    return a.V * (int64_t)sizeof(T) > 128 * 1024 ? launch_distill_k<T, 8, true>(a, s) : launch_distill_k<T, 4, true>(a, s);
 }
 
 struct Teacher {
@@ -461,6 +554,8 @@ ce_status distill(const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1
     pb.err = reinterpret_cast<uint32_t*>(ws + kWsErrOffset);
     pb.n_dev = reinterpret_cast<int64_t*>(ws + kWsCountOffset);
     pb.ticket = reinterpret_cast<uint32_t*>(ws + kWsTicketOffset);
+    pb.row_claim = reinterpret_cast<uint32_t*>(ws + kWsRowClaimOffset);
+    pb.row_done = reinterpret_cast<uint32_t*>(ws + kWsRowDoneOffset);
     pb.loss_rows = reduce ? reinterpret_cast<float*>(ws + l.loss) : loss_out;
     cudaError_t e = launch_count(pb, n_out, s);
     if (e != cudaSuccess) return launch_failed();
@@ -485,6 +580,7 @@ ce_status distill(const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1
     d.n_count = pb.n_dev;
     d.mean_out = reduce ? loss_out : nullptr;
     d.ticket = pb.ticket;
+    d.claim = pb.row_claim;
     bool after = false;  // the gradient from the statistics, in a launch of its own
     if (grad) {
         const int64_t es = elem_size(dtype);

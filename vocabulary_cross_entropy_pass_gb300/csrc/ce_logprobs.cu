@@ -4,12 +4,10 @@
 //   lp_j = x_j - logsumexp(x),   H = -sum_j exp(lp_j) lp_j,
 //   top: the K largest x in falling order (ties: the lower column first), with lp
 //
-// Bound by HBM: every logit is read once.  ce_scan_kernel is a persistent grid, two CTAs
-// per SM; a warp of each keeps a ring of 16 KB tiles filled with bulk copies, segment
-// after segment and row after row, and eight warps take them out, sum the statistics and
-// select candidates (ce_rowscan.cuh), so the copies go on while a row is finished.  A
-// row in one piece is finished by the CTA that read it, a row in segments by
-// ce_join_kernel from their partial results.
+// Bound by HBM: every logit is read once (and with top_k an eighth again, from L2).
+// ce_scan_kernel streams rows, or segments of few rows (ce_rowscan.cuh); a row in one
+// piece is finished by its side warps, a row in segments by ce_join_kernel from their
+// partial results.
 #include <math.h>
 
 #include "ce_rowscan.h"
@@ -17,56 +15,55 @@
 namespace gbce {
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
-
-// Whether row r is left out.  All scanning threads; a barrier where a row has several tokens.
-__device__ __forceinline__ bool row_skipped(const RowTokens& t, int64_t r) {
-    if (t.n == 0) return false;
-    if (t.n == 1) return t.at(r, 0) == t.ignore_idx;
-    bool keep = false;
-    for (int k = threadIdx.x; k < t.n; k += kScanThreads) keep |= t.at(r, k) != t.ignore_idx;
-    return scan_count(keep) == 0;
-}
-
-__device__ __forceinline__ void write_skipped(const ScanArgs& p, int64_t r) {
-    const int tid = threadIdx.x;
+__device__ __forceinline__ void write_skipped(const ScanArgs& p, int64_t r, int tid) {
     if (tid == 0) {
         if (p.entropy) p.entropy[r] = 0.f;
         if (p.stats) p.stats[r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
     }
-    for (int k = tid; k < p.tokens.n; k += kScanThreads) p.logprobs[r * p.tokens.n + k] = 0.f;
-    for (int k = tid; k < p.top_k; k += kScanThreads) {
+    for (int k = tid; k < p.tokens.n; k += kSideThreads) p.logprobs[r * p.tokens.n + k] = 0.f;
+    for (int k = tid; k < p.top_k; k += kSideThreads) {
         p.top_tokens[r * p.top_k + k] = p.tokens.ignore_idx;
         p.top_logprobs[r * p.top_k + k] = 0.f;
     }
 }
 
+// A thread's given token of a row and its logit (the first kSideThreads of them).
+template <typename T>
+struct Given {
+    int64_t y = 0;
+    float x = 0.f;
+    __device__ __forceinline__ void load(const ScanArgs& p, int64_t r, const char* row, int k) {
+        if (k >= p.tokens.n) return;
+        y = p.tokens.at(r, k);
+        if (y >= 0 && y < p.V) x = Vec<T>::load1(row + y * sizeof(T));
+    }
+};
+
 // A row's outputs from its statistics and its candidates in falling order (c of them).
 template <typename T>
-__device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const Stat& t, const uint64_t* top, int c) {
-    const int tid = threadIdx.x;
+__device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const char* x, const Stat& t,
+                                           const uint64_t* top, int c, Given<T> given, int tid) {
     const bool none = stat_none(t.m, t.d);
-    const float logd = none ? 0.f : logf(t.d);
+    const float logd = none ? 0.f : stat_logd(t, p.L);
     if (tid == 0) {
-        const float h = none ? 0.f : logd - kLn2 * t.s / t.d;
+        const float h = none ? 0.f : stat_entropy(t);
         if (p.entropy) p.entropy[r] = h;
         if (p.stats) p.stats[r] = make_float4(t.m, logd, h, 0.f);
     }
-    const char* x = p.x + p.row.at(r) * sizeof(T);
-    for (int k = tid; k < p.tokens.n; k += kScanThreads) {
-        const int64_t y = p.tokens.at(r, k);
+    for (int k = tid; k < p.tokens.n; k += kSideThreads) {
+        if (k >= kSideThreads) given.load(p, r, x, k);
         float lp = 0.f;
-        if (y != p.tokens.ignore_idx) {
-            if (y < 0 || y >= p.V) {
+        if (given.y != p.tokens.ignore_idx) {
+            if (given.y < 0 || given.y >= p.V) {
                 lp = NAN;
                 atomicOr(p.err, CE_DEVERR_TARGET_RANGE);
             } else {
-                lp = none ? -INFINITY : (Vec<T>::load1(x + y * sizeof(T)) - t.m) - logd;
+                lp = none ? -INFINITY : (given.x - t.m) - logd;
             }
         }
         p.logprobs[r * p.tokens.n + k] = lp;
     }
-    for (int k = tid; k < p.top_k; k += kScanThreads) {
+    for (int k = tid; k < p.top_k; k += kSideThreads) {
         int64_t token = -1;  // NaN is no alternative: a row of fewer than K others ends so
         float lp = NAN;
         if (k < c) {
@@ -78,226 +75,218 @@ __device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const S
     }
 }
 
-// Shared memory: the ring, its barriers, the candidates.
-constexpr int kTileBytes = kScanTileVecs * 16;
-constexpr int scan_stages(bool top) { return top ? 4 : 6; }  // two CTAs of 228 KB
-constexpr size_t scan_smem(bool top) {
-    return (size_t)scan_stages(top) * kTileBytes + (top ? sizeof(TopSmem) : 0);
+// Shared memory: the ring, and with top_k the candidates and the groups' maxima.
+constexpr int kTileBytes = kTileVecs * 16;
+constexpr int kPlaces = 2;  // of the queue: a row in the stream, one with the side warps
+constexpr int scan_stages(int gm) { return gm ? 4 : 6; }
+constexpr size_t scan_smem(int gm) {
+    return (size_t)scan_stages(gm) * kTileBytes + (gm ? sizeof(TopSmem) + kPlaces * kTopHeads * 2 : 0);
 }
 
-struct Segment {
-    const char* x;     // the row
-    Span16 sp;
-    int64_t v0, v1;    // its vectors of the body
-    bool first, last;
-};
-template <int ES>
-__device__ __forceinline__ Segment segment(const ScanArgs& p, int64_t r, int seg) {
-    Segment g;
-    g.x = p.x + p.row.at(r) * ES;
-    g.sp = span16<ES>(g.x, 0, p.V);
-    g.first = seg == 0;
-    g.last = seg == p.segs - 1;
-    g.v0 = min(g.sp.nv, seg * p.per);
-    g.v1 = g.last ? g.sp.nv : min(g.sp.nv, g.v0 + p.per);
-    return g;
-}
-
-template <typename T, bool TOP, bool ENT>
-__global__ void __launch_bounds__(kScanThreads + 32, 2) ce_scan_kernel(const __grid_constant__ ScanArgs p) {
+template <typename T, int GM, bool ENT>  // GM: 0 without top_k, else as main_stats
+__global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_constant__ ScanArgs p) {
     using VT = Vec<T>;
-    constexpr int VEC = VT::kElems, ES = sizeof(T), STAGES = scan_stages(TOP);
+    constexpr int ES = sizeof(T), STAGES = scan_stages(GM);
     extern __shared__ __align__(128) unsigned char sm[];
-    __shared__ RingBars bars;
-    __shared__ float4 red[kScanThreads / 32];
+    __shared__ RowBars bars;
     unsigned char* ring = sm;
     TopSmem& top = *reinterpret_cast<TopSmem*>(sm + (size_t)STAGES * kTileBytes);
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (tid == 0) ring_init(bars, STAGES);
+    uint16_t* heads = reinterpret_cast<uint16_t*>(sm + (size_t)STAGES * kTileBytes + sizeof(TopSmem));
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) row_bars_init(bars);
     __syncthreads();
-    const int64_t items = p.N * p.segs;
-    auto row_of = [&](int64_t item) { return p.segs == 1 ? item : item / p.segs; };
 
-    if (tid >= kScanThreads) {  // the copying warp
+    if (threadIdx.x < kMainThreads) {
+        Turn at, q;
+        for (;; q.next(kPlaces)) {
+            if (!row_wait(bars, &bars.ready[q.s], q.ph)) return;
+            const int64_t row = bars.item[q.s].row, nv = bars.item[q.s].nv;
+            const int skip = bars.item[q.s].skip;
+            if (row < 0) return;
+            if (skip)
+                warp_arrive(&bars.done[q.s]);
+            else if (!main_stats<T, 4, ENT, GM>(bars, at, STAGES, ring, q.s, nv, p.L, heads + q.s * kTopHeads))
+                return;
+            warp_arrive(&bars.free_[q.s]);
+        }
+    }
+
+    if (threadIdx.x < kMainThreads + 32) {  // the copying warp
         const uint64_t policy = l2_evict_first_policy();
-        RingAt at;
+        Turn at, q;
         uint32_t issued = 0;
-        const bool lists = p.tokens.n > 1;
-        int64_t y = p.tokens.n == 1 && blockIdx.x < items ? p.tokens.at(row_of(blockIdx.x), 0) : 0;
-        for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-            const int64_t r = row_of(item), next = item + gridDim.x;
-            bool skip = p.tokens.n == 1 && y == p.tokens.ignore_idx;
-            if (p.tokens.n == 1 && next < items) y = p.tokens.at(row_of(next), 0);
-            if (lists) {
+        bool ok = true;
+        const int64_t items = p.N * p.segs;
+        auto row_of = [&](int64_t item) { return p.segs == 1 ? item : item / p.segs; };
+        const bool one = p.tokens.n == 1;
+        int64_t y = one && blockIdx.x < items ? p.tokens.at(row_of(blockIdx.x), 0) : 0;  // loaded an item ahead
+        for (int64_t item = blockIdx.x; ok; item += gridDim.x, q.next(kPlaces)) {
+            const bool more = item < items;
+            const int64_t r = more ? row_of(item) : -1;
+            bool skip = one && y == p.tokens.ignore_idx;
+            if (one && item + gridDim.x < items) y = p.tokens.at(row_of(item + gridDim.x), 0);
+            if (more && p.tokens.n > 1) {  // left out when all are ignored
                 bool keep = false;
                 for (int k = lane; k < p.tokens.n; k += 32) keep |= p.tokens.at(r, k) != p.tokens.ignore_idx;
                 skip = !__any_sync(kFull, keep);
             }
-            if (skip) continue;
-            bool ok = true;
             if (lane == 0) {
-                const Segment g = segment<ES>(p, r, (int)(item - r * p.segs));
-                const char* body = g.x + g.sp.h1 * ES;
-                for (int64_t f = g.v0; ok && f < g.v1; f += kScanTileVecs)
-                    ok = ring_put(bars, at, issued, STAGES, ring, kTileBytes, body + f * 16,
-                                  (uint32_t)min((int64_t)kScanTileVecs, g.v1 - f) * 16u, policy);
+                ok = row_wait(bars, &bars.free_[q.s], q.ph ^ 1u);
+                if (ok) {
+                    RowItem& it = bars.item[q.s];
+                    it.row = r;
+                    int64_t v0 = 0, v1 = 0;
+                    const char* body = nullptr;
+                    if (more) {
+                        const int seg = (int)(item - r * p.segs);
+                        const char* x = p.x + p.row.at(r) * ES;
+                        const Span16 sp = span16<ES>(x, 0, p.V);
+                        const bool last = seg == p.segs - 1;
+                        v0 = min(sp.nv, seg * p.per);
+                        v1 = last ? sp.nv : min(sp.nv, v0 + p.per);
+                        body = x + sp.h1 * ES;
+                        it.x = x;
+                        it.item = item;
+                        it.v0 = v0;
+                        it.nv = v1 - v0;
+                        // the elements before the body go with the first segment, those after it with the last
+                        it.head = seg == 0 ? (int)sp.h1 : 0;
+                        it.h1 = (int)sp.h1;
+                        it.tail = (int)sp.t0;
+                        it.tails = last ? (int)(p.V - sp.t0) : 0;
+                        it.skip = skip;
+                    }
+                    mbar_arrive(&bars.ready[q.s]);
+                    if (!skip)
+                        for (int64_t v = v0; ok && v < v1; v += kTileVecs)
+                            ok = ring_put(bars, at, issued, STAGES, ring, kTileBytes, body + v * 16,
+                                          (uint32_t)min((int64_t)kTileVecs, v1 - v) * 16u, policy);
+                }
                 if (!ok) ring_drain(bars, issued, STAGES);
             }
-            if (!__shfl_sync(kFull, ok, 0)) break;
+            ok = __shfl_sync(kFull, (int)(ok && more), 0);
         }
         return;
     }
 
-    RingAt at;
-    int64_t y = p.tokens.n == 1 && blockIdx.x < items ? p.tokens.at(row_of(blockIdx.x), 0) : 0;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t r = row_of(item), next = item + gridDim.x;
-        bool skip = p.tokens.n == 1 && y == p.tokens.ignore_idx;
-        if (p.tokens.n == 1 && next < items) y = p.tokens.at(row_of(next), 0);
-        if (p.tokens.n > 1) skip = row_skipped(p.tokens, r);
-        if (skip) {
-            if (!p.part) write_skipped(p, r);
-            continue;
-        }
-        const Segment g = segment<ES>(p, r, (int)(item - r * p.segs));
-        // the elements before the body go with the first segment, those after it with the last
-        const bool head = g.first && tid < g.sp.h1;
-        const bool tail = g.last && g.sp.t0 + tid < p.V;
-        const float xh = head ? VT::load1(g.x + tid * ES) : -INFINITY;
-        const float xt = tail ? VT::load1(g.x + (g.sp.t0 + tid) * ES) : -INFINITY;
-        Stat st = stat_identity();
-        TopState ts = {};
-        typename VT::Max gm[kScanVecs];
-        int has = 0;
-        if constexpr (TOP) {
-            ts = top_start(top, p.top_k);
-#pragma unroll
-            for (int i = 0; i < kScanVecs; ++i) gm[i] = VT::max_init();
-            if (head) has = 1;
-        }
-        const int ntiles = (int)((g.v1 - g.v0 + kScanTileVecs - 1) / kScanTileVecs);
-        for (int t = 0; t < ntiles || t == 0; ++t) {
-            const int64_t f = g.v0 + (int64_t)t * kScanTileVecs;
-            const int n = (int)min((int64_t)kScanTileVecs, g.v1 - f);
-            const T* tile = reinterpret_cast<const T*>(ring + (size_t)at.s * kTileBytes);
-            uint4 raw[kScanVecs];
-            bool have[kScanVecs];
-            if (ntiles > 0) ring_wait(bars, at);
-#pragma unroll
-            for (int i = 0; i < kScanVecs; ++i) {
-                have[i] = tid + i * kScanThreads < n;
-                if (have[i]) raw[i] = reinterpret_cast<const uint4*>(tile)[tid + i * kScanThreads];
-            }
-            float mx = stat_tile<T, kScanVecs, ENT, TOP>(st, raw, have, p.L, gm);
-            if constexpr (TOP) {
-                const bool edge = t == 0 && head;
-                bool raised = false;
-                if (edge) mx = fmaxf(mx, xh);
-                if (t == 0) {
-#pragma unroll
-                    for (int i = 0; i < kScanVecs; ++i) has |= have[i] ? 1 << i : 0;
-                }
-                if ((t & (t + 1)) == 0) raised = top_raise<T, kScanVecs>(top, ts, gm, has, edge ? xh : -INFINITY);
-                top_tile<T>(top, ts, have[0] || edge, mx, tile, n, (uint32_t)(g.sp.h1 + f * VEC), edge, xh, tid);
-                if (t == 0) ts.recount(top);
-                else if (raised) ts.strict = true;
-            }
-            if (ntiles > 0) ring_release(bars, at, STAGES);
-        }
-        if (head) stat_add(st, xh, p.L);
-        if (tail) stat_add(st, xt, p.L);
-        int c = 0;
-        if constexpr (TOP) {
-            const bool more = tail && ts.takes(xt);
-            if (scan_count(more) > 0) {
-                if (ts.bound + VEC > kTopCap) ts.compact(top);
-                if (more && ts.takes(xt)) top_push_one(top, xt, (uint32_t)(g.sp.t0 + tid));
-            }
-            ts.recount(top);
-            if (ts.bound > 2 * p.top_k + 32) {
-                top_raise<T, kScanVecs>(top, ts, gm, has, -INFINITY);
-                top_prune(top, ts);
-            }
-            ts.compact(top);
-            c = ts.bound;
-        }
-        st = stat_block(st, p.L, red);
-        if (p.part) {
-            if (tid == 0) p.part[item] = make_float4(st.m, st.d, st.s, __int_as_float(c));
-            for (int k = tid; k < c; k += kScanThreads) p.cand[item * p.top_k + k] = top.buf[k];
+    const int tid = threadIdx.x - kMainThreads - 32;
+    Turn q;
+    for (;; q.next(kPlaces)) {
+        if (side_any(!row_wait(bars, &bars.ready[q.s], q.ph))) break;
+        const RowItem& it = bars.item[q.s];
+        const int64_t r = it.row;
+        if (r < 0) break;
+        if (it.skip) {
+            if (!p.part) write_skipped(p, r, tid);
         } else {
-            finish_row<T>(p, r, st, top.buf, c);
+            Given<T> given;
+            if (!p.part) given.load(p, r, it.x, tid);
+            const int64_t ce = edge_column(it);
+            const float xe = ce >= 0 ? VT::load1(it.x + ce * ES) : -INFINITY;
+            if (side_any(!row_wait(bars, &bars.done[q.s], q.ph))) break;
+            const Stat st = row_stats<ENT>(bars.part[q.s], ce >= 0, xe, p.L);
+            int c = 0;
+            if constexpr (GM != 0) {
+                constexpr int unit = GM == 1 ? 32 : 8;
+                const int groups = (int)((it.nv + kTileVecs - 1) / kTileVecs) * (kTileVecs / unit);
+                const int64_t col0 = it.h1 + it.v0 * VT::kElems;
+                c = top_select<T>(top, heads + q.s * kTopHeads, groups, unit,
+                                  reinterpret_cast<const uint4*>(it.x + col0 * ES), it.nv, (uint32_t)col0, p.top_k,
+                                  ce >= 0 && tid < 32, ce < it.head, xe, (uint32_t)ce, tid);
+            }
+            if (p.part) {
+                if (tid == 0) p.part[it.item] = make_float4(st.m, st.d, st.s, __int_as_float(c));
+                for (int k = tid; k < c; k += kSideThreads) p.cand[it.item * p.top_k + k] = top.buf[k];
+            } else {
+                finish_row<T>(p, r, it.x, st, top.buf, c, given, tid);
+            }
         }
-        scan_sync();
+        side_sync();
+        if (tid == 0) mbar_arrive(&bars.free_[q.s]);
     }
     if (tid == 0 && bars.gone) atomicOr(p.err, CE_DEVERR_TIMEOUT);
 }
 
 // A row's segments put together.
 template <typename T>
-__global__ void __launch_bounds__(kScanThreads) ce_join_kernel(const __grid_constant__ ScanArgs p) {
-    extern __shared__ __align__(16) unsigned char sm[];
-    __shared__ float4 red[kScanThreads / 32];
+__global__ void __launch_bounds__(kSideThreads) ce_join_kernel(const __grid_constant__ ScanArgs p) {
+    extern __shared__ __align__(128) unsigned char sm[];
+    __shared__ float4 red[kSideThreads / 32];
     TopSmem& top = *reinterpret_cast<TopSmem*>(sm);
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int64_t r = blockIdx.x;
-    if (row_skipped(p.tokens, r)) {
-        write_skipped(p, r);
+    const char* x = p.x + p.row.at(r) * sizeof(T);
+    Given<T> given;
+    given.load(p, r, x, tid);
+    bool keep = p.tokens.n == 0;
+    for (int k = tid; k < p.tokens.n; k += kSideThreads)
+        keep |= (k == tid ? given.y : p.tokens.at(r, k)) != p.tokens.ignore_idx;
+    if (!side_any(keep)) {
+        write_skipped(p, r, tid);
         return;
     }
     Stat st = stat_identity();
-    if (tid < p.segs) {
-        const float4 v = p.part[r * p.segs + tid];
-        st = Stat{v.x, v.y, v.z};
+    for (int k = tid; k < p.segs; k += kSideThreads) {
+        const float4 v = p.part[r * p.segs + k];
+        st = stat_combine(st, Stat{v.x, v.y, v.z}, p.L);
     }
-    st = stat_block(st, p.L, red);
+    st = stat_warp<true>(st, p.L);
+    if (lane == 0) red[tid >> 5] = make_float4(st.m, st.d, st.s, 0.f);
+    if (tid == 0) top.count = 0;
+    side_sync();
+    st = stat_identity();
+    if (lane < kSideThreads / 32) st = Stat{red[lane].x, red[lane].y, red[lane].z};
+    st = stat_warp<true>(st, p.L);
     int c = 0;
     if (p.top_k > 0) {
-        TopState ts = {};
-        ts.K = p.top_k;
-        ts.all = true;
-        ts.T = -INFINITY;
-        if (tid == 0) top.count = 0;
-        scan_sync();
-        for (int g = 0; g < p.segs; ++g) {
-            const int n = __float_as_int(p.part[r * p.segs + g].w);
-            if (ts.bound + n > kTopCap) ts.compact(top);
-            const int base = ts.bound;
-            for (int k = tid; k < n; k += kScanThreads) top.buf[base + k] = p.cand[(r * p.segs + g) * p.top_k + k];
-            ts.bound += n;
-            if (tid == 0) top.count = ts.bound;
+        TopGate g;
+        g.K = p.top_k;
+        g.all = true;
+        // a warp a segment, as many at a time as the buffer has room for
+        const int together = max(1, min(p.segs, (kTopCap - p.top_k) / p.top_k));
+        for (int g0 = 0; g0 < p.segs; g0 += together) {
+            const int n = min(together, p.segs - g0);
+            top_room(top, g, n * p.top_k, tid);
+            for (int k = tid >> 5; k < n; k += kSideThreads / 32) {
+                const int64_t item = r * p.segs + g0 + k;
+                const int have = __float_as_int(p.part[item].w);
+                int base = 0;
+                if (lane == 0) base = atomicAdd(&top.count, have);
+                base = __shfl_sync(kFull, base, 0);
+                for (int u = lane; u < have; u += 32) top.buf[base + u] = p.cand[item * p.top_k + u];
+            }
         }
-        ts.compact(top);
-        c = ts.bound;
+        c = top_finish(top, p.top_k, tid);
     }
-    finish_row<T>(p, r, st, top.buf, c);
+    finish_row<T>(p, r, x, st, top.buf, c, given, tid);
 }
 
-template <typename T, bool TOP, bool ENT>
+template <typename T, int GM, bool ENT>
 cudaError_t launch_scan_t(const ScanArgs& a, cudaStream_t s) {
-    constexpr size_t smem = scan_smem(TOP);
-    auto* k = ce_scan_kernel<T, TOP, ENT>;
+    constexpr size_t smem = scan_smem(GM);
+    auto* k = ce_scan_kernel<T, GM, ENT>;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
     if (e != cudaSuccess) return e;
     int64_t grid = a.N * a.segs;
     if (grid > kScanSlots) grid = kScanSlots;
-    k<<<(unsigned)grid, kScanThreads + 32, smem, s>>>(a);
+    k<<<(unsigned)grid, kRowThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_scan_type(const ScanArgs& a, bool entropy, cudaStream_t s) {
-    if (a.top_k > 0) return entropy ? launch_scan_t<T, true, true>(a, s) : launch_scan_t<T, true, false>(a, s);
-    return entropy ? launch_scan_t<T, false, true>(a, s) : launch_scan_t<T, false, false>(a, s);
+    if (a.top_k > kFewTop) return entropy ? launch_scan_t<T, 2, true>(a, s) : launch_scan_t<T, 2, false>(a, s);
+    if (a.top_k > 0) return entropy ? launch_scan_t<T, 1, true>(a, s) : launch_scan_t<T, 1, false>(a, s);
+    return entropy ? launch_scan_t<T, 0, true>(a, s) : launch_scan_t<T, 0, false>(a, s);
 }
 
 template <typename T>
 cudaError_t launch_join(const ScanArgs& a, cudaStream_t s) {
-    const size_t smem = a.top_k > 0 ? sizeof(TopSmem) : 0;
+    const size_t smem = sizeof(TopSmem);
     auto* k = ce_join_kernel<T>;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)a.N, kScanThreads, smem, s>>>(a);
+    k<<<(unsigned)a.N, kSideThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -352,8 +341,8 @@ extern "C" size_t ce_logprobs_workspace_bytes(int64_t N, int64_t V, ce_dtype dty
     if (dtype < CE_F32 || dtype > CE_F16 || N < 0 || N > 0x7fffffffLL || V < 1 || V > 0x7fffffffLL || top_k < 0 ||
         top_k > kMaxTop)
         return 0;
-    const ScanPlan pl = plan_scan(N, V, elem_size(dtype));
-    if (pl.segs == 1) return kWsHeaderBytes;
+    const ScanPlan pl = plan_scan(N, V, elem_size(dtype), top_k);
+    if (pl.segs <= 1) return pl.segs ? kWsHeaderBytes : 0;
     return kWsHeaderBytes + part_bytes(N, pl.segs) + align_up((size_t)N * pl.segs * top_k * 8, 256);
 }
 
@@ -379,7 +368,8 @@ extern "C" ce_status ce_logprobs_fwd(const void* logits, ce_dtype dtype, int64_t
         if (workspace_bytes < ce_logprobs_workspace_bytes(N, V, dtype, top_k)) return CE_ERR_WORKSPACE_TOO_SMALL;
     }
     if (N == 0) return CE_OK;
-    const ScanPlan pl = plan_scan(N, V, elem_size(dtype));
+    const ScanPlan pl = plan_scan(N, V, elem_size(dtype), top_k);
+    if (pl.segs == 0) return CE_ERR_INVALID_ARG;
     char* ws = static_cast<char*>(workspace);
     ScanArgs a = {};
     a.x = static_cast<const char*>(logits);

@@ -1,23 +1,37 @@
 // ce_rowscan.cuh -- what the passes over rows of logits share: a row's softmax
 // statistics, and the exact selection of its largest logits on the way.
 //
-// Statistics of a set of logits x at the scale L = log2(e) / temperature, with
-// y = (x - m) L: the maximum m, d = sum 2^y and s = sum y 2^y, so that
-//   log-probability = (x - m) / temperature - log d,   entropy = log d - ln 2 * s / d
-// (the differences x - m are taken first: a row that lies at -3e4, or at the type's
-// lowest value, keeps its digits).  An infinite or missing logit counts for
-// nothing in d and s; a NaN makes both NaN.
+// Statistics of a set of logits x at the scale L = log2(e) / temperature: the maximum m,
+// d = sum 2^y and s = sum y 2^y with y = x L - M, M = m L rounded (one fused step from x, and
+// M is a reference like any other: what its rounding shifts is given back in log d), so
+//   log d = ln 2 (log2 d - (m L - M)),  log-probability = (x - m) / temperature - log d,
+//   entropy = ln 2 (log2 d - s / d).
+// Where M leaves float32 (a row at the type's lowest value) y = (x - m) L.  A logit of
+// -inf counts for nothing in d and s; a NaN makes both NaN.
+//
+// The streaming kernels built on this (ce_logprobs.cu, ce_distill.cu) are persistent;
+// the warps of a CTA have three parts and meet at mbarriers alone:
+//   the copying warp  takes rows (or segments of rows), describes each in a slot of a short
+//                     queue and copies its 16-byte aligned body tile by tile into a ring
+//                     (1-D bulk copies);
+//   eight main warps  take the tiles out, sum the statistics and, where a gradient
+//                     is written, take the row's tiles a second time; a row costs
+//                     them a warp reduction and no barrier of their own;
+//   four side warps   do what a row has beside its stream, while the main warps are
+//                     on the next: the elements around the body, the given or listed
+//                     tokens, the largest logits, the outputs.
+// (With the eight warps doing all of it between barriers, a row of 32000 columns cost
+// them as much again as its tiles did: 16384 rows 210 us.)
 //
 // Selection of the K largest, ties to the lowest column: a candidate is the key
-// (value, ~column), so keys differ and their order is the answer's.  A threshold T
-// under which no logit can be among the K largest keeps nearly all logits out: the
-// K-th largest of the maxima of 256 (K over 64: 1024) groups of the logits read so
-// far, which K logits at least are not below.  It is taken in the first tile and
-// again in tiles 1, 3, 7, ..., so of random logits about K (1 + ln 2) come in at
-// each and 1.2 K to 1.4 K are left at the end; in between only what is above T
-// counts, since K logits not below it lie in columns before.
-// A tile that could overfill the buffer (equal or rising logits) is taken vector by
-// vector with the buffer sorted in between, so any row is exact in bounded time.
+// (value, ~column), so keys differ and their order is the answer's.  The main warps
+// leave the maximum of each group of 32 vectors (K over 64: of 8) of the row; T, the
+// K-th largest of them, is a value that K logits at least are not below, so only the
+// groups that reach it are read again, from L2, and of random logits 1.1 K to 1.4 K are
+// candidates.  Short rows have too few groups: their vectors' maxima are taken first.
+// Groups are read in the order of their columns, in batches that the buffer has room
+// for after it was sorted and cut to K, and once K candidates are held only what is
+// above T counts: equal or ordered logits cost time, not exactness.
 #pragma once
 
 #include "ce_device.cuh"
@@ -35,136 +49,171 @@ struct Stat {
 __device__ __forceinline__ Stat stat_identity() { return Stat{-INFINITY, 0.f, 0.f}; }
 
 constexpr float kFarBelow = -1e4f;  // 2^kFarBelow is 0, and so is its product with it
+constexpr float kRefMost = 1e38f;   // a reference this far out is not used
+constexpr float kLn2f = 0.6931471805599453f;
+
+__device__ __forceinline__ float stat_ref(float m, float L) { return __fmul_rn(m, L); }
+// The exponent by which what is relative to m counts relative to the larger top.
+__device__ __forceinline__ float stat_shift(float m, float top, float L) {
+    return m == top ? 0.f : fmaxf(stat_ref(m, L) - stat_ref(top, L), kFarBelow);
+}
 
 __device__ __forceinline__ Stat stat_combine(const Stat& a, const Stat& b, float L) {
     const float m = fmaxf(a.m, b.m);
-    const float ya = a.m == m ? 0.f : fmaxf((a.m - m) * L, kFarBelow);
-    const float yb = b.m == m ? 0.f : fmaxf((b.m - m) * L, kFarBelow);
+    const float ya = stat_shift(a.m, m, L), yb = stat_shift(b.m, m, L);
     const float fa = ex2_approx(ya), fb = ex2_approx(yb);
     return Stat{m, fa * a.d + fb * b.d, fa * fmaf(a.d, ya, a.s) + fb * fmaf(b.d, yb, b.s)};
 }
 
+// The warp's statistics, in every lane: one maximum, one factor a lane, plain sums.
+template <bool ENT>
 __device__ __forceinline__ Stat stat_warp(Stat a, float L) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        Stat b;
-        b.m = __shfl_xor_sync(kFull, a.m, off);
-        b.d = __shfl_xor_sync(kFull, a.d, off);
-        b.s = __shfl_xor_sync(kFull, a.s, off);
-        a = stat_combine(a, b, L);
-    }
-    return a;
+    const float m = warp_max_redux(a.m);
+    const float y = stat_shift(a.m, m, L), f = ex2_approx(y);
+    Stat r{m, f * a.d, ENT ? f * fmaf(a.d, y, a.s) : 0.f};
+    r.d = warp_allsum(r.d);
+    if (ENT) r.s = warp_allsum(r.s);
+    return r;
 }
+
+// log sum exp((x - m) / temperature), 0 where nothing is allowed.
+__device__ __forceinline__ float stat_logd(const Stat& t, float L) {
+    const float M = stat_ref(t.m, L);
+    return kLn2f * (log2f(t.d) - (fabsf(M) < kRefMost ? fmaf(t.m, L, -M) : 0.f));
+}
+__device__ __forceinline__ float stat_entropy(const Stat& t) { return kLn2f * (log2f(t.d) - t.s / t.d); }
 
 // Nothing is allowed in the row (every logit -inf).
 __device__ __forceinline__ bool stat_none(float m, float d) { return m == -INFINITY && d == d; }
 
 // One logit more.
 __device__ __forceinline__ void stat_add(Stat& a, float x, float L) {
-    Stat b{x == x ? x : -INFINITY, x == -INFINITY ? 0.f : (x == x && x != INFINITY ? 1.f : NAN), 0.f};
+    const float M = stat_ref(x, L), y = fabsf(M) < kRefMost ? fmaf(x, L, -M) : 0.f;
+    Stat b{x, ex2_approx(y), 0.f};
+    b.s = b.d * y;
+    if (x == -INFINITY) b.d = 0.f;
+    if (x == INFINITY || x != x) b = Stat{x == x ? x : -INFINITY, NAN, NAN};
     a = stat_combine(a, b, L);
 }
 
-// The vectors of one tile that a thread holds (have: those that are there).  ENT: s as
-// well.  GM: the running maxima of the thread's vector places, kept packed.
-template <typename T, int NV, bool ENT, bool GM>
-__device__ __forceinline__ float stat_tile(Stat& a, const uint4 (&raw)[NV], const bool (&have)[NV], float L,
-                                           typename Vec<T>::Max (&gm)[NV]) {
+// e = 2^y of one vector's logits relative to m, added to d2 and (ENT) with y to s2.  FAR: y
+// = (x - m) L, ref = -m (else ref = -M); LOW: some logit may be -inf.
+template <typename T, bool ENT, bool FAR, bool LOW>
+__device__ __forceinline__ void stat_vector(const uint4& raw, float ref, float L, float2& d2, float2& s2) {
     using VT = Vec<T>;
     constexpr int PP = VT::kElems / 2;
-    typename VT::Max tm = VT::max_init();
+    const float2 R = make_float2(ref, ref), LL = make_float2(L, L);
+    float2 x[PP];
+    VT::unpack2(raw, x);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (!have[i]) continue;
-        tm = VT::max_acc(tm, raw[i]);
-        if (GM) gm[i] = VT::max_acc(gm[i], raw[i]);
+    for (int k = 0; k < PP; ++k) {
+        float2 y = FAR ? __fmul2_rn(__fadd2_rn(x[k], R), LL) : __ffma2_rn(x[k], LL, R);
+        const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+        d2 = __fadd2_rn(d2, e);
+        if (ENT) {
+            if (LOW) y = make_float2(fmaxf(y.x, kFarBelow), fmaxf(y.y, kFarBelow));
+            s2 = __ffma2_rn(e, y, s2);
+        }
     }
-    const float top = VT::max_done(tm);
+}
+// What is rarely met, out of the way: a row at the type's lowest value, logits of -inf
+// under an entropy.
+template <typename T, bool ENT>
+__device__ __forceinline__ float4 stat_far(const uint4* src, int n, float m, float L) {
+    float2 d2 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
+    const bool near = fabsf(stat_ref(m, L)) < kRefMost || m == -INFINITY;
+    const float ref = m == -INFINITY ? 0.f : (near ? -stat_ref(m, L) : -m);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        if (near) stat_vector<T, ENT, false, true>(src[i * kMainThreads], ref, L, d2, s2);
+        else stat_vector<T, ENT, true, true>(src[i * kMainThreads], ref, L, d2, s2);
+    }
+    return make_float4(d2.x, d2.y, s2.x, s2.y);
+}
+
+// A thread's vectors of a tile: src[0], src[kMainThreads], ..., n of them (FULL: NV).
+// ENT: s as well.  GM: each vector's maximum into gm (-inf where there is none).
+template <typename T, int NV, bool FULL, bool ENT, bool GM>
+__device__ __forceinline__ void stat_tile(Stat& a, const uint4* src, int n, float L, float (&gm)[NV]) {
+    using VT = Vec<T>;
+    uint4 raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (FULL || i < n) raw[i] = src[i * kMainThreads];
+    float top;
+    if (GM) {
+        top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            gm[i] = FULL || i < n ? VT::vmax(raw[i]) : -INFINITY;
+            top = fmaxf(top, gm[i]);
+        }
+    } else {
+        typename VT::Max tm = VT::max_init();
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (FULL || i < n) tm = VT::max_acc(tm, raw[i]);
+        top = VT::max_done(tm);
+    }
     if (top > a.m) {
-        const float y = fmaxf((a.m - top) * L, kFarBelow), f = ex2_approx(y);
+        const float y = stat_shift(a.m, top, L), f = ex2_approx(y);
         if (ENT) a.s = f * fmaf(a.d, y, a.s);
         a.d *= f;
         a.m = top;
     }
-    const float nm = a.m == -INFINITY ? 0.f : -a.m;
-    const float2 NM = make_float2(nm, nm), LL = make_float2(L, L);
     float2 d2 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
+    const float ref = a.m == -INFINITY ? 0.f : -stat_ref(a.m, L);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (have[i]) {
-            float2 x[PP];
-            VT::unpack2(raw[i], x);
-#pragma unroll
-            for (int k = 0; k < PP; ++k) {
-                float2 y = __fmul2_rn(__fadd2_rn(x[k], NM), LL);
-                const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                d2 = __fadd2_rn(d2, e);
-                if (ENT) {
-                    y.x = fmaxf(y.x, kFarBelow);
-                    y.y = fmaxf(y.y, kFarBelow);
-                    s2 = __ffma2_rn(e, y, s2);
-                }
-            }
-        }
+    for (int i = 0; i < NV; ++i)
+        if (FULL || i < n) stat_vector<T, ENT, false, false>(raw[i], ref, L, d2, s2);
+    // (0 times -inf, or a NaN, which d shows too)
+    if (!(fabsf(ref) < kRefMost) || (ENT && s2.x + s2.y != s2.x + s2.y)) {
+        const float4 v = stat_far<T, ENT>(src, FULL ? NV : n, a.m, L);
+        d2 = make_float2(v.x, v.y);
+        s2 = make_float2(v.z, v.w);
     }
     a.d += d2.x + d2.y;
     if (ENT) a.s += s2.x + s2.y;
-    return top;
 }
 
-// ----------------------------------------------------------------- barriers
-// Over the kScanThreads threads that read tiles (others may belong to the CTA).  Not the
-// aligned form (bar.sync): that one says that the warp's lanes arrive together, and
-// where they do not (after a lane's own work or a wait that lanes leave one by one)
-// a later __syncwarp is taken for done and lane 0 hands a slot back before the others
-// have read it.
-__device__ __forceinline__ void scan_sync() {
+// ----------------------------------------------------------------- side warps
+// The kSideThreads threads of the side warps (and of the kernels that are all of
+// them), numbered from 0.  Not the aligned form (bar.sync): a warp's lanes may come one
+// by one, after a lane's own work or a wait.
+__device__ __forceinline__ void side_sync() {
     __syncwarp();
-    asm volatile("barrier.sync 1, %0;" ::"n"(kScanThreads) : "memory");
+    asm volatile("barrier.sync 1, %0;" ::"n"(kSideThreads) : "memory");
 }
-__device__ __forceinline__ int scan_count(bool v) {  // how many threads passed true
+__device__ __forceinline__ bool side_any(bool v) {
     uint32_t n;
     __syncwarp();
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.red.popc.u32 %0, 1, %2, p;\n\t}"
+        "barrier.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(n)
-        : "r"((uint32_t)v), "n"(kScanThreads)
+        : "r"((uint32_t)v), "n"(kSideThreads)
         : "memory");
-    return (int)n;
+    return n != 0;
 }
-
-// Every thread's statistics combined in a fixed order; all threads get them.
-// `red`: a slot for each warp, not used by others until the next barrier.
-__device__ __forceinline__ Stat stat_block(Stat a, float L, float4* red) {
-    a = stat_warp(a, L);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float4(a.m, a.d, a.s, 0.f);
-    scan_sync();
-    Stat t = stat_identity();
-#pragma unroll
-    for (int w = 0; w < kScanThreads / 32; ++w) {
-        const float4 v = red[w];
-        t = stat_combine(t, Stat{v.x, v.y, v.z}, L);
-    }
-    return t;
-}
-__device__ __forceinline__ float scan_sum(float v, float* red) {
+// Over the side warps, in a fixed order; `red` is not used by others until the next barrier.
+__device__ __forceinline__ float side_sum(float v, float* red, int tid) {
     v = warp_allsum(v);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    scan_sync();
+    if ((tid & 31) == 0) red[tid >> 5] = v;
+    side_sync();
     float t = 0.f;
 #pragma unroll
-    for (int w = 0; w < kScanThreads / 32; ++w) t += red[w];
+    for (int w = 0; w < kSideThreads / 32; ++w) t += red[w];
     return t;
 }
-__device__ __forceinline__ float scan_max(float v, float* red) {
+__device__ __forceinline__ float side_max(float v, float* red, int tid) {
     v = warp_allmax(v);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    scan_sync();
+    if ((tid & 31) == 0) red[tid >> 5] = v;
+    side_sync();
     float t = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kScanThreads / 32; ++w) t = fmaxf(t, red[w]);
+    for (int w = 0; w < kSideThreads / 32; ++w) t = fmaxf(t, red[w]);
     return t;
 }
 
@@ -180,66 +229,68 @@ __device__ __forceinline__ float key_value(uint64_t k) {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
 __device__ __forceinline__ uint32_t key_column(uint64_t k) { return 0xffffffffu - (uint32_t)k; }
+// The first 16 bits of a value's key: they order values rounded down to them (a NaN, the
+// maximum of nothing else, as -inf).
+constexpr uint32_t kLowestHead = 0x007fu;
+__device__ __forceinline__ uint32_t value_head(float x) {
+    return x == x ? (uint32_t)(top_key(x, 0) >> 48) : kLowestHead;
+}
 
 struct TopSmem {
     uint64_t buf[kTopCap];
-    int cnt[16];
-    int count;
+    uint16_t vheads[kTopHeads];  // of a short row's vectors
+    uint16_t list[kTopHeads];    // groups to be read again
+    int count, listed;
+    uint32_t kth;
 };
 
-// The largest 16-bit head of an ordered value that at least K of the groups' maxima
-// reach, where each thread brings n of them (v); as the value it stands for, rounded
-// down.  False: there are fewer than K groups (a group without logits is no group).
-template <int NG>
-__device__ __forceinline__ bool kth_group(TopSmem& s, const uint32_t (&v)[NG], int K, float& T) {
-    uint32_t head = 0;
-    if (NG > 1) {
-        if (threadIdx.x < 16) s.cnt[threadIdx.x] = 0;
-        scan_sync();
-    }
+// The largest head that at least K of the n heads reach; 0: fewer than K are not 0.  One warp.
+__device__ __forceinline__ uint32_t kth_head(const uint16_t* heads, int n, int K) {
+    const int lane = threadIdx.x & 31;
+    uint32_t kth = 0;
     for (int b = 15; b >= 0; --b) {
-        const uint32_t cand = head | (1u << b);
-        int n;
-        if (NG == 1) {
-            n = scan_count(v[0] >= cand);
-        } else {
-            int own = 0;
-#pragma unroll
-            for (int i = 0; i < NG; ++i) own += v[i] >= cand;
-            own = (int)__reduce_add_sync(kFull, (unsigned)own);
-            if ((threadIdx.x & 31) == 0) atomicAdd(&s.cnt[b], own);
-            scan_sync();
-            n = s.cnt[b];
+        const uint32_t cand = kth | (1u << b);
+        int own = 0;
+        for (int k = lane * 8; k < n; k += 256) {
+            const uint4 u = *reinterpret_cast<const uint4*>(heads + k);  // past n: zeros
+            own += ((u.x & 0xffffu) >= cand) + ((u.x >> 16) >= cand) + ((u.y & 0xffffu) >= cand) +
+                   ((u.y >> 16) >= cand) + ((u.z & 0xffffu) >= cand) + ((u.z >> 16) >= cand) +
+                   ((u.w & 0xffffu) >= cand) + ((u.w >> 16) >= cand);
         }
-        if (n >= K) head = cand;
-        if (n == K) break;
+        const int c = (int)__reduce_add_sync(kFull, (unsigned)own);
+        if (c >= K) kth = cand;
+        if (c == K) break;
     }
-    T = head <= 0x007fu ? -INFINITY : key_value((uint64_t)head << 48);
-    return head != 0;
+    return kth;
 }
-__device__ __forceinline__ uint32_t value_head(float x) { return (uint32_t)(top_key(x, 0) >> 48); }
 
-// The first c keys of buf in falling order.  All threads, between barriers.
-__device__ __forceinline__ void top_sort(TopSmem& s, int c) {
-    const int tid = threadIdx.x;
-    if (c <= kScanThreads) {
-        // few: each key's rank is the number of larger ones
-        const uint64_t own = tid < c ? s.buf[tid] : 0;
-        int r = 0;
-        if ((tid & ~31) < c)
-            for (int k = 0; k < c; ++k) r += s.buf[k] > own;
-        scan_sync();
-        if (tid < c) s.buf[r] = own;
-        scan_sync();
+// The first c keys of buf in falling order.  All side threads, between barriers.
+__device__ __forceinline__ void top_sort(TopSmem& s, int c, int tid) {
+    if (c <= 2 * kSideThreads) {
+        // few: a key's rank is the number of larger ones
+        const uint64_t k0 = tid < c ? s.buf[tid] : 0, k1 = tid + kSideThreads < c ? s.buf[tid + kSideThreads] : 0;
+        int r0 = 0, r1 = 0;
+        if ((tid & ~31) < c) {
+#pragma unroll 4
+            for (int k = 0; k < c; ++k) {
+                const uint64_t o = s.buf[k];
+                r0 += o > k0;
+                r1 += o > k1;
+            }
+        }
+        side_sync();
+        if (tid < c) s.buf[r0] = k0;
+        if (tid + kSideThreads < c) s.buf[r1] = k1;
+        side_sync();
         return;
     }
-    int n = 2 * kScanThreads;
+    int n = 4 * kSideThreads;
     while (n < c) n *= 2;
-    for (int k = c + tid; k < n; k += kScanThreads) s.buf[k] = 0;
-    scan_sync();
+    for (int k = c + tid; k < n; k += kSideThreads) s.buf[k] = 0;
+    side_sync();
     for (int size = 2; size <= n; size *= 2) {
         for (int step = size / 2; step > 0; step /= 2) {
-            for (int p = tid; p < n / 2; p += kScanThreads) {
+            for (int p = tid; p < n / 2; p += kSideThreads) {
                 const int lo = p & (step - 1), i = 2 * (p - lo) + lo, j = i + step;
                 const uint64_t a = s.buf[i], b = s.buf[j];
                 if ((a < b) == ((i & size) == 0)) {
@@ -247,216 +298,212 @@ __device__ __forceinline__ void top_sort(TopSmem& s, int c) {
                     s.buf[j] = a;
                 }
             }
-            scan_sync();
+            side_sync();
         }
     }
 }
 
-// The state of a selection, the same in every thread of the CTA.
-struct TopState {
+// What a selection lets in, the same in every side thread.
+struct TopGate {
     int K;
-    int bound;     // candidates held, at most
     float T;
-    bool all;      // no threshold yet: every logit counts
-    bool strict;   // K logits not below T are held: only what is above it counts
-
+    bool all;      // no threshold: every number counts
+    bool strict;   // K candidates not below T are held, of columns before: only what is above T counts
     __device__ __forceinline__ bool takes(float x) const { return all ? x == x : (strict ? x > T : x >= T); }
-
-    // Sorts what is held and keeps the K largest.
-    __device__ __forceinline__ void compact(TopSmem& s) {
-        scan_sync();
-        const int c = s.count;
-        top_sort(s, c);
-        bound = c < K ? c : K;
-        if (c >= K) {
-            T = key_value(s.buf[K - 1]);
-            all = false;
-            strict = true;
-        }
-        scan_sync();
-        if (threadIdx.x == 0) s.count = bound;
-        scan_sync();
-    }
-
-    // What the buffer holds now.
-    __device__ __forceinline__ void recount(TopSmem& s) {
-        scan_sync();
-        bound = s.count;
-        if (!all && bound >= K) strict = true;
-        scan_sync();
-    }
 };
 
-// Vectors [i0, i1) of each lane that `hit`: a warp takes a lane's logits together.
-// tile: its vectors, nvec of them; col0: the column of its first logit.
-template <typename T>
-__device__ __forceinline__ void top_push(TopSmem& s, const TopState& st, bool hit, const T* tile, int nvec,
-                                         uint32_t col0, int i0, int i1) {
-    constexpr int VEC = Vec<T>::kElems;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned todo = __ballot_sync(kFull, hit);
-    const int i = i0 + lane / VEC, e = lane % VEC;  // VEC * kScanVecs <= 32
-    while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int v = warp * 32 + src + i * kScanThreads;
-        float x = NAN;
-        if (i < i1 && v < nvec) x = to_f32(tile[v * VEC + e]);
-        const bool ok = st.takes(x);
-        const unsigned m = __ballot_sync(kFull, ok);
-        if (m == 0u) continue;
-        int base = 0;
-        if (lane == 0) base = atomicAdd(&s.count, __popc(m));
-        base = __shfl_sync(kFull, base, 0);
-        if (ok) s.buf[base + __popc(m & ((1u << lane) - 1u))] = top_key(x, col0 + (uint32_t)(v * VEC + e));
-    }
-}
-__device__ __forceinline__ void top_push_one(TopSmem& s, float x, uint32_t column) {
-    s.buf[atomicAdd(&s.count, 1)] = top_key(x, column);
-}
-
-__device__ __forceinline__ TopState top_start(TopSmem& s, int K) {
-    TopState st;
-    st.K = K;
-    st.bound = 0;
-    st.T = -INFINITY;
-    st.all = true;
-    st.strict = false;
-    if (threadIdx.x == 0) s.count = 0;
-    return st;
-}
-
-// Raises the threshold from the groups' running maxima (has: the thread's group i has a
-// logit).  What is held and not below the new threshold was let in by the old one; the
-// present tile is to be taken with `takes` as it is then.
-template <typename T, int NV>
-__device__ __forceinline__ bool top_raise(TopSmem& s, TopState& st, const typename Vec<T>::Max (&gm)[NV], int has,
-                                          float edge) {
-    using VT = Vec<T>;
-    float t;
-    bool ok;
-    if (st.K <= 64) {
-        float f = edge;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) f = fmaxf(f, VT::max_done(gm[i]));
-        const uint32_t v[1] = {has ? value_head(f) : 0u};
-        ok = kth_group<1>(s, v, st.K, t);
-    } else {
-        uint32_t v[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const float f = VT::max_done(gm[i]);
-            v[i] = (has >> i) & 1 ? value_head(i == 0 ? fmaxf(f, edge) : f) : 0u;
+// How many candidates are held; sorted and cut to K where there is no room for `more`.
+__device__ __forceinline__ int top_room(TopSmem& s, TopGate& g, int more, int tid) {
+    side_sync();
+    int c = s.count;
+    if (c + more > kTopCap) {
+        top_sort(s, c, tid);
+        if (c >= g.K) {
+            c = g.K;
+            g.T = key_value(s.buf[c - 1]);
+            g.all = false;
         }
-        ok = kth_group<NV>(s, v, st.K, t);
+        side_sync();
+        if (tid == 0) s.count = c;
     }
-    const bool up = ok && (st.all || t > st.T);
-    if (up) {
-        st.T = t;
-        st.all = false;
-        st.strict = false;
-    }
-    return up;
+    g.strict = !g.all && c >= g.K;
+    side_sync();
+    return c;
 }
-
-// Drops what is held below the threshold.
-__device__ __forceinline__ void top_prune(TopSmem& s, TopState& st) {
-    constexpr int EACH = kTopCap / kScanThreads;
+__device__ __forceinline__ void top_push(TopSmem& s, bool ok, float x, uint32_t column) {
+    const unsigned m = __ballot_sync(kFull, ok);
+    if (m == 0u) return;
     const int lane = threadIdx.x & 31;
-    scan_sync();
-    const int c = s.count;
-    uint64_t k[EACH];
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-        const int at = i * kScanThreads + threadIdx.x;
-        k[i] = at < c ? s.buf[at] : 0;
-    }
-    scan_sync();
-    if (threadIdx.x == 0) s.count = 0;
-    scan_sync();
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-        if (i * kScanThreads >= c) break;
-        const bool ok = k[i] != 0 && (st.all || key_value(k[i]) >= st.T);
-        const unsigned m = __ballot_sync(kFull, ok);
-        int base = 0;
-        if (lane == 0 && m) base = atomicAdd(&s.count, __popc(m));
-        base = __shfl_sync(kFull, base, 0);
-        if (ok) s.buf[base + __popc(m & ((1u << lane) - 1u))] = k[i];
-    }
+    int base = 0;
+    if (lane == 0) base = atomicAdd(&s.count, __popc(m));
+    base = __shfl_sync(kFull, base, 0);
+    if (ok) s.buf[base + __popc(m & ((1u << lane) - 1u))] = top_key(x, column);
 }
 
-// A tile's candidates.  top: the maximum of the thread's logits in it (and of
-// `edge`, an element before the tile's vectors, where has_edge).
+// The candidates' buffer sorted and cut to K; how many there are.
+__device__ __forceinline__ int top_finish(TopSmem& s, int K, int tid) {
+    side_sync();
+    const int c = s.count;
+    top_sort(s, c, tid);
+    return c < K ? c : K;
+}
+
+// The K largest of a row's (segment's) logits into the front of s.buf, in falling order;
+// returns how many there are.  body: its nv vectors in global memory, their first logit of
+// column col0; heads: the groups' maxima, G of them (zeros up to a multiple of 256), `unit`
+// vectors each.  xe, ce: the thread's element around the body (before: it lies before the
+// body), where has_edge.  All side threads.
 template <typename T>
-__device__ __forceinline__ void top_tile(TopSmem& s, TopState& st, bool has, float top, const T* tile, int nvec,
-                                         uint32_t col0, bool has_edge, float edge, uint32_t edge_col) {
-    constexpr int VEC = Vec<T>::kElems;
-    constexpr int EACH = VEC * kScanVecs + 1;
-    bool hit = has && st.takes(top);
-    int nh = scan_count(hit);
-    if (nh == 0) return;
-    if (st.bound + nh * EACH > kTopCap) {
-        st.recount(s);
-        if (st.bound >= 2 * st.K && st.bound >= 64) {
-            st.compact(s);
-            hit = has && st.takes(top);
-            nh = scan_count(hit);
-            if (nh == 0) return;
+__device__ __forceinline__ int top_select(TopSmem& s, const uint16_t* heads, int G, int unit, const uint4* body,
+                                          int64_t nv, uint32_t col0, int K, bool has_edge, bool before, float xe,
+                                          uint32_t ce, int tid) {
+    using VT = Vec<T>;
+    constexpr int VEC = VT::kElems;
+    const int lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) s.count = 0;
+    if (G < 2 * K && nv <= kTopHeads) {
+        for (int v = tid; v < kTopHeads; v += kSideThreads) {
+            uint32_t h = 0;
+            if (v < nv) h = value_head(VT::vmax(__ldg(body + v)));
+            s.vheads[v] = (uint16_t)h;
+            if (v >= ((nv + 255) & ~255)) break;
+        }
+        heads = s.vheads;
+        G = (int)nv;
+        unit = 1;
+    }
+    side_sync();
+    if (warp == 0) {
+        const uint32_t kth = kth_head(heads, G, K);
+        int n = 0;
+        for (int k0 = 0; k0 < G; k0 += 32) {
+            const bool in = k0 + lane < G && heads[k0 + lane] >= (kth ? kth : 1u);
+            const unsigned m = __ballot_sync(kFull, in);
+            if (in) s.list[n + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(k0 + lane);
+            n += __popc(m);
+        }
+        if (lane == 0) {
+            s.kth = kth;
+            s.listed = n;
         }
     }
-    if (st.bound + nh * EACH <= kTopCap) {
-        if (hit && has_edge && st.takes(edge)) top_push_one(s, edge, edge_col);
-        top_push<T>(s, st, hit, tile, nvec, col0, 0, kScanVecs);
-        st.bound += nh * EACH;
-        return;
+    side_sync();
+    const uint32_t kth = s.kth;
+    TopGate g;
+    g.K = K;
+    g.all = kth == 0;
+    g.strict = false;
+    g.T = kth <= kLowestHead ? -INFINITY : key_value((uint64_t)kth << 48);
+    top_push(s, has_edge && before && g.takes(xe), xe, ce);
+    // a warp takes 32 vectors at a time, twice in a batch; the next batch's are on their way
+    constexpr int STEPS = 2, WARPS = kSideThreads / 32;
+    const int per = 32 / unit, batch = STEPS * WARPS * per, listed = s.listed;
+    uint4 next[STEPS];
+    int64_t vn[STEPS];
+    auto fetch = [&](int b) {
+#pragma unroll
+        for (int u = 0; u < STEPS; ++u) {
+            const int e = b + (u * WARPS + warp) * per + lane / unit;
+            vn[u] = e < listed ? (int64_t)s.list[e] * unit + lane % unit : nv;
+            if (vn[u] < nv) next[u] = __ldg(body + vn[u]);
+        }
+    };
+    fetch(0);
+    for (int b = 0; b < listed; b += batch) {
+        uint4 raw[STEPS];
+        int64_t v[STEPS];
+#pragma unroll
+        for (int u = 0; u < STEPS; ++u) {
+            raw[u] = next[u];
+            v[u] = vn[u];
+        }
+        fetch(b + batch);
+        top_room(s, g, STEPS * kSideThreads * VEC, tid);
+#pragma unroll
+        for (int u = 0; u < STEPS; ++u) {
+            const bool hit = v[u] < nv && (g.all || g.takes(VT::vmax(raw[u])));
+            if (!__any_sync(kFull, hit)) continue;
+            float x[VEC];
+            VT::unpack(raw[u], x);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k)
+                top_push(s, hit && g.takes(x[k]), x[k], col0 + (uint32_t)(v[u] * VEC + k));
+        }
     }
-    if (hit && has_edge && st.takes(edge)) top_push_one(s, edge, edge_col);  // fewer than VEC in all
-    for (int i = 0; i < kScanVecs; ++i) {
-        st.recount(s);
-        if (st.bound + kScanThreads * VEC > kTopCap) st.compact(s);
-        top_push<T>(s, st, hit, tile, nvec, col0, i, i + 1);
-    }
-    st.recount(s);
+    top_room(s, g, kSideThreads, tid);
+    top_push(s, has_edge && !before && g.takes(xe), xe, ce);
+    return top_finish(s, K, tid);
 }
 
-// ----------------------------------------------------------------- the ring
-// Tiles of a row's 16-byte aligned body, copied into a ring of shared memory by one
-// thread of a warp of its own (1-D bulk copies).  full[s] completes when the tile in slot
-// s has landed, empty[s] when every reading warp is done with it.  Every wait is
-// bounded: one that gives up raises `gone` and the error word; the copying thread then
-// issues no more, waits (bounded) for what it has issued and leaves, and the readers
-// run through their rows without waiting.
-constexpr int kRingMost = 12;
-struct RingBars {
+// ----------------------------------------------------------------- the ring and the queue
+// full[s] completes when the tile in slot s has landed, empty[s] when every main warp
+// is done with it.  A row's slot in the queue: ready when the copying warp has described
+// it, done when every main warp has left its statistics, stored when every main warp has
+// stored its gradient, prep when the side warps have worked on its list, and free when
+// the main warps and the side warps need it no more.  Every wait is bounded: one that
+// gives up raises `gone`, which ends all others; the copying warp then issues no more and
+// leaves when what it has issued has landed (bounded too).
+constexpr int kRingMost = 6;
+constexpr int kQueue = 3;  // places at most
+struct RowItem {
+    const char* x;      // the row
+    char* out;          // its gradient, or NULL
+    int64_t row;        // -1: no more
+    int64_t v0, nv;     // its first vector of the body and how many
+    int64_t item;       // number of the row or segment
+    int h1;             // where the body starts
+    int head, tail;     // elements before it that go with the item, where those after it start
+    int tails;          // how many
+    int skip;           // not read
+};
+struct RowBars {
     uint64_t full[kRingMost], empty[kRingMost];
+    uint64_t ready[kQueue], done[kQueue], stored[kQueue], prep[kQueue], free_[kQueue];
+    RowItem item[kQueue];
+    float4 part[kQueue][kMainThreads / 32];
     volatile int gone;
 };
-struct RingAt {
+__device__ __forceinline__ void row_bars_init(RowBars& b) {
+    constexpr int W = kMainThreads / 32;
+    for (int s = 0; s < kRingMost; ++s) {
+        mbar_init(&b.full[s], 1);
+        mbar_init(&b.empty[s], W);
+    }
+    for (int s = 0; s < kQueue; ++s) {
+        mbar_init(&b.ready[s], 1);
+        mbar_init(&b.done[s], W);
+        mbar_init(&b.stored[s], W);
+        mbar_init(&b.prep[s], 1);
+        mbar_init(&b.free_[s], W + 1);
+    }
+    b.gone = 0;
+    fence_barrier_init();
+}
+// False: gave up, or another wait has.
+__device__ __forceinline__ bool row_wait(RowBars& b, uint64_t* bar, uint32_t ph) {
+    if (mbar_try_wait(bar, ph)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1; !b.gone; ++it) {
+        if (mbar_try_wait(bar, ph)) return true;
+        if ((it & 255u) == 0u && global_timer_ns() - t0 > kWaitLimitNs) b.gone = 1;
+    }
+    return false;
+}
+// A place in the ring or the queue: slot and phase.
+struct Turn {
     int s = 0;
     uint32_t ph = 0;
-    __device__ __forceinline__ void next(int stages) {
-        if (++s == stages) {
+    __device__ __forceinline__ void next(int n) {
+        if (++s == n) {
             s = 0;
             ph ^= 1u;
         }
     }
 };
-__device__ __forceinline__ void ring_init(RingBars& b, int stages) {
-    for (int s = 0; s < stages; ++s) {
-        mbar_init(&b.full[s], 1);
-        mbar_init(&b.empty[s], kScanThreads / 32);
-    }
-    b.gone = 0;
-    fence_barrier_init();
-}
-// The copying thread: `bytes` (a multiple of 16, not 0) of src into the next slot.
-__device__ __forceinline__ bool ring_put(RingBars& b, RingAt& at, uint32_t& issued, int stages, unsigned char* ring,
+// The copying thread: a tile of `bytes` (a multiple of 16, not 0) into the next slot.
+__device__ __forceinline__ bool ring_put(RowBars& b, Turn& at, uint32_t& issued, int stages, unsigned char* ring,
                                          int slot_bytes, const void* src, uint32_t bytes, uint64_t policy) {
-    if (!mbar_wait_bounded(&b.empty[at.s], at.ph ^ 1u)) {
-        b.gone = 1;
-        return false;
-    }
+    if (!row_wait(b, &b.empty[at.s], at.ph ^ 1u)) return false;
     mbar_arrive_expect_tx(&b.full[at.s], bytes);
     tma_load_1d(ring + (size_t)at.s * slot_bytes, src, bytes, &b.full[at.s], policy);
     at.next(stages);
@@ -464,19 +511,96 @@ __device__ __forceinline__ bool ring_put(RingBars& b, RingAt& at, uint32_t& issu
     return true;
 }
 // Before the copying thread leaves early: every copy issued lands.
-__device__ __forceinline__ void ring_drain(RingBars& b, uint32_t issued, int stages) {
+__device__ __forceinline__ void ring_drain(RowBars& b, uint32_t issued, int stages) {
     for (int s = 0; s < stages; ++s)
         if (issued > (uint32_t)s)
             (void)mbar_wait_bounded(&b.full[s], ((issued - 1u - (uint32_t)s) / (uint32_t)stages) & 1u);
 }
-// A reading thread: the slot `at` has landed (or the ring is gone).
-__device__ __forceinline__ void ring_wait(RingBars& b, const RingAt& at) {
-    if (!b.gone && !mbar_wait_bounded(&b.full[at.s], at.ph)) b.gone = 1;
-}
-__device__ __forceinline__ void ring_release(RingBars& b, RingAt& at, int stages) {
+// A warp is done with something: lane 0 arrives for all.  A ring's slot is handed back
+// once its values have been used, not behind the loads: where the warp's global stores
+// were backed up, the loads waited behind them and the arrival did not, and the next tile
+// landed first (in one of 100 launches of 1219 rows of 20011 float32 columns).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&b.empty[at.s]);
-    at.next(stages);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// First pass over a row's tiles by the main warps: the warp's statistics go to part, and
+// (GM: 1 a group of 32 vectors, 2 of 8) the groups' maxima to heads.
+template <typename T, int NV, bool ENT, int GM>
+__device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, const unsigned char* ring, int q,
+                                           int64_t nv, float L, uint16_t* heads) {
+    constexpr int TILE = kMainThreads * NV;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Stat st = stat_identity();
+    for (; nv > 0; nv -= TILE) {
+        const uint4* src = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16) + tid;
+        float gm[NV];
+        if (!row_wait(b, &b.full[at.s], at.ph)) return false;
+        int mine = NV;
+        if (nv >= TILE) {
+            stat_tile<T, NV, true, ENT, GM != 0>(st, src, NV, L, gm);
+        } else {
+            mine = max(0, min(NV, ((int)nv - tid + kMainThreads - 1) / kMainThreads));
+            stat_tile<T, NV, false, ENT, GM != 0>(st, src, mine, L, gm);
+        }
+        warp_arrive(&b.empty[at.s]);
+        at.next(stages);
+        if (GM == 1) {
+            // lane i keeps group i's; 0 where the group has no vector
+            float own = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const float m = warp_max_redux(gm[i]);
+                if (lane == i) own = m;
+            }
+            if (lane < NV)
+                heads[lane * (kMainThreads / 32) + warp] =
+                    (uint16_t)(lane * kMainThreads + warp * 32 < nv ? value_head(own) : 0u);
+            heads += TILE / 32;
+        } else if (GM == 2) {
+            float own = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float m = gm[i];
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+                if ((lane & 7) == i) own = m;
+            }
+            const int i = lane & 7, first = i * kMainThreads + (tid & ~7);
+            if (i < NV) heads[first / 8] = (uint16_t)(first < nv ? value_head(own) : 0u);
+            heads += TILE / 8;
+        }
+    }
+    st = stat_warp<ENT>(st, L);
+    if (lane == 0) b.part[q][warp] = make_float4(st.m, st.d, st.s, 0.f);
+    warp_arrive(&b.done[q]);
+    return true;
+}
+
+// A row's statistics from the main warps' and the elements around its body (lanes 8 and
+// on hold one each); the same in every lane.
+template <bool ENT>
+__device__ __forceinline__ Stat row_stats(const float4* part, bool has_edge, float xe, float L) {
+    constexpr int W = kMainThreads / 32;
+    const int lane = threadIdx.x & 31;
+    Stat st = stat_identity();
+    if (lane < W) {
+        const float4 v = part[lane];
+        st = Stat{v.x, v.y, v.z};
+    } else if (has_edge) {
+        stat_add(st, xe, L);
+    }
+    return stat_warp<ENT>(st, L);
+}
+// The element around the body that lane 8 + k takes, k counting those before it first: its
+// column, or -1.
+__device__ __forceinline__ int64_t edge_column(const RowItem& it) {
+    const int k = (int)(threadIdx.x & 31) - kMainThreads / 32;
+    if (k < 0) return -1;
+    if (k < it.head) return k;
+    return k - it.head < it.tails ? it.tail + (k - it.head) : -1;
 }
 
 // ----------------------------------------------------------------- rows

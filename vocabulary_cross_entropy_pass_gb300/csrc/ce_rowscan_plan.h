@@ -7,14 +7,18 @@
 
 namespace gbce {
 
-constexpr int kScanThreads = 256;                            // threads that read a tile
-constexpr int kScanVecs = 4;                                 // 16-byte vectors of it a thread takes
-constexpr int kScanTileVecs = kScanThreads * kScanVecs;      // 16 KB
+constexpr int kMainThreads = 256;                            // threads that read a tile
+constexpr int kSideThreads = 128;                            // threads beside them
+constexpr int kRowThreads = kMainThreads + 32 + kSideThreads;  // and the copying warp
+constexpr int kTileVecs = kMainThreads * 4;                  // 16-byte vectors of a tile: 16 KB
 constexpr int kTopCap = 4096;                                // candidates held at a time
+constexpr int kTopHeads = 2048;                              // groups' maxima of a row or segment
 constexpr int kMaxTop = 256;                                 // likeliest tokens a call may ask for
+constexpr int kFewTop = 64;                                  // up to here groups of 32 vectors, else of 8
 constexpr int kMaxListed = 1024;                             // given or teacher's tokens of a row
-constexpr int kMaxSegments = 64;
-constexpr int64_t kScanSlots = 304;                          // CTAs that run at a time: two on each of 152 SMs
+constexpr int kMaxSegments = 1024;
+constexpr int64_t kSMs = 152;
+constexpr int64_t kScanSlots = 2 * kSMs;                     // CTAs that run at a time
 
 struct ScanPlan {
     int segs;      // segments of a row
@@ -22,19 +26,21 @@ struct ScanPlan {
 };
 
 // Few rows are cut so that every SM has a part; from four rounds of whole rows on
-// a row stays in one piece.
-inline ScanPlan plan_scan(int64_t N, int64_t V, int es) {
+// a row stays in one piece, as far as its groups' maxima have room.  segs is 0 where
+// they have none.
+inline ScanPlan plan_scan(int64_t N, int64_t V, int es, int top_k) {
     const int64_t nv = V * es / 16;
-    const int64_t tiles = (nv + kScanTileVecs - 1) / kScanTileVecs;
+    const int64_t tiles = (nv + kTileVecs - 1) / kTileVecs;
     int64_t segs = 1;
     if (N > 0 && N < 4 * kScanSlots) segs = (4 * kScanSlots + N - 1) / N;
     if (segs > tiles) segs = tiles;
-    if (segs > kMaxSegments) segs = kMaxSegments;
     if (segs < 1) segs = 1;
+    const int64_t room = top_k <= 0 ? nv : (int64_t)kTopHeads * (top_k <= kFewTop ? 32 : 8);
+    if (nv > segs * room) segs = (nv + room - 1) / room;
     ScanPlan p;
     p.per = (nv + segs - 1) / segs;
     if (p.per < 1) p.per = 1;
-    p.segs = (int)segs;
+    p.segs = segs > kMaxSegments ? 0 : (int)segs;
     return p;
 }
 

@@ -19,8 +19,19 @@
 namespace gbce {
 namespace {
 
-constexpr int kThreads = kScanThreads;
+constexpr int kThreads = 256;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// The CTA's sum of v, in a fixed order.
+__device__ __forceinline__ float cta_sum(float v, float* red) {
+    v = warp_allsum(v);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) t += red[w];
+    return t;
+}
 
 struct Listed {
     int col[kMaxListed];
@@ -79,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) ce_softgrad_kernel(const __grid_cons
         }
         const unsigned m = __ballot_sync(kFull, in);
         if (lane == 0) wn[warp] = __popc(m);
-        scan_sync();
+        __syncthreads();
         int at = listed, all = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
@@ -93,13 +104,13 @@ __global__ void __launch_bounds__(kThreads) ce_softgrad_kernel(const __grid_cons
             ls.x[at] = VT::load1(x + (int64_t)col * ES);
         }
         listed += all;
-        scan_sync();
+        __syncthreads();
     }
     bool zero = stat_none(st.x, st.y);
     float a, b = 0.f;
     if (distill) {
         zero |= p.tokens.at(r, 0) == p.tokens.ignore_idx;
-        zero |= scan_count(bad) > 0;
+        zero |= __syncthreads_or(bad) != 0;
         // Q: 0 where the teacher gives no token any probability, NaN where its logits are no numbers
         const float Q = st.w != st.w         ? st.w
                         : st.z == -INFINITY  ? 0.f
@@ -108,8 +119,8 @@ __global__ void __launch_bounds__(kThreads) ce_softgrad_kernel(const __grid_cons
         a = gt * Q;
     } else {
         if (p.tokens.n > 0) {
-            zero |= scan_count(keep) == 0;
-            total = scan_sum(total, red);
+            zero |= __syncthreads_or(keep) == 0;
+            total = cta_sum(total, red);
         }
         b = SECOND ? -__ldg(p.grad_entropy + r) : 0.f;
         a = SECOND ? fmaf(b, st.z, -total) : -total;
