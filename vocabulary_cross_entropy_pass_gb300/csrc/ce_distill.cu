@@ -48,6 +48,9 @@ struct DistillArgs {
     int stages, slots;
 };
 
+constexpr int kPlaces = 3;  // of the queue: a row in the stream, its list ready; the next; the one before
+constexpr int kRowThreads = kMainThreads + 32 + kSideThreads;
+
 // A row's list in shared memory: the present row's and the next one's.
 constexpr int kLists = 2;
 struct ListEntry {
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kerne
     if (threadIdx.x < kMainThreads) {
         const int tid = threadIdx.x;
         Turn at, q;
-        for (int par = 0;; q.next(kQueue), par ^= 1) {
+        for (int par = 0;; q.next(kPlaces), par ^= 1) {
             if (!row_wait(bars, &bars.ready[q.s], q.ph)) return;
             const RowItem& it = bars.item[q.s];
             const int64_t r = it.row, nv = it.nv;
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kerne
                     it.skip = y == p.tokens.ignore_idx;
                 }
                 mbar_arrive(&bars.ready[q.s]);
-                q.next(kQueue);
+                q.next(kPlaces);
             };
             int64_t r = blockIdx.x, r1 = r + gridDim.x, r2 = 0;
             int64_t y = token(r), y1 = token(r1), y2 = 0;
@@ -306,12 +309,12 @@ __global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kerne
         }
         side_sync();
         if (tid == 0) mbar_arrive(&bars.free_[qf.s]);
-        qf.next(kQueue);
+        qf.next(kPlaces);
         return true;
     };
     Turn q;
     bool fine = true;
-    for (;; q.next(kQueue)) {
+    for (;; q.next(kPlaces)) {
         if (side_any(!row_wait(bars, &bars.ready[q.s], q.ph))) {
             fine = false;
             break;

@@ -15,19 +15,21 @@
 namespace gbce {
 namespace {
 
-__device__ __forceinline__ void write_skipped(const ScanArgs& p, int64_t r, int tid) {
-    if (tid == 0) {
+// A row's outputs by the lanes of one warp.
+__device__ __forceinline__ void write_skipped(const ScanArgs& p, int64_t r) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
         if (p.entropy) p.entropy[r] = 0.f;
         if (p.stats) p.stats[r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
     }
-    for (int k = tid; k < p.tokens.n; k += kSideThreads) p.logprobs[r * p.tokens.n + k] = 0.f;
-    for (int k = tid; k < p.top_k; k += kSideThreads) {
+    for (int k = lane; k < p.tokens.n; k += 32) p.logprobs[r * p.tokens.n + k] = 0.f;
+    for (int k = lane; k < p.top_k; k += 32) {
         p.top_tokens[r * p.top_k + k] = p.tokens.ignore_idx;
         p.top_logprobs[r * p.top_k + k] = 0.f;
     }
 }
 
-// A thread's given token of a row and its logit (the first kSideThreads of them).
+// A lane's given token of a row and its logit (the first 32 of them).
 template <typename T>
 struct Given {
     int64_t y = 0;
@@ -42,16 +44,17 @@ struct Given {
 // A row's outputs from its statistics and its candidates in falling order (c of them).
 template <typename T>
 __device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const char* x, const Stat& t,
-                                           const uint64_t* top, int c, Given<T> given, int tid) {
+                                           const uint64_t* top, int c, Given<T> given) {
+    const int lane = threadIdx.x & 31;
     const bool none = stat_none(t.m, t.d);
     const float logd = none ? 0.f : stat_logd(t, p.L);
-    if (tid == 0) {
+    if (lane == 0) {
         const float h = none ? 0.f : stat_entropy(t);
         if (p.entropy) p.entropy[r] = h;
         if (p.stats) p.stats[r] = make_float4(t.m, logd, h, 0.f);
     }
-    for (int k = tid; k < p.tokens.n; k += kSideThreads) {
-        if (k >= kSideThreads) given.load(p, r, x, k);
+    for (int k = lane; k < p.tokens.n; k += 32) {
+        if (k >= 32) given.load(p, r, x, k);
         float lp = 0.f;
         if (given.y != p.tokens.ignore_idx) {
             if (given.y < 0 || given.y >= p.V) {
@@ -63,7 +66,7 @@ __device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const c
         }
         p.logprobs[r * p.tokens.n + k] = lp;
     }
-    for (int k = tid; k < p.top_k; k += kSideThreads) {
+    for (int k = lane; k < p.top_k; k += 32) {
         int64_t token = -1;  // NaN is no alternative: a row of fewer than K others ends so
         float lp = NAN;
         if (k < c) {
@@ -75,23 +78,26 @@ __device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const c
     }
 }
 
-// Shared memory: the ring, and with top_k the candidates and the groups' maxima.
+// Shared memory: the ring, and with top_k each side warp's candidates and the groups'
+// maxima of each place of the queue.
 constexpr int kTileBytes = kTileVecs * 16;
-constexpr int kPlaces = 2;  // of the queue: a row in the stream, one with the side warps
+constexpr int kPlaces = 4;  // of the queue: a row in the stream, three with the side warps
+constexpr int kSideWarps = 3;
+constexpr int kScanThreads = kMainThreads + 32 + kSideWarps * 32;
 constexpr int scan_stages(int gm) { return gm ? 4 : 6; }
 constexpr size_t scan_smem(int gm) {
-    return (size_t)scan_stages(gm) * kTileBytes + (gm ? sizeof(TopSmem) + kPlaces * kTopHeads * 2 : 0);
+    return (size_t)scan_stages(gm) * kTileBytes + (gm ? kSideWarps * sizeof(TopSmem) + kPlaces * kTopHeads * 2 : 0);
 }
 
 template <typename T, int GM, bool ENT>  // GM: 0 without top_k, else as main_stats
-__global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_constant__ ScanArgs p) {
+__global__ void __launch_bounds__(kScanThreads, 2) ce_scan_kernel(const __grid_constant__ ScanArgs p) {
     using VT = Vec<T>;
     constexpr int ES = sizeof(T), STAGES = scan_stages(GM);
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ RowBars bars;
     unsigned char* ring = sm;
-    TopSmem& top = *reinterpret_cast<TopSmem*>(sm + (size_t)STAGES * kTileBytes);
-    uint16_t* heads = reinterpret_cast<uint16_t*>(sm + (size_t)STAGES * kTileBytes + sizeof(TopSmem));
+    uint16_t* heads = reinterpret_cast<uint16_t*>(sm + (size_t)STAGES * kTileBytes);  // [kPlaces][kTopHeads]
+    TopSmem* tops = reinterpret_cast<TopSmem*>(heads + kPlaces * kTopHeads);           // [kSideWarps]
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) row_bars_init(bars);
     __syncthreads();
@@ -120,8 +126,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
         auto row_of = [&](int64_t item) { return p.segs == 1 ? item : item / p.segs; };
         const bool one = p.tokens.n == 1;
         int64_t y = one && blockIdx.x < items ? p.tokens.at(row_of(blockIdx.x), 0) : 0;  // loaded an item ahead
-        for (int64_t item = blockIdx.x; ok; item += gridDim.x, q.next(kPlaces)) {
+        int ends = kSideWarps;  // an end mark for each side warp
+        for (int64_t item = blockIdx.x; ok && ends > 0; item += gridDim.x, q.next(kPlaces)) {
             const bool more = item < items;
+            if (!more) --ends;
             const int64_t r = more ? row_of(item) : -1;
             bool skip = one && y == p.tokens.ignore_idx;
             if (one && item + gridDim.x < items) y = p.tokens.at(row_of(item + gridDim.x), 0);
@@ -164,101 +172,89 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
                 }
                 if (!ok) ring_drain(bars, issued, STAGES);
             }
-            ok = __shfl_sync(kFull, (int)(ok && more), 0);
+            ok = __shfl_sync(kFull, (int)ok, 0);
         }
         return;
     }
 
-    const int tid = threadIdx.x - kMainThreads - 32;
-    Turn q;
-    for (;; q.next(kPlaces)) {
-        if (side_any(!row_wait(bars, &bars.ready[q.s], q.ph))) break;
-        const RowItem& it = bars.item[q.s];
+    // a side warp takes every kSideWarps-th item
+    const int side = (threadIdx.x - kMainThreads - 32) >> 5;
+    TopSmem& top = tops[side];
+    for (uint32_t turn = side;; turn += kSideWarps) {
+        const int q = (int)(turn % kPlaces);
+        const uint32_t ph = (turn / kPlaces) & 1u;
+        if (!__all_sync(kFull, row_wait(bars, &bars.ready[q], ph))) break;
+        const RowItem& it = bars.item[q];
         const int64_t r = it.row;
         if (r < 0) break;
         if (it.skip) {
-            if (!p.part) write_skipped(p, r, tid);
+            if (!p.part) write_skipped(p, r);
         } else {
             Given<T> given;
-            if (!p.part) given.load(p, r, it.x, tid);
+            if (!p.part) given.load(p, r, it.x, lane);
             const int64_t ce = edge_column(it);
             const float xe = ce >= 0 ? VT::load1(it.x + ce * ES) : -INFINITY;
-            if (side_any(!row_wait(bars, &bars.done[q.s], q.ph))) break;
-            const Stat st = row_stats<ENT>(bars.part[q.s], ce >= 0, xe, p.L);
+            if (!__all_sync(kFull, row_wait(bars, &bars.done[q], ph))) break;
+            const Stat st = row_stats<ENT>(bars.part[q], ce >= 0, xe, p.L);
             int c = 0;
             if constexpr (GM != 0) {
                 constexpr int unit = GM == 1 ? 32 : 8;
                 const int groups = (int)((it.nv + kTileVecs - 1) / kTileVecs) * (kTileVecs / unit);
                 const int64_t col0 = it.h1 + it.v0 * VT::kElems;
-                c = top_select<T>(top, heads + q.s * kTopHeads, groups, unit,
-                                  reinterpret_cast<const uint4*>(it.x + col0 * ES), it.nv, (uint32_t)col0, p.top_k,
-                                  ce >= 0 && tid < 32, ce < it.head, xe, (uint32_t)ce, tid);
+                c = top_select<T, unit>(top, heads + q * kTopHeads, groups,
+                                        reinterpret_cast<const uint4*>(it.x + col0 * ES), it.nv, (uint32_t)col0,
+                                        p.top_k, ce >= 0, ce < it.head, xe, (uint32_t)ce);
             }
             if (p.part) {
-                if (tid == 0) p.part[it.item] = make_float4(st.m, st.d, st.s, __int_as_float(c));
-                for (int k = tid; k < c; k += kSideThreads) p.cand[it.item * p.top_k + k] = top.buf[k];
+                if (lane == 0) p.part[it.item] = make_float4(st.m, st.d, st.s, __int_as_float(c));
+                for (int k = lane; k < c; k += 32) p.cand[it.item * p.top_k + k] = top.buf[k];
             } else {
-                finish_row<T>(p, r, it.x, st, top.buf, c, given, tid);
+                finish_row<T>(p, r, it.x, st, top.buf, c, given);
             }
         }
-        side_sync();
-        if (tid == 0) mbar_arrive(&bars.free_[q.s]);
+        warp_arrive(&bars.free_[q]);
     }
-    if (tid == 0 && bars.gone) atomicOr(p.err, CE_DEVERR_TIMEOUT);
+    if (lane == 0 && bars.gone) atomicOr(p.err, CE_DEVERR_TIMEOUT);
 }
 
-// A row's segments put together.
+// A row's segments put together by a warp.
+constexpr int kJoinWarps = 4;
 template <typename T>
-__global__ void __launch_bounds__(kSideThreads) ce_join_kernel(const __grid_constant__ ScanArgs p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(const __grid_constant__ ScanArgs p) {
     extern __shared__ __align__(128) unsigned char sm[];
-    __shared__ float4 red[kSideThreads / 32];
-    TopSmem& top = *reinterpret_cast<TopSmem*>(sm);
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t r = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    TopSmem& top = reinterpret_cast<TopSmem*>(sm)[warp];
+    const int64_t r = (int64_t)blockIdx.x * kJoinWarps + warp;
+    if (r >= p.N) return;
     const char* x = p.x + p.row.at(r) * sizeof(T);
     Given<T> given;
-    given.load(p, r, x, tid);
+    given.load(p, r, x, lane);
     bool keep = p.tokens.n == 0;
-    for (int k = tid; k < p.tokens.n; k += kSideThreads)
-        keep |= (k == tid ? given.y : p.tokens.at(r, k)) != p.tokens.ignore_idx;
-    if (!side_any(keep)) {
-        write_skipped(p, r, tid);
+    for (int k = lane; k < p.tokens.n; k += 32)
+        keep |= (k == lane ? given.y : p.tokens.at(r, k)) != p.tokens.ignore_idx;
+    if (!__any_sync(kFull, keep)) {
+        write_skipped(p, r);
         return;
     }
     Stat st = stat_identity();
-    for (int k = tid; k < p.segs; k += kSideThreads) {
+    for (int k = lane; k < p.segs; k += 32) {
         const float4 v = p.part[r * p.segs + k];
         st = stat_combine(st, Stat{v.x, v.y, v.z}, p.L);
     }
     st = stat_warp<true>(st, p.L);
-    if (lane == 0) red[tid >> 5] = make_float4(st.m, st.d, st.s, 0.f);
-    if (tid == 0) top.count = 0;
-    side_sync();
-    st = stat_identity();
-    if (lane < kSideThreads / 32) st = Stat{red[lane].x, red[lane].y, red[lane].z};
-    st = stat_warp<true>(st, p.L);
-    int c = 0;
+    TopGate g(p.top_k, -INFINITY);
     if (p.top_k > 0) {
-        TopGate g;
-        g.K = p.top_k;
-        g.all = true;
-        // a warp a segment, as many at a time as the buffer has room for
-        const int together = max(1, min(p.segs, (kTopCap - p.top_k) / p.top_k));
-        for (int g0 = 0; g0 < p.segs; g0 += together) {
-            const int n = min(together, p.segs - g0);
-            top_room(top, g, n * p.top_k, tid);
-            for (int k = tid >> 5; k < n; k += kSideThreads / 32) {
-                const int64_t item = r * p.segs + g0 + k;
-                const int have = __float_as_int(p.part[item].w);
-                int base = 0;
-                if (lane == 0) base = atomicAdd(&top.count, have);
-                base = __shfl_sync(kFull, base, 0);
-                for (int u = lane; u < have; u += 32) top.buf[base + u] = p.cand[item * p.top_k + u];
-            }
+        for (int k = 0; k < p.segs; ++k) {
+            const int64_t item = r * p.segs + k;
+            const int have = __float_as_int(p.part[item].w);
+            top_room(top, g, have);
+            for (int u = lane; u < have; u += 32) top.buf[g.held + u] = p.cand[item * p.top_k + u];
+            g.held += have;
         }
-        c = top_finish(top, p.top_k, tid);
+        top_sort(top, g.held);
+        if (g.held > p.top_k) g.held = p.top_k;
     }
-    finish_row<T>(p, r, x, st, top.buf, c, given, tid);
+    finish_row<T>(p, r, x, st, top.buf, g.held, given);
 }
 
 template <typename T, int GM, bool ENT>
@@ -269,7 +265,7 @@ cudaError_t launch_scan_t(const ScanArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     int64_t grid = a.N * a.segs;
     if (grid > kScanSlots) grid = kScanSlots;
-    k<<<(unsigned)grid, kRowThreads, smem, s>>>(a);
+    k<<<(unsigned)grid, kScanThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -282,11 +278,11 @@ cudaError_t launch_scan_type(const ScanArgs& a, bool entropy, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_join(const ScanArgs& a, cudaStream_t s) {
-    const size_t smem = sizeof(TopSmem);
+    const size_t smem = kJoinWarps * sizeof(TopSmem);
     auto* k = ce_join_kernel<T>;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)a.N, kSideThreads, smem, s>>>(a);
+    k<<<(unsigned)((a.N + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, smem, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -17,9 +17,9 @@
 //   eight main warps  take the tiles out, sum the statistics and, where a gradient
 //                     is written, take the row's tiles a second time; a row costs
 //                     them a warp reduction and no barrier of their own;
-//   four side warps   do what a row has beside its stream, while the main warps are
-//                     on the next: the elements around the body, the given or listed
-//                     tokens, the largest logits, the outputs.
+//   the side warps    do what a row has beside its stream, while the main warps are
+//                     on the next ones: the elements around the body, the given or
+//                     listed tokens, the largest logits, the outputs.
 // (With the eight warps doing all of it between barriers, a row of 32000 columns cost
 // them as much again as its tiles did: 16384 rows 210 us.)
 //
@@ -29,9 +29,11 @@
 // K-th largest of them, is a value that K logits at least are not below, so only the
 // groups that reach it are read again, from L2, and of random logits 1.1 K to 1.4 K are
 // candidates.  Short rows have too few groups: their vectors' maxima are taken first.
-// Groups are read in the order of their columns, in batches that the buffer has room
-// for after it was sorted and cut to K, and once K candidates are held only what is
-// above T counts: equal or ordered logits cost time, not exactness.
+// Groups are read in the order of their columns, and where the buffer of candidates has
+// no room it is sorted and cut to K; once K are held only what is above T counts:
+// equal or ordered logits cost time, not exactness.  A row's selection is one warp's
+// work, without barriers, and three rows' go on at a time (four warps at one row's, with a
+// barrier for each step: 17 us a row of 128000 columns, K = 64, beside the stream).
 #pragma once
 
 #include "ce_device.cuh"
@@ -131,30 +133,34 @@ __device__ __forceinline__ float4 stat_far(const uint4* src, int n, float m, flo
     return make_float4(d2.x, d2.y, s2.x, s2.y);
 }
 
+__device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ __nv_bfloat162 max_of(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmax2(a, b); }
+__device__ __forceinline__ __half2 max_of(__half2 a, __half2 b) { return __hmax2(a, b); }
+template <typename M>
+__device__ __forceinline__ M max_from(M own, int lanes) {  // the maximum of the lane that is `lanes` away
+    static_assert(sizeof(M) == 4, "a register");
+    const uint32_t o = __shfl_xor_sync(kFull, *reinterpret_cast<const uint32_t*>(&own), lanes);
+    return *reinterpret_cast<const M*>(&o);
+}
+
 // A thread's vectors of a tile: src[0], src[kMainThreads], ..., n of them (FULL: NV).
-// ENT: s as well.  GM: each vector's maximum into gm (-inf where there is none).
-template <typename T, int NV, bool FULL, bool ENT, bool GM>
-__device__ __forceinline__ void stat_tile(Stat& a, const uint4* src, int n, float L, float (&gm)[NV]) {
+// ENT: s as well.  gm: each vector's maximum, packed (-inf where there is none).
+template <typename T, int NV, bool FULL, bool ENT>
+__device__ __forceinline__ void stat_tile(Stat& a, const uint4* src, int n, float L,
+                                          typename Vec<T>::Max (&gm)[NV]) {
     using VT = Vec<T>;
     uint4 raw[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (FULL || i < n) raw[i] = src[i * kMainThreads];
-    float top;
-    if (GM) {
-        top = -INFINITY;
+    typename VT::Max tm = VT::max_init();
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            gm[i] = FULL || i < n ? VT::vmax(raw[i]) : -INFINITY;
-            top = fmaxf(top, gm[i]);
-        }
-    } else {
-        typename VT::Max tm = VT::max_init();
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (FULL || i < n) tm = VT::max_acc(tm, raw[i]);
-        top = VT::max_done(tm);
+    for (int i = 0; i < NV; ++i) {
+        gm[i] = VT::max_init();
+        if (FULL || i < n) gm[i] = VT::max_acc(gm[i], raw[i]);
+        tm = max_of(tm, gm[i]);
     }
+    const float top = VT::max_done(tm);
     if (top > a.m) {
         const float y = stat_shift(a.m, top, L), f = ex2_approx(y);
         if (ENT) a.s = f * fmaf(a.d, y, a.s);
@@ -236,61 +242,68 @@ __device__ __forceinline__ uint32_t value_head(float x) {
     return x == x ? (uint32_t)(top_key(x, 0) >> 48) : kLowestHead;
 }
 
-struct TopSmem {
+// The candidates of one warp's selection.
+struct alignas(16) TopSmem {
     uint64_t buf[kTopCap];
-    uint16_t vheads[kTopHeads];  // of a short row's vectors
-    uint16_t list[kTopHeads];    // groups to be read again
-    int count, listed;
-    uint32_t kth;
+    int bins[128];
 };
 
-// The largest head that at least K of the n heads reach; 0: fewer than K are not 0.  One warp.
-__device__ __forceinline__ uint32_t kth_head(const uint16_t* heads, int n, int K) {
+// 32 NK keys in falling order by a warp: key i of lane l is the one at 32 i + l.
+template <int NK>
+__device__ __forceinline__ void sort_keys(uint64_t (&k)[NK]) {
     const int lane = threadIdx.x & 31;
-    uint32_t kth = 0;
-    for (int b = 15; b >= 0; --b) {
-        const uint32_t cand = kth | (1u << b);
-        int own = 0;
-        for (int k = lane * 8; k < n; k += 256) {
-            const uint4 u = *reinterpret_cast<const uint4*>(heads + k);  // past n: zeros
-            own += ((u.x & 0xffffu) >= cand) + ((u.x >> 16) >= cand) + ((u.y & 0xffffu) >= cand) +
-                   ((u.y >> 16) >= cand) + ((u.z & 0xffffu) >= cand) + ((u.z >> 16) >= cand) +
-                   ((u.w & 0xffffu) >= cand) + ((u.w >> 16) >= cand);
-        }
-        const int c = (int)__reduce_add_sync(kFull, (unsigned)own);
-        if (c >= K) kth = cand;
-        if (c == K) break;
-    }
-    return kth;
-}
-
-// The first c keys of buf in falling order.  All side threads, between barriers.
-__device__ __forceinline__ void top_sort(TopSmem& s, int c, int tid) {
-    if (c <= 2 * kSideThreads) {
-        // few: a key's rank is the number of larger ones
-        const uint64_t k0 = tid < c ? s.buf[tid] : 0, k1 = tid + kSideThreads < c ? s.buf[tid + kSideThreads] : 0;
-        int r0 = 0, r1 = 0;
-        if ((tid & ~31) < c) {
-#pragma unroll 4
-            for (int k = 0; k < c; ++k) {
-                const uint64_t o = s.buf[k];
-                r0 += o > k0;
-                r1 += o > k1;
+#pragma unroll
+    for (int size = 2; size <= 32 * NK; size *= 2) {
+#pragma unroll
+        for (int step = size / 2; step > 0; step /= 2) {
+            if (step >= 32) {
+#pragma unroll
+                for (int i = 0; i < NK; ++i) {
+                    const int j = i ^ (step / 32);
+                    if (j < i) continue;
+                    const bool down = ((32 * i) & size) == 0;
+                    const uint64_t hi = k[i] > k[j] ? k[i] : k[j], lo = k[i] > k[j] ? k[j] : k[i];
+                    k[i] = down ? hi : lo;
+                    k[j] = down ? lo : hi;
+                }
+            } else {
+                const bool low = (lane & step) == 0;
+#pragma unroll
+                for (int i = 0; i < NK; ++i) {
+                    const uint64_t o = __shfl_xor_sync(kFull, k[i], step);
+                    const bool down = ((32 * i + lane) & size) == 0;
+                    k[i] = (k[i] > o) == (down == low) ? k[i] : o;
+                }
             }
         }
-        side_sync();
-        if (tid < c) s.buf[r0] = k0;
-        if (tid + kSideThreads < c) s.buf[r1] = k1;
-        side_sync();
-        return;
     }
-    int n = 4 * kSideThreads;
+}
+template <int NK>
+__device__ __forceinline__ void sort_few(TopSmem& s, int c) {
+    const int lane = threadIdx.x & 31;
+    uint64_t k[NK];
+#pragma unroll
+    for (int i = 0; i < NK; ++i) k[i] = 32 * i + lane < c ? s.buf[32 * i + lane] : 0;
+    sort_keys<NK>(k);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) s.buf[32 * i + lane] = k[i];
+    __syncwarp();
+}
+
+// The first c keys of buf in falling order.  One warp.
+__device__ __forceinline__ void top_sort(TopSmem& s, int c) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    if (c <= 1) return;
+    if (c <= 32) return sort_few<1>(s, c);
+    if (c <= 128) return sort_few<4>(s, c);
+    int n = 256;
     while (n < c) n *= 2;
-    for (int k = c + tid; k < n; k += kSideThreads) s.buf[k] = 0;
-    side_sync();
+    for (int k = c + lane; k < n; k += 32) s.buf[k] = 0;
+    __syncwarp();
     for (int size = 2; size <= n; size *= 2) {
         for (int step = size / 2; step > 0; step /= 2) {
-            for (int p = tid; p < n / 2; p += kSideThreads) {
+            for (int p = lane; p < n / 2; p += 32) {
                 const int lo = p & (step - 1), i = 2 * (p - lo) + lo, j = i + step;
                 const uint64_t a = s.buf[i], b = s.buf[j];
                 if ((a < b) == ((i & size) == 0)) {
@@ -298,141 +311,239 @@ __device__ __forceinline__ void top_sort(TopSmem& s, int c, int tid) {
                     s.buf[j] = a;
                 }
             }
-            side_sync();
+            __syncwarp();
         }
     }
 }
 
-// What a selection lets in, the same in every side thread.
+// What a selection lets in, the same in every lane.
 struct TopGate {
     int K;
-    float T;
-    bool all;      // no threshold: every number counts
+    int held;      // candidates
+    float T;       // under it no logit can be among the K largest
     bool strict;   // K candidates not below T are held, of columns before: only what is above T counts
-    __device__ __forceinline__ bool takes(float x) const { return all ? x == x : (strict ? x > T : x >= T); }
+    float floor;   // what is let in is not below this: T, or the next value above it
+
+    __device__ __forceinline__ TopGate(int K, float T) : K(K), held(0), T(T), strict(false), floor(T) {}
 };
 
-// How many candidates are held; sorted and cut to K where there is no room for `more`.
-__device__ __forceinline__ int top_room(TopSmem& s, TopGate& g, int more, int tid) {
-    side_sync();
-    int c = s.count;
-    if (c + more > kTopCap) {
-        top_sort(s, c, tid);
-        if (c >= g.K) {
-            c = g.K;
-            g.T = key_value(s.buf[c - 1]);
-            g.all = false;
+// Room for `more` candidates: where there is none, what is held is sorted and cut to K.
+__device__ __forceinline__ void top_room(TopSmem& s, TopGate& g, int more) {
+    if (g.held + more > kTopCap) {
+        top_sort(s, g.held);
+        if (g.held >= g.K) {
+            g.held = g.K;
+            g.T = key_value(s.buf[g.K - 1]);
+            g.strict = false;
         }
-        side_sync();
-        if (tid == 0) s.count = c;
+        __syncwarp();
     }
-    g.strict = !g.all && c >= g.K;
-    side_sync();
-    return c;
-}
-__device__ __forceinline__ void top_push(TopSmem& s, bool ok, float x, uint32_t column) {
-    const unsigned m = __ballot_sync(kFull, ok);
-    if (m == 0u) return;
-    const int lane = threadIdx.x & 31;
-    int base = 0;
-    if (lane == 0) base = atomicAdd(&s.count, __popc(m));
-    base = __shfl_sync(kFull, base, 0);
-    if (ok) s.buf[base + __popc(m & ((1u << lane) - 1u))] = top_key(x, column);
+    if (!g.strict && g.held >= g.K) {
+        g.strict = true;
+        const int b = __float_as_int(g.T + 0.f);  // above +inf: a NaN, that nothing reaches
+        g.floor = __int_as_float(b >= 0 ? b + 1 : b - 1);
+    }
 }
 
-// The candidates' buffer sorted and cut to K; how many there are.
-__device__ __forceinline__ int top_finish(TopSmem& s, int K, int tid) {
-    side_sync();
-    const int c = s.count;
-    top_sort(s, c, tid);
-    return c < K ? c : K;
+// The k-th logit of a vector.
+__device__ __forceinline__ uint32_t pick_word(const uint4& r, int k) {
+    return k & 2 ? (k & 1 ? r.w : r.z) : (k & 1 ? r.y : r.x);
+}
+template <typename T>
+__device__ __forceinline__ float pick(const uint4& r, int k) {
+    if constexpr (sizeof(T) == 4) {
+        return __uint_as_float(pick_word(r, k));
+    } else {
+        const float2 v = Vec<T>::unpack_pair(pick_word(r, k >> 1));
+        return k & 1 ? v.y : v.x;
+    }
+}
+// The logits of each lane's vector (have: it has one) that the gate lets in; col: the
+// column of its first.
+template <typename T>
+__device__ __forceinline__ void top_push(TopSmem& s, TopGate& g, bool have, const uint4& raw, uint32_t col) {
+    using VT = Vec<T>;
+    constexpr int VEC = VT::kElems;
+    const int lane = threadIdx.x & 31;
+    unsigned ok = 0;
+    if (__any_sync(kFull, have && VT::vmax(raw) >= g.floor)) {
+        float x[VEC];
+        VT::unpack(raw, x);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) ok |= x[k] >= g.floor ? 1u << k : 0u;
+        if (!have) ok = 0;
+    }
+    for (;;) {
+        const unsigned m = __ballot_sync(kFull, ok != 0u);
+        if (m == 0u) return;
+        if (ok) {
+            const int k = __ffs(ok) - 1;
+            s.buf[g.held + __popc(m & ((1u << lane) - 1u))] = top_key(pick<T>(raw, k), col + (uint32_t)k);
+            ok &= ok - 1u;
+        }
+        g.held += __popc(m);
+    }
+}
+__device__ __forceinline__ void top_push_one(TopSmem& s, TopGate& g, bool ok, float x, uint32_t col) {
+    const unsigned m = __ballot_sync(kFull, ok && x >= g.floor);
+    const int lane = threadIdx.x & 31;
+    if ((m >> lane) & 1u) s.buf[g.held + __popc(m & ((1u << lane) - 1u))] = top_key(x, col);
+    g.held += __popc(m);
+}
+
+// A head that at least K of the n heads reach, few more where the heads are fine enough
+// (0: fewer than K are not 0).  Heads are counted by their distance below the largest in
+// 128 bins, which one sum over them turns into the answer; where K lie further down, in
+// wider bins.  Of many heads for each of the K only the maximum of eight, or two, counts.
+__device__ __forceinline__ uint32_t kth_head(TopSmem& s, const uint16_t* heads, int n, int K) {
+    const int lane = threadIdx.x & 31;
+    auto of_eight = [&](int k) {  // maxima in both halves
+        const uint4 u = *reinterpret_cast<const uint4*>(heads + k);
+        return __vmaxu2(__vmaxu2(u.x, u.y), __vmaxu2(u.z, u.w));
+    };
+    uint32_t m = 0;
+    for (int k = lane * 8; k < n; k += 256) m = __vmaxu2(m, of_eight(k));
+    m = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
+    if (K == 1 || m == 0) return m;
+    for (int shift = 1; shift <= 9; shift += 4) {
+        const uint32_t span = 128u << shift;
+        *reinterpret_cast<int4*>(s.bins + 4 * lane) = make_int4(0, 0, 0, 0);
+        __syncwarp();
+        auto bin = [&](uint32_t h) {
+            const uint32_t d = m - h;
+            if (d < span && h) atomicAdd(&s.bins[d >> shift], 1);
+        };
+        if (n >= 24 * K) {
+            for (int k = lane * 8; k < n; k += 256) {
+                const uint32_t v = of_eight(k);
+                bin(max(v & 0xffffu, v >> 16));
+            }
+        } else {
+            const bool pairs = n >= 6 * K;
+            for (int k = lane * 2; k < n; k += 64) {
+                const uint32_t u = *reinterpret_cast<const uint32_t*>(heads + k);
+                const uint32_t a = u & 0xffffu, c = u >> 16;
+                bin(max(a, c));
+                if (!pairs) bin(min(a, c));
+            }
+        }
+        __syncwarp();
+        const int4 c = *reinterpret_cast<const int4*>(s.bins + 4 * lane);
+        const int own = c.x + c.y + c.z + c.w;
+        int upto = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += u;
+        }
+        __syncwarp();
+        const unsigned there = __ballot_sync(kFull, upto >= K);
+        if (there) {
+            const int l = __ffs(there) - 1, before = upto - own;  // the bin in which the K-th lies
+            int b = before + c.x >= K ? 0 : before + c.x + c.y >= K ? 1 : before + c.x + c.y + c.z >= K ? 2 : 3;
+            b = __shfl_sync(kFull, 4 * lane + b, l);
+            const uint32_t d = (((uint32_t)b + 1u) << shift) - 1u;  // the bin's far end
+            return m > d ? m - d : 1u;
+        }
+    }
+    return 0;
+}
+
+// The heads that reach kth (1 at least), listed in place by their numbers, in order: the
+// list never reaches a head that has not been looked at.  How many there are.
+__device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t kth) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t least = kth ? kth : 1u;
+    int listed = 0;
+    for (int k0 = 0; k0 < n; k0 += 256) {
+        const int k = k0 + lane * 8;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (k < n) u = *reinterpret_cast<const uint4*>(heads + k);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        unsigned ok = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ok |= (w[i] & 0xffffu) >= least ? 1u << (2 * i) : 0u;
+            ok |= (w[i] >> 16) >= least ? 2u << (2 * i) : 0u;
+        }
+        int at = __popc(ok);
+        const int own = at;
+        if (!__any_sync(kFull, ok != 0u)) continue;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFull, at, o);
+            if (lane >= o) at += v;
+        }
+        const int all = __shfl_sync(kFull, at, 31);
+        at += listed - own;
+        for (; ok; ok &= ok - 1u) heads[at++] = (uint16_t)(k + __ffs(ok) - 1);
+        listed += all;
+        __syncwarp();
+    }
+    __syncwarp();
+    return listed;
+}
+
+// The listed groups' vectors, 32 at a time and the next ones on their way.
+template <typename T, int UNIT>
+__device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t* list, int listed, const uint4* body,
+                                         int64_t nv, uint32_t col0) {
+    constexpr int VEC = Vec<T>::kElems, AHEAD = 4, PER = 32 / UNIT;
+    const int lane = threadIdx.x & 31;
+    const int last = nv < 0x7fffffff ? (int)nv : 0x7fffffff;
+    uint4 raw[AHEAD];
+    int v[AHEAD];  // the vector, or -1
+    auto fetch = [&](int b, uint4& to, int& vec) {
+        const int e = b + lane / UNIT;
+        vec = -1;
+        if (e < listed) {
+            const int at = (int)list[e] * UNIT + lane % UNIT;
+            if (at < last) {
+                vec = at;
+                to = __ldg(body + at);
+            }
+        }
+    };
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) fetch(a * PER, raw[a], v[a]);
+    for (int b = 0; b < listed; b += AHEAD * PER) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            if (b + a * PER >= listed) break;
+            top_room(s, g, 32 * VEC);
+            top_push<T>(s, g, v[a] >= 0, raw[a], col0 + (uint32_t)(v[a] * VEC));
+            fetch(b + (AHEAD + a) * PER, raw[a], v[a]);
+        }
+    }
 }
 
 // The K largest of a row's (segment's) logits into the front of s.buf, in falling order;
-// returns how many there are.  body: its nv vectors in global memory, their first logit of
-// column col0; heads: the groups' maxima, G of them (zeros up to a multiple of 256), `unit`
-// vectors each.  xe, ce: the thread's element around the body (before: it lies before the
-// body), where has_edge.  All side threads.
-template <typename T>
-__device__ __forceinline__ int top_select(TopSmem& s, const uint16_t* heads, int G, int unit, const uint4* body,
-                                          int64_t nv, uint32_t col0, int K, bool has_edge, bool before, float xe,
-                                          uint32_t ce, int tid) {
+// returns how many there are.  One warp.  body: its nv vectors in global memory, their
+// first logit of column col0; heads: the groups' maxima, G of them (zeros up to a multiple
+// of eight), UNIT vectors each, overwritten.  xe, ce: the lane's element around the body
+// (before: it lies before the body), where has_edge.
+template <typename T, int UNIT>
+__device__ __forceinline__ int top_select(TopSmem& s, uint16_t* heads, int G, const uint4* body, int64_t nv,
+                                          uint32_t col0, int K, bool has_edge, bool before, float xe, uint32_t ce) {
     using VT = Vec<T>;
-    constexpr int VEC = VT::kElems;
-    const int lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) s.count = 0;
-    if (G < 2 * K && nv <= kTopHeads) {
-        for (int v = tid; v < kTopHeads; v += kSideThreads) {
-            uint32_t h = 0;
-            if (v < nv) h = value_head(VT::vmax(__ldg(body + v)));
-            s.vheads[v] = (uint16_t)h;
-            if (v >= ((nv + 255) & ~255)) break;
-        }
-        heads = s.vheads;
+    const int lane = threadIdx.x & 31;
+    const bool brief = G < 2 * K && nv <= kTopHeads;  // too few groups: each vector is one
+    if (brief) {
+        for (int v = lane; v < (((int)nv + 255) & ~255); v += 32)
+            heads[v] = (uint16_t)(v < nv ? value_head(VT::vmax(__ldg(body + v))) : 0u);
         G = (int)nv;
-        unit = 1;
+        __syncwarp();
     }
-    side_sync();
-    if (warp == 0) {
-        const uint32_t kth = kth_head(heads, G, K);
-        int n = 0;
-        for (int k0 = 0; k0 < G; k0 += 32) {
-            const bool in = k0 + lane < G && heads[k0 + lane] >= (kth ? kth : 1u);
-            const unsigned m = __ballot_sync(kFull, in);
-            if (in) s.list[n + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(k0 + lane);
-            n += __popc(m);
-        }
-        if (lane == 0) {
-            s.kth = kth;
-            s.listed = n;
-        }
-    }
-    side_sync();
-    const uint32_t kth = s.kth;
-    TopGate g;
-    g.K = K;
-    g.all = kth == 0;
-    g.strict = false;
-    g.T = kth <= kLowestHead ? -INFINITY : key_value((uint64_t)kth << 48);
-    top_push(s, has_edge && before && g.takes(xe), xe, ce);
-    // a warp takes 32 vectors at a time, twice in a batch; the next batch's are on their way
-    constexpr int STEPS = 2, WARPS = kSideThreads / 32;
-    const int per = 32 / unit, batch = STEPS * WARPS * per, listed = s.listed;
-    uint4 next[STEPS];
-    int64_t vn[STEPS];
-    auto fetch = [&](int b) {
-#pragma unroll
-        for (int u = 0; u < STEPS; ++u) {
-            const int e = b + (u * WARPS + warp) * per + lane / unit;
-            vn[u] = e < listed ? (int64_t)s.list[e] * unit + lane % unit : nv;
-            if (vn[u] < nv) next[u] = __ldg(body + vn[u]);
-        }
-    };
-    fetch(0);
-    for (int b = 0; b < listed; b += batch) {
-        uint4 raw[STEPS];
-        int64_t v[STEPS];
-#pragma unroll
-        for (int u = 0; u < STEPS; ++u) {
-            raw[u] = next[u];
-            v[u] = vn[u];
-        }
-        fetch(b + batch);
-        top_room(s, g, STEPS * kSideThreads * VEC, tid);
-#pragma unroll
-        for (int u = 0; u < STEPS; ++u) {
-            const bool hit = v[u] < nv && (g.all || g.takes(VT::vmax(raw[u])));
-            if (!__any_sync(kFull, hit)) continue;
-            float x[VEC];
-            VT::unpack(raw[u], x);
-#pragma unroll
-            for (int k = 0; k < VEC; ++k)
-                top_push(s, hit && g.takes(x[k]), x[k], col0 + (uint32_t)(v[u] * VEC + k));
-        }
-    }
-    top_room(s, g, kSideThreads, tid);
-    top_push(s, has_edge && !before && g.takes(xe), xe, ce);
-    return top_finish(s, K, tid);
+    const uint32_t kth = kth_head(s, heads, G, K);
+    const int listed = list_heads(heads, G, kth);
+    TopGate g(K, kth <= kLowestHead ? -INFINITY : key_value((uint64_t)kth << 48));
+    top_push_one(s, g, has_edge && before, xe, ce);
+    if (brief) top_take<T, 1>(s, g, heads, listed, body, nv, col0);
+    else top_take<T, UNIT>(s, g, heads, listed, body, nv, col0);
+    top_room(s, g, 32);
+    top_push_one(s, g, has_edge && !before, xe, ce);
+    top_sort(s, g.held);
+    return g.held < K ? g.held : K;
 }
 
 // ----------------------------------------------------------------- the ring and the queue
@@ -444,7 +555,7 @@ __device__ __forceinline__ int top_select(TopSmem& s, const uint16_t* heads, int
 // gives up raises `gone`, which ends all others; the copying warp then issues no more and
 // leaves when what it has issued has landed (bounded too).
 constexpr int kRingMost = 6;
-constexpr int kQueue = 3;  // places at most
+constexpr int kQueue = 4;  // places at most
 struct RowItem {
     const char* x;      // the row
     char* out;          // its gradient, or NULL
@@ -530,46 +641,46 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 template <typename T, int NV, bool ENT, int GM>
 __device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, const unsigned char* ring, int q,
                                            int64_t nv, float L, uint16_t* heads) {
+    using VT = Vec<T>;
     constexpr int TILE = kMainThreads * NV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Stat st = stat_identity();
     for (; nv > 0; nv -= TILE) {
         const uint4* src = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16) + tid;
-        float gm[NV];
+        typename VT::Max gm[NV];
         if (!row_wait(b, &b.full[at.s], at.ph)) return false;
         int mine = NV;
         if (nv >= TILE) {
-            stat_tile<T, NV, true, ENT, GM != 0>(st, src, NV, L, gm);
+            stat_tile<T, NV, true, ENT>(st, src, NV, L, gm);
         } else {
             mine = max(0, min(NV, ((int)nv - tid + kMainThreads - 1) / kMainThreads));
-            stat_tile<T, NV, false, ENT, GM != 0>(st, src, mine, L, gm);
+            stat_tile<T, NV, false, ENT>(st, src, mine, L, gm);
         }
         warp_arrive(&b.empty[at.s]);
         at.next(stages);
-        if (GM == 1) {
+        if constexpr (GM == 1) {
             // lane i keeps group i's; 0 where the group has no vector
             float own = -INFINITY;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const float m = warp_max_redux(gm[i]);
+                const float m = warp_max_redux(VT::max_done(gm[i]));
                 if (lane == i) own = m;
             }
             if (lane < NV)
                 heads[lane * (kMainThreads / 32) + warp] =
                     (uint16_t)(lane * kMainThreads + warp * 32 < nv ? value_head(own) : 0u);
             heads += TILE / 32;
-        } else if (GM == 2) {
-            float own = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float m = gm[i];
-                m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-                m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
-                if ((lane & 7) == i) own = m;
-            }
-            const int i = lane & 7, first = i * kMainThreads + (tid & ~7);
-            if (i < NV) heads[first / 8] = (uint16_t)(first < nv ? value_head(own) : 0u);
+        } else if constexpr (GM == 2) {
+            // over eight lanes, of four vectors at once: each step sends what the other lane goes on
+            // with, so lane l ends with vector l % 4
+            static_assert(NV == 4, "two steps halve four vectors");
+            const bool odd = lane & 1, two = lane & 2;
+            typename VT::Max u = max_of(odd ? gm[1] : gm[0], max_from(odd ? gm[0] : gm[1], 1));
+            typename VT::Max w = max_of(odd ? gm[3] : gm[2], max_from(odd ? gm[2] : gm[3], 1));
+            u = max_of(two ? w : u, max_from(two ? u : w, 2));
+            u = max_of(u, max_from(u, 4));
+            const int first = (lane & 3) * kMainThreads + (tid & ~7);
+            if ((lane & 4) == 0) heads[first / 8] = (uint16_t)(first < nv ? value_head(VT::max_done(u)) : 0u);
             heads += TILE / 8;
         }
     }

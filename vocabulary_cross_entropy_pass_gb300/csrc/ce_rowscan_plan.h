@@ -9,12 +9,11 @@ namespace gbce {
 
 constexpr int kMainThreads = 256;                            // threads that read a tile
 constexpr int kSideThreads = 128;                            // threads beside them
-constexpr int kRowThreads = kMainThreads + 32 + kSideThreads;  // and the copying warp
 constexpr int kTileVecs = kMainThreads * 4;                  // 16-byte vectors of a tile: 16 KB
-constexpr int kTopCap = 4096;                                // candidates held at a time
+constexpr int kTopCap = 1024;                                // candidates held at a time
 constexpr int kTopHeads = 2048;                              // groups' maxima of a row or segment
 constexpr int kMaxTop = 256;                                 // likeliest tokens a call may ask for
-constexpr int kFewTop = 64;                                  // up to here groups of 32 vectors, else of 8
+constexpr int kFewTop = 8;                                   // up to here groups of 32 vectors, else of 8
 constexpr int kMaxListed = 1024;                             // given or teacher's tokens of a row
 constexpr int kMaxSegments = 1024;
 constexpr int64_t kSMs = 152;
