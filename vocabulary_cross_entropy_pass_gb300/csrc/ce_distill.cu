@@ -9,10 +9,10 @@
 //
 // Bound by HBM: a logit read, a gradient written.  ce_distill_kernel streams whole rows
 // (ce_rowscan.cuh): the statistics in a first pass, the gradient in a second, whose tiles
-// come from L2, which the first was asked to keep them in.  The side warps work on the
-// list of the row to come: the teacher's softmax, the student's logits of its tokens, and a
-// hash table that finds tokens listed twice; then on the loss of the row before and, once
-// its gradient is stored, on its listed columns again.
+// come from L2, which the first was asked to keep them in.  Each side warp takes every
+// third row: its list while the rows before are streamed (the teacher's softmax, the
+// student's logits of its tokens, a hash table that finds tokens listed twice), then
+// its loss and, once its gradient is stored, its listed columns again.
 #include <math.h>
 
 #include <type_traits>
@@ -48,42 +48,41 @@ struct DistillArgs {
     int stages, slots;
 };
 
-constexpr int kPlaces = 3;  // of the queue: a row in the stream, its list ready; the next; the one before
-constexpr int kRowThreads = kMainThreads + 32 + kSideThreads;
+constexpr int kPlaces = 6;  // of the queue: a row in the stream, two ahead, three behind
 
-// A row's list in shared memory: the present row's and the next one's.
-constexpr int kLists = 2;
+// An entry of a row's list, in shared memory.
 struct ListEntry {
     float q, lq;  // the teacher's probability and its log
     float x;      // the student's logit
     int col;      // -1: left out; below: token -2 - col, listed before (counts for the loss alone)
 };
+// What the main warps need of a row's list for its gradient.
 struct ListRow {
     float Q;          // the summed probability
-    float zm, logs;   // the teacher's maximum, log of its sum
     float em, ed;     // statistics of the student's logits around the body
-    int bad, again;   // a token out of range; a token listed twice
+    int bad;          // a token out of range
 };
 inline int list_slots(int K) {
     int n = 64;
     while (n < 2 * K) n *= 2;
     return n;
 }
+inline size_t list_bytes(int K, bool grad) {  // of the three side warps
+    return kSideWarps * ((size_t)K * sizeof(ListEntry) + (grad ? (size_t)list_slots(K) * 2 : 0));
+}
 
 template <typename T, int NV, bool GRAD>
-__global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kernel(const __grid_constant__ DistillArgs p) {
+__global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_distill_kernel(const __grid_constant__ DistillArgs p) {
     using VT = Vec<T>;
     constexpr int ES = sizeof(T), PP = VT::kElems / 2;
     constexpr int TILE = kMainThreads * NV;  // vectors
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ RowBars bars;
-    __shared__ ListRow lists[kLists];
-    __shared__ float red[4][kSideThreads / 32];
-    __shared__ double dred[kSideThreads / 32];
+    __shared__ ListRow lists[kPlaces];
+    __shared__ double dred[kSideWarps];
     __shared__ int last;
     unsigned char* ring = sm;
     const int lane = threadIdx.x & 31, K = p.tokens.n;
-    ListEntry* entries = reinterpret_cast<ListEntry*>(sm + (size_t)p.stages * TILE * 16);
     if (threadIdx.x == 0) row_bars_init(bars);
     __syncthreads();
 
@@ -105,7 +104,7 @@ __global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kerne
     if (threadIdx.x < kMainThreads) {
         const int tid = threadIdx.x;
         Turn at, q;
-        for (int par = 0;; q.next(kPlaces), par ^= 1) {
+        for (;; q.next(kPlaces)) {
             if (!row_wait(bars, &bars.ready[q.s], q.ph)) return;
             const RowItem& it = bars.item[q.s];
             const int64_t r = it.row, nv = it.nv;
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kerne
             if (!main_stats<T, NV, false, 0>(bars, at, p.stages, ring, q.s, nv, p.L, nullptr)) return;
             if constexpr (GRAD) {
                 if (!row_wait(bars, &bars.done[q.s], q.ph) || !row_wait(bars, &bars.prep[q.s], q.ph)) return;
-                const ListRow& l = lists[par];
+                const ListRow& l = lists[q.s];
                 Stat st = stat_identity();
                 if (lane < kMainThreads / 32) st = Stat{bars.part[q.s][lane].x, bars.part[q.s][lane].y, 0.f};
                 else if (lane == kMainThreads / 32) st = Stat{l.em, l.ed, 0.f};
@@ -186,8 +185,8 @@ __global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kerne
             Turn at, q;
             uint32_t issued = 0;
             bool ok = true, started = false;
-            // rows: the CTA's first two, then the next that no CTA has claimed; each is known two ahead and in
-            // the queue one ahead of its copies, so the side warps work on its list meanwhile
+            // rows: the CTA's first three, then the next that no CTA has claimed; each is in the queue two
+            // ahead of its copies, so the side warps work on its list meanwhile
             auto token = [&](int64_t r) { return r < p.N ? p.tokens.at(r, 0) : 0; };
             auto publish = [&](int64_t r, int64_t y) {
                 ok = ok && row_wait(bars, &bars.free_[q.s], q.ph ^ 1u);
@@ -209,18 +208,20 @@ __global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kerne
                 mbar_arrive(&bars.ready[q.s]);
                 q.next(kPlaces);
             };
-            int64_t r = blockIdx.x, r1 = r + gridDim.x, r2 = 0;
-            int64_t y = token(r), y1 = token(r1), y2 = 0;
+            int64_t r = blockIdx.x, r1 = r + gridDim.x, r2 = r1 + gridDim.x, r3 = 0;
+            int64_t y = token(r), y1 = token(r1), y2 = token(r2), y3 = 0;
             auto claim = [&]() {
-                if (r1 >= p.N) return;
+                r3 = p.N;
+                if (r2 >= p.N) return;
                 if (!started) griddep_wait();  // the kernel before zeroes the counter
                 started = true;
-                r2 = 2 * (int64_t)gridDim.x + atomicAdd(p.claim, 1u);
-                y2 = token(r2);
+                r3 = 3 * (int64_t)gridDim.x + atomicAdd(p.claim, 1u);
+                y3 = token(r3);
             };
             publish(r, y);
+            publish(r1, y1);
             while (ok && r < p.N) {
-                publish(r1, y1);
+                publish(r2, y2);
                 const bool skip = y == p.tokens.ignore_idx;
                 const char* x = p.x + p.row.at(r) * ES;
                 const Span16 sp = span16<ES>(x, 0, p.V);
@@ -239,182 +240,138 @@ __global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kerne
                 y = y1;
                 r1 = r2;
                 y1 = y2;
+                r2 = r3;
+                y2 = y3;
             }
+            publish(p.N, 0);  // an end mark for each side warp
             if (!ok) ring_drain(bars, issued, p.stages);
         }
         return;
     }
 
-    const int tid = threadIdx.x - kMainThreads - 32;
-    int* key = reinterpret_cast<int*>(entries + kLists * K);  // [slots] a token, or -1
-    int* first = key + p.slots;                               // [slots] its first entry
-    // the row whose loss is still to come
-    bool pending = false;
-    float xe = 0.f;
-    int64_t ce = -1;
-    Turn qf;
-    int par = 0;  // the list of the row at hand; the other one is the pending row's
-    auto finish = [&]() -> bool {
-        if (!pending) return true;
-        pending = false;
-        const RowItem& it = bars.item[qf.s];
-        ListRow& l = lists[par ^ 1];
-        const ListEntry* e = entries + (par ^ 1) * K;
+    // a side warp takes every kSideWarps-th row
+    const int tid = threadIdx.x - kMainThreads - 32, side = tid >> 5;
+    ListEntry* e = reinterpret_cast<ListEntry*>(sm + (size_t)p.stages * TILE * 16) + side * K;
+    uint16_t* slots = reinterpret_cast<uint16_t*>(sm + (size_t)p.stages * TILE * 16 +
+                                                  (size_t)kSideWarps * K * sizeof(ListEntry)) + side * p.slots;
+    for (uint32_t turn = side;; turn += kSideWarps) {
+        const int q = (int)(turn % kPlaces);
+        const uint32_t ph = (turn / kPlaces) & 1u;
+        if (!__all_sync(kFull, row_wait(bars, &bars.ready[q], ph))) break;
+        const RowItem& it = bars.item[q];
         const int64_t r = it.row;
-        if (side_any(!row_wait(bars, &bars.done[qf.s], qf.ph))) return false;
-        if (!it.skip) {
-            const Stat st = row_stats<false>(bars.part[qf.s], ce >= 0, xe, p.L);
-            const bool none = stat_none(st.m, st.d);
-            const float logd = none ? 0.f : stat_logd(st, p.L);
-            float loss = 0.f;
-            for (int k = tid; k < K; k += kSideThreads) {
-                if (e[k].q == 0.f) continue;
-                const float lp = none ? -INFINITY : (e[k].x - st.m) * p.scale - logd;
-                loss += e[k].q * (e[k].lq - lp);
-            }
-            loss = side_sum(loss, red[2], tid);
-            need_count();
-            if (tid == 0) {
-                if (l.bad) atomicOr(p.err, CE_DEVERR_TARGET_RANGE);
-                p.loss[r] = l.bad ? NAN : p.tau * p.tau * loss;
-                if (p.stats) p.stats[r] = make_float4(st.m, logd, l.zm, l.logs);
-            }
-            if constexpr (GRAD) {
-                const float gt = row_scale(r), a = gt * l.Q, shift = -logd * kLog2e, nm = -st.m;
-                const bool zero = l.bad || none;
-                auto grad = [&](float v) { return ex2_approx(fmaf(v + nm, p.L, shift)) * a; };
-                if (tid < 32 && ce >= 0) VT::store1(it.out + ce * ES, zero ? 0.f : grad(xe));
-                if (side_any(!row_wait(bars, &bars.stored[qf.s], qf.ph))) return false;
-                for (int k = tid; k < K && !zero; k += kSideThreads) {
-                    const int col = e[k].col;
-                    if (col < 0) continue;
-                    float c = e[k].q;
-                    if (l.again) {  // in list order
-                        c = 0.f;
-                        for (int j = 0; j < K; ++j)
-                            if (e[j].col == col || e[j].col == -2 - col) c += e[j].q;
-                    }
-                    VT::store1(it.out + (int64_t)col * ES, fmaf(-gt, c, grad(e[k].x)));
-                }
-            }
-        } else {
-            if (tid == 0) {
+        if (r < 0) break;
+        const int64_t ce = edge_column(it);
+        if (it.skip) {
+            if (lane == 0) {
                 p.loss[r] = 0.f;
                 if (p.stats) p.stats[r] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
             }
-            if constexpr (GRAD) {
-                if (tid < 32 && ce >= 0) VT::store1(it.out + ce * ES, 0.f);
-                if (side_any(!row_wait(bars, &bars.stored[qf.s], qf.ph))) return false;
-            }
+            if (GRAD && ce >= 0) VT::store1(it.out + ce * ES, 0.f);
+            warp_arrive(&bars.prep[q]);
+            warp_arrive(&bars.free_[q]);
+            continue;
         }
-        side_sync();
-        if (tid == 0) mbar_arrive(&bars.free_[qf.s]);
-        qf.next(kPlaces);
-        return true;
-    };
-    Turn q;
-    bool fine = true;
-    for (;; q.next(kPlaces)) {
-        if (side_any(!row_wait(bars, &bars.ready[q.s], q.ph))) {
-            fine = false;
-            break;
+        const float xe = ce >= 0 ? VT::load1(it.x + ce * ES) : -INFINITY;
+        bool bad = false;
+        float zm = -INFINITY;
+#pragma unroll 4
+        for (int k = lane; k < K; k += 32) {
+            const int64_t y = p.tokens.at(r, k);
+            const float z = teacher_at(p.teacher, p.teacher_dtype, p.trow.at(r) + k * p.tstep);
+            const bool there = y != p.tokens.ignore_idx, in = there && y >= 0 && y < p.V;
+            bad |= there && !in;
+            // without a gradient the row's logits are not replaced: they are fetched once it lies in L2
+            e[k] = ListEntry{0.f, in ? z : -INFINITY, GRAD && in ? VT::load1(it.x + y * ES) : 0.f, in ? (int)y : -1};
+            zm = fmaxf(zm, in ? z : -INFINITY);
         }
-        const RowItem& it = bars.item[q.s];
-        const int64_t r = it.row;
-        if (r < 0) break;
-        ListRow& l = lists[par];
-        ListEntry* e = entries + par * K;
-        const int64_t cnew = edge_column(it);
-        float xnew = -INFINITY;
-        if (cnew >= 0) xnew = VT::load1(it.x + cnew * ES);
-        if (!it.skip) {
-            bool bad = false;
-            float zm = -INFINITY;
-            for (int k = tid; k < K; k += kSideThreads) {
-                const int64_t y = p.tokens.at(r, k);
-                const float z = teacher_at(p.teacher, p.teacher_dtype, p.trow.at(r) + k * p.tstep);
-                ListEntry n{0.f, -INFINITY, 0.f, -1};
-                if (y != p.tokens.ignore_idx) {
-                    if (y < 0 || y >= p.V) {
-                        bad = true;
-                    } else {
-                        n.lq = z;
-                        n.x = VT::load1(it.x + y * ES);
-                        n.col = (int)y;
-                    }
-                }
-                e[k] = n;
-                zm = fmaxf(zm, n.lq);
-            }
-            zm = side_max(zm, red[0], tid);
-            float sum = 0.f;
-            for (int k = tid; k < K; k += kSideThreads)
-                if (e[k].lq != -INFINITY) sum += ex2_approx((e[k].lq - zm) * p.L);
-            sum = side_sum(sum, red[1], tid);
-            const bool nothing = zm == -INFINITY && sum == 0.f;  // no token has any probability
-            const float logs = nothing ? 0.f : logf(sum);
-            for (int k = tid; k < K; k += kSideThreads) {
-                if (e[k].lq == -INFINITY) continue;
-                const float lq = p.normalize ? (e[k].lq - zm) * p.scale - logs : e[k].lq * p.scale;
-                e[k].lq = lq;
-                e[k].q = ex2_approx(lq * kLog2e);
-            }
-            // tokens listed twice: the first entry of each writes for all
-            bool again = false;
-            if (GRAD) {
-                for (int k = tid; k < p.slots; k += kSideThreads) {
-                    key[k] = -1;
-                    first[k] = 0x7fffffff;
-                }
-                side_sync();
-                auto slot_of = [&](int col, bool insert) {
-                    uint32_t h = ((uint32_t)col * 2654435761u) >> 7;
-                    for (;; ++h) {
-                        h &= (uint32_t)p.slots - 1u;
-                        const int was = insert ? atomicCAS(&key[h], -1, col) : key[h];
-                        if (was == col || (insert && was == -1)) return (int)h;
-                    }
-                };
-                for (int k = tid; k < K; k += kSideThreads)
-                    if (e[k].col >= 0) atomicMin(&first[slot_of(e[k].col, true)], k);
-                side_sync();
-                for (int k = tid; k < K; k += kSideThreads)
-                    if (e[k].col >= 0 && first[slot_of(e[k].col, false)] != k) {
+        bad = __any_sync(kFull, bad);
+        zm = warp_max_redux(zm);
+        float sum = 0.f;
+        for (int k = lane; k < K; k += 32)
+            if (e[k].lq != -INFINITY) sum += ex2_approx((e[k].lq - zm) * p.L);
+        sum = warp_allsum(sum);
+        const bool nothing = zm == -INFINITY && sum == 0.f;  // no token has any probability
+        const float logs = nothing ? 0.f : logf(sum);
+        const float Q = nothing       ? 0.f
+                        : sum != sum  ? sum
+                        : p.normalize ? 1.f
+                                      : ex2_approx((zm * p.scale + logs) * kLog2e);
+        for (int k = lane; k < K; k += 32) {
+            if (e[k].lq == -INFINITY) continue;
+            const float lq = p.normalize ? (e[k].lq - zm) * p.scale - logs : e[k].lq * p.scale;
+            e[k].lq = lq;
+            e[k].q = ex2_approx(lq * kLog2e);
+        }
+        bool again = false;
+        if constexpr (GRAD) {
+            // of a token's entries one, the first to find a slot, writes for all
+            for (int k = lane; k < p.slots; k += 32) slots[k] = 0xffffu;
+            __syncwarp();
+            for (int k = lane; k < K; k += 32) {
+                const int col = e[k].col;
+                if (col < 0) continue;
+                for (uint32_t h = ((uint32_t)col * 2654435761u) >> 7;; ++h) {
+                    h &= (uint32_t)p.slots - 1u;
+                    const unsigned short was = atomicCAS(reinterpret_cast<unsigned short*>(&slots[h]),
+                                                         (unsigned short)0xffffu, (unsigned short)k);
+                    if (was == 0xffffu) break;
+                    if (e[was].col == col) {
                         again = true;
-                        e[k].col = -2 - e[k].col;
+                        e[k].col = -2 - col;
+                        break;
                     }
-            }
-            const bool any_bad = side_any(bad), any_again = side_any(again);
-            if (tid < 32) {
-                Stat st = stat_identity();
-                if (cnew >= 0) stat_add(st, xnew, p.L);
-                st = stat_warp<false>(st, p.L);
-                if (tid == 0) {
-                    l.Q = nothing       ? 0.f
-                          : sum != sum  ? sum
-                          : p.normalize ? 1.f
-                                        : ex2_approx((zm * p.scale + logs) * kLog2e);
-                    l.zm = zm;
-                    l.logs = logs;
-                    l.em = st.m;
-                    l.ed = st.d;
-                    l.bad = any_bad;
-                    l.again = any_again;
                 }
             }
+            again = __any_sync(kFull, again);
+            Stat es = stat_identity();
+            if (ce >= 0) stat_add(es, xe, p.L);
+            es = stat_warp<false>(es, p.L);
+            if (lane == 0) lists[q] = ListRow{Q, es.m, es.d, bad};
         }
-        side_sync();
-        if (tid == 0) mbar_arrive(&bars.prep[q.s]);
-        if (!(fine = finish())) break;
-        pending = true;
-        xe = xnew;
-        ce = cnew;
-        qf = q;
-        par ^= 1;
+        warp_arrive(&bars.prep[q]);
+
+        if (!__all_sync(kFull, row_wait(bars, &bars.done[q], ph))) break;
+        const Stat st = row_stats<false>(bars.part[q], ce >= 0, xe, p.L);
+        const bool none = stat_none(st.m, st.d);
+        const float logd = none ? 0.f : stat_logd(st, p.L);
+        float loss = 0.f;
+#pragma unroll 8
+        for (int k = lane; k < K; k += 32) {
+            if (e[k].q == 0.f) continue;
+            const float x = GRAD ? e[k].x : VT::load1(it.x + (int64_t)e[k].col * ES);
+            const float lp = none ? -INFINITY : (x - st.m) * p.scale - logd;
+            loss += e[k].q * (e[k].lq - lp);
+        }
+        loss = warp_allsum(loss);
+        need_count();
+        if (lane == 0) {
+            if (bad) atomicOr(p.err, CE_DEVERR_TARGET_RANGE);
+            p.loss[r] = bad ? NAN : p.tau * p.tau * loss;
+            if (p.stats) p.stats[r] = make_float4(st.m, logd, zm, logs);
+        }
+        if constexpr (GRAD) {
+            const float gt = row_scale(r), a = gt * Q, shift = -logd * kLog2e, nm = -st.m;
+            const bool zero = bad || none;
+            auto grad = [&](float v) { return ex2_approx(fmaf(v + nm, p.L, shift)) * a; };
+            if (ce >= 0) VT::store1(it.out + ce * ES, zero ? 0.f : grad(xe));
+            if (!__all_sync(kFull, row_wait(bars, &bars.stored[q], ph))) break;
+            for (int k = lane; k < K && !zero; k += 32) {
+                const int col = e[k].col;
+                if (col < 0) continue;
+                float c = e[k].q;
+                if (again) {  // in list order
+                    c = 0.f;
+                    for (int j = 0; j < K; ++j)
+                        if (e[j].col == col || e[j].col == -2 - col) c += e[j].q;
+                }
+                VT::store1(it.out + (int64_t)col * ES, fmaf(-gt, c, grad(e[k].x)));
+            }
+        }
+        warp_arrive(&bars.free_[q]);
     }
-    if (fine) finish();
     need_count();
-    if (tid == 0 && bars.gone) atomicOr(p.err, CE_DEVERR_TIMEOUT);
+    if (lane == 0 && bars.gone) atomicOr(p.err, CE_DEVERR_TIMEOUT);
     // the mean: the last CTA to finish sums the rows' losses in a fixed order
     if (p.mean_out) {
         __threadfence();
@@ -433,7 +390,7 @@ __global__ void __launch_bounds__(kRowThreads, NV == 4 ? 2 : 1) ce_distill_kerne
         side_sync();
         if (tid == 0) {
             double t = 0.0;
-            for (int w = 0; w < kSideThreads / 32; ++w) t += dred[w];
+            for (int w = 0; w < kSideWarps; ++w) t += dred[w];
             p.mean_out[0] = (float)(t / (double)(*p.n_count));  // NaN when every row is ignored
         }
     }
@@ -456,14 +413,15 @@ template <typename T, int NV, bool GRAD>
 cudaError_t launch_distill_k(DistillArgs a, cudaStream_t s) {
     auto* k = ce_distill_kernel<T, NV, GRAD>;
     a.slots = GRAD ? list_slots(a.tokens.n) : 0;
-    const size_t list = (size_t)kLists * a.tokens.n * sizeof(ListEntry) + (size_t)a.slots * 8;
-    constexpr size_t tile = kMainThreads * NV * 16, room = (NV == 4 ? 111 : 222) * 1024;
+    const size_t list = list_bytes(a.tokens.n, GRAD);
+    constexpr bool one = GRAD && NV == 8;  // CTA per SM
+    constexpr size_t tile = kMainThreads * NV * 16, room = (one ? 222 : 111) * 1024;
     a.stages = (int)((room - list) / tile);
     if (a.stages > kRingMost) a.stages = kRingMost;
     const size_t smem = a.stages * tile + list;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
     if (e != cudaSuccess) return e;
-    int64_t grid = NV == 4 ? kScanSlots : kSMs;
+    int64_t grid = one ? kSMs : kScanSlots;
     if (grid > a.N) grid = a.N;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -479,7 +437,7 @@ cudaError_t launch_distill_k(DistillArgs a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_distill_t(const DistillArgs& a, cudaStream_t s) {
-    if (!a.out) return launch_distill_k<T, 4, false>(a, s);
+    if (!a.out) return launch_distill_k<T, 8, false>(a, s);
     // rows over 128 KB: one CTA per SM with tiles of 32 KB, so fewer rows wait in L2 for
     // their second pass
     return a.V * (int64_t)sizeof(T) > 128 * 1024 ? launch_distill_k<T, 8, true>(a, s) : launch_distill_k<T, 4, true>(a, s);

@@ -80,27 +80,30 @@ __device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const c
 
 // Shared memory: the ring, and with top_k each side warp's candidates and the groups'
 // maxima of each place of the queue.
-constexpr int kTileBytes = kTileVecs * 16;
+// Vectors of a tile that a thread takes: eight where their maxima are not kept.
+constexpr int scan_vecs(int gm) { return gm ? 4 : 8; }
 constexpr int kPlaces = 4;  // of the queue: a row in the stream, three with the side warps
-constexpr int kSideWarps = 3;
-constexpr int kScanThreads = kMainThreads + 32 + kSideWarps * 32;
-constexpr int scan_stages(int gm) { return gm ? 4 : 6; }
+constexpr int scan_stages(int gm) { return gm ? 4 : 3; }
 constexpr size_t scan_smem(int gm) {
-    return (size_t)scan_stages(gm) * kTileBytes + (gm ? kSideWarps * sizeof(TopSmem) + kPlaces * kTopHeads * 2 : 0);
+    return (size_t)scan_stages(gm) * kMainThreads * scan_vecs(gm) * 16 + (gm ? kSideWarps * sizeof(TopSmem) + kPlaces * kTopHeads * 2 : 0);
 }
 
 template <typename T, int GM, bool ENT>  // GM: 0 without top_k, else as main_stats
-__global__ void __launch_bounds__(kScanThreads, 2) ce_scan_kernel(const __grid_constant__ ScanArgs p) {
+__global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_constant__ ScanArgs p) {
     using VT = Vec<T>;
-    constexpr int ES = sizeof(T), STAGES = scan_stages(GM);
+    constexpr int ES = sizeof(T), STAGES = scan_stages(GM), NV = scan_vecs(GM), TILE = kMainThreads * NV;
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ RowBars bars;
     unsigned char* ring = sm;
-    uint16_t* heads = reinterpret_cast<uint16_t*>(sm + (size_t)STAGES * kTileBytes);  // [kPlaces][kTopHeads]
+    uint16_t* heads = reinterpret_cast<uint16_t*>(sm + (size_t)STAGES * TILE * 16);  // [kPlaces][kTopHeads]
     TopSmem* tops = reinterpret_cast<TopSmem*>(heads + kPlaces * kTopHeads);           // [kSideWarps]
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) row_bars_init(bars);
+    if (threadIdx.x == 0) {
+        row_bars_init(bars);
+        if (p.part && blockIdx.x == 0) *p.err = 0u;
+    }
     __syncthreads();
+    griddep_launch_dependents();  // the kernel that puts segments together waits for this one's end itself
 
     if (threadIdx.x < kMainThreads) {
         Turn at, q;
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) ce_scan_kernel(const __grid_c
             if (row < 0) return;
             if (skip)
                 warp_arrive(&bars.done[q.s]);
-            else if (!main_stats<T, 4, ENT, GM>(bars, at, STAGES, ring, q.s, nv, p.L, heads + q.s * kTopHeads))
+            else if (!main_stats<T, NV, ENT, GM>(bars, at, STAGES, ring, q.s, nv, p.L, heads + q.s * kTopHeads))
                 return;
             warp_arrive(&bars.free_[q.s]);
         }
@@ -166,9 +169,9 @@ __global__ void __launch_bounds__(kScanThreads, 2) ce_scan_kernel(const __grid_c
                     }
                     mbar_arrive(&bars.ready[q.s]);
                     if (!skip)
-                        for (int64_t v = v0; ok && v < v1; v += kTileVecs)
-                            ok = ring_put(bars, at, issued, STAGES, ring, kTileBytes, body + v * 16,
-                                          (uint32_t)min((int64_t)kTileVecs, v1 - v) * 16u, policy);
+                        for (int64_t v = v0; ok && v < v1; v += TILE)
+                            ok = ring_put(bars, at, issued, STAGES, ring, TILE * 16, body + v * 16,
+                                          (uint32_t)min((int64_t)TILE, v1 - v) * 16u, policy);
                 }
                 if (!ok) ring_drain(bars, issued, STAGES);
             }
@@ -225,6 +228,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(const __grid_c
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     TopSmem& top = reinterpret_cast<TopSmem*>(sm)[warp];
     const int64_t r = (int64_t)blockIdx.x * kJoinWarps + warp;
+    griddep_wait();
     if (r >= p.N) return;
     const char* x = p.x + p.row.at(r) * sizeof(T);
     Given<T> given;
@@ -265,7 +269,7 @@ cudaError_t launch_scan_t(const ScanArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     int64_t grid = a.N * a.segs;
     if (grid > kScanSlots) grid = kScanSlots;
-    k<<<(unsigned)grid, kScanThreads, smem, s>>>(a);
+    k<<<(unsigned)grid, kRowThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -282,8 +286,16 @@ cudaError_t launch_join(const ScanArgs& a, cudaStream_t s) {
     auto* k = ce_join_kernel<T>;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
     if (e != cudaSuccess) return e;
-    k<<<(unsigned)((a.N + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, smem, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    set_pdl_attr(&attr[0]);
+    cfg.gridDim = dim3((unsigned)((a.N + kJoinWarps - 1) / kJoinWarps));
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 cudaError_t launch_scan(const ScanArgs& a, int dtype, bool entropy, cudaStream_t s) {
@@ -389,7 +401,8 @@ extern "C" ce_status ce_logprobs_fwd(const void* logits, ce_dtype dtype, int64_t
         a.cand = reinterpret_cast<uint64_t*>(ws + kWsHeaderBytes + part_bytes(N, pl.segs));
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(a.err, 0, 4, s);
+    // rows in segments: the first kernel starts the error word, the second one adds to it
+    cudaError_t e = a.part ? cudaSuccess : cudaMemsetAsync(a.err, 0, 4, s);
     if (e == cudaSuccess) e = launch_scan(a, dtype, entropy || stats, s);
     if (e == cudaSuccess && a.part) {
         if (dtype == CE_F32) e = launch_join<float>(a, s);

@@ -42,6 +42,8 @@
 #include "ce_rowscan_plan.h"
 #include "ce_span.cuh"
 
+#include <type_traits>
+
 namespace gbce {
 
 // ----------------------------------------------------------------- statistics
@@ -98,39 +100,46 @@ __device__ __forceinline__ void stat_add(Stat& a, float x, float L) {
     a = stat_combine(a, b, L);
 }
 
-// e = 2^y of one vector's logits relative to m, added to d2 and (ENT) with y to s2.  FAR: y
-// = (x - m) L, ref = -m (else ref = -M); LOW: some logit may be -inf.
-template <typename T, bool ENT, bool FAR, bool LOW>
-__device__ __forceinline__ void stat_vector(const uint4& raw, float ref, float L, float2& d2, float2& s2) {
+// The larger of two, a NaN where either is one.
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, float b, float) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(b));
+    return __float_as_uint(r);
+}
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, float b, __nv_bfloat16) {
+    return bf162_bits(__hmax2_nan(as_bf162(a), __float2bfloat162_rn(b)));
+}
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, float b, __half) {
+    return h2_bits(__hmax2_nan(as_h2(a), __float2half2_rn(b)));
+}
+
+// e = 2^y of one vector's logits, added to d2 and (ENT) with y to s2: y = (x + add) L +
+// ref, add 0 but where SLOW.  least (ENT): where 2^y is 0, a logit counts as this one, so no
+// 0 is multiplied with -inf; taken on packed pairs in 16 bits (SLOW: on y).
+template <typename T, bool ENT, bool SLOW>
+__device__ __forceinline__ void stat_vector(uint4 raw, float ref, float add, float least, float L, float2& d2,
+                                            float2& s2) {
     using VT = Vec<T>;
     constexpr int PP = VT::kElems / 2;
-    const float2 R = make_float2(ref, ref), LL = make_float2(L, L);
+    const float2 R = make_float2(ref, ref), AD = make_float2(add, add), LL = make_float2(L, L);
+    if (ENT && !SLOW) {
+        raw.x = max_nan(raw.x, least, T());
+        raw.y = max_nan(raw.y, least, T());
+        raw.z = max_nan(raw.z, least, T());
+        raw.w = max_nan(raw.w, least, T());
+    }
     float2 x[PP];
     VT::unpack2(raw, x);
 #pragma unroll
     for (int k = 0; k < PP; ++k) {
-        float2 y = FAR ? __fmul2_rn(__fadd2_rn(x[k], R), LL) : __ffma2_rn(x[k], LL, R);
+        float2 y = __ffma2_rn(SLOW ? __fadd2_rn(x[k], AD) : x[k], LL, R);
         const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
         d2 = __fadd2_rn(d2, e);
         if (ENT) {
-            if (LOW) y = make_float2(fmaxf(y.x, kFarBelow), fmaxf(y.y, kFarBelow));
+            if (SLOW) y = make_float2(fmaxf(y.x, kFarBelow), fmaxf(y.y, kFarBelow));
             s2 = __ffma2_rn(e, y, s2);
         }
     }
-}
-// What is rarely met, out of the way: a row at the type's lowest value, logits of -inf
-// under an entropy.
-template <typename T, bool ENT>
-__device__ __forceinline__ float4 stat_far(const uint4* src, int n, float m, float L) {
-    float2 d2 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
-    const bool near = fabsf(stat_ref(m, L)) < kRefMost || m == -INFINITY;
-    const float ref = m == -INFINITY ? 0.f : (near ? -stat_ref(m, L) : -m);
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-        if (near) stat_vector<T, ENT, false, true>(src[i * kMainThreads], ref, L, d2, s2);
-        else stat_vector<T, ENT, true, true>(src[i * kMainThreads], ref, L, d2, s2);
-    }
-    return make_float4(d2.x, d2.y, s2.x, s2.y);
 }
 
 __device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
@@ -143,21 +152,32 @@ __device__ __forceinline__ M max_from(M own, int lanes) {  // the maximum of the
     return *reinterpret_cast<const M*>(&o);
 }
 
-// A thread's vectors of a tile: src[0], src[kMainThreads], ..., n of them (FULL: NV).
-// ENT: s as well.  gm: each vector's maximum, packed (-inf where there is none).
-template <typename T, int NV, bool FULL, bool ENT>
+// A thread's vectors of a tile: src[0], src[kMainThreads], ..., n of them.  ENT: s as well.
+// gm: each vector's maximum, packed (-inf where there is none).
+template <typename T>
+__device__ __forceinline__ uint4 all_low() {  // a vector of -inf, which counts for nothing
+    const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+    return make_uint4(w, w, w, w);
+}
+template <typename T, int NV, bool ENT>
 __device__ __forceinline__ void stat_tile(Stat& a, const uint4* src, int n, float L,
                                           typename Vec<T>::Max (&gm)[NV]) {
     using VT = Vec<T>;
     uint4 raw[NV];
+    if (n == NV) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (FULL || i < n) raw[i] = src[i * kMainThreads];
+        for (int i = 0; i < NV; ++i) raw[i] = src[i * kMainThreads];
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            raw[i] = all_low<T>();
+            if (i < n) raw[i] = src[i * kMainThreads];
+        }
+    }
     typename VT::Max tm = VT::max_init();
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        gm[i] = VT::max_init();
-        if (FULL || i < n) gm[i] = VT::max_acc(gm[i], raw[i]);
+        gm[i] = VT::max_acc(VT::max_init(), raw[i]);
         tm = max_of(tm, gm[i]);
     }
     const float top = VT::max_done(tm);
@@ -169,14 +189,19 @@ __device__ __forceinline__ void stat_tile(Stat& a, const uint4* src, int n, floa
     }
     float2 d2 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
     const float ref = a.m == -INFINITY ? 0.f : -stat_ref(a.m, L);
+    // 2^y is 0 from 150 down; the distance leaves room for the rounding to 16 bits (2^-9 of
+    // the maximum).  Without a maximum 2^y is 0 for any logit there is.
+    const float top_or_low = a.m == -INFINITY ? kFarBelow : a.m;
+    const float least = ENT ? top_or_low - fmaxf(200.f / L, fabsf(top_or_low) * 0.015625f) : 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (FULL || i < n) stat_vector<T, ENT, false, false>(raw[i], ref, L, d2, s2);
-    // (0 times -inf, or a NaN, which d shows too)
-    if (!(fabsf(ref) < kRefMost) || (ENT && s2.x + s2.y != s2.x + s2.y)) {
-        const float4 v = stat_far<T, ENT>(src, FULL ? NV : n, a.m, L);
-        d2 = make_float2(v.x, v.y);
-        s2 = make_float2(v.z, v.w);
+    for (int i = 0; i < NV; ++i) stat_vector<T, ENT, false>(raw[i], ref, 0.f, least, L, d2, s2);
+    // rarely met: a row at the type's lowest value (of float16, where `least` is none of its)
+    const bool far = !(fabsf(ref) < kRefMost);
+    if (far || (ENT && std::is_same<T, __half>::value && least < -65504.f)) {
+        d2 = s2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i)
+            stat_vector<T, ENT, true>(src[i * kMainThreads], far ? 0.f : ref, far ? -a.m : 0.f, 0.f, L, d2, s2);
     }
     a.d += d2.x + d2.y;
     if (ENT) a.s += s2.x + s2.y;
@@ -235,12 +260,37 @@ __device__ __forceinline__ float key_value(uint64_t k) {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xffffffffu));
 }
 __device__ __forceinline__ uint32_t key_column(uint64_t k) { return 0xffffffffu - (uint32_t)k; }
-// The first 16 bits of a value's key: they order values rounded down to them (a NaN, the
-// maximum of nothing else, as -inf).
-constexpr uint32_t kLowestHead = 0x007fu;
-__device__ __forceinline__ uint32_t value_head(float x) {
-    return x == x ? (uint32_t)(top_key(x, 0) >> 48) : kLowestHead;
-}
+// A value's place among the values of T in 16 bits: exact in the 16-bit types, of float32
+// the first 16 bits of its key, which order values rounded down to them.  A NaN (the
+// maximum of nothing else) counts as -inf, the lowest.
+template <typename T>
+struct Head;
+template <>
+struct Head<float> {
+    static constexpr uint32_t lowest = 0x007fu;
+    static constexpr bool exact = false;
+    __device__ __forceinline__ static uint32_t of(float x) { return x == x ? (uint32_t)(top_key(x, 0) >> 48) : lowest; }
+    __device__ __forceinline__ static float value(uint32_t h) { return key_value((uint64_t)h << 48); }
+};
+template <>
+struct Head<__nv_bfloat16> {
+    static constexpr uint32_t lowest = 0x007fu;
+    static constexpr bool exact = true;
+    __device__ __forceinline__ static uint32_t of(float x) { return Head<float>::of(x); }
+    __device__ __forceinline__ static float value(uint32_t h) { return key_value((uint64_t)h << 48); }
+};
+template <>
+struct Head<__half> {
+    static constexpr uint32_t lowest = 0x03ffu;
+    static constexpr bool exact = true;
+    __device__ __forceinline__ static uint32_t of(float x) {
+        const uint32_t b = __half_as_ushort(__float2half_rn(x + 0.f));
+        return x == x ? (b & 0x8000u ? ~b & 0xffffu : b | 0x8000u) : lowest;
+    }
+    __device__ __forceinline__ static float value(uint32_t h) {
+        return __half2float(__ushort_as_half((unsigned short)(h & 0x8000u ? h & 0x7fffu : ~h)));
+    }
+};
 
 // The candidates of one warp's selection.
 struct alignas(16) TopSmem {
@@ -248,61 +298,61 @@ struct alignas(16) TopSmem {
     int bins[128];
 };
 
-// 32 NK keys in falling order by a warp: key i of lane l is the one at 32 i + l.
-template <int NK>
-__device__ __forceinline__ void sort_keys(uint64_t (&k)[NK]) {
+// The first c keys of buf in falling order.  One warp.  Neither unrolled nor inlined, like the
+// searches below: the side warps' code shares the instruction cache with the main loop.
+static __device__ __noinline__ void top_sort(TopSmem& s, int c) {
     const int lane = threadIdx.x & 31;
+    __syncwarp();
+    if (c <= 1) return;
+    int n = 32;
+    while (n < c) n *= 2;
+    if (n <= 128) {
+        // four keys a lane in registers: key i of lane l is the one at 32 i + l
+        uint64_t k[4];
 #pragma unroll
-    for (int size = 2; size <= 32 * NK; size *= 2) {
+        for (int i = 0; i < 4; ++i) k[i] = 32 * i + lane < c ? s.buf[32 * i + lane] : 0;
+#pragma unroll 1
+        for (int size = 2; size <= n; size *= 2) {
+            if (size > 64) {  // step 64: keys 0 and 2, 1 and 3
 #pragma unroll
-        for (int step = size / 2; step > 0; step /= 2) {
-            if (step >= 32) {
-#pragma unroll
-                for (int i = 0; i < NK; ++i) {
-                    const int j = i ^ (step / 32);
-                    if (j < i) continue;
-                    const bool down = ((32 * i) & size) == 0;
-                    const uint64_t hi = k[i] > k[j] ? k[i] : k[j], lo = k[i] > k[j] ? k[j] : k[i];
-                    k[i] = down ? hi : lo;
-                    k[j] = down ? lo : hi;
+                for (int i = 0; i < 2; ++i) {
+                    const uint64_t hi = k[i] > k[i + 2] ? k[i] : k[i + 2], lo = k[i] > k[i + 2] ? k[i + 2] : k[i];
+                    k[i] = hi;
+                    k[i + 2] = lo;
                 }
-            } else {
+            }
+            if (size > 32) {  // step 32: keys 0 and 1, 2 and 3
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const bool down = ((32 * i) & size) == 0;
+                    const uint64_t hi = k[i] > k[i + 1] ? k[i] : k[i + 1], lo = k[i] > k[i + 1] ? k[i + 1] : k[i];
+                    k[i] = down ? hi : lo;
+                    k[i + 1] = down ? lo : hi;
+                }
+            }
+#pragma unroll 1
+            for (int step = min(size / 2, 16); step > 0; step /= 2) {
                 const bool low = (lane & step) == 0;
 #pragma unroll
-                for (int i = 0; i < NK; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     const uint64_t o = __shfl_xor_sync(kFull, k[i], step);
                     const bool down = ((32 * i + lane) & size) == 0;
                     k[i] = (k[i] > o) == (down == low) ? k[i] : o;
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.buf[32 * i + lane] = k[i];
+        __syncwarp();
+        return;
     }
-}
-template <int NK>
-__device__ __forceinline__ void sort_few(TopSmem& s, int c) {
-    const int lane = threadIdx.x & 31;
-    uint64_t k[NK];
-#pragma unroll
-    for (int i = 0; i < NK; ++i) k[i] = 32 * i + lane < c ? s.buf[32 * i + lane] : 0;
-    sort_keys<NK>(k);
-#pragma unroll
-    for (int i = 0; i < NK; ++i) s.buf[32 * i + lane] = k[i];
-    __syncwarp();
-}
-
-// The first c keys of buf in falling order.  One warp.
-__device__ __forceinline__ void top_sort(TopSmem& s, int c) {
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
-    if (c <= 1) return;
-    if (c <= 32) return sort_few<1>(s, c);
-    if (c <= 128) return sort_few<4>(s, c);
-    int n = 256;
-    while (n < c) n *= 2;
     for (int k = c + lane; k < n; k += 32) s.buf[k] = 0;
     __syncwarp();
+#pragma unroll 1
     for (int size = 2; size <= n; size *= 2) {
+#pragma unroll 1
         for (int step = size / 2; step > 0; step /= 2) {
+#pragma unroll 2
             for (int p = lane; p < n / 2; p += 32) {
                 const int lo = p & (step - 1), i = 2 * (p - lo) + lo, j = i + step;
                 const uint64_t a = s.buf[i], b = s.buf[j];
@@ -391,91 +441,134 @@ __device__ __forceinline__ void top_push_one(TopSmem& s, TopGate& g, bool ok, fl
     g.held += __popc(m);
 }
 
-// A head that at least K of the n heads reach, few more where the heads are fine enough
-// (0: fewer than K are not 0).  Heads are counted by their distance below the largest in
-// 128 bins, which one sum over them turns into the answer; where K lie further down, in
-// wider bins.  Of many heads for each of the K only the maximum of eight, or two, counts.
-__device__ __forceinline__ uint32_t kth_head(TopSmem& s, const uint16_t* heads, int n, int K) {
+__device__ __forceinline__ uint32_t head_of_eight(const uint16_t* heads, int k) {  // maxima in both halves
+    const uint4 u = *reinterpret_cast<const uint4*>(heads + k);
+    return __vmaxu2(__vmaxu2(u.x, u.y), __vmaxu2(u.z, u.w));
+}
+// Heads (of eight, or two, the maximum: fold) counted by their distance below `top` (those
+// above it as none) in 128 bins of 2^shift: the bin in which the K-th lies, and in the
+// upper half how many lie in it and above it.  128: in none.
+static __device__ __noinline__ uint32_t head_bin(TopSmem& s, const uint16_t* heads, int n, int K, uint32_t top,
+                                                 int shift, int fold) {
     const int lane = threadIdx.x & 31;
-    auto of_eight = [&](int k) {  // maxima in both halves
-        const uint4 u = *reinterpret_cast<const uint4*>(heads + k);
-        return __vmaxu2(__vmaxu2(u.x, u.y), __vmaxu2(u.z, u.w));
+    const uint32_t span = 128u << shift;
+    *reinterpret_cast<int4*>(s.bins + 4 * lane) = make_int4(0, 0, 0, 0);
+    __syncwarp();
+    auto bin = [&](uint32_t h) {
+        const uint32_t d = h < top ? top - h : 0u;
+        if (d < span && h) atomicAdd(&s.bins[d >> shift], 1);
     };
-    uint32_t m = 0;
-    for (int k = lane * 8; k < n; k += 256) m = __vmaxu2(m, of_eight(k));
-    m = __reduce_max_sync(kFull, max(m & 0xffffu, m >> 16));
-    if (K == 1 || m == 0) return m;
-    for (int shift = 1; shift <= 9; shift += 4) {
-        const uint32_t span = 128u << shift;
-        *reinterpret_cast<int4*>(s.bins + 4 * lane) = make_int4(0, 0, 0, 0);
-        __syncwarp();
-        auto bin = [&](uint32_t h) {
-            const uint32_t d = m - h;
-            if (d < span && h) atomicAdd(&s.bins[d >> shift], 1);
-        };
-        if (n >= 24 * K) {
-            for (int k = lane * 8; k < n; k += 256) {
-                const uint32_t v = of_eight(k);
-                bin(max(v & 0xffffu, v >> 16));
-            }
-        } else {
-            const bool pairs = n >= 6 * K;
-            for (int k = lane * 2; k < n; k += 64) {
-                const uint32_t u = *reinterpret_cast<const uint32_t*>(heads + k);
-                const uint32_t a = u & 0xffffu, c = u >> 16;
-                bin(max(a, c));
-                if (!pairs) bin(min(a, c));
-            }
+    if (fold == 8) {
+        for (int k = lane * 8; k < n; k += 256) {
+            const uint32_t v = head_of_eight(heads, k);
+            bin(max(v & 0xffffu, v >> 16));
         }
-        __syncwarp();
-        const int4 c = *reinterpret_cast<const int4*>(s.bins + 4 * lane);
-        const int own = c.x + c.y + c.z + c.w;
-        int upto = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(kFull, upto, o);
-            if (lane >= o) upto += u;
-        }
-        __syncwarp();
-        const unsigned there = __ballot_sync(kFull, upto >= K);
-        if (there) {
-            const int l = __ffs(there) - 1, before = upto - own;  // the bin in which the K-th lies
-            int b = before + c.x >= K ? 0 : before + c.x + c.y >= K ? 1 : before + c.x + c.y + c.z >= K ? 2 : 3;
-            b = __shfl_sync(kFull, 4 * lane + b, l);
-            const uint32_t d = (((uint32_t)b + 1u) << shift) - 1u;  // the bin's far end
-            return m > d ? m - d : 1u;
+    } else {
+        for (int k = lane * 2; k < n; k += 64) {
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(heads + k);
+            const uint32_t a = u & 0xffffu, c = u >> 16;
+            bin(max(a, c));
+            if (fold == 1) bin(min(a, c));
         }
     }
-    return 0;
+    __syncwarp();
+    const int4 c = *reinterpret_cast<const int4*>(s.bins + 4 * lane);
+    const int own = c.x + c.y + c.z + c.w;
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += u;
+    }
+    __syncwarp();
+    const unsigned there = __ballot_sync(kFull, sum >= K);
+    if (there == 0u) return 128u;
+    const int l = __ffs(there) - 1, before = sum - own;
+    const int e0 = before + c.x, e1 = e0 + c.y, e2 = e1 + c.z;
+    const int b = e0 >= K ? 0 : e1 >= K ? 1 : e2 >= K ? 2 : 3;
+    const uint32_t said = (uint32_t)(4 * lane + b) | (uint32_t)(b == 0 ? e0 : b == 1 ? e1 : b == 2 ? e2 : sum) << 16;
+    return __shfl_sync(kFull, said, l);
 }
 
-// The heads that reach kth (1 at least), listed in place by their numbers, in order: the
-// list never reaches a head that has not been looked at.  How many there are.
-__device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t kth) {
+// The least head that is read again: at least K of the n heads reach it (0: fewer than K are
+// not 0).  It is sought below the largest head, in wider bins where K lie further down.
+// Of many heads for each of the K only the maximum of eight, or two, counts: few more than
+// K reach that too.  Where many more than K do (equal heads: a mask, a constant row), the
+// K-th itself is sought (many).
+__device__ __forceinline__ uint32_t kth_head(TopSmem& s, const uint16_t* heads, int n, int K, bool& many) {
     const int lane = threadIdx.x & 31;
-    const uint32_t least = kth ? kth : 1u;
+    many = false;
+    uint32_t top = 0;
+    for (int k = lane * 8; k < n; k += 256) top = __vmaxu2(top, head_of_eight(heads, k));
+    top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
+    if (top == 0) return 0;
+    int fold = n >= 24 * K ? 8 : (n >= 6 * K ? 2 : 1);
+    int shift = 1;
+#pragma unroll 1
+    for (;;) {
+        const uint32_t said = head_bin(s, heads, n, K, top, shift, fold), b = said & 0xffffu;
+        const int upto = (int)(said >> 16);
+        if (b == 128u) {  // further down, or (a second time, without folding) nowhere
+            if (shift == 9 && fold == 1) return 0;
+            if (shift == 9) fold = 1;
+            else shift += 4;
+            continue;
+        }
+        if (!many && upto <= 2 * K + 16) {
+            const uint32_t far = ((b + 1u) << shift) - 1u;  // the bin's far end
+            return top > far ? top - far : 1u;
+        }
+        // what lies above the bin counts in the next, finer one's first bin
+        const uint32_t near = b << shift;
+        top = top > near ? top - near : 1u;
+        if (many && shift == 0) return top;
+        shift = !many ? shift : shift > 5 ? 5 : shift > 1 ? 1 : 0;
+        if (!many && shift == 1) shift = 0;
+        many = true;
+        fold = 1;
+    }
+}
+
+// The heads that reach `least` (1 at least), listed in place by their numbers, in order: the
+// list never reaches a head that has not been looked at.  Of those equal to `least` the
+// first `ties`.  How many there are.
+__device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t least, int ties) {
+    const int lane = threadIdx.x & 31;
+    if (least == 0) least = 1;
     int listed = 0;
     for (int k0 = 0; k0 < n; k0 += 256) {
         const int k = k0 + lane * 8;
         uint4 u = make_uint4(0, 0, 0, 0);
         if (k < n) u = *reinterpret_cast<const uint4*>(heads + k);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        unsigned ok = 0;
+        unsigned ok = 0, tie = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             ok |= (w[i] & 0xffffu) >= least ? 1u << (2 * i) : 0u;
             ok |= (w[i] >> 16) >= least ? 2u << (2 * i) : 0u;
+            tie |= (w[i] & 0xffffu) == least ? 1u << (2 * i) : 0u;
+            tie |= (w[i] >> 16) == least ? 2u << (2 * i) : 0u;
         }
-        int at = __popc(ok);
-        const int own = at;
         if (!__any_sync(kFull, ok != 0u)) continue;
+        auto upto = [&](int v) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(kFull, at, o);
-            if (lane >= o) at += v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int b = __shfl_up_sync(kFull, v, o);
+                if (lane >= o) v += b;
+            }
+            return v;
+        };
+        if (ties != 0x7fffffff) {
+            const int own = __popc(tie), sum = upto(own);
+            int room = ties - (sum - own);  // of this lane's
+            ties = max(0, ties - __shfl_sync(kFull, sum, 31));
+            unsigned drop = tie;
+            for (; drop && room > 0; --room) drop &= drop - 1u;
+            ok &= ~drop;
         }
-        const int all = __shfl_sync(kFull, at, 31);
-        at += listed - own;
+        const int own = __popc(ok), sum = upto(own);
+        const int all = __shfl_sync(kFull, sum, 31);
+        int at = listed + sum - own;
         for (; ok; ok &= ok - 1u) heads[at++] = (uint16_t)(k + __ffs(ok) - 1);
         listed += all;
         __syncwarp();
@@ -484,20 +577,20 @@ __device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t kth) 
     return listed;
 }
 
-// The listed groups' vectors, 32 at a time and the next ones on their way.
-template <typename T, int UNIT>
-__device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t* list, int listed, const uint4* body,
-                                         int64_t nv, uint32_t col0) {
-    constexpr int VEC = Vec<T>::kElems, AHEAD = 4, PER = 32 / UNIT;
-    const int lane = threadIdx.x & 31;
+// The listed groups' vectors (2^wide of each), 32 at a time and the next ones on their way.
+template <typename T>
+__device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t* list, int listed, int wide,
+                                         const uint4* body, int64_t nv, uint32_t col0) {
+    constexpr int VEC = Vec<T>::kElems, AHEAD = 4;
+    const int lane = threadIdx.x & 31, per = 32 >> wide;
     const int last = nv < 0x7fffffff ? (int)nv : 0x7fffffff;
     uint4 raw[AHEAD];
     int v[AHEAD];  // the vector, or -1
     auto fetch = [&](int b, uint4& to, int& vec) {
-        const int e = b + lane / UNIT;
+        const int e = b + (lane >> wide);
         vec = -1;
         if (e < listed) {
-            const int at = (int)list[e] * UNIT + lane % UNIT;
+            const int at = ((int)list[e] << wide) + (lane & ((1 << wide) - 1));
             if (at < last) {
                 vec = at;
                 to = __ldg(body + at);
@@ -505,15 +598,19 @@ __device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t*
         }
     };
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a) fetch(a * PER, raw[a], v[a]);
-    for (int b = 0; b < listed; b += AHEAD * PER) {
+    for (int a = 0; a < AHEAD; ++a) fetch(a * per, raw[a], v[a]);
+#pragma unroll 1
+    for (int b = 0; b < listed; b += per) {
+        const uint4 now = raw[0];
+        const int vec = v[0];
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            if (b + a * PER >= listed) break;
-            top_room(s, g, 32 * VEC);
-            top_push<T>(s, g, v[a] >= 0, raw[a], col0 + (uint32_t)(v[a] * VEC));
-            fetch(b + (AHEAD + a) * PER, raw[a], v[a]);
+        for (int a = 0; a + 1 < AHEAD; ++a) {
+            raw[a] = raw[a + 1];
+            v[a] = v[a + 1];
         }
+        fetch(b + AHEAD * per, raw[AHEAD - 1], v[AHEAD - 1]);
+        top_room(s, g, 32 * VEC);
+        top_push<T>(s, g, vec >= 0, now, col0 + (uint32_t)(vec * VEC));
     }
 }
 
@@ -530,16 +627,19 @@ __device__ __forceinline__ int top_select(TopSmem& s, uint16_t* heads, int G, co
     const bool brief = G < 2 * K && nv <= kTopHeads;  // too few groups: each vector is one
     if (brief) {
         for (int v = lane; v < (((int)nv + 255) & ~255); v += 32)
-            heads[v] = (uint16_t)(v < nv ? value_head(VT::vmax(__ldg(body + v))) : 0u);
+            heads[v] = (uint16_t)(v < nv ? Head<T>::of(VT::vmax(__ldg(body + v))) : 0u);
         G = (int)nv;
         __syncwarp();
     }
-    const uint32_t kth = kth_head(s, heads, G, K);
-    const int listed = list_heads(heads, G, kth);
-    TopGate g(K, kth <= kLowestHead ? -INFINITY : key_value((uint64_t)kth << 48));
+    bool many;
+    const uint32_t kth = kth_head(s, heads, G, K, many);
+    // where the head says the value, K groups of the K-th are enough of its equals
+    const bool exact = many && (Head<T>::exact || kth <= Head<T>::lowest);
+    const int listed = list_heads(heads, G, kth, exact ? K : 0x7fffffff);
+    TopGate g(K, kth <= Head<T>::lowest ? -INFINITY : Head<T>::value(kth));
     top_push_one(s, g, has_edge && before, xe, ce);
-    if (brief) top_take<T, 1>(s, g, heads, listed, body, nv, col0);
-    else top_take<T, UNIT>(s, g, heads, listed, body, nv, col0);
+    constexpr int WIDE = UNIT == 32 ? 5 : 3;
+    top_take<T>(s, g, heads, listed, brief ? 0 : WIDE, body, nv, col0);
     top_room(s, g, 32);
     top_push_one(s, g, has_edge && !before, xe, ce);
     top_sort(s, g.held);
@@ -555,7 +655,7 @@ __device__ __forceinline__ int top_select(TopSmem& s, uint16_t* heads, int G, co
 // gives up raises `gone`, which ends all others; the copying warp then issues no more and
 // leaves when what it has issued has landed (bounded too).
 constexpr int kRingMost = 6;
-constexpr int kQueue = 4;  // places at most
+constexpr int kQueue = 6;  // places at most
 struct RowItem {
     const char* x;      // the row
     char* out;          // its gradient, or NULL
@@ -649,13 +749,8 @@ __device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, con
         const uint4* src = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16) + tid;
         typename VT::Max gm[NV];
         if (!row_wait(b, &b.full[at.s], at.ph)) return false;
-        int mine = NV;
-        if (nv >= TILE) {
-            stat_tile<T, NV, true, ENT>(st, src, NV, L, gm);
-        } else {
-            mine = max(0, min(NV, ((int)nv - tid + kMainThreads - 1) / kMainThreads));
-            stat_tile<T, NV, false, ENT>(st, src, mine, L, gm);
-        }
+        stat_tile<T, NV, ENT>(st, src, nv >= TILE ? NV : max(0, min(NV, ((int)nv - tid + kMainThreads - 1) / kMainThreads)),
+                              L, gm);
         warp_arrive(&b.empty[at.s]);
         at.next(stages);
         if constexpr (GM == 1) {
@@ -668,7 +763,7 @@ __device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, con
             }
             if (lane < NV)
                 heads[lane * (kMainThreads / 32) + warp] =
-                    (uint16_t)(lane * kMainThreads + warp * 32 < nv ? value_head(own) : 0u);
+                    (uint16_t)(lane * kMainThreads + warp * 32 < nv ? Head<T>::of(own) : 0u);
             heads += TILE / 32;
         } else if constexpr (GM == 2) {
             // over eight lanes, of four vectors at once: each step sends what the other lane goes on
@@ -680,7 +775,7 @@ __device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, con
             u = max_of(two ? w : u, max_from(two ? u : w, 2));
             u = max_of(u, max_from(u, 4));
             const int first = (lane & 3) * kMainThreads + (tid & ~7);
-            if ((lane & 4) == 0) heads[first / 8] = (uint16_t)(first < nv ? value_head(VT::max_done(u)) : 0u);
+            if ((lane & 4) == 0) heads[first / 8] = (uint16_t)(first < nv ? Head<T>::of(VT::max_done(u)) : 0u);
             heads += TILE / 8;
         }
     }

@@ -8,7 +8,9 @@
 namespace gbce {
 
 constexpr int kMainThreads = 256;                            // threads that read a tile
-constexpr int kSideThreads = 128;                            // threads beside them
+constexpr int kSideWarps = 3;                                // warps beside them
+constexpr int kSideThreads = 32 * kSideWarps;
+constexpr int kRowThreads = kMainThreads + 32 + kSideThreads;  // and the copying warp
 constexpr int kTileVecs = kMainThreads * 4;                  // 16-byte vectors of a tile: 16 KB
 constexpr int kTopCap = 1024;                                // candidates held at a time
 constexpr int kTopHeads = 2048;                              // groups' maxima of a row or segment
@@ -24,16 +26,23 @@ struct ScanPlan {
     int64_t per;   // whole vectors in a segment
 };
 
-// Few rows are cut so that every SM has a part; from four rounds of whole rows on
-// a row stays in one piece, as far as its groups' maxima have room.  segs is 0 where
-// they have none.
+// Rows are cut where that ends sooner: the rounds of kScanSlots CTAs times a segment's
+// tiles and what it costs beside them (seven tenths of a tile's time), and two tiles' time
+// for putting segments together.  A segment's groups' maxima have to have room; segs is 0
+// where they have none.
 inline ScanPlan plan_scan(int64_t N, int64_t V, int es, int top_k) {
     const int64_t nv = V * es / 16;
     const int64_t tiles = (nv + kTileVecs - 1) / kTileVecs;
     int64_t segs = 1;
-    if (N > 0 && N < 4 * kScanSlots) segs = (4 * kScanSlots + N - 1) / N;
-    if (segs > tiles) segs = tiles;
-    if (segs < 1) segs = 1;
+    double least = 0;
+    for (int64_t s = 1; s <= 64 && s <= (tiles > 1 ? tiles : 1) && N > 0 && N < 64 * kScanSlots; ++s) {
+        const double rounds = (double)((N * s + kScanSlots - 1) / kScanSlots);
+        const double time = rounds * ((double)tiles / s + 0.7) + (s > 1 ? 2 : 0);
+        if (s == 1 || time < least) {
+            least = time;
+            segs = s;
+        }
+    }
     const int64_t room = top_k <= 0 ? nv : (int64_t)kTopHeads * (top_k <= kFewTop ? 32 : 8);
     if (nv > segs * room) segs = (nv + room - 1) / room;
     ScanPlan p;

@@ -212,12 +212,14 @@ cudaError_t launch_softgrad_t(const SoftGradArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Runs of 32 KB; longer ones where the grid would not hold them, shorter ones (down to
-// 4 KB) where few rows leave SMs without.
+// Runs of 32 KB; longer ones under long lists, which every CTA of a row walks through,
+// while that leaves the SMs several rounds, and where the grid would not hold them;
+// shorter ones (down to 4 KB) where few rows leave SMs without.
 cudaError_t launch_softgrad(SoftGradArgs a, int dtype, cudaStream_t s) {
     const int vec = 16 / elem_size(dtype);
     a.cols = (int64_t)kThreads * 8 * vec;
     while (a.cols > kThreads * vec && a.N * ((a.V + a.cols - 1) / a.cols) < 2 * kScanSlots) a.cols /= 2;
+    while (a.tokens.n > 32 && a.cols < a.V && a.N * ((a.V + 2 * a.cols - 1) / (2 * a.cols)) >= 4096) a.cols *= 2;
     while (a.N * ((a.V + a.cols - 1) / a.cols) > 0x7fffffffLL) a.cols *= 2;
     a.runs = (a.V + a.cols - 1) / a.cols;
     if (dtype == CE_F32) return launch_softgrad_t<float>(a, s);
