@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
         const int tid = threadIdx.x;
         Turn at, q;
         for (;; q.next(kPlaces)) {
-            if (!row_wait(bars, &bars.ready[q.s], q.ph)) return;
+            if (!warp_wait(bars, &bars.ready[q.s], q.ph)) return;
             const RowItem& it = bars.item[q.s];
             const int64_t r = it.row, nv = it.nv;
             if (r < 0) return;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
             }
             if (!main_stats<T, NV, false, 0>(bars, at, p.stages, ring, q.s, nv, p.L, nullptr)) return;
             if constexpr (GRAD) {
-                if (!row_wait(bars, &bars.done[q.s], q.ph) || !row_wait(bars, &bars.prep[q.s], q.ph)) return;
+                if (!warp_wait(bars, &bars.done[q.s], q.ph) || !warp_wait(bars, &bars.prep[q.s], q.ph)) return;
                 const ListRow& l = lists[q.s];
                 Stat st = stat_identity();
                 if (lane < kMainThreads / 32) st = Stat{bars.part[q.s][lane].x, bars.part[q.s][lane].y, 0.f};
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
                 };
                 for (int64_t f = 0; f < nv; f += TILE, to += TILE) {
                     const uint4* tile = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16) + tid;
-                    if (!row_wait(bars, &bars.full[at.s], at.ph)) return;
+                    if (!warp_wait(bars, &bars.full[at.s], at.ph)) return;
                     const int64_t n = nv - f - tid;  // vectors from this thread's first on
                     if (fused && !zero && nv - f >= TILE) {
                         uint4 raw[NV];
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
     for (uint32_t turn = side;; turn += kSideWarps) {
         const int q = (int)(turn % kPlaces);
         const uint32_t ph = (turn / kPlaces) & 1u;
-        if (!__all_sync(kFull, row_wait(bars, &bars.ready[q], ph))) break;
+        if (!warp_wait(bars, &bars.ready[q], ph)) break;
         const RowItem& it = bars.item[q];
         const int64_t r = it.row;
         if (r < 0) break;
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
         }
         warp_arrive(&bars.prep[q]);
 
-        if (!__all_sync(kFull, row_wait(bars, &bars.done[q], ph))) break;
+        if (!warp_wait(bars, &bars.done[q], ph)) break;
         const Stat st = row_stats<false>(bars.part[q], ce >= 0, xe, p.L);
         const bool none = stat_none(st.m, st.d);
         const float logd = none ? 0.f : stat_logd(st, p.L);
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
             const bool zero = bad || none;
             auto grad = [&](float v) { return ex2_approx(fmaf(v + nm, p.L, shift)) * a; };
             if (ce >= 0) VT::store1(it.out + ce * ES, zero ? 0.f : grad(xe));
-            if (!__all_sync(kFull, row_wait(bars, &bars.stored[q], ph))) break;
+            if (!warp_wait(bars, &bars.stored[q], ph)) break;
             for (int k = lane; k < K && !zero; k += 32) {
                 const int col = e[k].col;
                 if (col < 0) continue;

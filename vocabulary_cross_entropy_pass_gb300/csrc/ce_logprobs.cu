@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
     if (threadIdx.x < kMainThreads) {
         Turn at, q;
         for (;; q.next(kPlaces)) {
-            if (!row_wait(bars, &bars.ready[q.s], q.ph)) return;
+            if (!warp_wait(bars, &bars.ready[q.s], q.ph)) return;
             const int64_t row = bars.item[q.s].row, nv = bars.item[q.s].nv;
             const int skip = bars.item[q.s].skip;
             if (row < 0) return;
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
     for (uint32_t turn = side;; turn += kSideWarps) {
         const int q = (int)(turn % kPlaces);
         const uint32_t ph = (turn / kPlaces) & 1u;
-        if (!__all_sync(kFull, row_wait(bars, &bars.ready[q], ph))) break;
+        if (!warp_wait(bars, &bars.ready[q], ph)) break;
         const RowItem& it = bars.item[q];
         const int64_t r = it.row;
         if (r < 0) break;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
             if (!p.part) given.load(p, r, it.x, lane);
             const int64_t ce = edge_column(it);
             const float xe = ce >= 0 ? VT::load1(it.x + ce * ES) : -INFINITY;
-            if (!__all_sync(kFull, row_wait(bars, &bars.done[q], ph))) break;
+            if (!warp_wait(bars, &bars.done[q], ph)) break;
             const Stat st = row_stats<ENT>(bars.part[q], ce >= 0, xe, p.L);
             int c = 0;
             if constexpr (GM != 0) {
@@ -241,23 +241,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(const __grid_c
         return;
     }
     Stat st = stat_identity();
-    for (int k = lane; k < p.segs; k += 32) {
-        const float4 v = p.part[r * p.segs + k];
+    const float4* part = p.part + r * p.segs;
+    const uint64_t* cand = p.cand + r * p.segs * p.top_k;
+    TopGate g(p.top_k, -INFINITY);
+    for (int k0 = 0; k0 < p.segs; k0 += 32) {
+        const float4 v = k0 + lane < p.segs ? part[k0 + lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         st = stat_combine(st, Stat{v.x, v.y, v.z}, p.L);
+        // the candidates of 32 segments, top_k places each
+        const int have = __float_as_int(v.w), most = min(32, p.segs - k0) * p.top_k;
+#pragma unroll 4
+        for (int u0 = 0; u0 < most; u0 += 32) {
+            const int u = u0 + lane, seg = u / max(p.top_k, 1);
+            const int here = __shfl_sync(kFull, have, seg & 31);
+            const bool ok = u < most && u - seg * p.top_k < here;
+            const uint64_t key = ok ? cand[(int64_t)k0 * p.top_k + u] : 0;
+            top_room(top, g, 32);
+            const unsigned m = __ballot_sync(kFull, ok);
+            if (ok) top.buf[g.held + __popc(m & ((1u << lane) - 1u))] = key;
+            g.held += __popc(m);
+        }
     }
     st = stat_warp<true>(st, p.L);
-    TopGate g(p.top_k, -INFINITY);
-    if (p.top_k > 0) {
-        for (int k = 0; k < p.segs; ++k) {
-            const int64_t item = r * p.segs + k;
-            const int have = __float_as_int(p.part[item].w);
-            top_room(top, g, have);
-            for (int u = lane; u < have; u += 32) top.buf[g.held + u] = p.cand[item * p.top_k + u];
-            g.held += have;
-        }
-        top_sort(top, g.held);
-        if (g.held > p.top_k) g.held = p.top_k;
-    }
+    top_sort(top, g.held);
+    if (g.held > p.top_k) g.held = p.top_k;
     finish_row<T>(p, r, x, st, top.buf, g.held, given);
 }
 

@@ -298,54 +298,42 @@ struct alignas(16) TopSmem {
     int bins[128];
 };
 
+// Few keys: a key's rank is the number of larger ones (75 keys: half the instructions of
+// a sorting network).
+template <int NK>
+__device__ __forceinline__ void sort_by_rank(TopSmem& s, int c) {
+    const int lane = threadIdx.x & 31;
+    uint64_t k[NK];
+    int r[NK];
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        k[i] = 32 * i + lane < c ? s.buf[32 * i + lane] : 0;
+        r[i] = 0;
+    }
+#pragma unroll 4
+    for (int j = 0; j < c; ++j) {
+        const uint64_t o = s.buf[j];
+#pragma unroll
+        for (int i = 0; i < NK; ++i) r[i] += o > k[i];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+        if (32 * i + lane < c) s.buf[r[i]] = k[i];
+    __syncwarp();
+}
+
 // The first c keys of buf in falling order.  One warp.  Neither unrolled nor inlined, like the
 // searches below: the side warps' code shares the instruction cache with the main loop.
 static __device__ __noinline__ void top_sort(TopSmem& s, int c) {
     const int lane = threadIdx.x & 31;
     __syncwarp();
     if (c <= 1) return;
-    int n = 32;
+    if (c <= 32) return sort_by_rank<1>(s, c);
+    if (c <= 64) return sort_by_rank<2>(s, c);
+    if (c <= 128) return sort_by_rank<4>(s, c);
+    int n = 256;
     while (n < c) n *= 2;
-    if (n <= 128) {
-        // four keys a lane in registers: key i of lane l is the one at 32 i + l
-        uint64_t k[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) k[i] = 32 * i + lane < c ? s.buf[32 * i + lane] : 0;
-#pragma unroll 1
-        for (int size = 2; size <= n; size *= 2) {
-            if (size > 64) {  // step 64: keys 0 and 2, 1 and 3
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint64_t hi = k[i] > k[i + 2] ? k[i] : k[i + 2], lo = k[i] > k[i + 2] ? k[i + 2] : k[i];
-                    k[i] = hi;
-                    k[i + 2] = lo;
-                }
-            }
-            if (size > 32) {  // step 32: keys 0 and 1, 2 and 3
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const bool down = ((32 * i) & size) == 0;
-                    const uint64_t hi = k[i] > k[i + 1] ? k[i] : k[i + 1], lo = k[i] > k[i + 1] ? k[i + 1] : k[i];
-                    k[i] = down ? hi : lo;
-                    k[i + 1] = down ? lo : hi;
-                }
-            }
-#pragma unroll 1
-            for (int step = min(size / 2, 16); step > 0; step /= 2) {
-                const bool low = (lane & step) == 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint64_t o = __shfl_xor_sync(kFull, k[i], step);
-                    const bool down = ((32 * i + lane) & size) == 0;
-                    k[i] = (k[i] > o) == (down == low) ? k[i] : o;
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s.buf[32 * i + lane] = k[i];
-        __syncwarp();
-        return;
-    }
     for (int k = c + lane; k < n; k += 32) s.buf[k] = 0;
     __syncwarp();
 #pragma unroll 1
@@ -502,6 +490,20 @@ __device__ __forceinline__ uint32_t kth_head(TopSmem& s, const uint16_t* heads, 
     for (int k = lane * 8; k < n; k += 256) top = __vmaxu2(top, head_of_eight(heads, k));
     top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
     if (top == 0) return 0;
+    if (K == 1) {
+        many = true;  // the K-th itself
+        return top;
+    }
+    if (n <= 32) {
+        // a head a lane: its bits from the first
+        const uint32_t h = lane < n ? heads[lane] : 0u;
+        uint32_t kth = 0;
+#pragma unroll 1
+        for (uint32_t bit = 0x8000u; bit; bit >>= 1)
+            if (__popc(__ballot_sync(kFull, h >= (kth | bit))) >= K) kth |= bit;
+        many = true;
+        return kth;
+    }
     int fold = n >= 24 * K ? 8 : (n >= 6 * K ? 2 : 1);
     int shift = 1;
 #pragma unroll 1
@@ -700,6 +702,10 @@ __device__ __forceinline__ bool row_wait(RowBars& b, uint64_t* bar, uint32_t ph)
     }
     return false;
 }
+// The same answer in every lane.
+__device__ __forceinline__ bool warp_wait(RowBars& b, uint64_t* bar, uint32_t ph) {
+    return __all_sync(kFull, row_wait(b, bar, ph));
+}
 // A place in the ring or the queue: slot and phase.
 struct Turn {
     int s = 0;
@@ -748,7 +754,7 @@ __device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, con
     for (; nv > 0; nv -= TILE) {
         const uint4* src = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16) + tid;
         typename VT::Max gm[NV];
-        if (!row_wait(b, &b.full[at.s], at.ph)) return false;
+        if (!warp_wait(b, &b.full[at.s], at.ph)) return false;
         stat_tile<T, NV, ENT>(st, src, nv >= TILE ? NV : max(0, min(NV, ((int)nv - tid + kMainThreads - 1) / kMainThreads)),
                               L, gm);
         warp_arrive(&b.empty[at.s]);
