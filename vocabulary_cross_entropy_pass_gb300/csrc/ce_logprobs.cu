@@ -80,22 +80,21 @@ __device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const c
 
 // Shared memory: the ring, and with top_k each side warp's candidates and the groups'
 // maxima of each place of the queue.
-// Vectors of a tile that a thread takes: eight where their maxima are not kept.
-constexpr int scan_vecs(int gm) { return gm ? 4 : 8; }
+constexpr int kTileBytes = kTileVecs * 16;
 constexpr int kPlaces = 4;  // of the queue: a row in the stream, three with the side warps
-constexpr int scan_stages(int gm) { return gm ? 4 : 3; }
-constexpr size_t scan_smem(int gm) {
-    return (size_t)scan_stages(gm) * kMainThreads * scan_vecs(gm) * 16 + (gm ? kSideWarps * sizeof(TopSmem) + kPlaces * kTopHeads * 2 : 0);
+constexpr int scan_stages(bool top) { return top ? 2 : 3; }
+constexpr size_t scan_smem(bool top) {
+    return (size_t)scan_stages(top) * kTileBytes + (top ? kSideWarps * sizeof(TopSmem) + kPlaces * kTopHeads * 2 : 0);
 }
 
-template <typename T, int GM, bool ENT>  // GM: 0 without top_k, else as main_stats
+template <typename T, bool TOP, bool ENT>
 __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_constant__ ScanArgs p) {
     using VT = Vec<T>;
-    constexpr int ES = sizeof(T), STAGES = scan_stages(GM), NV = scan_vecs(GM), TILE = kMainThreads * NV;
+    constexpr int ES = sizeof(T), STAGES = scan_stages(TOP);
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ RowBars bars;
     unsigned char* ring = sm;
-    uint16_t* heads = reinterpret_cast<uint16_t*>(sm + (size_t)STAGES * TILE * 16);  // [kPlaces][kTopHeads]
+    uint16_t* heads = reinterpret_cast<uint16_t*>(sm + (size_t)STAGES * kTileBytes);  // [kPlaces][kTopHeads]
     TopSmem* tops = reinterpret_cast<TopSmem*>(heads + kPlaces * kTopHeads);           // [kSideWarps]
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -114,7 +113,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
             if (row < 0) return;
             if (skip)
                 warp_arrive(&bars.done[q.s]);
-            else if (!main_stats<T, NV, ENT, GM>(bars, at, STAGES, ring, q.s, nv, p.L, heads + q.s * kTopHeads))
+            else if (!main_stats<T, 8, ENT, TOP>(bars, at, STAGES, ring, q.s, nv, p.L, heads + q.s * kTopHeads))
                 return;
             warp_arrive(&bars.free_[q.s]);
         }
@@ -128,14 +127,21 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
         const int64_t items = p.N * p.segs;
         auto row_of = [&](int64_t item) { return p.segs == 1 ? item : item / p.segs; };
         const bool one = p.tokens.n == 1;
-        int64_t y = one && blockIdx.x < items ? p.tokens.at(row_of(blockIdx.x), 0) : 0;  // loaded an item ahead
+        auto token = [&](int64_t item) -> int64_t {
+            return one && item < items ? p.tokens.at(row_of(item), 0) : 0;
+        };
+        const bool late = p.V * ES > STAGES * kTileBytes;
+        int64_t item = blockIdx.x, next = item + gridDim.x;
+        int64_t y = token(item), y1 = token(next);  // loaded an item ahead
         int ends = kSideWarps;  // an end mark for each side warp
-        for (int64_t item = blockIdx.x; ok && ends > 0; item += gridDim.x, q.next(kPlaces)) {
+        for (; ok && ends > 0; q.next(kPlaces)) {
             const bool more = item < items;
             if (!more) --ends;
             const int64_t r = more ? row_of(item) : -1;
+            int64_t after = next + gridDim.x;
+            const bool claims = p.claim && next < items && lane == 0;
+            if (claims && !late) after = 2 * (int64_t)gridDim.x + atomicAdd(p.claim, 1u);
             bool skip = one && y == p.tokens.ignore_idx;
-            if (one && item + gridDim.x < items) y = p.tokens.at(row_of(item + gridDim.x), 0);
             if (more && p.tokens.n > 1) {  // left out when all are ignored
                 bool keep = false;
                 for (int k = lane; k < p.tokens.n; k += 32) keep |= p.tokens.at(r, k) != p.tokens.ignore_idx;
@@ -169,13 +175,19 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
                     }
                     mbar_arrive(&bars.ready[q.s]);
                     if (!skip)
-                        for (int64_t v = v0; ok && v < v1; v += TILE)
-                            ok = ring_put(bars, at, issued, STAGES, ring, TILE * 16, body + v * 16,
-                                          (uint32_t)min((int64_t)TILE, v1 - v) * 16u, policy);
+                        for (int64_t v = v0; ok && v < v1; v += kTileVecs)
+                            ok = ring_put(bars, at, issued, STAGES, ring, kTileBytes, body + v * 16,
+                                          (uint32_t)min((int64_t)kTileVecs, v1 - v) * 16u, policy);
                 }
                 if (!ok) ring_drain(bars, issued, STAGES);
             }
             ok = __shfl_sync(kFull, (int)ok, 0);
+            if (claims && late) after = 2 * (int64_t)gridDim.x + atomicAdd(p.claim, 1u);
+            after = __shfl_sync(kFull, after, 0);
+            item = next;
+            next = after;
+            y = y1;
+            y1 = token(next);
         }
         return;
     }
@@ -200,13 +212,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
             if (!warp_wait(bars, &bars.done[q], ph)) break;
             const Stat st = row_stats<ENT>(bars.part[q], ce >= 0, xe, p.L);
             int c = 0;
-            if constexpr (GM != 0) {
-                constexpr int unit = GM == 1 ? 32 : 8;
-                const int groups = (int)((it.nv + kTileVecs - 1) / kTileVecs) * (kTileVecs / unit);
+            if constexpr (TOP) {
+                const int groups = (int)((it.nv + kTileVecs - 1) / kTileVecs) * kMainThreads;
                 const int64_t col0 = it.h1 + it.v0 * VT::kElems;
-                c = top_select<T, unit>(top, heads + q * kTopHeads, groups,
-                                        reinterpret_cast<const uint4*>(it.x + col0 * ES), it.nv, (uint32_t)col0,
-                                        p.top_k, ce >= 0, ce < it.head, xe, (uint32_t)ce);
+                c = top_select<T>(top, heads + q * kTopHeads, groups,
+                                  reinterpret_cast<const uint4*>(it.x + col0 * ES), it.nv, (uint32_t)col0, p.top_k,
+                                  ce >= 0, xe, (uint32_t)ce);
             }
             if (p.part) {
                 if (lane == 0) p.part[it.item] = make_float4(st.m, st.d, st.s, __int_as_float(c));
@@ -267,10 +278,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(const __grid_c
     finish_row<T>(p, r, x, st, top.buf, g.held, given);
 }
 
-template <typename T, int GM, bool ENT>
+template <typename T, bool TOP, bool ENT>
 cudaError_t launch_scan_t(const ScanArgs& a, cudaStream_t s) {
-    constexpr size_t smem = scan_smem(GM);
-    auto* k = ce_scan_kernel<T, GM, ENT>;
+    constexpr size_t smem = scan_smem(TOP);
+    auto* k = ce_scan_kernel<T, TOP, ENT>;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), smem);
     if (e != cudaSuccess) return e;
     int64_t grid = a.N * a.segs;
@@ -281,9 +292,8 @@ cudaError_t launch_scan_t(const ScanArgs& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_scan_type(const ScanArgs& a, bool entropy, cudaStream_t s) {
-    if (a.top_k > kFewTop) return entropy ? launch_scan_t<T, 2, true>(a, s) : launch_scan_t<T, 2, false>(a, s);
-    if (a.top_k > 0) return entropy ? launch_scan_t<T, 1, true>(a, s) : launch_scan_t<T, 1, false>(a, s);
-    return entropy ? launch_scan_t<T, 0, true>(a, s) : launch_scan_t<T, 0, false>(a, s);
+    if (a.top_k > 0) return entropy ? launch_scan_t<T, true, true>(a, s) : launch_scan_t<T, true, false>(a, s);
+    return entropy ? launch_scan_t<T, false, true>(a, s) : launch_scan_t<T, false, false>(a, s);
 }
 
 template <typename T>
@@ -408,7 +418,8 @@ extern "C" ce_status ce_logprobs_fwd(const void* logits, ce_dtype dtype, int64_t
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // rows in segments: the first kernel starts the error word, the second one adds to it
-    cudaError_t e = a.part ? cudaSuccess : cudaMemsetAsync(a.err, 0, 4, s);
+    a.claim = a.part ? nullptr : reinterpret_cast<uint32_t*>(ws + kWsRowClaimOffset);
+    cudaError_t e = a.part ? cudaSuccess : cudaMemsetAsync(ws, 0, kWsHeaderBytes, s);
     if (e == cudaSuccess) e = launch_scan(a, dtype, entropy || stats, s);
     if (e == cudaSuccess && a.part) {
         if (dtype == CE_F32) e = launch_join<float>(a, s);

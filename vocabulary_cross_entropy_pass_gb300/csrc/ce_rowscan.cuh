@@ -24,16 +24,19 @@
 // them as much again as its tiles did: 16384 rows 210 us.)
 //
 // Selection of the K largest, ties to the lowest column: a candidate is the key
-// (value, ~column), so keys differ and their order is the answer's.  The main warps
-// leave the maximum of each group of 32 vectors (K over 64: of 8) of the row; T, the
-// K-th largest of them, is a value that K logits at least are not below, so only the
-// groups that reach it are read again, from L2, and of random logits 1.1 K to 1.4 K are
-// candidates.  Short rows have too few groups: their vectors' maxima are taken first.
-// Groups are read in the order of their columns, and where the buffer of candidates has
-// no room it is sorted and cut to K; once K are held only what is above T counts:
-// equal or ordered logits cost time, not exactness.  A row's selection is one warp's
-// work, without barriers, and three rows' go on at a time (four warps at one row's, with a
-// barrier for each step: 17 us a row of 128000 columns, K = 64, beside the stream).
+// (value, ~column), so keys differ and their order is the answer's.  Each main thread
+// leaves the maximum of its vectors of a tile, eight neighbours (a line of 128 bytes), which
+// the statistics want anyway (over eight threads' vectors, by shuffles, it cost half as
+// much again as the statistics).
+// T, the K-th largest of these, is a value that K logits at least are not below, so only
+// the groups that reach it are read again, from L2, and of random logits 1.1 K to 1.4 K
+// are candidates.  Short rows have too few groups: their vectors' maxima are taken first.
+// Where the buffer of candidates has no room it is sorted and cut to K, and what comes
+// later has to be above the K-th key; where equal logits abound (a mask) only groups
+// above T are read, and the equals in order from the row's start.  So any row is exact.
+// A row's selection is one warp's work, without barriers, and three rows' go on at a time
+// (four warps at one row's, with a barrier for each step: 17 us a row of 128000 columns,
+// K = 64, beside the stream).
 #pragma once
 
 #include "ce_device.cuh"
@@ -142,44 +145,38 @@ __device__ __forceinline__ void stat_vector(uint4 raw, float ref, float add, flo
     }
 }
 
-__device__ __forceinline__ float max_of(float a, float b) { return fmaxf(a, b); }
-__device__ __forceinline__ __nv_bfloat162 max_of(__nv_bfloat162 a, __nv_bfloat162 b) { return __hmax2(a, b); }
-__device__ __forceinline__ __half2 max_of(__half2 a, __half2 b) { return __hmax2(a, b); }
-template <typename M>
-__device__ __forceinline__ M max_from(M own, int lanes) {  // the maximum of the lane that is `lanes` away
-    static_assert(sizeof(M) == 4, "a register");
-    const uint32_t o = __shfl_xor_sync(kFull, *reinterpret_cast<const uint32_t*>(&own), lanes);
-    return *reinterpret_cast<const M*>(&o);
-}
-
-// A thread's vectors of a tile: src[0], src[kMainThreads], ..., n of them.  ENT: s as well.
-// gm: each vector's maximum, packed (-inf where there is none).
 template <typename T>
 __device__ __forceinline__ uint4 all_low() {  // a vector of -inf, which counts for nothing
     const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
     return make_uint4(w, w, w, w);
 }
+// A thread's vectors of a tile: NV neighbours, n of them there.  It takes them in an order of
+// its own (`turn`), so eight threads next to each other meet in no bank of shared memory.
+template <int NV>
+__device__ __forceinline__ int tile_turn() {
+    return NV == 8 ? threadIdx.x & 7 : (threadIdx.x >> 1) & 3;
+}
+// ENT: s as well.  Returns their maximum.
 template <typename T, int NV, bool ENT>
-__device__ __forceinline__ void stat_tile(Stat& a, const uint4* src, int n, float L,
-                                          typename Vec<T>::Max (&gm)[NV]) {
+__device__ __forceinline__ float stat_tile(Stat& a, const uint4* tile, int nv, float L) {
     using VT = Vec<T>;
+    static_assert(NV == 8 || NV == 4, "the orders");
+    const uint4* src = tile + threadIdx.x * NV;
+    const int turn = tile_turn<NV>(), n = min(NV, nv - (int)threadIdx.x * NV);
     uint4 raw[NV];
     if (n == NV) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) raw[i] = src[i * kMainThreads];
+        for (int i = 0; i < NV; ++i) raw[i] = src[i ^ turn];
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             raw[i] = all_low<T>();
-            if (i < n) raw[i] = src[i * kMainThreads];
+            if ((i ^ turn) < n) raw[i] = src[i ^ turn];
         }
     }
     typename VT::Max tm = VT::max_init();
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        gm[i] = VT::max_acc(VT::max_init(), raw[i]);
-        tm = max_of(tm, gm[i]);
-    }
+    for (int i = 0; i < NV; ++i) tm = VT::max_acc(tm, raw[i]);
     const float top = VT::max_done(tm);
     if (top > a.m) {
         const float y = stat_shift(a.m, top, L), f = ex2_approx(y);
@@ -201,10 +198,11 @@ __device__ __forceinline__ void stat_tile(Stat& a, const uint4* src, int n, floa
         d2 = s2 = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int i = 0; i < n; ++i)
-            stat_vector<T, ENT, true>(src[i * kMainThreads], far ? 0.f : ref, far ? -a.m : 0.f, 0.f, L, d2, s2);
+            stat_vector<T, ENT, true>(src[i], far ? 0.f : ref, far ? -a.m : 0.f, 0.f, L, d2, s2);
     }
     a.d += d2.x + d2.y;
     if (ENT) a.s += s2.x + s2.y;
+    return top;
 }
 
 // ----------------------------------------------------------------- side warps
@@ -277,7 +275,7 @@ struct Head<__nv_bfloat16> {
     static constexpr uint32_t lowest = 0x007fu;
     static constexpr bool exact = true;
     __device__ __forceinline__ static uint32_t of(float x) { return Head<float>::of(x); }
-    __device__ __forceinline__ static float value(uint32_t h) { return key_value((uint64_t)h << 48); }
+    __device__ __forceinline__ static float value(uint32_t h) { return __uint_as_float((h & 0x8000u ? h & 0x7fffu : ~h & 0xffffu) << 16); }
 };
 template <>
 struct Head<__half> {
@@ -354,33 +352,28 @@ static __device__ __noinline__ void top_sort(TopSmem& s, int c) {
     }
 }
 
-// What a selection lets in, the same in every lane.
+// What a selection lets in, the same in every lane: logits above T, and those equal to it of
+// columns below C.
 struct TopGate {
     int K;
     int held;      // candidates
-    float T;       // under it no logit can be among the K largest
-    bool strict;   // K candidates not below T are held, of columns before: only what is above T counts
-    float floor;   // what is let in is not below this: T, or the next value above it
+    float T;
+    uint32_t C;
 
-    __device__ __forceinline__ TopGate(int K, float T) : K(K), held(0), T(T), strict(false), floor(T) {}
+    __device__ __forceinline__ TopGate(int K, float T) : K(K), held(0), T(T), C(0xffffffffu) {}
+    __device__ __forceinline__ bool takes(float x, uint32_t col) const { return x > T || (x == T && col < C); }
 };
 
 // Room for `more` candidates: where there is none, what is held is sorted and cut to K.
 __device__ __forceinline__ void top_room(TopSmem& s, TopGate& g, int more) {
-    if (g.held + more > kTopCap) {
-        top_sort(s, g.held);
-        if (g.held >= g.K) {
-            g.held = g.K;
-            g.T = key_value(s.buf[g.K - 1]);
-            g.strict = false;
-        }
-        __syncwarp();
+    if (g.held + more <= kTopCap) return;
+    top_sort(s, g.held);
+    if (g.held >= g.K) {
+        g.held = g.K;
+        g.T = key_value(s.buf[g.K - 1]);
+        g.C = key_column(s.buf[g.K - 1]);
     }
-    if (!g.strict && g.held >= g.K) {
-        g.strict = true;
-        const int b = __float_as_int(g.T + 0.f);  // above +inf: a NaN, that nothing reaches
-        g.floor = __int_as_float(b >= 0 ? b + 1 : b - 1);
-    }
+    __syncwarp();
 }
 
 // The k-th logit of a vector.
@@ -397,33 +390,38 @@ __device__ __forceinline__ float pick(const uint4& r, int k) {
     }
 }
 // The logits of each lane's vector (have: it has one) that the gate lets in; col: the
-// column of its first.
+// column of its first.  equal: those equal to T alone.
 template <typename T>
-__device__ __forceinline__ void top_push(TopSmem& s, TopGate& g, bool have, const uint4& raw, uint32_t col) {
+__device__ __forceinline__ void top_push(TopSmem& s, TopGate& g, bool have, const uint4& raw, uint32_t col,
+                                         bool equal = false) {
     using VT = Vec<T>;
     constexpr int VEC = VT::kElems;
     const int lane = threadIdx.x & 31;
     unsigned ok = 0;
-    if (__any_sync(kFull, have && VT::vmax(raw) >= g.floor)) {
+    if (__any_sync(kFull, have && VT::vmax(raw) >= g.T)) {
         float x[VEC];
         VT::unpack(raw, x);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) ok |= x[k] >= g.floor ? 1u << k : 0u;
+        for (int k = 0; k < VEC; ++k) ok |= x[k] >= g.T && !(equal && x[k] > g.T) ? 1u << k : 0u;
         if (!have) ok = 0;
     }
-    for (;;) {
-        const unsigned m = __ballot_sync(kFull, ok != 0u);
-        if (m == 0u) return;
+    while (__any_sync(kFull, ok != 0u)) {
+        bool in = false;
+        uint64_t key = 0;
         if (ok) {
             const int k = __ffs(ok) - 1;
-            s.buf[g.held + __popc(m & ((1u << lane) - 1u))] = top_key(pick<T>(raw, k), col + (uint32_t)k);
+            const float x = pick<T>(raw, k);
+            key = top_key(x, col + (uint32_t)k);
+            in = g.takes(x, col + (uint32_t)k);
             ok &= ok - 1u;
         }
+        const unsigned m = __ballot_sync(kFull, in);
+        if (in) s.buf[g.held + __popc(m & ((1u << lane) - 1u))] = key;
         g.held += __popc(m);
     }
 }
 __device__ __forceinline__ void top_push_one(TopSmem& s, TopGate& g, bool ok, float x, uint32_t col) {
-    const unsigned m = __ballot_sync(kFull, ok && x >= g.floor);
+    const unsigned m = __ballot_sync(kFull, ok && g.takes(x, col));
     const int lane = threadIdx.x & 31;
     if ((m >> lane) & 1u) s.buf[g.held + __popc(m & ((1u << lane) - 1u))] = top_key(x, col);
     g.held += __popc(m);
@@ -531,10 +529,20 @@ __device__ __forceinline__ uint32_t kth_head(TopSmem& s, const uint16_t* heads, 
     }
 }
 
-// The heads that reach `least` (1 at least), listed in place by their numbers, in order: the
-// list never reaches a head that has not been looked at.  Of those equal to `least` the
-// first `ties`.  How many there are.
-__device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t least, int ties) {
+// How many heads reach `least`, 1 at least.
+__device__ __forceinline__ int count_heads(const uint16_t* heads, int n, uint32_t least) {
+    const uint32_t two = least | (least << 16);
+    uint32_t sum = 0;
+    for (int k = (threadIdx.x & 31) * 8; k < n; k += 256) {
+        const uint4 u = *reinterpret_cast<const uint4*>(heads + k);
+        sum += __vsetgeu2(u.x, two) + __vsetgeu2(u.y, two) + __vsetgeu2(u.z, two) + __vsetgeu2(u.w, two);
+    }
+    return __reduce_add_sync(kFull, (sum & 0xffffu) + (sum >> 16));
+}
+
+// The heads that reach `least` (1 at least), listed in place by their numbers: the list never
+// reaches a head that has not been looked at.  How many there are.
+__device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t least) {
     const int lane = threadIdx.x & 31;
     if (least == 0) least = 1;
     int listed = 0;
@@ -543,32 +551,20 @@ __device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t least
         uint4 u = make_uint4(0, 0, 0, 0);
         if (k < n) u = *reinterpret_cast<const uint4*>(heads + k);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        unsigned ok = 0, tie = 0;
+        unsigned ok = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             ok |= (w[i] & 0xffffu) >= least ? 1u << (2 * i) : 0u;
             ok |= (w[i] >> 16) >= least ? 2u << (2 * i) : 0u;
-            tie |= (w[i] & 0xffffu) == least ? 1u << (2 * i) : 0u;
-            tie |= (w[i] >> 16) == least ? 2u << (2 * i) : 0u;
         }
         if (!__any_sync(kFull, ok != 0u)) continue;
-        auto upto = [&](int v) {
+        const int own = __popc(ok);
+        int sum = own;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int b = __shfl_up_sync(kFull, v, o);
-                if (lane >= o) v += b;
-            }
-            return v;
-        };
-        if (ties != 0x7fffffff) {
-            const int own = __popc(tie), sum = upto(own);
-            int room = ties - (sum - own);  // of this lane's
-            ties = max(0, ties - __shfl_sync(kFull, sum, 31));
-            unsigned drop = tie;
-            for (; drop && room > 0; --room) drop &= drop - 1u;
-            ok &= ~drop;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int b = __shfl_up_sync(kFull, sum, o);
+            if (lane >= o) sum += b;
         }
-        const int own = __popc(ok), sum = upto(own);
         const int all = __shfl_sync(kFull, sum, 31);
         int at = listed + sum - own;
         for (; ok; ok &= ok - 1u) heads[at++] = (uint16_t)(k + __ffs(ok) - 1);
@@ -579,21 +575,35 @@ __device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t least
     return listed;
 }
 
-// The listed groups' vectors (2^wide of each), 32 at a time and the next ones on their way.
+// The listed groups' vectors, 32 at a time and the next ones on their way.  wide: a group is
+// eight vectors (four from vector `halves` on), else one.  equal: every vector from the
+// first on, for logits equal to T alone, until `equal` of them are held (or K and all after
+// them come behind those).
 template <typename T>
-__device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t* list, int listed, int wide,
-                                         const uint4* body, int64_t nv, uint32_t col0) {
+__device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t* list, int listed, bool wide,
+                                         const uint4* body, int64_t nv, uint32_t col0, int equal) {
     constexpr int VEC = Vec<T>::kElems, AHEAD = 4;
-    const int lane = threadIdx.x & 31, per = 32 >> wide;
+    static_assert(kTileVecs == 8 * kMainThreads, "eight vectors of a tile a thread");
+    const int lane = threadIdx.x & 31, per = wide ? 4 : 32, had = g.held;
     const int last = nv < 0x7fffffff ? (int)nv : 0x7fffffff;
+    const int halves = last - 1 - (last - 1) % kTileVecs + ((last - 1) % kTileVecs < kTileVecs / 2 ? 0 : kTileVecs);
+    if (equal) listed = last;
     uint4 raw[AHEAD];
     int v[AHEAD];  // the vector, or -1
     auto fetch = [&](int b, uint4& to, int& vec) {
-        const int e = b + (lane >> wide);
+        const int e = b + (wide ? lane >> 3 : lane);
         vec = -1;
         if (e < listed) {
-            const int at = ((int)list[e] << wide) + (lane & ((1 << wide) - 1));
-            if (at < last) {
+            int at = equal ? e : (int)list[e];
+            bool there = true;
+            if (wide) {
+                at = at * 8 + (lane & 7);
+                if (at >= halves) {
+                    there = (lane & 4) == 0;
+                    at = halves + (at - halves) / 8 * 4 + (lane & 3);
+                }
+            }
+            if (there && at < last) {
                 vec = at;
                 to = __ldg(body + at);
             }
@@ -612,18 +622,18 @@ __device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t*
         }
         fetch(b + AHEAD * per, raw[AHEAD - 1], v[AHEAD - 1]);
         top_room(s, g, 32 * VEC);
-        top_push<T>(s, g, vec >= 0, now, col0 + (uint32_t)(vec * VEC));
+        if (equal && (g.held >= had + equal || g.C != 0xffffffffu)) break;
+        top_push<T>(s, g, vec >= 0, now, col0 + (uint32_t)(vec * VEC), equal != 0);
     }
 }
 
 // The K largest of a row's (segment's) logits into the front of s.buf, in falling order;
 // returns how many there are.  One warp.  body: its nv vectors in global memory, their
 // first logit of column col0; heads: the groups' maxima, G of them (zeros up to a multiple
-// of eight), UNIT vectors each, overwritten.  xe, ce: the lane's element around the body
-// (before: it lies before the body), where has_edge.
-template <typename T, int UNIT>
+// of eight), overwritten.  xe, ce: the lane's element around the body, where has_edge.
+template <typename T>
 __device__ __forceinline__ int top_select(TopSmem& s, uint16_t* heads, int G, const uint4* body, int64_t nv,
-                                          uint32_t col0, int K, bool has_edge, bool before, float xe, uint32_t ce) {
+                                          uint32_t col0, int K, bool has_edge, float xe, uint32_t ce) {
     using VT = Vec<T>;
     const int lane = threadIdx.x & 31;
     const bool brief = G < 2 * K && nv <= kTopHeads;  // too few groups: each vector is one
@@ -635,15 +645,19 @@ __device__ __forceinline__ int top_select(TopSmem& s, uint16_t* heads, int G, co
     }
     bool many;
     const uint32_t kth = kth_head(s, heads, G, K, many);
-    // where the head says the value, K groups of the K-th are enough of its equals
-    const bool exact = many && (Head<T>::exact || kth <= Head<T>::lowest);
-    const int listed = list_heads(heads, G, kth, exact ? K : 0x7fffffff);
-    TopGate g(K, kth <= Head<T>::lowest ? -INFINITY : Head<T>::value(kth));
-    top_push_one(s, g, has_edge && before, xe, ce);
-    constexpr int WIDE = UNIT == 32 ? 5 : 3;
-    top_take<T>(s, g, heads, listed, brief ? 0 : WIDE, body, nv, col0);
-    top_room(s, g, 32);
-    top_push_one(s, g, has_edge && !before, xe, ce);
+    // Where the head says the value and many groups reach it, its equals are not all read.
+    const bool exact = many && (Head<T>::exact || kth <= Head<T>::lowest) && count_heads(heads, G, kth) > 2 * K + 32;
+    const int listed = list_heads(heads, G, exact ? kth + 1 : kth);
+    const float T0 = kth <= Head<T>::lowest ? -INFINITY : Head<T>::value(kth);
+    TopGate g(K, T0);
+    top_push_one(s, g, has_edge, xe, ce);
+    if (exact) g.C = 0;  // first what is above T
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+        top_take<T>(s, g, heads, listed, !brief && pass == 0, body, nv, col0, pass ? K : 0);
+        if (pass || !exact || g.T != T0) break;  // (T has risen where K are above T0)
+        g.C = 0xffffffffu;
+    }
     top_sort(s, g.held);
     return g.held < K ? g.held : K;
 }
@@ -743,47 +757,27 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 }
 
 // First pass over a row's tiles by the main warps: the warp's statistics go to part, and
-// (GM: 1 a group of 32 vectors, 2 of 8) the groups' maxima to heads.
-template <typename T, int NV, bool ENT, int GM>
+// with GM the maximum of each thread's vectors of a tile to heads: eight neighbours, or four
+// in a last tile that is half full or less.
+template <typename T, int NV, bool ENT, bool GM>
 __device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, const unsigned char* ring, int q,
                                            int64_t nv, float L, uint16_t* heads) {
-    using VT = Vec<T>;
     constexpr int TILE = kMainThreads * NV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Stat st = stat_identity();
     for (; nv > 0; nv -= TILE) {
-        const uint4* src = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16) + tid;
-        typename VT::Max gm[NV];
+        const uint4* tile = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16);
         if (!warp_wait(b, &b.full[at.s], at.ph)) return false;
-        stat_tile<T, NV, ENT>(st, src, nv >= TILE ? NV : max(0, min(NV, ((int)nv - tid + kMainThreads - 1) / kMainThreads)),
-                              L, gm);
+        const int left = nv < TILE ? (int)nv : TILE;
+        const bool half = NV == 8 && left <= TILE / 2;  // half the work
+        const float top =
+            half ? stat_tile<T, 4, ENT>(st, tile, left, L) : stat_tile<T, NV, ENT>(st, tile, left, L);
+        if constexpr (GM) {
+            heads[tid] = (uint16_t)(tid * (half ? 4 : NV) < left ? Head<T>::of(top) : 0u);  // 0: no vector
+            heads += kMainThreads;
+        }
         warp_arrive(&b.empty[at.s]);
         at.next(stages);
-        if constexpr (GM == 1) {
-            // lane i keeps group i's; 0 where the group has no vector
-            float own = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const float m = warp_max_redux(VT::max_done(gm[i]));
-                if (lane == i) own = m;
-            }
-            if (lane < NV)
-                heads[lane * (kMainThreads / 32) + warp] =
-                    (uint16_t)(lane * kMainThreads + warp * 32 < nv ? Head<T>::of(own) : 0u);
-            heads += TILE / 32;
-        } else if constexpr (GM == 2) {
-            // over eight lanes, of four vectors at once: each step sends what the other lane goes on
-            // with, so lane l ends with vector l % 4
-            static_assert(NV == 4, "two steps halve four vectors");
-            const bool odd = lane & 1, two = lane & 2;
-            typename VT::Max u = max_of(odd ? gm[1] : gm[0], max_from(odd ? gm[0] : gm[1], 1));
-            typename VT::Max w = max_of(odd ? gm[3] : gm[2], max_from(odd ? gm[2] : gm[3], 1));
-            u = max_of(two ? w : u, max_from(two ? u : w, 2));
-            u = max_of(u, max_from(u, 4));
-            const int first = (lane & 3) * kMainThreads + (tid & ~7);
-            if ((lane & 4) == 0) heads[first / 8] = (uint16_t)(first < nv ? Head<T>::of(VT::max_done(u)) : 0u);
-            heads += TILE / 8;
-        }
     }
     st = stat_warp<ENT>(st, L);
     if (lane == 0) b.part[q][warp] = make_float4(st.m, st.d, st.s, 0.f);

@@ -24,6 +24,7 @@ struct ScanArgs {
     int64_t* top_tokens;   // [N][top_k]
     float* top_logprobs;
     float4* stats;         // [N] {m, log d, entropy, 0}
+    uint32_t* claim;       // rows taken beyond each CTA's first two, or NULL: every gridDim.x-th item
     uint32_t* err;
 };
 // The gradient p_j (a + b lp_j) of every row, and what its listed tokens get.

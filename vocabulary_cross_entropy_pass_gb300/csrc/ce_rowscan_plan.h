@@ -11,11 +11,10 @@ constexpr int kMainThreads = 256;                            // threads that rea
 constexpr int kSideWarps = 3;                                // warps beside them
 constexpr int kSideThreads = 32 * kSideWarps;
 constexpr int kRowThreads = kMainThreads + 32 + kSideThreads;  // and the copying warp
-constexpr int kTileVecs = kMainThreads * 4;                  // 16-byte vectors of a tile: 16 KB
+constexpr int kTileVecs = kMainThreads * 8;                  // 16-byte vectors of a tile: 32 KB
 constexpr int kTopCap = 1024;                                // candidates held at a time
 constexpr int kTopHeads = 2048;                              // groups' maxima of a row or segment
 constexpr int kMaxTop = 256;                                 // likeliest tokens a call may ask for
-constexpr int kFewTop = 8;                                   // up to here groups of 32 vectors, else of 8
 constexpr int kMaxListed = 1024;                             // given or teacher's tokens of a row
 constexpr int kMaxSegments = 1024;
 constexpr int64_t kSMs = 152;
@@ -27,23 +26,23 @@ struct ScanPlan {
 };
 
 // Rows are cut where that ends sooner: the rounds of kScanSlots CTAs times a segment's
-// tiles and what it costs beside them (seven tenths of a tile's time), and two tiles' time
+// tiles and what it costs beside them (four tenths of a tile's time), and one tile's time
 // for putting segments together.  A segment's groups' maxima have to have room; segs is 0
 // where they have none.
 inline ScanPlan plan_scan(int64_t N, int64_t V, int es, int top_k) {
     const int64_t nv = V * es / 16;
-    const int64_t tiles = (nv + kTileVecs - 1) / kTileVecs;
+    const int64_t parts = nv / (kTileVecs / 2);  // of 16 KB at least
     int64_t segs = 1;
     double least = 0;
-    for (int64_t s = 1; s <= 64 && s <= (tiles > 1 ? tiles : 1) && N > 0 && N < 64 * kScanSlots; ++s) {
+    for (int64_t s = 1; s <= 64 && s <= (parts > 1 ? parts : 1) && N > 0 && N < 64 * kScanSlots; ++s) {
         const double rounds = (double)((N * s + kScanSlots - 1) / kScanSlots);
-        const double time = rounds * ((double)tiles / s + 0.7) + (s > 1 ? 2 : 0);
+        const double time = rounds * ((double)nv / kTileVecs / s + 0.4) + (s > 1 ? 1 : 0);
         if (s == 1 || time < least) {
             least = time;
             segs = s;
         }
     }
-    const int64_t room = top_k <= 0 ? nv : (int64_t)kTopHeads * (top_k <= kFewTop ? 32 : 8);
+    const int64_t room = top_k <= 0 ? nv : (int64_t)(kTopHeads / kMainThreads) * kTileVecs;
     if (nv > segs * room) segs = (nv + room - 1) / room;
     ScanPlan p;
     p.per = (nv + segs - 1) / segs;
