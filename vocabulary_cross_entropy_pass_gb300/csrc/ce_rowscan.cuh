@@ -150,15 +150,26 @@ __device__ __forceinline__ uint4 all_low() {  // a vector of -inf, which counts 
     const uint32_t w = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
     return make_uint4(w, w, w, w);
 }
+// A warp is done with something: lane 0 arrives for all.  A ring's slot is handed back
+// once its values have been used, not behind the loads: where the warp's global stores
+// were backed up, the loads waited behind them and the arrival did not, and the next tile
+// landed first (in one of 100 launches of 1219 rows of 20011 float32 columns).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // A thread's vectors of a tile: NV neighbours, n of them there.  It takes them in an order of
 // its own (`turn`), so eight threads next to each other meet in no bank of shared memory.
 template <int NV>
 __device__ __forceinline__ int tile_turn() {
     return NV == 8 ? threadIdx.x & 7 : (threadIdx.x >> 1) & 3;
 }
-// ENT: s as well.  Returns their maximum.
+// ENT: s as well.  Returns their maximum.  The tile is handed back (empty) when every
+// lane's maximum is known, so all have their values, and the sums go on in registers: with two
+// slots both are in flight most of the time.
 template <typename T, int NV, bool ENT>
-__device__ __forceinline__ float stat_tile(Stat& a, const uint4* tile, int nv, float L) {
+__device__ __forceinline__ float stat_tile(Stat& a, const uint4* tile, int nv, float L, uint64_t* empty) {
     using VT = Vec<T>;
     static_assert(NV == 8 || NV == 4, "the orders");
     const uint4* src = tile + threadIdx.x * NV;
@@ -184,22 +195,26 @@ __device__ __forceinline__ float stat_tile(Stat& a, const uint4* tile, int nv, f
         a.d *= f;
         a.m = top;
     }
-    float2 d2 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
     const float ref = a.m == -INFINITY ? 0.f : -stat_ref(a.m, L);
     // 2^y is 0 from 150 down; the distance leaves room for the rounding to 16 bits (2^-9 of
     // the maximum).  Without a maximum 2^y is 0 for any logit there is.
     const float top_or_low = a.m == -INFINITY ? kFarBelow : a.m;
     const float least = ENT ? top_or_low - fmaxf(200.f / L, fabsf(top_or_low) * 0.015625f) : 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) stat_vector<T, ENT, false>(raw[i], ref, 0.f, least, L, d2, s2);
     // rarely met: a row at the type's lowest value (of float16, where `least` is none of its)
     const bool far = !(fabsf(ref) < kRefMost);
-    if (far || (ENT && std::is_same<T, __half>::value && least < -65504.f)) {
+    const bool slow = far || (ENT && std::is_same<T, __half>::value && least < -65504.f);
+    const bool again = __any_sync(kFull, slow);
+    if (!again) warp_arrive(empty);
+    float2 d2 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) stat_vector<T, ENT, false>(raw[i], ref, 0.f, least, L, d2, s2);
+    if (slow) {
         d2 = s2 = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int i = 0; i < n; ++i)
             stat_vector<T, ENT, true>(src[i], far ? 0.f : ref, far ? -a.m : 0.f, 0.f, L, d2, s2);
     }
+    if (again) warp_arrive(empty);
     a.d += d2.x + d2.y;
     if (ENT) a.s += s2.x + s2.y;
     return top;
@@ -747,15 +762,6 @@ __device__ __forceinline__ void ring_drain(RowBars& b, uint32_t issued, int stag
         if (issued > (uint32_t)s)
             (void)mbar_wait_bounded(&b.full[s], ((issued - 1u - (uint32_t)s) / (uint32_t)stages) & 1u);
 }
-// A warp is done with something: lane 0 arrives for all.  A ring's slot is handed back
-// once its values have been used, not behind the loads: where the warp's global stores
-// were backed up, the loads waited behind them and the arrival did not, and the next tile
-// landed first (in one of 100 launches of 1219 rows of 20011 float32 columns).
-__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
 // First pass over a row's tiles by the main warps: the warp's statistics go to part, and
 // with GM the maximum of each thread's vectors of a tile to heads: eight neighbours, or four
 // in a last tile that is half full or less.
@@ -771,12 +777,12 @@ __device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, con
         const int left = nv < TILE ? (int)nv : TILE;
         const bool half = NV == 8 && left <= TILE / 2;  // half the work
         const float top =
-            half ? stat_tile<T, 4, ENT>(st, tile, left, L) : stat_tile<T, NV, ENT>(st, tile, left, L);
+            half ? stat_tile<T, 4, ENT>(st, tile, left, L, &b.empty[at.s])
+                 : stat_tile<T, NV, ENT>(st, tile, left, L, &b.empty[at.s]);
         if constexpr (GM) {
             heads[tid] = (uint16_t)(tid * (half ? 4 : NV) < left ? Head<T>::of(top) : 0u);  // 0: no vector
             heads += kMainThreads;
         }
-        warp_arrive(&b.empty[at.s]);
         at.next(stages);
     }
     st = stat_warp<ENT>(st, L);
