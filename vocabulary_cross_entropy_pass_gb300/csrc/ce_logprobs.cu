@@ -41,10 +41,16 @@ struct Given {
     }
 };
 
-// A row's outputs from its statistics and its candidates in falling order (c of them).
+// What is subtracted of a logit to give its log-probability; log d is +inf where nothing is
+// allowed: every log-probability is -inf then.
+struct RowNorm {
+    float m, logd;
+};
+
+// A row's outputs from its statistics, but for its likeliest tokens.
 template <typename T>
-__device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const char* x, const Stat& t,
-                                           const uint64_t* top, int c, Given<T> given) {
+__device__ __forceinline__ RowNorm finish_row(const ScanArgs& p, int64_t r, const char* x, const Stat& t,
+                                              Given<T> given) {
     const int lane = threadIdx.x & 31;
     const bool none = stat_none(t.m, t.d);
     const float logd = none ? 0.f : stat_logd(t, p.L);
@@ -66,12 +72,17 @@ __device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const c
         }
         p.logprobs[r * p.tokens.n + k] = lp;
     }
-    for (int k = lane; k < p.top_k; k += 32) {
+    return none ? RowNorm{0.f, INFINITY} : RowNorm{t.m, logd};
+}
+
+// The likeliest tokens from the candidates in falling order (c of them).
+__device__ __forceinline__ void finish_top(const ScanArgs& p, int64_t r, RowNorm n, const uint64_t* top, int c) {
+    for (int k = threadIdx.x & 31; k < p.top_k; k += 32) {
         int64_t token = -1;  // NaN is no alternative: a row of fewer than K others ends so
         float lp = NAN;
         if (k < c) {
             token = key_column(top[k]);
-            lp = none ? -INFINITY : (key_value(top[k]) - t.m) - logd;
+            lp = (key_value(top[k]) - n.m) - n.logd;
         }
         p.top_tokens[r * p.top_k + k] = token;
         p.top_logprobs[r * p.top_k + k] = lp;
@@ -81,10 +92,9 @@ __device__ __forceinline__ void finish_row(const ScanArgs& p, int64_t r, const c
 // Shared memory: the ring, and with top_k each side warp's candidates and the groups'
 // maxima of each place of the queue.
 constexpr int kTileBytes = kTileVecs * 16;
-constexpr int kPlaces = 4;  // of the queue: a row in the stream, three with the side warps
 constexpr int scan_stages(bool top) { return top ? 2 : 3; }
 constexpr size_t scan_smem(bool top) {
-    return (size_t)scan_stages(top) * kTileBytes + (top ? kSideWarps * sizeof(TopSmem) + kPlaces * kTopHeads * 2 : 0);
+    return (size_t)scan_stages(top) * kTileBytes + (top ? kSideWarps * sizeof(TopSmem) + kHeadsRoom * 2 : 0);
 }
 
 template <typename T, bool TOP, bool ENT>
@@ -94,8 +104,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ RowBars bars;
     unsigned char* ring = sm;
-    uint16_t* heads = reinterpret_cast<uint16_t*>(sm + (size_t)STAGES * kTileBytes);  // [kPlaces][kTopHeads]
-    TopSmem* tops = reinterpret_cast<TopSmem*>(heads + kPlaces * kTopHeads);           // [kSideWarps]
+    uint16_t* heads = reinterpret_cast<uint16_t*>(sm + (size_t)STAGES * kTileBytes);  // [p.places][p.heads]
+    TopSmem* tops = reinterpret_cast<TopSmem*>(heads + kHeadsRoom);  // [kSideWarps]
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         row_bars_init(bars);
@@ -106,14 +116,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
 
     if (threadIdx.x < kMainThreads) {
         Turn at, q;
-        for (;; q.next(kPlaces)) {
+        for (;; q.next(p.places)) {
             if (!warp_wait(bars, &bars.ready[q.s], q.ph)) return;
             const int64_t row = bars.item[q.s].row, nv = bars.item[q.s].nv;
             const int skip = bars.item[q.s].skip;
             if (row < 0) return;
             if (skip)
                 warp_arrive(&bars.done[q.s]);
-            else if (!main_stats<T, 8, ENT, TOP>(bars, at, STAGES, ring, q.s, nv, p.L, heads + q.s * kTopHeads))
+            else if (!main_stats<T, 8, ENT, TOP>(bars, at, STAGES, ring, q.s, nv, p.L, heads + q.s * p.heads))
                 return;
             warp_arrive(&bars.free_[q.s]);
         }
@@ -134,7 +144,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
         int64_t item = blockIdx.x, next = item + gridDim.x;
         int64_t y = token(item), y1 = token(next);  // loaded an item ahead
         int ends = kSideWarps;  // an end mark for each side warp
-        for (; ok && ends > 0; q.next(kPlaces)) {
+        for (; ok && ends > 0; q.next(p.places)) {
             const bool more = item < items;
             if (!more) --ends;
             const int64_t r = more ? row_of(item) : -1;
@@ -195,11 +205,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
     // a side warp takes every kSideWarps-th item
     const int side = (threadIdx.x - kMainThreads - 32) >> 5;
     TopSmem& top = tops[side];
-    for (uint32_t turn = side;; turn += kSideWarps) {
-        const int q = (int)(turn % kPlaces);
-        const uint32_t ph = (turn / kPlaces) & 1u;
-        if (!warp_wait(bars, &bars.ready[q], ph)) break;
-        const RowItem& it = bars.item[q];
+    Turn q;
+    for (int k = 0; k < side; ++k) q.next(p.places);
+    for (;;) {
+        if (!warp_wait(bars, &bars.ready[q.s], q.ph)) break;
+        const RowItem& it = bars.item[q.s];
         const int64_t r = it.row;
         if (r < 0) break;
         if (it.skip) {
@@ -209,24 +219,29 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
             if (!p.part) given.load(p, r, it.x, lane);
             const int64_t ce = edge_column(it);
             const float xe = ce >= 0 ? VT::load1(it.x + ce * ES) : -INFINITY;
-            if (!warp_wait(bars, &bars.done[q], ph)) break;
-            const Stat st = row_stats<ENT>(bars.part[q], ce >= 0, xe, p.L);
-            int c = 0;
+            if (!warp_wait(bars, &bars.done[q.s], q.ph)) break;
+            const Stat st = row_stats<ENT>(bars.part[q.s], ce >= 0, xe, p.L);
+            RowNorm norm = {};
+            if (!p.part)
+                norm = finish_row<T>(p, r, it.x, st, given);
+            else if (lane == 0)
+                p.part[it.item] = make_float4(st.m, st.d, st.s, 0.f);
             if constexpr (TOP) {
                 const int groups = (int)((it.nv + kTileVecs - 1) / kTileVecs) * kMainThreads;
                 const int64_t col0 = it.h1 + it.v0 * VT::kElems;
-                c = top_select<T>(top, heads + q * kTopHeads, groups,
+                const int c = top_select<T>(top, heads + q.s * p.heads, groups,
                                   reinterpret_cast<const uint4*>(it.x + col0 * ES), it.nv, (uint32_t)col0, p.top_k,
                                   ce >= 0, xe, (uint32_t)ce);
-            }
-            if (p.part) {
-                if (lane == 0) p.part[it.item] = make_float4(st.m, st.d, st.s, __int_as_float(c));
-                for (int k = lane; k < c; k += 32) p.cand[it.item * p.top_k + k] = top.buf[k];
-            } else {
-                finish_row<T>(p, r, it.x, st, top.buf, c, given);
+                if (!p.part) {
+                    finish_top(p, it.row, norm, top.buf, c);
+                } else {
+                    if (lane == 0) p.part[it.item].w = __int_as_float(c);
+                    for (int k = lane; k < c; k += 32) p.cand[it.item * p.top_k + k] = top.buf[k];
+                }
             }
         }
-        warp_arrive(&bars.free_[q]);
+        warp_arrive(&bars.free_[q.s]);
+        for (int k = 0; k < kSideWarps; ++k) q.next(p.places);
     }
     if (lane == 0 && bars.gone) atomicOr(p.err, CE_DEVERR_TIMEOUT);
 }
@@ -275,7 +290,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(const __grid_c
     st = stat_warp<true>(st, p.L);
     top_sort(top, g.held);
     if (g.held > p.top_k) g.held = p.top_k;
-    finish_row<T>(p, r, x, st, top.buf, g.held, given);
+    const RowNorm norm = finish_row<T>(p, r, x, st, given);
+    finish_top(p, r, norm, top.buf, g.held);
 }
 
 template <typename T, bool TOP, bool ENT>
@@ -404,6 +420,8 @@ extern "C" ce_status ce_logprobs_fwd(const void* logits, ce_dtype dtype, int64_t
     a.scale = 1.f;
     a.segs = pl.segs;
     a.per = pl.per;
+    a.places = pl.places;
+    a.heads = pl.heads;
     a.tokens = row_tokens(tokens, token_strides, given, dim0, dim1, ignore_idx);
     a.top_k = top_k;
     a.logprobs = logprobs;

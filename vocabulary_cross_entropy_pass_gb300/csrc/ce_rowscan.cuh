@@ -159,6 +159,11 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+__device__ __forceinline__ uint4 ld_smem(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
 // A thread's vectors of a tile: NV neighbours, n of them there.  It takes them in an order of
 // its own (`turn`), so eight threads next to each other meet in no bank of shared memory.
 template <int NV>
@@ -174,15 +179,16 @@ __device__ __forceinline__ float stat_tile(Stat& a, const uint4* tile, int nv, f
     static_assert(NV == 8 || NV == 4, "the orders");
     const uint4* src = tile + threadIdx.x * NV;
     const int turn = tile_turn<NV>(), n = min(NV, nv - (int)threadIdx.x * NV);
+    const uint32_t at = smem_u32(src) + turn * 16u;  // of 16 bytes times NV: the i-th one's is at ^ 16 i
     uint4 raw[NV];
     if (n == NV) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) raw[i] = src[i ^ turn];
+        for (int i = 0; i < NV; ++i) raw[i] = ld_smem(at ^ (16u * i));
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             raw[i] = all_low<T>();
-            if ((i ^ turn) < n) raw[i] = src[i ^ turn];
+            if ((i ^ turn) < n) raw[i] = ld_smem(at ^ (16u * i));
         }
     }
     typename VT::Max tm = VT::max_init();
@@ -308,7 +314,7 @@ struct Head<__half> {
 // The candidates of one warp's selection.
 struct alignas(16) TopSmem {
     uint64_t buf[kTopCap];
-    int bins[128];
+    int bins[160];  // of heads; then vectors to be looked at: 31 left over and 128 more
 };
 
 // Few keys: a key's rank is the number of larger ones (75 keys: half the instructions of
@@ -572,18 +578,10 @@ __device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t least
             ok |= (w[i] & 0xffffu) >= least ? 1u << (2 * i) : 0u;
             ok |= (w[i] >> 16) >= least ? 2u << (2 * i) : 0u;
         }
-        if (!__any_sync(kFull, ok != 0u)) continue;
-        const int own = __popc(ok);
-        int sum = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int b = __shfl_up_sync(kFull, sum, o);
-            if (lane >= o) sum += b;
+        for (unsigned m; (m = __ballot_sync(kFull, ok != 0u)) != 0u; ok &= ok - 1u) {  // few: one of a lane's at a time
+            if (ok) heads[listed + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(k + __ffs(ok) - 1);
+            listed += __popc(m);
         }
-        const int all = __shfl_sync(kFull, sum, 31);
-        int at = listed + sum - own;
-        for (; ok; ok &= ok - 1u) heads[at++] = (uint16_t)(k + __ffs(ok) - 1);
-        listed += all;
         __syncwarp();
     }
     __syncwarp();
@@ -593,16 +591,21 @@ __device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t least
 // The listed groups' vectors, 32 at a time and the next ones on their way.  wide: a group is
 // eight vectors (four from vector `halves` on), else one.  equal: every vector from the
 // first on, for logits equal to T alone, until `equal` of them are held (or K and all after
-// them come behind those).
+// them come behind those).  Most vectors of a listed group have no candidate: those that
+// reach T are queued first and looked at when each lane has one (read twice, but a third
+// of the instructions).
 template <typename T>
 __device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t* list, int listed, bool wide,
                                          const uint4* body, int64_t nv, uint32_t col0, int equal) {
-    constexpr int VEC = Vec<T>::kElems, AHEAD = 4;
+    using VT = Vec<T>;
+    constexpr int VEC = VT::kElems, AHEAD = 2;
     static_assert(kTileVecs == 8 * kMainThreads, "eight vectors of a tile a thread");
     const int lane = threadIdx.x & 31, per = wide ? 4 : 32, had = g.held;
     const int last = nv < 0x7fffffff ? (int)nv : 0x7fffffff;
     const int halves = last - 1 - (last - 1) % kTileVecs + ((last - 1) % kTileVecs < kTileVecs / 2 ? 0 : kTileVecs);
     if (equal) listed = last;
+    int* queue = s.bins;  // vectors
+    int queued = 0;
     uint4 raw[AHEAD];
     int v[AHEAD];  // the vector, or -1
     auto fetch = [&](int b, uint4& to, int& vec) {
@@ -626,19 +629,35 @@ __device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t*
     };
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a) fetch(a * per, raw[a], v[a]);
+    bool more = listed > 0;
 #pragma unroll 1
-    for (int b = 0; b < listed; b += per) {
-        const uint4 now = raw[0];
-        const int vec = v[0];
+    for (int b = 0; more || queued > 0; b += AHEAD * per) {
 #pragma unroll
-        for (int a = 0; a + 1 < AHEAD; ++a) {
-            raw[a] = raw[a + 1];
-            v[a] = v[a + 1];
+        for (int a = 0; a < AHEAD; ++a) {
+            const bool hit = v[a] >= 0 && VT::vmax(raw[a]) >= g.T;
+            const unsigned m = __ballot_sync(kFull, hit);
+            if (hit) queue[queued + __popc(m & ((1u << lane) - 1u))] = v[a];
+            queued += __popc(m);
+            fetch(b + (AHEAD + a) * per, raw[a], v[a]);
         }
-        fetch(b + AHEAD * per, raw[AHEAD - 1], v[AHEAD - 1]);
-        top_room(s, g, 32 * VEC);
-        if (equal && (g.held >= had + equal || g.C != 0xffffffffu)) break;
-        top_push<T>(s, g, vec >= 0, now, col0 + (uint32_t)(vec * VEC), equal != 0);
+        more = b + AHEAD * per < listed;
+        __syncwarp();
+        int at = 0;
+#pragma unroll 1
+        for (; queued - at >= 32 || (!more && queued > at); at += 32) {
+            const int vec = at + lane < queued ? queue[at + lane] : -1;
+            uint4 now = make_uint4(0, 0, 0, 0);
+            if (vec >= 0) now = __ldg(body + vec);
+            top_room(s, g, 32 * VEC);
+            if (equal && (g.held >= had + equal || g.C != 0xffffffffu)) return;
+            top_push<T>(s, g, vec >= 0, now, col0 + (uint32_t)(vec * VEC), equal != 0);
+        }
+        const int left = max(0, queued - at);  // fewer than 32
+        const int keep = lane < left ? queue[at + lane] : 0;
+        __syncwarp();
+        if (lane < left) queue[lane] = keep;
+        __syncwarp();
+        queued = left;
     }
 }
 
@@ -686,7 +705,6 @@ __device__ __forceinline__ int top_select(TopSmem& s, uint16_t* heads, int G, co
 // gives up raises `gone`, which ends all others; the copying warp then issues no more and
 // leaves when what it has issued has landed (bounded too).
 constexpr int kRingMost = 6;
-constexpr int kQueue = 6;  // places at most
 struct RowItem {
     const char* x;      // the row
     char* out;          // its gradient, or NULL

@@ -15,6 +15,7 @@ struct ScanArgs {
     float L, scale;        // log2(e) / temperature, 1 / temperature
     int segs;              // segments of a row, `per` vectors of its body in each
     int64_t per;
+    int places, heads;     // of the queue; groups' maxima of each
     RowTokens tokens;
     float4* part;          // [N][segs] {m, d, s, candidates}, or NULL: one segment, finished in place
     uint64_t* cand;        // [N][segs][top_k]

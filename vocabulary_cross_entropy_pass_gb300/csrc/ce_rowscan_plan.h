@@ -13,7 +13,9 @@ constexpr int kSideThreads = 32 * kSideWarps;
 constexpr int kRowThreads = kMainThreads + 32 + kSideThreads;  // and the copying warp
 constexpr int kTileVecs = kMainThreads * 8;                  // 16-byte vectors of a tile: 32 KB
 constexpr int kTopCap = 1024;                                // candidates held at a time
-constexpr int kTopHeads = 2048;                              // groups' maxima of a row or segment
+constexpr int kTopHeads = 2048;                              // groups' maxima of a row or segment at most
+constexpr int kQueue = 6;                                    // rows or segments a CTA has begun at most
+constexpr int kHeadsRoom = 4 * kTopHeads;                    // for theirs
 constexpr int kMaxTop = 256;                                 // likeliest tokens a call may ask for
 constexpr int kMaxListed = 1024;                             // given or teacher's tokens of a row
 constexpr int kMaxSegments = 1024;
@@ -23,6 +25,8 @@ constexpr int64_t kScanSlots = 2 * kSMs;                     // CTAs that run at
 struct ScanPlan {
     int segs;      // segments of a row
     int64_t per;   // whole vectors in a segment
+    int places;    // of the queue of rows or segments that are begun
+    int heads;     // room for groups' maxima at each
 };
 
 // Rows are cut where that ends sooner: the rounds of kScanSlots CTAs times a segment's
@@ -48,6 +52,15 @@ inline ScanPlan plan_scan(int64_t N, int64_t V, int es, int top_k) {
     p.per = (nv + segs - 1) / segs;
     if (p.per < 1) p.per = 1;
     p.segs = segs > kMaxSegments ? 0 : (int)segs;
+    // A group for each main thread of a tile; where these may be too few for top_k, a short
+    // row's vectors are groups.  As many places as the maxima leave: three rows are with the side
+    // warps, and one alone to stream ahead leaves the main warps waiting.
+    p.heads = 0;
+    p.places = kQueue;
+    if (top_k > 0 && p.segs > 0) {
+        p.heads = 2 * top_k > kMainThreads ? kTopHeads : (int)((p.per + kTileVecs - 1) / kTileVecs) * kMainThreads;
+        if (p.places > kHeadsRoom / p.heads) p.places = kHeadsRoom / p.heads;
+    }
     return p;
 }
 
