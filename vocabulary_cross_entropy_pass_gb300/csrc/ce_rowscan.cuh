@@ -602,7 +602,6 @@ __device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t*
     static_assert(kTileVecs == 8 * kMainThreads, "eight vectors of a tile a thread");
     const int lane = threadIdx.x & 31, per = wide ? 4 : 32, had = g.held;
     const int last = nv < 0x7fffffff ? (int)nv : 0x7fffffff;
-    const int halves = last - 1 - (last - 1) % kTileVecs + ((last - 1) % kTileVecs < kTileVecs / 2 ? 0 : kTileVecs);
     if (equal) listed = last;
     int* queue = s.bins;  // vectors
     int queued = 0;
@@ -613,15 +612,8 @@ __device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t*
         vec = -1;
         if (e < listed) {
             int at = equal ? e : (int)list[e];
-            bool there = true;
-            if (wide) {
-                at = at * 8 + (lane & 7);
-                if (at >= halves) {
-                    there = (lane & 4) == 0;
-                    at = halves + (at - halves) / 8 * 4 + (lane & 3);
-                }
-            }
-            if (there && at < last) {
+            if (wide) at = at * 8 + (lane & 7);
+            if (at < last) {
                 vec = at;
                 to = __ldg(body + at);
             }
@@ -793,12 +785,15 @@ __device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, con
         const uint4* tile = reinterpret_cast<const uint4*>(ring + (size_t)at.s * TILE * 16);
         if (!warp_wait(b, &b.full[at.s], at.ph)) return false;
         const int left = nv < TILE ? (int)nv : TILE;
-        const bool half = NV == 8 && left <= TILE / 2;  // half the work
-        const float top =
-            half ? stat_tile<T, 4, ENT>(st, tile, left, L, &b.empty[at.s])
-                 : stat_tile<T, NV, ENT>(st, tile, left, L, &b.empty[at.s]);
+        float top = -INFINITY;
+        if (!GM && NV == 8 && left <= TILE / 2)  // half the work for each warp
+            top = stat_tile<T, GM ? NV : 4, ENT>(st, tile, left, L, &b.empty[at.s]);
+        else if (!GM || left > warp * 32 * NV)
+            top = stat_tile<T, NV, ENT>(st, tile, left, L, &b.empty[at.s]);
+        else
+            warp_arrive(&b.empty[at.s]);
         if constexpr (GM) {
-            heads[tid] = (uint16_t)(tid * (half ? 4 : NV) < left ? Head<T>::of(top) : 0u);  // 0: no vector
+            heads[tid] = (uint16_t)(tid * NV < left ? Head<T>::of(top) : 0u);  // 0: no vector
             heads += kMainThreads;
         }
         at.next(stages);
