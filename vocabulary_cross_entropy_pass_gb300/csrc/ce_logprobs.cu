@@ -22,7 +22,9 @@ __device__ __forceinline__ void write_skipped(const ScanArgs& p, int64_t r) {
         if (p.entropy) p.entropy[r] = 0.f;
         if (p.stats) p.stats[r] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
     }
+#pragma unroll 1
     for (int k = lane; k < p.tokens.n; k += 32) p.logprobs[r * p.tokens.n + k] = 0.f;
+#pragma unroll 1
     for (int k = lane; k < p.top_k; k += 32) {
         p.top_tokens[r * p.top_k + k] = p.tokens.ignore_idx;
         p.top_logprobs[r * p.top_k + k] = 0.f;
@@ -59,6 +61,7 @@ __device__ __forceinline__ RowNorm finish_row(const ScanArgs& p, int64_t r, cons
         if (p.entropy) p.entropy[r] = h;
         if (p.stats) p.stats[r] = make_float4(t.m, logd, h, 0.f);
     }
+#pragma unroll 1
     for (int k = lane; k < p.tokens.n; k += 32) {
         if (k >= 32) given.load(p, r, x, k);
         float lp = 0.f;
@@ -77,6 +80,7 @@ __device__ __forceinline__ RowNorm finish_row(const ScanArgs& p, int64_t r, cons
 
 // The likeliest tokens from the candidates in falling order (c of them).
 __device__ __forceinline__ void finish_top(const ScanArgs& p, int64_t r, RowNorm n, const uint64_t* top, int c) {
+#pragma unroll 1
     for (int k = threadIdx.x & 31; k < p.top_k; k += 32) {
         int64_t token = -1;  // NaN is no alternative: a row of fewer than K others ends so
         float lp = NAN;
@@ -154,6 +158,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
             bool skip = one && y == p.tokens.ignore_idx;
             if (more && p.tokens.n > 1) {  // left out when all are ignored
                 bool keep = false;
+#pragma unroll 1
                 for (int k = lane; k < p.tokens.n; k += 32) keep |= p.tokens.at(r, k) != p.tokens.ignore_idx;
                 skip = !__any_sync(kFull, keep);
             }
@@ -236,6 +241,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) ce_scan_kernel(const __grid_co
                     finish_top(p, it.row, norm, top.buf, c);
                 } else {
                     if (lane == 0) p.part[it.item].w = __int_as_float(c);
+#pragma unroll 1
                     for (int k = lane; k < c; k += 32) p.cand[it.item * p.top_k + k] = top.buf[k];
                 }
             }
@@ -260,6 +266,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(const __grid_c
     Given<T> given;
     given.load(p, r, x, lane);
     bool keep = p.tokens.n == 0;
+#pragma unroll 1
     for (int k = lane; k < p.tokens.n; k += 32)
         keep |= (k == lane ? given.y : p.tokens.at(r, k)) != p.tokens.ignore_idx;
     if (!__any_sync(kFull, keep)) {

@@ -353,6 +353,7 @@ static __device__ __noinline__ void top_sort(TopSmem& s, int c) {
     if (c <= 128) return sort_by_rank<4>(s, c);
     int n = 256;
     while (n < c) n *= 2;
+#pragma unroll 1
     for (int k = c + lane; k < n; k += 32) s.buf[k] = 0;
     __syncwarp();
 #pragma unroll 1
@@ -466,11 +467,13 @@ static __device__ __noinline__ uint32_t head_bin(TopSmem& s, const uint16_t* hea
         if (d < span && h) atomicAdd(&s.bins[d >> shift], 1);
     };
     if (fold == 8) {
+#pragma unroll 1
         for (int k = lane * 8; k < n; k += 256) {
             const uint32_t v = head_of_eight(heads, k);
             bin(max(v & 0xffffu, v >> 16));
         }
     } else {
+#pragma unroll 1
         for (int k = lane * 2; k < n; k += 64) {
             const uint32_t u = *reinterpret_cast<const uint32_t*>(heads + k);
             const uint32_t a = u & 0xffffu, c = u >> 16;
@@ -506,6 +509,7 @@ __device__ __forceinline__ uint32_t kth_head(TopSmem& s, const uint16_t* heads, 
     const int lane = threadIdx.x & 31;
     many = false;
     uint32_t top = 0;
+#pragma unroll 1
     for (int k = lane * 8; k < n; k += 256) top = __vmaxu2(top, head_of_eight(heads, k));
     top = __reduce_max_sync(kFull, max(top & 0xffffu, top >> 16));
     if (top == 0) return 0;
@@ -554,6 +558,7 @@ __device__ __forceinline__ uint32_t kth_head(TopSmem& s, const uint16_t* heads, 
 __device__ __forceinline__ int count_heads(const uint16_t* heads, int n, uint32_t least) {
     const uint32_t two = least | (least << 16);
     uint32_t sum = 0;
+#pragma unroll 1
     for (int k = (threadIdx.x & 31) * 8; k < n; k += 256) {
         const uint4 u = *reinterpret_cast<const uint4*>(heads + k);
         sum += __vsetgeu2(u.x, two) + __vsetgeu2(u.y, two) + __vsetgeu2(u.z, two) + __vsetgeu2(u.w, two);
@@ -567,6 +572,7 @@ __device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t least
     const int lane = threadIdx.x & 31;
     if (least == 0) least = 1;
     int listed = 0;
+#pragma unroll 1
     for (int k0 = 0; k0 < n; k0 += 256) {
         const int k = k0 + lane * 8;
         uint4 u = make_uint4(0, 0, 0, 0);
@@ -578,6 +584,7 @@ __device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t least
             ok |= (w[i] & 0xffffu) >= least ? 1u << (2 * i) : 0u;
             ok |= (w[i] >> 16) >= least ? 2u << (2 * i) : 0u;
         }
+#pragma unroll 1
         for (unsigned m; (m = __ballot_sync(kFull, ok != 0u)) != 0u; ok &= ok - 1u) {  // few: one of a lane's at a time
             if (ok) heads[listed + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(k + __ffs(ok) - 1);
             listed += __popc(m);
@@ -664,6 +671,7 @@ __device__ __forceinline__ int top_select(TopSmem& s, uint16_t* heads, int G, co
     const int lane = threadIdx.x & 31;
     const bool brief = G < 2 * K && nv <= kTopHeads;  // too few groups: each vector is one
     if (brief) {
+#pragma unroll 1
         for (int v = lane; v < (((int)nv + 255) & ~255); v += 32)
             heads[v] = (uint16_t)(v < nv ? Head<T>::of(VT::vmax(__ldg(body + v))) : 0u);
         G = (int)nv;
