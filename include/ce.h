@@ -545,7 +545,9 @@ ce_status ce_logits_process_bwd(const void* grad_out, const int64_t grad_out_str
  *   stats          float32 [N][4], 16-byte aligned, or NULL: {max, log sum exp(x - max),
  *                  entropy, 0} for ce_logprobs_bwd.
  *   workspace      ce_logprobs_workspace_bytes(dim0*dim1, V, dtype, top_k) bytes, 16-byte
- *                  aligned, no initialisation; not shared by calls that may overlap.
+ *                  aligned, no initialisation; not shared by calls that may overlap.  0 bytes,
+ *                  and CE_ERR_INVALID_ARG from the call: sizes out of range, or top_k with
+ *                  rows of more than 256 MiB (V times the type's size).
  * A row whose given tokens (one at least) are all ignore_idx is not read: zeros, and
  * ignore_idx for its top tokens.  A row of -inf throughout (a mask that allows
  * nothing) has log-probabilities of -inf, entropy 0 and top tokens 0, 1, 2, ...  A NaN

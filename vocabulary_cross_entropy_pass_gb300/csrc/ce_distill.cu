@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
         bad = __any_sync(kFull, bad);
         zm = warp_max_redux(zm);
         float sum = 0.f;
+#pragma unroll 1
         for (int k = lane; k < K; k += 32)
             if (e[k].lq != -INFINITY) sum += ex2_approx((e[k].lq - zm) * p.L);
         sum = warp_allsum(sum);
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
                         : sum != sum  ? sum
                         : p.normalize ? 1.f
                                       : ex2_approx((zm * p.scale + logs) * kLog2e);
+#pragma unroll 1
         for (int k = lane; k < K; k += 32) {
             if (e[k].lq == -INFINITY) continue;
             const float lq = p.normalize ? (e[k].lq - zm) * p.scale - logs : e[k].lq * p.scale;
@@ -306,8 +308,10 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
         bool again = false;
         if constexpr (GRAD) {
             // of a token's entries one, the first to find a slot, writes for all
+#pragma unroll 1
             for (int k = lane; k < p.slots; k += 32) slots[k] = 0xffffu;
             __syncwarp();
+#pragma unroll 1
             for (int k = lane; k < K; k += 32) {
                 const int col = e[k].col;
                 if (col < 0) continue;
@@ -356,12 +360,14 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
             auto grad = [&](float v) { return ex2_approx(fmaf(v + nm, p.L, shift)) * a; };
             if (ce >= 0) VT::store1(it.out + ce * ES, zero ? 0.f : grad(xe));
             if (!warp_wait(bars, &bars.stored[q], ph)) break;
+#pragma unroll 1
             for (int k = lane; k < K && !zero; k += 32) {
                 const int col = e[k].col;
                 if (col < 0) continue;
                 float c = e[k].q;
                 if (again) {  // in list order
                     c = 0.f;
+#pragma unroll 1
                     for (int j = 0; j < K; ++j)
                         if (e[j].col == col || e[j].col == -2 - col) c += e[j].q;
                 }

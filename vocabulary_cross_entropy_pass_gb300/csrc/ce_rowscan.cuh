@@ -36,7 +36,9 @@
 // above T are read, and the equals in order from the row's start.  So any row is exact.
 // A row's selection is one warp's work, without barriers, and three rows' go on at a time
 // (four warps at one row's, with a barrier for each step: 17 us a row of 128000 columns,
-// K = 64, beside the stream).
+// K = 64, beside the stream).  Its code and the main loop share the instruction cache, and
+// outgrew it once: loops are not unrolled here (8 of 16384 x 32000 with entropy: 259 us
+// unrolled, 219 not).
 #pragma once
 
 #include "ce_device.cuh"
@@ -233,38 +235,6 @@ __device__ __forceinline__ float stat_tile(Stat& a, const uint4* tile, int nv, f
 __device__ __forceinline__ void side_sync() {
     __syncwarp();
     asm volatile("barrier.sync 1, %0;" ::"n"(kSideThreads) : "memory");
-}
-__device__ __forceinline__ bool side_any(bool v) {
-    uint32_t n;
-    __syncwarp();
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.red.or.pred q, 1, %2, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(n)
-        : "r"((uint32_t)v), "n"(kSideThreads)
-        : "memory");
-    return n != 0;
-}
-// Over the side warps, in a fixed order; `red` is not used by others until the next barrier.
-__device__ __forceinline__ float side_sum(float v, float* red, int tid) {
-    v = warp_allsum(v);
-    if ((tid & 31) == 0) red[tid >> 5] = v;
-    side_sync();
-    float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < kSideThreads / 32; ++w) t += red[w];
-    return t;
-}
-__device__ __forceinline__ float side_max(float v, float* red, int tid) {
-    v = warp_allmax(v);
-    if ((tid & 31) == 0) red[tid >> 5] = v;
-    side_sync();
-    float t = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kSideThreads / 32; ++w) t = fmaxf(t, red[w]);
-    return t;
 }
 
 // ----------------------------------------------------------------- the largest
@@ -596,7 +566,7 @@ __device__ __forceinline__ int list_heads(uint16_t* heads, int n, uint32_t least
 }
 
 // The listed groups' vectors, 32 at a time and the next ones on their way.  wide: a group is
-// eight vectors (four from vector `halves` on), else one.  equal: every vector from the
+// eight vectors, else one.  equal: every vector from the
 // first on, for logits equal to T alone, until `equal` of them are held (or K and all after
 // them come behind those).  Most vectors of a listed group have no candidate: those that
 // reach T are queued first and looked at when each lane has one (read twice, but a third
@@ -781,8 +751,9 @@ __device__ __forceinline__ void ring_drain(RowBars& b, uint32_t issued, int stag
             (void)mbar_wait_bounded(&b.full[s], ((issued - 1u - (uint32_t)s) / (uint32_t)stages) & 1u);
 }
 // First pass over a row's tiles by the main warps: the warp's statistics go to part, and
-// with GM the maximum of each thread's vectors of a tile to heads: eight neighbours, or four
-// in a last tile that is half full or less.
+// with GM the maximum of each thread's vectors of a tile to heads.  A warp without a vector
+// of a last tile passes it by; there is one body for every tile (a second one for half a tile cost
+// more, beside the side warps' code in the instruction cache, than it saved).
 template <typename T, int NV, bool ENT, bool GM>
 __device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, const unsigned char* ring, int q,
                                            int64_t nv, float L, uint16_t* heads) {
@@ -794,9 +765,7 @@ __device__ __forceinline__ bool main_stats(RowBars& b, Turn& at, int stages, con
         if (!warp_wait(b, &b.full[at.s], at.ph)) return false;
         const int left = nv < TILE ? (int)nv : TILE;
         float top = -INFINITY;
-        if (!GM && NV == 8 && left <= TILE / 2)  // half the work for each warp
-            top = stat_tile<T, GM ? NV : 4, ENT>(st, tile, left, L, &b.empty[at.s]);
-        else if (!GM || left > warp * 32 * NV)
+        if (left > warp * 32 * NV)
             top = stat_tile<T, NV, ENT>(st, tile, left, L, &b.empty[at.s]);
         else
             warp_arrive(&b.empty[at.s]);

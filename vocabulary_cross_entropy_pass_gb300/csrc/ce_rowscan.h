@@ -12,7 +12,7 @@ struct ScanArgs {
     const char* x;
     RowAddr row;
     int64_t N, V;
-    float L, scale;        // log2(e) / temperature, 1 / temperature
+    float L;               // log2(e) / temperature
     int segs;              // segments of a row, `per` vectors of its body in each
     int64_t per;
     int places, heads;     // of the queue; groups' maxima of each
