@@ -7,6 +7,9 @@ itself; a loss sums K such terms in float32: temperature^2 2^-24 sum q (300 + 4 
 rounded products, then one rounding to the storage type.
 """
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -254,6 +257,79 @@ def test_autograd_and_differences():
     h = y * 1.0
     pkg.distillation_loss(h, t, z, reduce_loss=True, inplace_grad=True).backward()
     assert bool(torch.isfinite(y.grad).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("V,N", [(61, 20), (4096, 700), (70001, 400)])
+def test_tokens_listed_often(V, N, dtype):
+    # long lists of tokens drawn with replacement: of 61 columns each about 17 times, of others some
+    # twice.  A column's entries are summed: at most 48 roundings, of the 200 that the bound allows.
+    g = rng(V)
+    x = (torch.randn(N, V, generator=g, device=DEV) * 3).to(dtype)
+    t = torch.randint(0, V, (N, 1024), generator=g, device=DEV)
+    t[::4, 1:] = t[::4, :1].clone()  # one token throughout ...
+    t[::4, 40:] = -100               # ... of 40 entries
+    z = torch.randn(N, 1024, generator=g, device=DEV) * 4
+    check(x, t, z, 2.0, True, True)
+    check(x, t[:, :300], z[:, :300], 1.0, True, False, in_place=True)
+
+
+def test_second_backward_of_logits_given_up():
+    """The first backward pass has replaced the logits: a second one is refused, not wrong."""
+    x, t, z = make(5, 100, 6, torch.float32, 4, ignored=0.0)
+    y = x.clone().requires_grad_()
+    h = y * 1.0
+    loss = pkg.distillation_loss(h, t, z, reduce_loss=True, inplace_grad=True)
+    loss.backward(retain_graph=True)
+    once = y.grad.clone()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    assert torch.equal(y.grad, once)
+    y = x.clone().requires_grad_()
+    loss = pkg.distillation_loss(y * 1.0, t, z, reduce_loss=True)
+    loss.backward(retain_graph=True)
+    assert torch.equal(y.grad, once)
+    loss.backward()
+    assert torch.equal(y.grad, 2 * once)
+
+
+PROGRAM = """
+import torch
+import vocabulary_cross_entropy_pass_gb300 as pkg
+x = torch.randn(20, 640, device="cuda")
+t = torch.randint(0, 640, (20, 4), device="cuda")
+z = torch.randn(20, 4, device="cuda")
+ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+s = pkg.ce_logprobs_fwd(x, t, stats=True)[4]
+d = pkg.ce_distill_fwd(x, t, z, stats=True)[1]
+g = torch.ones(20, 4, device="cuda")
+torch.cuda.synchronize()
+calls = [lambda: pkg.ce_logprobs_fwd(x, t, top_k=3), lambda: pkg.ce_logprobs_bwd(x, s, t, grad_logprobs=g),
+         lambda: pkg.ce_distill_fwd_bwd(x, t, z), lambda: pkg.ce_distill_bwd(x, t, z, d)]
+for call in calls:
+    call()
+torch.cuda.synchronize()
+for call in calls:
+    with torch.cuda.stream(torch.cuda.Stream()):
+        graph = torch.cuda.CUDAGraph()
+        graph.capture_begin()
+        status, _ = pkg.ce_get_error(ws)  # waits, which a capture does not allow
+        try:
+            graph.capture_end()
+            print("captured")
+        except RuntimeError:
+            pass
+    assert status == pkg.CEError(5).status == 5, status
+    call()
+torch.cuda.synchronize()
+print("done")
+"""
+
+
+def test_a_refused_wait_is_not_the_next_launch_s_failure():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", PROGRAM], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("done"), r.stdout + r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("N", [6, 1300])

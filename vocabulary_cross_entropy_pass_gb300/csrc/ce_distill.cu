@@ -62,6 +62,7 @@ struct ListRow {
     float em, ed;     // statistics of the student's logits around the body
     int bad;          // a token out of range
 };
+constexpr unsigned kTwice = 0x8000u;  // of a slot, beside the number of the entry that found it first
 inline int list_slots(int K) {
     int n = 64;
     while (n < 2 * K) n *= 2;
@@ -320,9 +321,11 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
                     const unsigned short was = atomicCAS(reinterpret_cast<unsigned short*>(&slots[h]),
                                                          (unsigned short)0xffffu, (unsigned short)k);
                     if (was == 0xffffu) break;
-                    if (e[was].col == col) {
+                    if (e[was & 0x7fffu].col == col) {
                         again = true;
                         e[k].col = -2 - col;
+                        // (its two slots' word: kTwice may be there already)
+                        atomicOr(reinterpret_cast<unsigned*>(slots + (h & ~1u)), kTwice << (16u * (h & 1u)));
                         break;
                     }
                 }
@@ -359,19 +362,31 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
             const bool zero = bad || none;
             auto grad = [&](float v) { return ex2_approx(fmaf(v + nm, p.L, shift)) * a; };
             if (ce >= 0) VT::store1(it.out + ce * ES, zero ? 0.f : grad(xe));
+            if (again && !zero) {
+                // the sum of a token's entries, in an order of their own, at the one that writes
+#pragma unroll 1
+                for (int h = lane; h < p.slots; h += 32) {
+                    const unsigned mine = slots[h];
+#pragma unroll 1
+                    for (unsigned m = __ballot_sync(kFull, mine != 0xffffu && (mine & kTwice)); m; m &= m - 1u) {
+                        const int k = __shfl_sync(kFull, mine, __ffs(m) - 1) & 0x7fffu, col = e[k].col;
+                        float c = 0.f;
+#pragma unroll 1
+                        for (int j = lane; j < K; j += 32)
+                            if (e[j].col == col || e[j].col == -2 - col) c += e[j].q;
+                        c = warp_allsum(c);
+                        __syncwarp();
+                        if (lane == 0) e[k].q = c;
+                        __syncwarp();
+                    }
+                }
+            }
             if (!warp_wait(bars, &bars.stored[q], ph)) break;
 #pragma unroll 1
             for (int k = lane; k < K && !zero; k += 32) {
                 const int col = e[k].col;
                 if (col < 0) continue;
-                float c = e[k].q;
-                if (again) {  // in list order
-                    c = 0.f;
-#pragma unroll 1
-                    for (int j = 0; j < K; ++j)
-                        if (e[j].col == col || e[j].col == -2 - col) c += e[j].q;
-                }
-                VT::store1(it.out + (int64_t)col * ES, fmaf(-gt, c, grad(e[k].x)));
+                VT::store1(it.out + (int64_t)col * ES, fmaf(-gt, e[k].q, grad(e[k].x)));
             }
         }
         warp_arrive(&bars.free_[q]);
@@ -564,7 +579,7 @@ ce_status distill(const void* logits, ce_dtype dtype, int64_t dim0, int64_t dim1
     ce_distill_count_kernel<<<1, count ? kCountThreads : 32, 0, s>>>(tokens.t, tokens.row, N, t.ignore_idx, count, pb.err,
                                                                     pb.ticket, pb.row_claim, pb.n_dev, n_out);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return CE_ERR_LAUNCH;
+    if (e != cudaSuccess) return launch_failed();
     if (N == 0) return !reduce || launch_reduce_mean(pb, loss_out, s) == cudaSuccess ? CE_OK : launch_failed();
     DistillArgs d = {};
     d.x = static_cast<const char*>(logits);

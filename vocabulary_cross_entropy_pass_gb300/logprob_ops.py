@@ -162,6 +162,8 @@ class _Distillation(torch.autograd.Function):
         g = ce_distill_bwd(logits, tokens, teacher, stats, temperature=temperature, normalize=normalize,
                            ignore_idx=ignore_idx, reduce_loss=reduce_loss, dloss=_flat(grad_out), n_non_ignore=n,
                            grad=logits if inplace_grad else None)
+        if inplace_grad:  # a second pass through this graph, or another reader of the logits in it, is refused
+            torch.autograd.graph.increment_version(logits)
         return g, None, None, None, None, None, None, None
 
 
