@@ -11,7 +11,9 @@
 // listed columns.  Bound by HBM: a logit read, a gradient written.  A CTA streams a
 // run of a row's columns, by the output's 16-byte vectors, and then writes the run's
 // listed columns again; their logits are read before the stream, which may replace
-// them.  Tokens listed twice add up in list order.
+// them.  A token listed twice gets the sum of its entries.
+// Measured: 4096 x 128000 bf16, one token a row, 308 us (6.8 TB/s, the copy rate); 2048 x
+// 65536, 128 tokens, 101 us (5.1 TB/s), where every CTA's list comes before its stream.
 #include <math.h>
 
 #include "ce_rowscan.h"
@@ -36,7 +38,9 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
 struct Listed {
     int col[kMaxListed];
     float coef[kMaxListed], x[kMaxListed];
+    alignas(4) unsigned short slot[2 * kMaxListed];  // entries by their columns' hash
 };
+constexpr unsigned kTwice = 0x8000u;  // of a slot, beside the number of the entry that found it first
 
 template <typename T, bool SECOND>  // SECOND: b is not zero
 __global__ void __launch_bounds__(kThreads) ce_softgrad_kernel(const __grid_constant__ SoftGradArgs p) {
@@ -186,17 +190,58 @@ __global__ void __launch_bounds__(kThreads) ce_softgrad_kernel(const __grid_cons
         }
     }
     if (listed == 0) return;
-    __syncthreads();
-    for (int k = tid; k < listed; k += kThreads) {
-        const int col = ls.col[k];
+    // Of a token's entries one writes for all.  Up to 64 are looked at by each other; of more, the
+    // first to find a slot of a hash table writes, and a warp sums what belongs to it, in an
+    // order fixed by the list (4096 x 32000, bf16, 64 tokens: 98 us, with the table 105; 256: 143
+    // and 126; 1024: 1110 and 215).
+    if (listed <= 64) {
+        __syncthreads();
+        if (tid >= listed) return;
+        const int col = ls.col[tid];
         float c = 0.f;
         bool first = true;
         for (int j = 0; j < listed; ++j) {
             if (ls.col[j] != col) continue;
-            if (j < k) first = false;
+            if (j < tid) first = false;
             c += ls.coef[j];
         }
-        if (first) VT::store1(out + (int64_t)col * ES, grad(ls.x[k]) + c);
+        if (first) VT::store1(out + (int64_t)col * ES, grad(ls.x[tid]) + c);
+        return;
+    }
+    int slots = 64;
+    while (slots < 2 * listed) slots *= 2;
+    for (int h = tid; h < slots; h += kThreads) ls.slot[h] = 0xffffu;
+    __syncthreads();
+    for (int k = tid; k < listed; k += kThreads) {
+        const int col = ls.col[k];
+        for (uint32_t h = ((uint32_t)col * 2654435761u) >> 7;; ++h) {
+            h &= (uint32_t)slots - 1u;
+            const unsigned short was = atomicCAS(&ls.slot[h], (unsigned short)0xffffu, (unsigned short)k);
+            if (was == 0xffffu) break;
+            if (ls.col[was & 0x7fffu] == col) {
+                ls.col[k] = -2 - col;
+                atomicOr(reinterpret_cast<unsigned*>(&ls.slot[h & ~1u]), kTwice << (16u * (h & 1u)));
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    for (int h = warp * 32; h < slots; h += kThreads) {
+        const unsigned mine = ls.slot[h + lane];
+        for (unsigned m = __ballot_sync(kFull, mine != 0xffffu && (mine & kTwice)); m; m &= m - 1u) {
+            const int k = __shfl_sync(kFull, mine, __ffs(m) - 1) & 0x7fffu, col = ls.col[k];
+            float c = 0.f;
+            for (int j = lane; j < listed; j += 32)
+                if (ls.col[j] == col || ls.col[j] == -2 - col) c += ls.coef[j];
+            c = warp_allsum(c);
+            __syncwarp();
+            if (lane == 0) ls.coef[k] = c;
+        }
+    }
+    __syncthreads();
+    for (int k = tid; k < listed; k += kThreads) {
+        const int col = ls.col[k];
+        if (col >= 0) VT::store1(out + (int64_t)col * ES, grad(ls.x[k]) + ls.coef[k]);
     }
 }
 
@@ -212,14 +257,15 @@ cudaError_t launch_softgrad_t(const SoftGradArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Runs of 32 KB; longer ones under long lists, which every CTA of a row walks through,
-// while that leaves the SMs several rounds, and where the grid would not hold them;
+// Runs of 32 KB; longer ones under lists of more than 4, which every CTA of a row walks
+// through, while that leaves the SMs several rounds (20 tokens of 4096 x 128000 bf16: 326 us,
+// in runs of 32 KB 364), and where the grid would not hold them;
 // shorter ones (down to 4 KB) where few rows leave SMs without.
 cudaError_t launch_softgrad(SoftGradArgs a, int dtype, cudaStream_t s) {
     const int vec = 16 / elem_size(dtype);
     a.cols = (int64_t)kThreads * 8 * vec;
     while (a.cols > kThreads * vec && a.N * ((a.V + a.cols - 1) / a.cols) < 2 * kScanSlots) a.cols /= 2;
-    while (a.tokens.n > 32 && a.cols < a.V && a.N * ((a.V + 2 * a.cols - 1) / (2 * a.cols)) >= 4096) a.cols *= 2;
+    while (a.tokens.n > 4 && a.cols < a.V && a.N * ((a.V + 2 * a.cols - 1) / (2 * a.cols)) >= 4096) a.cols *= 2;
     while (a.N * ((a.V + a.cols - 1) / a.cols) > 0x7fffffffLL) a.cols *= 2;
     a.runs = (a.V + a.cols - 1) / a.cols;
     if (dtype == CE_F32) return launch_softgrad_t<float>(a, s);
