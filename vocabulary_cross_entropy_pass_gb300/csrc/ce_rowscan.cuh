@@ -603,7 +603,9 @@ __device__ __forceinline__ void top_take(TopSmem& s, TopGate& g, const uint16_t*
     for (int b = 0; more || queued > 0; b += AHEAD * per) {
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a) {
-            const bool hit = v[a] >= 0 && VT::vmax(raw[a]) >= g.T;
+            const float most = VT::vmax(raw[a]);
+            bool hit = v[a] >= 0 && most >= g.T;
+            if (g.C != 0xffffffffu) hit = hit && g.takes(most, col0 + (uint32_t)(v[a] * VEC));  // many equals
             const unsigned m = __ballot_sync(kFull, hit);
             if (hit) queue[queued + __popc(m & ((1u << lane) - 1u))] = v[a];
             queued += __popc(m);
