@@ -13,6 +13,9 @@
 // third row: its list while the rows before are streamed (the teacher's softmax, the
 // student's logits of its tokens, a hash table that finds tokens listed twice), then
 // its loss and, once its gradient is stored, its listed columns again.
+// Measured, bf16: 4096 x 128000, 64 tokens, loss and gradient 311 us (6.4 TB/s), 0.96 of the
+// copy rate; the loss alone of 2048 x 100277, 256 tokens, 77 us (5.4 TB/s).  Lists of 256
+// tokens and more are bound by the side warps (4096 x 32000: 64 tokens 97 us, 256 169, 1024 531).
 #include <math.h>
 
 #include <type_traits>
@@ -44,7 +47,7 @@ struct DistillArgs {
     const int64_t* n_dev;    // n_count for the mean's gradient, else NULL
     float* mean_out;         // or NULL
     uint32_t* ticket;        // CTAs done
-    uint32_t* claim;         // rows handed out beyond each CTA's first two
+    uint32_t* claim;         // rows handed out beyond each CTA's first three
     int stages, slots;
 };
 
@@ -498,7 +501,8 @@ template <typename T>
 cudaError_t launch_distill_t(const DistillArgs& a, cudaStream_t s) {
     if (!a.out) return launch_distill_k<T, 8, false>(a, s);
     // rows over 128 KB: one CTA per SM with tiles of 32 KB, so fewer rows wait in L2 for
-    // their second pass
+    // their second pass (4096 rows of 128000 bf16 columns 326 us, with two CTAs per SM 378; of
+    // 70000 193 and 197, of 60000 169 both ways; 8192 of 32000 262 and 175)
     return a.V * (int64_t)sizeof(T) > 128 * 1024 ? launch_distill_k<T, 8, true>(a, s) : launch_distill_k<T, 4, true>(a, s);
 }
 
