@@ -349,6 +349,16 @@ def test_autograd_and_differences():
     assert pkg.token_logprobs(x, None, top_k=2)[0] is None
 
 
+def test_autograd_of_lists_without_tokens():
+    x = logits(3, 40, torch.float32, 9).requires_grad_()
+    lp, ent, *_ = pkg.token_logprobs(x, torch.empty(3, 0, dtype=torch.int64, device=DEV), entropy=True)
+    assert lp.shape == (3, 0)
+    got, = torch.autograd.grad(lp.sum() + ent.sum(), x)
+    want, = torch.autograd.grad(pkg.token_logprobs(x, entropy=True)[1].sum(), x)
+    assert torch.equal(got, want)
+    assert bool((want != 0).any())
+
+
 def test_graph_and_streams():
     x = logits(6, 9000, torch.bfloat16, 1)
     t = torch.randint(0, 9000, (6,), generator=rng(1), device=DEV)
