@@ -6,8 +6,9 @@
 // M is a reference like any other: what its rounding shifts is given back in log d), so
 //   log d = ln 2 (log2 d - (m L - M)),  log-probability = (x - m) / temperature - log d,
 //   entropy = ln 2 (log2 d - s / d).
-// Where M leaves float32 (a row at the type's lowest value) y = (x - m) L.  A logit of
-// -inf counts for nothing in d and s; a NaN makes both NaN.
+// Where M is so large that its rounding would carry 2^y out of float32 (a row, or what a thread
+// has seen of it, at a mask's -1e30: y is off by 2^76 there) y = (x - m) L.  A logit of -inf counts for nothing in d and s; a NaN makes
+// both NaN.
 //
 // The streaming kernels built on this (ce_logprobs.cu, ce_distill.cu) are persistent;
 // the warps of a CTA have three parts and meet at mbarriers alone:
@@ -58,13 +59,23 @@ struct Stat {
 __device__ __forceinline__ Stat stat_identity() { return Stat{-INFINITY, 0.f, 0.f}; }
 
 constexpr float kFarBelow = -1e4f;  // 2^kFarBelow is 0, and so is its product with it
-constexpr float kRefMost = 1e38f;   // a reference this far out is not used
+// 2^31: a product below is off by 64 at most, so no 2^y leaves float32 for it.  A larger one is no reference.
+constexpr float kRefMost = 2147483648.f;
 constexpr float kLn2f = 0.6931471805599453f;
 
 __device__ __forceinline__ float stat_ref(float m, float L) { return __fmul_rn(m, L); }
-// The exponent by which what is relative to m counts relative to the larger top.
+// By how much the reference M falls short of m L; 0 where m itself is the reference.
+__device__ __forceinline__ float stat_short(float m, float M, float L) {
+    return fabsf(M) < kRefMost ? fmaf(m, L, -M) : 0.f;
+}
+// The exponent by which what is relative to m's reference counts relative to the larger top's.  Next to a
+// reference that is no product the smaller counts for nothing: two values there lie 2^7 apart, times L.  (Where
+// m alone is so far, below, M - T is -128 at most, the smaller's sum 2^31 and top's 2^-64 at least: less than
+// a rounding.)
 __device__ __forceinline__ float stat_shift(float m, float top, float L) {
-    return m == top ? 0.f : fmaxf(stat_ref(m, L) - stat_ref(top, L), kFarBelow);
+    const float T = stat_ref(top, L);
+    const float y = fabsf(T) < kRefMost ? fmaxf(stat_ref(m, L) - T, kFarBelow) : kFarBelow;
+    return m == top ? 0.f : y;
 }
 
 __device__ __forceinline__ Stat stat_combine(const Stat& a, const Stat& b, float L) {
@@ -88,7 +99,7 @@ __device__ __forceinline__ Stat stat_warp(Stat a, float L) {
 // log sum exp((x - m) / temperature), 0 where nothing is allowed.
 __device__ __forceinline__ float stat_logd(const Stat& t, float L) {
     const float M = stat_ref(t.m, L);
-    return kLn2f * (log2f(t.d) - (fabsf(M) < kRefMost ? fmaf(t.m, L, -M) : 0.f));
+    return kLn2f * (log2f(t.d) - stat_short(t.m, M, L));
 }
 __device__ __forceinline__ float stat_entropy(const Stat& t) { return kLn2f * (log2f(t.d) - t.s / t.d); }
 
@@ -97,7 +108,7 @@ __device__ __forceinline__ bool stat_none(float m, float d) { return m == -INFIN
 
 // One logit more.
 __device__ __forceinline__ void stat_add(Stat& a, float x, float L) {
-    const float M = stat_ref(x, L), y = fabsf(M) < kRefMost ? fmaf(x, L, -M) : 0.f;
+    const float y = stat_short(x, stat_ref(x, L), L);
     Stat b{x, ex2_approx(y), 0.f};
     b.s = b.d * y;
     if (x == -INFINITY) b.d = 0.f;
@@ -208,7 +219,8 @@ __device__ __forceinline__ float stat_tile(Stat& a, const uint4* tile, int nv, f
     // the maximum).  Without a maximum 2^y is 0 for any logit there is.
     const float top_or_low = a.m == -INFINITY ? kFarBelow : a.m;
     const float least = ENT ? top_or_low - fmaxf(200.f / L, fabsf(top_or_low) * 0.015625f) : 0.f;
-    // rarely met: a row at the type's lowest value (of float16, where `least` is none of its)
+    // rarely met: a thread that has seen only a mask's large values (in float16, where `least` is none of its).
+    // 4096 x 128000 bf16 with entropy, one token of 64 allowed, the rest -1e30: 193 us, -1e9 or -inf: 164
     const bool far = !(fabsf(ref) < kRefMost);
     const bool slow = far || (ENT && std::is_same<T, __half>::value && least < -65504.f);
     const bool again = __any_sync(kFull, slow);
