@@ -65,7 +65,6 @@ struct ListRow {
     float em, ed;     // statistics of the student's logits around the body
     int bad;          // a token out of range
 };
-constexpr unsigned kTwice = 0x8000u;  // of a slot, beside the number of the entry that found it first
 inline int list_slots(int K) {
     int n = 64;
     while (n < 2 * K) n *= 2;
@@ -313,24 +312,15 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
         if constexpr (GRAD) {
             // of a token's entries one, the first to find a slot, writes for all
 #pragma unroll 1
-            for (int k = lane; k < p.slots; k += 32) slots[k] = 0xffffu;
+            for (int k = lane; k < p.slots; k += 32) slots[k] = kSlotFree;
             __syncwarp();
 #pragma unroll 1
             for (int k = lane; k < K; k += 32) {
                 const int col = e[k].col;
                 if (col < 0) continue;
-                for (uint32_t h = ((uint32_t)col * 2654435761u) >> 7;; ++h) {
-                    h &= (uint32_t)p.slots - 1u;
-                    const unsigned short was = atomicCAS(reinterpret_cast<unsigned short*>(&slots[h]),
-                                                         (unsigned short)0xffffu, (unsigned short)k);
-                    if (was == 0xffffu) break;
-                    if (e[was & 0x7fffu].col == col) {
-                        again = true;
-                        e[k].col = -2 - col;
-                        // (its two slots' word: kTwice may be there already)
-                        atomicOr(reinterpret_cast<unsigned*>(slots + (h & ~1u)), kTwice << (16u * (h & 1u)));
-                        break;
-                    }
+                if (list_enter(slots, (uint32_t)p.slots, k, col, [&](int j) { return e[j].col; }, slot_cas)) {
+                    again = true;
+                    e[k].col = -2 - col;
                 }
             }
             again = __any_sync(kFull, again);
@@ -371,8 +361,8 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
                 for (int h = lane; h < p.slots; h += 32) {
                     const unsigned mine = slots[h];
 #pragma unroll 1
-                    for (unsigned m = __ballot_sync(kFull, mine != 0xffffu && (mine & kTwice)); m; m &= m - 1u) {
-                        const int k = __shfl_sync(kFull, mine, __ffs(m) - 1) & 0x7fffu, col = e[k].col;
+                    for (unsigned m = __ballot_sync(kFull, slot_twice(mine)); m; m &= m - 1u) {
+                        const int k = slot_entry(__shfl_sync(kFull, mine, __ffs(m) - 1)), col = e[k].col;
                         float c = 0.f;
 #pragma unroll 1
                         for (int j = lane; j < K; j += 32)

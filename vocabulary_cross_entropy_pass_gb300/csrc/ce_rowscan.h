@@ -3,6 +3,7 @@
 // ce_rowscan.cuh's row types.
 #pragma once
 
+#include "ce_list_table.h"
 #include "ce_rowscan.cuh"
 
 namespace gbce {
@@ -59,6 +60,11 @@ RowTokens row_tokens(const int64_t* tokens, const int64_t* strides, int64_t n, i
                      int64_t ignore_idx);
 ce_status check_grad(const void* logits, int dtype, int64_t dim0, int64_t dim1, int64_t V, const int64_t* strides,
                      const void* grad, const int64_t* grad_strides);
+
+// What list_enter changes a slot with.
+__device__ __forceinline__ uint32_t slot_cas(uint16_t* slot, uint32_t expected, uint32_t value) {
+    return atomicCAS(reinterpret_cast<unsigned short*>(slot), (unsigned short)expected, (unsigned short)value);
+}
 
 __device__ __forceinline__ float teacher_at(const void* z, int dtype, int64_t k) {
     if (dtype == CE_F32) return __ldg(static_cast<const float*>(z) + k);

@@ -38,9 +38,8 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
 struct Listed {
     int col[kMaxListed];
     float coef[kMaxListed], x[kMaxListed];
-    alignas(4) unsigned short slot[2 * kMaxListed];  // entries by their columns' hash
+    uint16_t slot[2 * kMaxListed];  // of the table that finds tokens listed twice (ce_list_table.h)
 };
-constexpr unsigned kTwice = 0x8000u;  // of a slot, beside the number of the entry that found it first
 
 template <typename T, bool SECOND>  // SECOND: b is not zero
 __global__ void __launch_bounds__(kThreads) ce_softgrad_kernel(const __grid_constant__ SoftGradArgs p) {
@@ -210,26 +209,17 @@ __global__ void __launch_bounds__(kThreads) ce_softgrad_kernel(const __grid_cons
     }
     int slots = 64;
     while (slots < 2 * listed) slots *= 2;
-    for (int h = tid; h < slots; h += kThreads) ls.slot[h] = 0xffffu;
+    for (int h = tid; h < slots; h += kThreads) ls.slot[h] = kSlotFree;
     __syncthreads();
     for (int k = tid; k < listed; k += kThreads) {
         const int col = ls.col[k];
-        for (uint32_t h = ((uint32_t)col * 2654435761u) >> 7;; ++h) {
-            h &= (uint32_t)slots - 1u;
-            const unsigned short was = atomicCAS(&ls.slot[h], (unsigned short)0xffffu, (unsigned short)k);
-            if (was == 0xffffu) break;
-            if (ls.col[was & 0x7fffu] == col) {
-                ls.col[k] = -2 - col;
-                atomicOr(reinterpret_cast<unsigned*>(&ls.slot[h & ~1u]), kTwice << (16u * (h & 1u)));
-                break;
-            }
-        }
+        if (list_enter(ls.slot, (uint32_t)slots, k, col, [&](int j) { return ls.col[j]; }, slot_cas)) ls.col[k] = -2 - col;
     }
     __syncthreads();
     for (int h = warp * 32; h < slots; h += kThreads) {
         const unsigned mine = ls.slot[h + lane];
-        for (unsigned m = __ballot_sync(kFull, mine != 0xffffu && (mine & kTwice)); m; m &= m - 1u) {
-            const int k = __shfl_sync(kFull, mine, __ffs(m) - 1) & 0x7fffu, col = ls.col[k];
+        for (unsigned m = __ballot_sync(kFull, slot_twice(mine)); m; m &= m - 1u) {
+            const int k = slot_entry(__shfl_sync(kFull, mine, __ffs(m) - 1)), col = ls.col[k];
             float c = 0.f;
             for (int j = lane; j < listed; j += 32)
                 if (ls.col[j] == col || ls.col[j] == -2 - col) c += ls.coef[j];
