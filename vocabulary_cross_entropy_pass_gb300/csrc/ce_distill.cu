@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(kRowThreads, GRAD && NV == 8 ? 1 : 2) ce_disti
                 }
             }
             if (!warp_wait(bars, &bars.stored[q], ph)) break;
+            __syncwarp();  // a listed column may be one of the elements around the body, that another lane has stored
 #pragma unroll 1
             for (int k = lane; k < K && !zero; k += 32) {
                 const int col = e[k].col;
