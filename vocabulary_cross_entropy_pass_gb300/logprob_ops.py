@@ -67,7 +67,7 @@ class _TokenLogprobs(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_lp, grad_ent, *_):
         logits, stats, tokens = ctx.saved_tensors
-        if grad_lp is not None and grad_lp.numel() == 0 and logits.numel() > 0:
+        if grad_lp is not None and grad_lp.dim() == logits.dim() and grad_lp.shape[-1] == 0:
             grad_lp = None  # lists of no tokens
         if grad_lp is None and grad_ent is None:
             return None, None, None, None, None
