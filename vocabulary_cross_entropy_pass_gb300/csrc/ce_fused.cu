@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (sizeof(T) == 4 ? 2 : 3) : 1) 
             }
         }
         const float mw = warp_allmax(mt);
-        const float mwl = (mw == -INFINITY) ? 0.f : mw * kLog2e;
+        const float mwl = -minus_ref(mw);
         float pv[NV][GRAD ? VEC : 1];
         float dt = 0.f, st = 0.f;
 #pragma unroll

@@ -214,7 +214,7 @@ __device__ __forceinline__ float4 epilogue_row(const LmArgs& p, uint32_t tbase, 
                 }
                 m = cm;
             }
-            const float nm = -m * kLog2e;
+            const float nm = minus_ref(m);
             const float2 NM = make_float2(nm, nm);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -241,7 +241,7 @@ __device__ __forceinline__ float4 epilogue_row(const LmArgs& p, uint32_t tbase, 
                 }
                 m = cm;
             }
-            const float nm = -m * kLog2e;
+            const float nm = minus_ref(m);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const float2 x = VT::unpack_pair(pk[e]);

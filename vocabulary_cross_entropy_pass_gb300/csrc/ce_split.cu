@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kSplitThreads) ce_split_stats_kernel(const __g
                 if (m != -INFINITY) d *= ex2_approx((m - vm) * kLog2e);
                 m = vm;
             }
-            const float nml = -m * kLog2e;
+            const float nml = minus_ref(m);
 #pragma unroll
             for (int u = 0; u < kSplitBatch; ++u) {
                 const int64_t v = vb + (int64_t)u * kSplitThreads;
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kSplitThreads) ce_split_stats_kernel(const __g
             if (m != -INFINITY) d *= ex2_approx((m - vm) * kLog2e);
             m = vm;
         }
-        const float nml = -m * kLog2e;
+        const float nml = minus_ref(m);
 #pragma unroll
         for (int u = 0; u < kSplitBatch; ++u) {
             const int64_t v = vb + (int64_t)u * kSplitThreads;

@@ -241,7 +241,7 @@ __device__ __forceinline__ void stats_tile(const uint4* tile, int tid, int nvec,
         }
         m = tmf;
     }
-    const float nml = (m == -INFINITY) ? 0.f : -m * kLog2e;
+    const float nml = minus_ref(m);
     const float2 L2 = make_float2(kLog2e, kLog2e);
     const float2 NM = make_float2(nml, nml);
 #pragma unroll

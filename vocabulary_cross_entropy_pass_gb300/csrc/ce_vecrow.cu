@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(THREADS, VrShape<THREADS>::kCtasPerSm)
                 }
                 m = vm;
             }
-            const float nml = -m * kLog2e;
+            const float nml = minus_ref(m);
             const float2 NM = make_float2(nml, nml);
 #pragma unroll
             for (int u = 0; u < kVrBatch; ++u) {
