@@ -497,8 +497,8 @@ typedef struct {
  * In CE_F32 a quotient is rounded once; in the 16-bit types it is a product with
  * the rounded reciprocal (at most 2^-23 of the value more, before the rounding to
  * the type).  A token that is not allowed gives mask_value whatever its logit (NaN
- * included); a row that allows none is mask_value throughout.  ce_fwd_bwd on
- * the result needs a finite mask_value (say -3e4: its smoothing term sums the
+ * included); a row that allows none is mask_value throughout.  ce_fwd_bwd with
+ * smoothing needs a finite mask_value (say -3e4: its smoothing term sums the
  * logits).  out may be the logits themselves (same strides).
  *   workspace    at least ce_logits_workspace_bytes(dim0*dim1, V, dtype, history_max,
  *                bias_max) bytes, 16-byte aligned, no initialisation; not shared

@@ -12,6 +12,7 @@ import vocabulary_cross_entropy_pass_gb300 as pkg
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda")
 E = 2.0 ** -24
+TINY = {torch.float32: 2.0 ** -125, torch.bfloat16: 2.0 ** -125, torch.float16: 2.0 ** -25}
 VALUES = [-1e4, -1e9, -2e9, -4e9, -1e10, -1e15, -1e20, -1e30, -1e33]
 PATHS = [("auto", pkg.CE_PATH_AUTO), ("row", pkg.CE_PATH_ROW), ("cluster", pkg.CE_PATH_CLUSTER),
          ("two_stage", pkg.CE_PATH_TWO_STAGE), ("stream", pkg.CE_PATH_STREAM), ("vecrow", pkg.CE_PATH_VECROW),
@@ -45,7 +46,7 @@ def check(x, t, loss, grad=None):
     p = torch.exp(y - lse[:, None])
     want = p.clone().scatter_add_(1, i[:, None], torch.full_like(xy, -1.0)[:, None])
     half = torch.finfo(x.dtype).eps / 2
-    off = (grad[0].double() - want).abs() - half * want.abs() * (1 + half) - E * (200 + 2 * lse.abs())[:, None] * p - 2.0 ** -125
+    off = (grad[0].double() - want).abs() - half * want.abs() * (1 + half) - E * (200 + 2 * lse.abs())[:, None] * p - TINY[x.dtype]
     off.scatter_(1, i[:, None], off.gather(1, i[:, None]) - 2 * E)  # the target's own difference
     assert float(off.max()) <= 0, float(off.max())
 
@@ -91,3 +92,40 @@ def test_class_weights_chunks_and_backward():
     t = t.clamp(max=23999)
     loss, lse = pkg.ce_vp_combine(parts, off, t)
     check(y, t, loss)
+
+
+@pytest.mark.parametrize("name,path", PATHS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("V", [4096, 12000, 50257])
+def test_masks_whose_sum_is_infinite(V, dtype, name, path):
+    """Without smoothing the sum of the logits is not part of the loss, so -inf and the lowest values are masks too."""
+    for value in (float(torch.finfo(dtype).min), -float("inf")):
+        for kind in ("front", "most"):
+            x, t = make(40, V, dtype, value, kind)
+            g = x.clone()
+            try:
+                loss = pkg.ce_fwd_bwd(g, t, label_smoothing=0.0, reduce_loss=False, force_path=path)
+            except pkg.CEError as e:
+                assert e.status == 8
+                return
+            check(x, t, loss, g)
+            check(x, t, pkg.ce_fwd_only(x, t, label_smoothing=0.0, reduce_loss=False, force_path=path))
+            loss = pkg.ce_fwd_bwd(x.clone(), t, label_smoothing=0.0, reduce_loss=True, force_path=path)
+            assert bool(torch.isfinite(loss).all())
+
+
+def test_processed_logits_into_the_loss():
+    """A mask of the default value, as process_logits leaves it, then the loss and its gradient."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    N, V = 24, 32000
+    x = (torch.randn(N, V, generator=g, device=DEV) * 3).to(torch.bfloat16)
+    bits = torch.randint(-2 ** 31, 2 ** 31, (N, (V + 31) // 32), generator=g, device=DEV).to(torch.int32)
+    y = pkg.ce_logits_process(x, mask=bits)
+    t = torch.argmax(y, 1)
+    z = y.unsqueeze(0)
+    grad = z.clone()
+    check(z, t.unsqueeze(0), pkg.ce_fwd_bwd(grad, t.unsqueeze(0), label_smoothing=0.0, reduce_loss=False), grad)
+    w = x.clone().requires_grad_()
+    loss = pkg.parallel_cross_entropy(pkg.process_logits(w, mask=bits).unsqueeze(0), t.unsqueeze(0), 0.0, True)
+    loss.backward()
+    assert bool(torch.isfinite(w.grad).all()) and bool(torch.isfinite(loss).all())

@@ -341,6 +341,12 @@ struct Part {
 
 __device__ __forceinline__ Part part_identity() { return Part{-INFINITY, 0.f, 0.f}; }
 
+// What smoothing adds to a loss: (a / V) of a sum over the vocabulary.  Without smoothing nothing, whatever
+// the sum: of logits masked by -inf, or by values as low as the type's, it is infinite.
+__device__ __forceinline__ float smoothing_term(float a_over_v, float sum) {
+    return a_over_v != 0.f ? a_over_v * sum : 0.f;
+}
+
 // Commutative combine: both terms are rescaled to the common max, so
 // combine(a, b) and combine(b, a) give the same bits.  This makes every lane
 // of a butterfly end with identical results.

@@ -682,7 +682,7 @@ ce_stream_kernel(const __grid_constant__ StreamArgs p) {
             if (ee >= 0) {
                 xe = VT::load1(rowp + ee * ES);
                 m = xe;
-                d2.x = 1.f;
+                d2.x = xe == -INFINITY ? 0.f : 1.f;
                 s2.x = xe;
             }
             if (ty < 0 && ee == y) xy_s[par] = xe;
@@ -767,8 +767,8 @@ ce_stream_kernel(const __grid_constant__ StreamArgs p) {
         const float wy = WT ? __ldg(p.cw + y) : 1.f;
         if (!(WT && GRAD) && tid == 0) {
             // weighted: (1-a) w_y (lse - x_y) + (a/V) (W lse - sum_j w_j x_j)
-            p.loss[r] = WT ? (1.f - p.a) * wy * (lse - xy) + p.a_over_v * (wsum * lse - G.S)
-                           : lse - (1.f - p.a) * xy - p.a_over_v * G.S;
+            p.loss[r] = WT ? (1.f - p.a) * wy * (lse - xy) + smoothing_term(p.a_over_v, wsum * lse - G.S)
+                           : lse - (1.f - p.a) * xy - smoothing_term(p.a_over_v, G.S);
             if (p.lse_out) p.lse_out[r] = lse;
         }
 
@@ -859,7 +859,7 @@ ce_stream_kernel(const __grid_constant__ StreamArgs p) {
                 if (tid == 0) {
                     float S = 0.f;
                     for (int w = 0; w < NW; ++w) S += sw_s[par * NW + w];
-                    p.loss[r] = (1.f - p.a) * wy * (lse - xy) + p.a_over_v * (wsum * lse - S);
+                    p.loss[r] = (1.f - p.a) * wy * (lse - xy) + smoothing_term(p.a_over_v, wsum * lse - S);
                     if (p.lse_out) p.lse_out[r] = lse;
                 }
             }

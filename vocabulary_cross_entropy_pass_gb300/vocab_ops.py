@@ -195,8 +195,8 @@ def ce_logits_process(logits: torch.Tensor, out: torch.Tensor | None = None, wor
     ``presence_penalty``, ``temperature`` float32 (N,); ``bias_tokens`` int64
     (N, K) and ``bias_values`` float32 (N, K); ``mask`` int32 (N, ceil(V/32)) or
     (ceil(V/32),), bit v % 32 of word v // 32 set where token v is allowed;
-    ``mask_value`` (default -inf; the cross-entropy pass needs a finite one,
-    say -3e4).  Tokens outside [0, V) are skipped; a row whose mask allows
+    ``mask_value`` (default -inf; the cross-entropy pass with smoothing needs a
+    finite one, say -3e4).  Tokens outside [0, V) are skipped; a row whose mask allows
     nothing is mask_value throughout."""
     return (_ext or _load()).logits_process(logits, out, workspace, stream, params)
 
