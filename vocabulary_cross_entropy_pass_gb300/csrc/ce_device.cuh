@@ -20,10 +20,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // Minus the reference of a running maximum m: exponentials are 2^(x log2e - m log2e) in one fused step.  The
 // product is off by up to 64 at 2^31, and soon by so much that 2^y leaves float32.  Below -2^30 (what a
-// thread has seen so far is a mask's -1e30, say) the reference is 0, and all such logits give 0, as they do
-// beside any larger one.  A row of nothing else has no result: its loss, lse - x, is lost in their size.
+// thread has seen so far is a mask's -1e30, say) the reference stays there, and such logits give 0, as they
+// do beside any larger one.  A row of nothing else has no result: its loss, lse - x, is lost in their size.
 constexpr float kLowestRef = -1073741824.f;
-__device__ __forceinline__ float minus_ref(float m) { return m < kLowestRef ? 0.f : -m * kLog2e; }
+__device__ __forceinline__ float minus_ref(float m) { return -fmaxf(m, kLowestRef) * kLog2e; }
 constexpr unsigned kFull = 0xffffffffu;
 // Bounded waits give up after this many nanoseconds of %globaltimer.
 constexpr uint64_t kWaitLimitNs = 1500ull * 1000ull * 1000ull;

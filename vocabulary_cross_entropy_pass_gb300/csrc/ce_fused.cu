@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? (sizeof(T) == 4 ? 2 : 3) : 1) 
             }
         }
         if (rank == 0 && tid == 0) {
-            p.loss[r] = lse - (1.f - p.a) * xy - smoothing_term(p.a_over_v, G.S);
+            p.loss[r] = lse - (1.f - p.a) * xy - p.a_over_v * G.S;
             if (p.lse_out) p.lse_out[r] = lse;
         }
         ++consumed;

@@ -248,7 +248,7 @@ ce_rows_kernel(const __grid_constant__ RowsArgs p) {
         const float lse = m + logf(d);
         const float xy = VT::load1(reinterpret_cast<const unsigned char*>(tile) + y * ES);
         if (lane == 0) {
-            p.loss[r] = lse - (1.f - p.a) * xy - smoothing_term(p.a_over_v, S);
+            p.loss[r] = lse - (1.f - p.a) * xy - p.a_over_v * S;
             if (p.lse_out) p.lse_out[r] = lse;
         }
 
