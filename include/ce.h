@@ -54,6 +54,9 @@
  *     rows on the 16-byte grid take the TMA kernels, others 16-byte loads
  *     between a scalar head and tail (CE_PATH_VECROW, the two-stage kernels,
  *     ce_bwd, ce_vp_partials);
+ *   - logits may be masked by any value below the others, -inf included where
+ *     there is no smoothing; a row whose every logit is below -2^30 has no
+ *     finite loss from ce_fwd_bwd and its kin;
  *   - errors found on the host are returned before anything is launched;
  *     a target outside [0, V) that is not ignore_idx is found on the device:
  *     that row gets loss NaN and a zero gradient, and the device error word

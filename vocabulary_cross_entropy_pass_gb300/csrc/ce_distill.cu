@@ -9,13 +9,16 @@
 //
 // Bound by HBM: a logit read, a gradient written.  ce_distill_kernel streams whole rows
 // (ce_rowscan.cuh): the statistics in a first pass, the gradient in a second, whose tiles
-// come from L2, which the first was asked to keep them in.  Each side warp takes every
+// come from L2, which the first was asked to keep them in, as far as the rows that are begun
+// fit: a row per SM (1 GB of logits in all: rows of 256 KB 1.02 times from HBM, of 512 KB 1.24,
+// of 1 MB 1.84; 1024 x 256000 float32 447 us, 0.70 of the copy rate).  Each side warp takes every
 // third row: its list while the rows before are streamed (the teacher's softmax, the
 // student's logits of its tokens, a hash table that finds tokens listed twice), then
 // its loss and, once its gradient is stored, its listed columns again.
 // Measured, bf16: 4096 x 128000, 64 tokens, loss and gradient 311 us (6.4 TB/s), 0.96 of the
 // copy rate; the loss alone of 2048 x 100277, 256 tokens, 77 us (5.4 TB/s).  Lists of 256
-// tokens and more are bound by the side warps (4096 x 32000: 64 tokens 97 us, 256 169, 1024 531).
+// tokens and more are bound by the side warps (4096 x 32000: 64 tokens 96 us, 256 169, 1024 343 of
+// distinct tokens and 552 of tokens drawn with replacement, whose repeats are summed).
 #include <math.h>
 
 #include <type_traits>
@@ -469,6 +472,8 @@ cudaError_t launch_distill_k(DistillArgs a, cudaStream_t s) {
     const size_t list = list_bytes(a.tokens.n, GRAD);
     constexpr bool one = GRAD && NV == 8;  // CTA per SM
     constexpr size_t tile = kMainThreads * NV * 16, room = (one ? 222 : 111) * 1024;
+    // (Without a gradient the lists leave three slots up to 320 tokens, two up to 1002 and then one; they bound
+    // the kernel by then: 2048 x 100277 bf16 with 320 tokens 97 us, 1002 177, 1003 170, 1024 157.)
     a.stages = (int)((room - list) / tile);
     if (a.stages > kRingMost) a.stages = kRingMost;
     const size_t smem = a.stages * tile + list;

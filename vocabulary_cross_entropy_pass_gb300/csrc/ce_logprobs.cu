@@ -12,7 +12,11 @@
 // Measured on bf16 rows of 128000 columns, 4096 of them: the given token alone 154 us (6.8
 // TB/s, the copy rate), with the entropy 155, with 20 likeliest 161, with 64 175 (5.9 TB/s),
 // with 256 what the side warps' selection takes; 4096 x 50257 70, 74 and (20) 90 us;
-// 256 x 128000, in segments, 31 us; 4 x 32000 12 us, two kernels' latency.
+// 256 x 128000 with the entropy and 20 likeliest, a row to a CTA, 31 us; 4 x 32000 with 5 likeliest, in
+// segments, 12 us, two kernels' latency.  float32, 20 and 64 likeliest: 4096 x 128000, every row in two
+// segments for its maxima's room, 330 and 361 us (5.8 TB/s), 4096 x 50257, in one piece, 143 and 170.
+// Given tokens from the 33rd on are loaded 32 at a time, each load waited for: 32 of 4096 x 128000 bf16
+// 164 us, 64 170, 256 201, 1024 378; 1024 of 4 x 32000 64 us.
 #include <math.h>
 
 #include "ce_rowscan.h"

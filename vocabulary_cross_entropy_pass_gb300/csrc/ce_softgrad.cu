@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(kThreads) ce_softgrad_kernel(const __grid_cons
     if (listed == 0) return;
     // Of a token's entries one writes for all.  Up to 64 are looked at by each other; of more, the
     // first to find a slot of a hash table writes, and a warp sums what belongs to it, in an
-    // order fixed by the list (4096 x 32000, bf16, 64 tokens: 98 us, with the table 105; 256: 143
-    // and 126; 1024: 1110 and 215).
+    // order fixed by the list (4096 x 32000, bf16, drawn with replacement, 64 tokens: 98 us, with the
+    // table 105; 256: 143 and 118; 1024: 1110 and 212).
     if (listed <= 64) {
         __syncthreads();
         if (tid >= listed) return;
