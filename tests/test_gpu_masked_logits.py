@@ -129,3 +129,49 @@ def test_processed_logits_into_the_loss():
     loss = pkg.parallel_cross_entropy(pkg.process_logits(w, mask=bits).unsqueeze(0), t.unsqueeze(0), 0.0, True)
     loss.backward()
     assert bool(torch.isfinite(w.grad).all()) and bool(torch.isfinite(loss).all())
+
+
+@pytest.mark.parametrize("name,path", PATHS)
+@pytest.mark.parametrize("smoothing", [0.0, 0.1])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_no_number_anywhere_in_the_row(name, path, smoothing, value):
+    """A NaN or +inf makes its row's loss NaN wherever it lies, among the elements around the aligned body as well."""
+    for V in (4099, 12000, 50257):
+        for dtype in (torch.float32, torch.bfloat16):
+            x = (torch.randn(1, 24, V, generator=torch.Generator(device=DEV).manual_seed(2), device=DEV) * 3).to(dtype)
+            t = torch.full((1, 24), 9, dtype=torch.int64, device=DEV)
+            for r, c in enumerate([0, 1, 2, 3, 4, 5, 6, 7, 8, V - 8, V - 7, V - 6, V - 5, V - 4, V - 3, V - 2, V - 1, V // 2]):
+                x[0, r, c] = value
+            try:
+                loss = pkg.ce_fwd_only(x, t, label_smoothing=smoothing, reduce_loss=False, force_path=path)
+            except pkg.CEError as e:
+                assert e.status == 8
+                continue
+            assert bool(loss[:18].isnan().all()) and bool(torch.isfinite(loss[18:]).all())
+            loss = pkg.ce_fwd_bwd(x.clone(), t, label_smoothing=smoothing, reduce_loss=False, force_path=path)
+            assert bool(loss[:18].isnan().all()) and bool(torch.isfinite(loss[18:]).all())
+
+
+@pytest.mark.parametrize("value", [-1e30, -float("inf")])
+def test_shards_chunks_and_weights(value):
+    V = 30011
+    x, t = make(40, V, torch.bfloat16, value, "front")
+    weights = torch.ones(V, device=DEV)
+    for smooth_free in (None, weights):
+        g = x.clone()
+        loss = pkg.ce_fwd_bwd(g, t, label_smoothing=0.0, reduce_loss=False, class_weights=smooth_free)
+        check(x, t, loss, g)
+    for chunks in (3, 8):
+        g = x.clone()
+        loss = pkg.ce_fwd_bwd(g, t, label_smoothing=0.0, reduce_loss=False, num_vocab_chunks=chunks)
+        check(x, t, loss, g)
+    off = [0, 5003, 15001, 20003, V]
+    parts = torch.stack([pkg.ce_vp_partials(x[:, :, a:b], t, a) for a, b in zip(off, off[1:])])
+    loss, lse = pkg.ce_vp_combine(parts, off, t)
+    check(x, t, loss)
+    grads = [pkg.ce_vp_bwd(x[:, :, a:b], t, a, V, lse) for a, b in zip(off, off[1:])]
+    check(x, t, loss, torch.cat(grads, 2))
+    x[0, 3, [0, 5002, 5003, V - 1]] = float("nan")
+    parts = torch.stack([pkg.ce_vp_partials(x[:, :, a:b], t, a) for a, b in zip(off, off[1:])])
+    loss, lse = pkg.ce_vp_combine(parts, off, t)
+    assert bool(loss.view(-1)[3].isnan()) and int(loss.isnan().sum()) == 1

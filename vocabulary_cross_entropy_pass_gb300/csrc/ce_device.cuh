@@ -341,6 +341,9 @@ struct Part {
 
 __device__ __forceinline__ Part part_identity() { return Part{-INFINITY, 0.f, 0.f}; }
 
+// v, or a NaN where x is one or infinite: what such a logit makes of its row's sum.
+__device__ __forceinline__ float no_number_or(float x, float v) { return v + (x - x); }
+
 // What smoothing adds to a loss: (a / V) of a sum over the vocabulary.  Without smoothing nothing, whatever
 // the sum: of logits masked by -inf, or by values as low as the type's, it is infinite.
 __device__ __forceinline__ float smoothing_term(float a_over_v, float sum) {

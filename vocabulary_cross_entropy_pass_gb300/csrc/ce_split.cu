@@ -138,9 +138,9 @@ __global__ void __launch_bounds__(kSplitThreads) ce_split_stats_kernel(const __g
     const int64_t ee = span16_edge(sp, k0, k1, threadIdx.x);
     if (ee >= 0) {
         const float x = VT::load1(row + ee * ES);  // the thread's first element
-        if (x > m) {
+        if (!(x <= m)) {
             m = x;
-            d = 1.f;  // exp(x - m); a -inf element adds nothing
+            d = no_number_or(x, 1.f);  // exp(x - m); a -inf element adds nothing
         }
         S = WT ? __ldg(p.cw + ee) * x : x;
     }

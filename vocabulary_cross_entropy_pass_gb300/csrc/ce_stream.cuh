@@ -682,7 +682,7 @@ ce_stream_kernel(const __grid_constant__ StreamArgs p) {
             if (ee >= 0) {
                 xe = VT::load1(rowp + ee * ES);
                 m = xe;
-                d2.x = xe == -INFINITY ? 0.f : 1.f;
+                d2.x = xe == -INFINITY ? 0.f : no_number_or(xe, 1.f);
                 s2.x = xe;
             }
             if (ty < 0 && ee == y) xy_s[par] = xe;

@@ -130,9 +130,9 @@ __global__ void __launch_bounds__(THREADS, VrShape<THREADS>::kCtasPerSm)
         float2 d2 = make_float2(0.f, 0.f), s2 = make_float2(0.f, 0.f);
         if (ee >= 0) {  // the thread's first element: exp(x - m) = 1 (nothing for -inf)
             const float x = VT::load1(row + ee * ES);
-            if (x > m) {
+            if (!(x <= m)) {
                 m = x;
-                d2.x = 1.f;
+                d2.x = no_number_or(x, 1.f);
             }
             s2.x = x;
         }

@@ -78,9 +78,9 @@ __global__ void __launch_bounds__(kVpThreads, 4) ce_vp_partials_kernel(const __g
         const int64_t ee = span16_edge(sp, 0, p.V, threadIdx.x);
         if (ee >= 0) {  // the thread's first element: exp(x - m) = 1 (nothing for -inf)
             const float x = VT::load1(row + ee * ES);
-            if (x > m) {
+            if (!(x <= m)) {
                 m = x;
-                d2.x = 1.f;
+                d2.x = no_number_or(x, 1.f);
             }
             s2.x = x;
         }
