@@ -344,11 +344,9 @@ __device__ __forceinline__ Part part_identity() { return Part{-INFINITY, 0.f, 0.
 // v, or a NaN where x is one or infinite: what such a logit makes of its row's sum.
 __device__ __forceinline__ float no_number_or(float x, float v) { return v + (x - x); }
 
-// What smoothing adds to a loss: (a / V) of a sum over the vocabulary.  Without smoothing nothing, whatever
-// the sum: of logits masked by -inf, or by values as low as the type's, it is infinite.
-__device__ __forceinline__ float smoothing_term(float a_over_v, float sum) {
-    return a_over_v != 0.f ? a_over_v * sum : 0.f;
-}
+// The sum over the vocabulary that smoothing adds a / V of to a loss.  Without smoothing it is left out, whatever
+// it is: of logits masked by -inf, or by values as low as the type's, it is infinite.
+__device__ __forceinline__ float smoothing_sum(float a_over_v, float sum) { return a_over_v != 0.f ? sum : 0.f; }
 
 // Commutative combine: both terms are rescaled to the common max, so
 // combine(a, b) and combine(b, a) give the same bits.  This makes every lane

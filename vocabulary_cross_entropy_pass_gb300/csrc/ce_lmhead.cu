@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(256) ce_lm_combine_kernel(const float4* __rest
     if (lane == 0) {
         const float xy = Vec<T>::load1(logits + row * ldl + y);
         const float l = G.m + logf(G.d);
-        loss[row] = l - (1.f - a) * xy - smoothing_term(a / (float)V, G.S);
+        loss[row] = l - (1.f - a) * xy - (a / (float)V) * smoothing_sum(a / (float)V, G.S);
         lse_out[row] = l;
     }
 }

@@ -247,9 +247,9 @@ __global__ void __launch_bounds__(kSplitThreads) ce_split_grad_kernel(const __gr
                 float loss;
                 if (WT)  // (1-a) w_y (lse - x_y) + (a/V) (W lse - sum_j w_j x_j)
                     loss = (1.f - p.a) * __ldg(p.cw + y) * (lse - xy) +
-                           smoothing_term(p.a_over_v, (float)(*p.wsum) * lse - G.S);
+                           p.a_over_v * ((float)(*p.wsum) * lse - smoothing_sum(p.a_over_v, G.S));
                 else
-                    loss = lse - (1.f - p.a) * xy - smoothing_term(p.a_over_v, G.S);
+                    loss = lse - (1.f - p.a) * xy - p.a_over_v * smoothing_sum(p.a_over_v, G.S);
                 p.loss[r] = loss;
                 if (p.lse_out) p.lse_out[r] = lse;
             }

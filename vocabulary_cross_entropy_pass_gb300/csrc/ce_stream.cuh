@@ -178,6 +178,11 @@ __device__ __forceinline__ void named_bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// (1-a) w_y (lse - x_y) + (a/V) (W lse - sum_j w_j x_j), the products rounded in this order.
+__device__ __forceinline__ float weighted_loss(float cy, float lse, float xy, float a_over_v, float wsum, float S) {
+    return fmaf(a_over_v, fmaf(wsum, lse, -smoothing_sum(a_over_v, S)), __fmul_rn(cy, lse - xy));
+}
+
 // Rows handed from the producer warp to the consumer warps ahead of their tiles.
 constexpr int kRowQ = 8;
 
@@ -766,9 +771,8 @@ ce_stream_kernel(const __grid_constant__ StreamArgs p) {
         const float xy = xy_s[par];
         const float wy = WT ? __ldg(p.cw + y) : 1.f;
         if (!(WT && GRAD) && tid == 0) {
-            // weighted: (1-a) w_y (lse - x_y) + (a/V) (W lse - sum_j w_j x_j)
-            p.loss[r] = WT ? (1.f - p.a) * wy * (lse - xy) + smoothing_term(p.a_over_v, wsum * lse - G.S)
-                           : lse - (1.f - p.a) * xy - smoothing_term(p.a_over_v, G.S);
+            p.loss[r] = WT ? weighted_loss((1.f - p.a) * wy, lse, xy, p.a_over_v, wsum, G.S)
+                           : lse - (1.f - p.a) * xy - p.a_over_v * smoothing_sum(p.a_over_v, G.S);
             if (p.lse_out) p.lse_out[r] = lse;
         }
 
@@ -859,7 +863,7 @@ ce_stream_kernel(const __grid_constant__ StreamArgs p) {
                 if (tid == 0) {
                     float S = 0.f;
                     for (int w = 0; w < NW; ++w) S += sw_s[par * NW + w];
-                    p.loss[r] = (1.f - p.a) * wy * (lse - xy) + smoothing_term(p.a_over_v, wsum * lse - S);
+                    p.loss[r] = weighted_loss((1.f - p.a) * wy, lse, xy, p.a_over_v, wsum, S);
                     if (p.lse_out) p.lse_out[r] = lse;
                 }
             }

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(THREADS, VrShape<THREADS>::kCtasPerSm)
         }
         const float lse = G.m + logf(G.d);
         if (tid == 0) {
-            p.loss[r] = lse - (1.f - p.a) * xy - smoothing_term(p.a_over_v, G.S);
+            p.loss[r] = lse - (1.f - p.a) * xy - p.a_over_v * smoothing_sum(p.a_over_v, G.S);
             if (p.lse_out) p.lse_out[r] = lse;
         }
         if (!GRAD) continue;

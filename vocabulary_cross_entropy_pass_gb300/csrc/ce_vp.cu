@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(256) ce_vp_combine_kernel(const __grid_constan
     }
     const float lse = G.m + logf(G.d);
     p.lse[r] = lse;
-    p.loss[r] = lse - (1.f - p.a) * xy - smoothing_term(p.a_over_v, G.S);
+    p.loss[r] = lse - (1.f - p.a) * xy - p.a_over_v * smoothing_sum(p.a_over_v, G.S);
 }
 
 template <typename T>
