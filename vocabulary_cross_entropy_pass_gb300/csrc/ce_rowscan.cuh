@@ -69,9 +69,9 @@ __device__ __forceinline__ float stat_short(float m, float M, float L) {
     return fabsf(M) < kRefMost ? fmaf(m, L, -M) : 0.f;
 }
 // The exponent by which what is relative to m's reference counts relative to the larger top's.  Next to a
-// reference that is no product the smaller counts for nothing: two values there lie 2^7 apart, times L.  (Where
-// m alone is so far, below, M - T is -128 at most, the smaller's sum 2^31 and top's 2^-64 at least: less than
-// a rounding.)
+// reference that is no product the smaller counts for nothing: two logits there lie 2^7 apart in the
+// exponent.  (Where m alone is so far, below, M - T is -128 at most, its sum 2^31 at most and top's 2^-64 at
+// least: less than a rounding.)
 __device__ __forceinline__ float stat_shift(float m, float top, float L) {
     const float T = stat_ref(top, L);
     const float y = fabsf(T) < kRefMost ? fmaxf(stat_ref(m, L) - T, kFarBelow) : kFarBelow;
