@@ -7,8 +7,8 @@
 //   log d = ln 2 (log2 d - (m L - M)),  log-probability = (x - m) / temperature - log d,
 //   entropy = ln 2 (log2 d - s / d).
 // Where M is so large that its rounding would carry 2^y out of float32 (a row, or what a thread
-// has seen of it, at a mask's -1e30: y is off by 2^76 there) y = (x - m) L.  A logit of -inf counts for nothing in d and s; a NaN makes
-// both NaN.
+// has seen of it, at a mask's -1e30: y is off by 2^76 there) y = (x - m) L.  A logit of -inf
+// counts for nothing in d and s; a NaN makes both NaN.
 //
 // The streaming kernels built on this (ce_logprobs.cu, ce_distill.cu) are persistent;
 // the warps of a CTA have three parts and meet at mbarriers alone:
